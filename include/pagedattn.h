@@ -86,7 +86,8 @@ typedef enum {
 #define PA_DEVERR_SLOT 2       /* a slot at or past num_blocks * block_size */
 #define PA_DEVERR_SEQ_LEN 4    /* seq_len above max_seq_len or the table's capacity */
 #define PA_DEVERR_TIMEOUT 8    /* a bounded wait for a TMA copy ran out (the work was abandoned) */
-#define PA_DEVERR_WORKSPACE 16 /* an FP8 prefill chunk's 16-bit copy did not fit (its rows were skipped) */
+#define PA_DEVERR_WORKSPACE 16 /* an FP8 or 4-bit prefill chunk's 16-bit copy did not fit (its rows were skipped) */
+#define PA_DEVERR_POSITION 32  /* a rotation position outside the cos/sin table (the row was skipped) */
 
 /* Library ABI version (major * 100 + minor). */
 int pa_version(void);
@@ -325,6 +326,140 @@ int pa_paged_attention_prefill_fp8(void* out, const void* q, const void* k_cache
                                    float scale, float k_scale, float v_scale, int num_q_heads,
                                    int num_kv_heads, int head_dim, int block_size, void* workspace,
                                    size_t workspace_bytes, int dtype, void* stream);
+
+/*
+ * Appending new tokens with the position rotation applied on the way: what
+ * pa_paged_kv_write (and its FP8 and 4-bit forms) does, with the rotation of
+ * the step's queries and keys in the same pass over them.
+ *   q             [num_tokens, num_q_heads, head_dim]; q_out likewise.  q_out
+ *                 may be q itself (same pointer and stride), and may not
+ *                 overlap any other input.  num_q_heads may be 0 (keys only).
+ *   key, value    [num_tokens, num_kv_heads, head_dim], left as they are.
+ *   *_stride      elements from one token's row to the next, a multiple of 8
+ *                 and at least the row's length; head rows lie head_dim apart
+ *                 within a token (so q, key and value may be slices of one
+ *                 fused projection's rows).
+ *   positions     int64 [num_tokens], the row of cos_sin for each token.
+ *   cos_sin       fp32 [max_positions, rot_dim]: rot_dim / 2 cosines, then
+ *                 rot_dim / 2 sines of the position's angles.
+ *   rot_dim       rotated dims of a head: a multiple of 16, 16 .. head_dim; the
+ *                 dims past it are copied.
+ *   interleaved   0: pair i is dims (i, i + rot_dim / 2); 1: (2i, 2i + 1).
+ * A pair (a, b) becomes (a cos - b sin, b cos + a sin), computed in fp32 with
+ * each product and each sum rounded; queries, and the keys of a 16-bit cache,
+ * are then rounded to `dtype`; the keys of an FP8 or 4-bit cache are quantised
+ * from the fp32 values.  Values are written as they are (or quantised).
+ * A negative slot means "no cache write" (the query row is still rotated); a
+ * slot past the pool is dropped and sets PA_DEVERR_SLOT.  A position outside
+ * 0 .. max_positions - 1 sets PA_DEVERR_POSITION and leaves the token's q_out
+ * row and cache slot unwritten.  Two rows naming one slot race.
+ */
+int pa_paged_rope_kv_write(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, const void* key,
+                           int64_t key_stride, const void* value, int64_t value_stride, void* k_cache,
+                           void* v_cache, const int64_t* slot_mapping, const int64_t* positions,
+                           const float* cos_sin, int max_positions, int num_tokens, int num_blocks,
+                           int num_q_heads, int num_kv_heads, int head_dim, int rot_dim, int interleaved,
+                           int block_size, int dtype, void* stream);
+
+/* The same into head-major FP8 (E4M3) pools (head_dim 128); k_scale and
+ * v_scale as in pa_paged_kv_write_fp8. */
+int pa_paged_rope_kv_write_fp8(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, const void* key,
+                               int64_t key_stride, const void* value, int64_t value_stride, void* k_cache,
+                               void* v_cache, const int64_t* slot_mapping, const int64_t* positions,
+                               const float* cos_sin, int max_positions, int num_tokens, int num_blocks,
+                               int num_q_heads, int num_kv_heads, int head_dim, int rot_dim, int interleaved,
+                               int block_size, int src_dtype, float k_scale, float v_scale, void* stream);
+
+/*
+ * 4-bit KV cache (head_dim 64 or 128): E2M1 codes with one E4M3 scale per
+ * group of 16 consecutive dims of a (token, kv head) row and one fp32 scale
+ * per pool; value = e2m1(code) * e4m3(group scale) * pool scale, 4.5 bits per
+ * value.  E2M1 magnitudes for codes 0 .. 7 are 0, 0.5, 1, 1.5, 2, 3, 4, 6; bit
+ * 3 is the sign.
+ *
+ * Pools are [num_blocks, num_kv_heads, pa_fp4_tile_bytes(head_dim)] bytes.  A
+ * tile holds the 16 token rows of one (block, kv head): 16 rows of head_dim / 2
+ * code bytes (dims 2j and 2j + 1 in the low and high nibble of byte j), then
+ * the group scales, [16 tokens][head_dim / 16] in a K tile and
+ * [head_dim / 16][16 tokens] in a V tile.  pa_copy_blocks copies blocks of such
+ * pools with head_dim = pa_fp4_tile_bytes / 16 and elem_bytes = 1.
+ *
+ * pa_paged_kv_write_fp4 quantises each group of new elements x (fp16/bf16
+ * `src_dtype`) in fp32, each step rounded to nearest even: y = x * (1.0f /
+ * pool scale); s = e4m3(max|y| / 6), saturating at 448; code = e2m1(y / s),
+ * saturating at 6.  A group whose s rounds to 0 gets zero codes; a NaN makes
+ * the group's scale NaN.  Other arguments as pa_paged_kv_write_fp8.
+ */
+int pa_fp4_tile_bytes(int head_dim);   /* 9 * head_dim; 0 for an unsupported head_dim */
+
+int pa_paged_kv_write_fp4(const void* key, const void* value, void* k_cache, void* v_cache,
+                          const int64_t* slot_mapping, int num_tokens, int num_blocks, int num_kv_heads,
+                          int head_dim, int block_size, int src_dtype, float k_scale, float v_scale, void* stream);
+
+/* pa_paged_rope_kv_write into 4-bit pools. */
+int pa_paged_rope_kv_write_fp4(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, const void* key,
+                               int64_t key_stride, const void* value, int64_t value_stride, void* k_cache,
+                               void* v_cache, const int64_t* slot_mapping, const int64_t* positions,
+                               const float* cos_sin, int max_positions, int num_tokens, int num_blocks,
+                               int num_q_heads, int num_kv_heads, int head_dim, int rot_dim, int interleaved,
+                               int block_size, int src_dtype, float k_scale, float v_scale, void* stream);
+
+/* Both 4-bit pools as 16-bit pools [num_blocks, 16, num_kv_heads, head_dim] of
+ * `dtype`: every value, rounded once (exact when the pool scale is a power of
+ * two and the value lies in dtype's range). */
+int pa_paged_kv_unpack_fp4(void* k_out, void* v_out, const void* k_cache, const void* v_cache, int num_blocks,
+                           int num_kv_heads, int head_dim, int block_size, float k_scale, float v_scale, int dtype,
+                           void* stream);
+
+/* Decode attention over a 4-bit cache: as pa_paged_attention_decode, with k_t
+ * and v_t the values above; q and out keep `dtype`; the workspace is sized by
+ * pa_decode_workspace_bytes. */
+int pa_paged_attention_decode_fp4(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                                  int num_seqs, int max_seq_len, int num_blocks, float scale, float k_scale,
+                                  float v_scale, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                  int partition_size, void* workspace, size_t workspace_bytes, int dtype,
+                                  void* stream);
+
+/* A continuous-batching step over a 4-bit cache: as
+ * pa_paged_attention_prefill_fp8, the chunks' 16-bit copy included
+ * (pa_prefill_fp8_workspace_bytes sizes the workspace; its chunk and
+ * PA_DEVERR_WORKSPACE rules hold). */
+int pa_paged_attention_prefill_fp4(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                                   const int32_t* cu_q_lens, int num_seqs, int num_tokens, int max_q_len,
+                                   int max_seq_len, int num_blocks, float scale, float k_scale, float v_scale,
+                                   int num_q_heads, int num_kv_heads, int head_dim, int block_size, void* workspace,
+                                   size_t workspace_bytes, int dtype, void* stream);
+
+/*
+ * Attention with modified scores over a 16-bit cache: pa_paged_attention_decode
+ * and pa_paged_attention_prefill (same arguments, workspaces and error rules)
+ * with, for query position i, key position j and query head h,
+ *   s = scale * q . k
+ *   s = softcap * tanh(s / softcap)     when softcap > 0 (at most PA_SOFTCAP_MAX)
+ *   s = s + alibi_slopes[h] * (j - i)   when alibi_slopes != NULL (fp32 [num_q_heads], device)
+ *   j is visible when i - window < j <= i (window > 0; 0: j <= i)
+ * Every query sees itself, so no row is empty.  Blocks that lie before every
+ * window of a row's queries are not read, and their table entries may hold
+ * anything (a block manager may have reused them).
+ */
+#define PA_SOFTCAP_MAX 1000.0f
+
+int pa_paged_attention_decode_mod(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                                  int num_seqs, int max_seq_len, int num_blocks, float scale, float softcap,
+                                  int window, const float* alibi_slopes, int num_q_heads, int num_kv_heads,
+                                  int head_dim, int block_size, int partition_size, void* workspace,
+                                  size_t workspace_bytes, int dtype, void* stream);
+
+int pa_paged_attention_prefill_mod(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                                   const int32_t* cu_q_lens, int num_seqs, int num_tokens, int max_q_len,
+                                   int max_seq_len, int num_blocks, float scale, float softcap, int window,
+                                   const float* alibi_slopes, int num_q_heads, int num_kv_heads, int head_dim,
+                                   int block_size, void* workspace, size_t workspace_bytes, int dtype,
+                                   void* stream);
 
 /*
  * Decode attention for callers that cannot allocate device memory.

@@ -11,15 +11,25 @@ from ._binding import (  # noqa: F401
     count_chunk_kv_tokens,
     decode_partition,
     decode_workspace_bytes,
+    fp4_tile_bytes,
     library_path,
     load_library,
     paged_attention_decode,
+    paged_attention_decode_fp4,
     paged_attention_decode_fp8,
+    paged_attention_decode_mod,
     paged_attention_prefill,
+    paged_attention_prefill_fp4,
     paged_attention_prefill_fp8,
+    paged_attention_prefill_mod,
     paged_kv_gather,
+    paged_kv_unpack_fp4,
     paged_kv_write,
+    paged_kv_write_fp4,
     paged_kv_write_fp8,
+    paged_rope_kv_write,
+    paged_rope_kv_write_fp4,
+    paged_rope_kv_write_fp8,
     prefill_fp8_workspace_bytes,
     prefill_workspace_bytes,
     selftest_wait_timeout,

@@ -24,7 +24,12 @@ _STATUS = {0: "PA_OK", 1: "PA_ERR_INVALID_ARG", 2: "PA_ERR_UNSUPPORTED",
 _p = ctypes.c_void_p
 _i32 = ctypes.c_int
 _f32 = ctypes.c_float
+_i64 = ctypes.c_int64
 _sz = ctypes.c_size_t
+
+# q_out, q, key and value with their token strides, the pools, slots, positions,
+# the cos/sin table and the sizes (the entry points differ after these)
+_ROPE = [_p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _p, _p, _p, _p] + [_i32] * 9
 
 _SIGNATURES = {
     "pa_version": (_i32, []),
@@ -47,6 +52,20 @@ _SIGNATURES = {
     "pa_prefill_fp8_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_int64]),
     "pa_paged_attention_prefill_fp8": (_i32, [_p, _p, _p, _p, _p, _i32, _p, _p, _i32, _i32, _i32, _i32, _i32,
                                               _f32, _f32, _f32, _i32, _i32, _i32, _i32, _p, _sz, _i32, _p]),
+    "pa_paged_rope_kv_write": (_i32, _ROPE + [_i32, _p]),
+    "pa_paged_rope_kv_write_fp8": (_i32, _ROPE + [_i32, _f32, _f32, _p]),
+    "pa_paged_rope_kv_write_fp4": (_i32, _ROPE + [_i32, _f32, _f32, _p]),
+    "pa_fp4_tile_bytes": (_i32, [_i32]),
+    "pa_paged_kv_write_fp4": (_i32, [_p, _p, _p, _p, _p, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _f32, _p]),
+    "pa_paged_kv_unpack_fp4": (_i32, [_p, _p, _p, _p, _i32, _i32, _i32, _i32, _f32, _f32, _i32, _p]),
+    "pa_paged_attention_decode_fp4": (_i32, [_p, _p, _p, _p, _p, _i32, _p, _i32, _i32, _i32, _f32, _f32, _f32,
+                                             _i32, _i32, _i32, _i32, _i32, _p, _sz, _i32, _p]),
+    "pa_paged_attention_prefill_fp4": (_i32, [_p, _p, _p, _p, _p, _i32, _p, _p, _i32, _i32, _i32, _i32, _i32,
+                                              _f32, _f32, _f32, _i32, _i32, _i32, _i32, _p, _sz, _i32, _p]),
+    "pa_paged_attention_decode_mod": (_i32, [_p, _p, _p, _p, _p, _i32, _p, _i32, _i32, _i32, _f32, _f32, _i32, _p,
+                                             _i32, _i32, _i32, _i32, _i32, _p, _sz, _i32, _p]),
+    "pa_paged_attention_prefill_mod": (_i32, [_p, _p, _p, _p, _p, _i32, _p, _p, _i32, _i32, _i32, _i32, _i32,
+                                              _f32, _f32, _i32, _p, _i32, _i32, _i32, _i32, _p, _sz, _i32, _p]),
     "pa_copy_blocks": (_i32, [_p, _p, _p, _i32, _i32, _i32, _i32, _i32, _p]),
     "pa_decode_partition": (_i32, [_i32, _i32]),
     "pa_selftest_wait_timeout": (_i32, [_p]),
@@ -256,11 +275,17 @@ def paged_attention_prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
 
 def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, pairs: torch.Tensor, stream=None) -> None:
     """In place: block pairs[i, 1] of both pools receives block pairs[i, 0]
-    (the copy-on-write step; pairs is a device int32 [n, 2] tensor)."""
+    (the copy-on-write step; pairs is a device int32 [n, 2] tensor).  Pools of
+    any kind: 16-bit, FP8, or 4-bit tiles [NB, Hkv, bytes]."""
     _cuda(k_cache, v_cache, pairs)
     _need(pairs.dtype == torch.int32 and pairs.dim() == 2 and pairs.shape[1] == 2, "pairs: int32 [n, 2]")
     _need(v_cache.shape == k_cache.shape and v_cache.dtype == k_cache.dtype, "cache shape/dtype")
-    NB, bs, H, D = k_cache.shape
+    if k_cache.dim() == 3:   # 4-bit tiles: 16 rows of codes and scales
+        NB, H, tile = k_cache.shape
+        _need(k_cache.element_size() == 1 and tile % 16 == 0, "4-bit pools: bytes [NB, Hkv, fp4_tile_bytes]")
+        D = tile // 16
+    else:
+        NB, bs, H, D = k_cache.shape
     rc = load_library().pa_copy_blocks(k_cache.data_ptr(), v_cache.data_ptr(), pairs.data_ptr(), pairs.shape[0],
                                        NB, H, D, k_cache.element_size(), _stream(stream))
     _check(rc, "pa_copy_blocks")
@@ -387,4 +412,277 @@ def paged_attention_prefill_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
         float(scale), float(k_scale), float(v_scale), Hq, Hkv, D, bs, _ptr(workspace), ws_bytes, _dt(q),
         _stream(stream))
     _check(rc, "pa_paged_attention_prefill_fp8")
+    return out
+
+
+# --------------------------------------------------------------------------
+# Rotation and append; 4-bit (E2M1) cache
+# --------------------------------------------------------------------------
+
+def _on_current(*ts) -> None:
+    """Every tensor on the current device (the library enqueues on its stream)."""
+    dev = torch.cuda.current_device()
+    for t in ts:
+        if t is not None:
+            _need(t.is_cuda and t.device.index == dev, "tensors must be on the current CUDA device")
+
+
+def _rows(t: torch.Tensor, what: str) -> int:
+    """Token stride (elements) of [T, H, D] rows whose heads are dense within a token."""
+    T, H, D = t.shape
+    _need(t.stride(2) == 1 and (H <= 1 or t.stride(1) == D), f"{what}: head rows must be dense within a token")
+    return t.stride(0) if T > 1 else H * D
+
+
+def _rope(name, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin, interleaved, q_out, stream,
+          pool, scales):
+    """The three rotate-and-append calls; `pool` is (num_blocks, num_kv_heads, head_dim, block_size)."""
+    _on_current(q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin, q_out)
+    NB, H, D, bs = pool
+    T, Hq = key.shape[0], q.shape[1]
+    _need(k_cache.is_contiguous() and v_cache.is_contiguous() and v_cache.shape == k_cache.shape, "cache shape")
+    _need(tuple(key.shape) == (T, H, D) and value.shape == key.shape and tuple(q.shape) == (T, Hq, D),
+          "q/key/value shape")
+    _need(q.dtype == key.dtype == value.dtype, "q/key/value dtype")
+    _need(slot_mapping.dtype == torch.int64 and slot_mapping.is_contiguous() and slot_mapping.numel() >= T,
+          "slot_mapping: int64 [num_tokens]")
+    _need(positions.dtype == torch.int64 and positions.is_contiguous() and positions.numel() >= T,
+          "positions: int64 [num_tokens]")
+    _need(cos_sin.dtype == torch.float32 and cos_sin.is_contiguous() and cos_sin.dim() == 2,
+          "cos_sin: float32 [max_positions, rot_dim]")
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+    _need(q_out.shape == q.shape and q_out.dtype == q.dtype, "q_out shape/dtype")
+    rc = getattr(load_library(), name)(
+        q_out.data_ptr(), _rows(q_out, "q_out"), q.data_ptr(), _rows(q, "q"), key.data_ptr(), _rows(key, "key"),
+        value.data_ptr(), _rows(value, "value"), k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(),
+        positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0], T, NB, Hq, H, D, cos_sin.shape[1],
+        int(bool(interleaved)), bs, _dt(q), *scales, _stream(stream))
+    _check(rc, name)
+    return q_out
+
+
+def paged_rope_kv_write(q: torch.Tensor, key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor,
+                        v_cache: torch.Tensor, slot_mapping: torch.Tensor, positions: torch.Tensor,
+                        cos_sin: torch.Tensor, interleaved: bool = False, q_out: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor:
+    """Rotate the step's queries and keys by their positions and write keys and
+    values into their slots of a 16-bit cache, in one pass; returns the rotated
+    queries (`q_out`, which may be `q` itself).
+
+    q [T, Hq, D], key/value [T, Hkv, D] may be slices of fused projection rows
+    (any token stride that is a multiple of 8 elements).  cos_sin is float32
+    [max_positions, rot_dim], cosines then sines; pairs are (i, i + rot_dim/2),
+    or (2i, 2i + 1) when interleaved."""
+    NB, bs, H, D = k_cache.shape
+    _need(k_cache.dtype == v_cache.dtype == key.dtype, "cache dtype")
+    return _rope("pa_paged_rope_kv_write", q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
+                 interleaved, q_out, stream, (NB, H, D, bs), ())
+
+
+def paged_rope_kv_write_fp8(q: torch.Tensor, key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor,
+                            v_cache: torch.Tensor, slot_mapping: torch.Tensor, positions: torch.Tensor,
+                            cos_sin: torch.Tensor, k_scale: float, v_scale: float, interleaved: bool = False,
+                            q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """`paged_rope_kv_write` into head-major FP8 (E4M3) pools [NB, Hkv, 16, 128]."""
+    _u8(k_cache), _u8(v_cache)
+    NB, H, bs, D = k_cache.shape
+    return _rope("pa_paged_rope_kv_write_fp8", q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
+                 interleaved, q_out, stream, (NB, H, D, bs), (float(k_scale), float(v_scale)))
+
+
+def fp4_tile_bytes(head_dim: int) -> int:
+    """Bytes of one (block, kv head) tile of a 4-bit cache; its pools are uint8
+    [num_blocks, num_kv_heads, fp4_tile_bytes(head_dim)]."""
+    n = int(load_library().pa_fp4_tile_bytes(head_dim))
+    _need(n > 0, "4-bit caches hold head_dim 64 or 128")
+    return n
+
+
+def _fp4_pool(k_cache: torch.Tensor, v_cache: torch.Tensor, D: int):
+    _need(k_cache.dim() == 3 and k_cache.element_size() == 1 and v_cache.element_size() == 1 and
+          k_cache.shape == v_cache.shape and k_cache.shape[2] == fp4_tile_bytes(D),
+          "4-bit pools: bytes [NB, Hkv, fp4_tile_bytes(head_dim)]")
+    return k_cache.shape[0], k_cache.shape[1]
+
+
+def paged_rope_kv_write_fp4(q: torch.Tensor, key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor,
+                            v_cache: torch.Tensor, slot_mapping: torch.Tensor, positions: torch.Tensor,
+                            cos_sin: torch.Tensor, k_scale: float, v_scale: float, interleaved: bool = False,
+                            q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """`paged_rope_kv_write` into 4-bit pools [NB, Hkv, fp4_tile_bytes(D)]."""
+    D = key.shape[2]
+    NB, H = _fp4_pool(k_cache, v_cache, D)
+    return _rope("pa_paged_rope_kv_write_fp4", q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
+                 interleaved, q_out, stream, (NB, H, D, PA_BLOCK_SIZE), (float(k_scale), float(v_scale)))
+
+
+def paged_kv_write_fp4(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                       slot_mapping: torch.Tensor, k_scale: float, v_scale: float, stream=None) -> None:
+    """In place: E2M1 codes and E4M3 group scales of key/value into the 4-bit
+    pools [NB, Hkv, fp4_tile_bytes(D)] (slot < 0: skipped)."""
+    _cuda(key, value, k_cache, v_cache, slot_mapping)
+    _on_current(key, value, k_cache, v_cache, slot_mapping)
+    T, H, D = key.shape
+    NB, H2 = _fp4_pool(k_cache, v_cache, D)
+    _need(H == H2 and value.shape == key.shape and value.dtype == key.dtype, "key/value/cache shapes")
+    _need(slot_mapping.dtype == torch.int64 and slot_mapping.numel() >= T, "slot_mapping: int64 [num_tokens]")
+    rc = load_library().pa_paged_kv_write_fp4(key.data_ptr(), value.data_ptr(), k_cache.data_ptr(),
+                                              v_cache.data_ptr(), slot_mapping.data_ptr(), T, NB, H, D,
+                                              PA_BLOCK_SIZE, _dt(key), float(k_scale), float(v_scale),
+                                              _stream(stream))
+    _check(rc, "pa_paged_kv_write_fp4")
+
+
+def paged_kv_unpack_fp4(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: float, v_scale: float,
+                        dtype: torch.dtype, stream=None):
+    """Both 4-bit pools as 16-bit pools [NB, 16, Hkv, D] of `dtype`."""
+    _cuda(k_cache, v_cache)
+    _on_current(k_cache, v_cache)
+    _need(k_cache.dim() == 3 and k_cache.shape[2] % 9 == 0, "4-bit pools: bytes [NB, Hkv, fp4_tile_bytes(head_dim)]")
+    D = k_cache.shape[2] // 9
+    NB, H = _fp4_pool(k_cache, v_cache, D)
+    k_out = torch.empty(NB, PA_BLOCK_SIZE, H, D, dtype=dtype, device=k_cache.device)
+    v_out = torch.empty_like(k_out)
+    rc = load_library().pa_paged_kv_unpack_fp4(k_out.data_ptr(), v_out.data_ptr(), k_cache.data_ptr(),
+                                               v_cache.data_ptr(), NB, H, D, PA_BLOCK_SIZE, float(k_scale),
+                                               float(v_scale), _dt(k_out), _stream(stream))
+    _check(rc, "pa_paged_kv_unpack_fp4")
+    return k_out, v_out
+
+
+def _tables(block_tables: torch.Tensor, seq_lens: torch.Tensor, B: int) -> None:
+    _need(block_tables.dtype == torch.int32 and seq_lens.dtype == torch.int32, "int32 tables")
+    _need(seq_lens.numel() == B and block_tables.dim() == 2 and block_tables.shape[0] >= B, "table shapes")
+
+
+def _out_ws(q, out, nbytes, workspace):
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out.shape == q.shape and out.dtype == q.dtype, "out shape/dtype")
+    workspace = _workspace(nbytes, q.device, workspace)
+    return out, workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def paged_attention_decode_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                               block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float, k_scale: float,
+                               v_scale: float, max_seq_len: int | None = None, out: torch.Tensor | None = None,
+                               partition_size: int = 0, workspace: torch.Tensor | None = None,
+                               stream=None) -> torch.Tensor:
+    """Decode attention over 4-bit pools [NB, Hkv, fp4_tile_bytes(D)]:
+    q [B, Hq, D] -> out [B, Hq, D]."""
+    _cuda(q, k_cache, v_cache, block_tables, seq_lens, out, workspace)
+    _on_current(q, k_cache, v_cache, block_tables, seq_lens, out, workspace)
+    B, Hq, D = q.shape
+    NB, Hkv = _fp4_pool(k_cache, v_cache, D)
+    _tables(block_tables, seq_lens, B)
+    if max_seq_len is None:
+        max_seq_len = int(seq_lens.max().item()) if B else 0
+    out, workspace, ws_bytes = _out_ws(q, out, decode_workspace_bytes(B, Hq, D, max_seq_len, partition_size),
+                                       workspace)
+    rc = load_library().pa_paged_attention_decode_fp4(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+        block_tables.shape[1], seq_lens.data_ptr(), B, max_seq_len, NB, float(scale), float(k_scale),
+        float(v_scale), Hq, Hkv, D, PA_BLOCK_SIZE, partition_size, _ptr(workspace), ws_bytes, _dt(q),
+        _stream(stream))
+    _check(rc, "pa_paged_attention_decode_fp4")
+    return out
+
+
+def paged_attention_prefill_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                block_tables: torch.Tensor, seq_lens: torch.Tensor, cu_q_lens: torch.Tensor,
+                                scale: float, k_scale: float, v_scale: float, max_q_len: int, max_seq_len: int,
+                                out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                                stream=None, chunk_kv_tokens: int | None = None) -> torch.Tensor:
+    """Causal varlen attention of new query rows over 4-bit pools (decodes,
+    speculative-verify rows and prefill chunks in one call).  `chunk_kv_tokens`
+    as in `paged_attention_prefill_fp8`."""
+    _cuda(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, out, workspace)
+    _on_current(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, out, workspace)
+    T, Hq, D = q.shape
+    NB, Hkv = _fp4_pool(k_cache, v_cache, D)
+    B = seq_lens.shape[0]
+    _tables(block_tables, seq_lens, B)
+    _need(cu_q_lens.shape[0] == B + 1 and cu_q_lens.dtype == torch.int32, "cu_q_lens")
+    if max_q_len > 8 and B > 0 and T > 0:
+        if chunk_kv_tokens is None:
+            chunk_kv_tokens = count_chunk_kv_tokens(seq_lens, cu_q_lens)
+        nbytes = prefill_fp8_workspace_bytes(B, T, Hq, Hkv, D, max_seq_len, block_tables.shape[1],
+                                             chunk_kv_tokens)
+    else:
+        nbytes = prefill_workspace_bytes(B, T, Hq, D, max_seq_len)
+    out, workspace, ws_bytes = _out_ws(q, out, nbytes, workspace)
+    rc = load_library().pa_paged_attention_prefill_fp4(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+        block_tables.shape[1], seq_lens.data_ptr(), cu_q_lens.data_ptr(), B, T, max_q_len, max_seq_len, NB,
+        float(scale), float(k_scale), float(v_scale), Hq, Hkv, D, PA_BLOCK_SIZE, _ptr(workspace), ws_bytes, _dt(q),
+        _stream(stream))
+    _check(rc, "pa_paged_attention_prefill_fp4")
+    return out
+
+
+# --------------------------------------------------------------------------
+# Modified scores (16-bit cache)
+# --------------------------------------------------------------------------
+
+def _slopes(alibi_slopes, Hq: int) -> None:
+    if alibi_slopes is not None:
+        _need(alibi_slopes.dtype == torch.float32 and alibi_slopes.is_contiguous() and alibi_slopes.numel() == Hq,
+              "alibi_slopes: float32 [num_q_heads]")
+
+
+def paged_attention_decode_mod(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                               block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float,
+                               max_seq_len: int | None = None, softcap: float = 0.0, window: int = 0,
+                               alibi_slopes: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                               partition_size: int = 0, workspace: torch.Tensor | None = None,
+                               stream=None) -> torch.Tensor:
+    """`paged_attention_decode` with modified scores: softcap * tanh(s / softcap)
+    when softcap > 0, plus alibi_slopes[h] * (key - query position), over the
+    last `window` positions when window > 0."""
+    _cuda(q, k_cache, v_cache, block_tables, seq_lens, out, workspace)
+    _on_current(q, k_cache, v_cache, block_tables, seq_lens, out, workspace, alibi_slopes)
+    B, Hq, D = q.shape
+    NB, bs, Hkv, D2 = k_cache.shape
+    _need(D2 == D and v_cache.shape == k_cache.shape and k_cache.dtype == v_cache.dtype == q.dtype,
+          "cache shape/dtype")
+    _tables(block_tables, seq_lens, B)
+    _slopes(alibi_slopes, Hq)
+    if max_seq_len is None:
+        max_seq_len = int(seq_lens.max().item()) if B else 0
+    out, workspace, ws_bytes = _out_ws(q, out, decode_workspace_bytes(B, Hq, D, max_seq_len, partition_size),
+                                       workspace)
+    rc = load_library().pa_paged_attention_decode_mod(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+        block_tables.shape[1], seq_lens.data_ptr(), B, max_seq_len, NB, float(scale), float(softcap), int(window),
+        _ptr(alibi_slopes), Hq, Hkv, D, bs, partition_size, _ptr(workspace), ws_bytes, _dt(q), _stream(stream))
+    _check(rc, "pa_paged_attention_decode_mod")
+    return out
+
+
+def paged_attention_prefill_mod(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                block_tables: torch.Tensor, seq_lens: torch.Tensor, cu_q_lens: torch.Tensor,
+                                scale: float, max_q_len: int, max_seq_len: int, softcap: float = 0.0,
+                                window: int = 0, alibi_slopes: torch.Tensor | None = None,
+                                out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                                stream=None) -> torch.Tensor:
+    """`paged_attention_prefill` (decode, verify and chunk rows in one call) with
+    modified scores, as `paged_attention_decode_mod`."""
+    _cuda(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, out, workspace)
+    _on_current(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, out, workspace, alibi_slopes)
+    T, Hq, D = q.shape
+    NB, bs, Hkv, D2 = k_cache.shape
+    _need(D2 == D and v_cache.shape == k_cache.shape and k_cache.dtype == v_cache.dtype == q.dtype,
+          "cache shape/dtype")
+    B = seq_lens.shape[0]
+    _tables(block_tables, seq_lens, B)
+    _need(cu_q_lens.shape[0] == B + 1 and cu_q_lens.dtype == torch.int32, "cu_q_lens")
+    _slopes(alibi_slopes, Hq)
+    out, workspace, ws_bytes = _out_ws(q, out, prefill_workspace_bytes(B, T, Hq, D, max_seq_len), workspace)
+    rc = load_library().pa_paged_attention_prefill_mod(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+        block_tables.shape[1], seq_lens.data_ptr(), cu_q_lens.data_ptr(), B, T, max_q_len, max_seq_len, NB,
+        float(scale), float(softcap), int(window), _ptr(alibi_slopes), Hq, Hkv, D, bs, _ptr(workspace), ws_bytes,
+        _dt(q), _stream(stream))
+    _check(rc, "pa_paged_attention_prefill_mod")
     return out

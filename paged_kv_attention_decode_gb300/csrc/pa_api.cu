@@ -215,6 +215,28 @@ int verify_rows_bound(int num_seqs, int num_tokens) {
 
 float scale_log2(float scale) { return scale * 1.4426950408889634f; }
 
+// What the pools hold.
+enum class Cache { k16, kFp8, kFp4 };
+
+// Bytes of one 4-bit (block, kv head) tile: 16 rows of head_dim / 2 code bytes
+// and head_dim / 16 group scales.
+int fp4_tile_bytes(int head_dim) { return PA_BLOCK_SIZE * (head_dim / 2 + head_dim / 16); }
+
+bool score_mod(pa::ScoreMod& m, float scale, float softcap, int window, const float* slopes) {
+    if (!std::isfinite(softcap) || softcap < 0.f || window < 0) return false;
+    m = pa::ScoreMod{};
+    if (softcap > PA_SOFTCAP_MAX) return false;
+    if (softcap > 0.f) {
+        m.cap_in = 2.f * scale_log2(scale) / softcap;
+        m.cap_log2 = scale_log2(softcap);
+        // a cap so small that these leave fp32's normal range
+        if (!std::isfinite(m.cap_in) || !std::isnormal(m.cap_log2)) return false;
+    }
+    m.window = window;
+    m.slopes = slopes;
+    return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -285,15 +307,17 @@ struct DecodeCall {
     pa::DecodeParams p;
     CUtensorMap kmap, vmap;
     int head_dim, dtype;
-    bool fp8;
+    Cache cache;
+    bool modified;
 };
 
 static int decode_prepare(DecodeCall& c, void* out, const void* q, const void* k_cache, const void* v_cache,
                           const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
                           const int32_t* cu_q_lens, int num_seqs, int max_seq_len, int num_blocks, float scale,
                           int num_q_heads, int num_kv_heads, int head_dim, int partition_size, void* workspace,
-                          size_t workspace_bytes, int dtype, int max_q, int max_rows, int num_rows, bool fp8 = false,
-                          float k_scale = 1.f, float v_scale = 1.f) {
+                          size_t workspace_bytes, int dtype, int max_q, int max_rows, int num_rows,
+                          Cache cache = Cache::k16, float k_scale = 1.f, float v_scale = 1.f,
+                          const pa::ScoreMod* mod = nullptr) {
     const int part = effective_partition(max_seq_len, partition_size);
     const int parts = parts_for(max_seq_len, part);
     if (parts > 65535) return PA_ERR_INVALID_ARG;   // partition index is a 16-bit field of the work list
@@ -302,10 +326,12 @@ static int decode_prepare(DecodeCall& c, void* out, const void* q, const void* k
     if (!aligned256(workspace)) return PA_ERR_INVALID_ARG;
     unsigned int* err = error_word();
     if (!err) return PA_ERR_CUDA;
-    const bool maps_ok = fp8 ? make_kv_map_fp8(&c.kmap, k_cache, num_blocks, num_kv_heads) &&
-                                   make_kv_map_fp8(&c.vmap, v_cache, num_blocks, num_kv_heads)
-                             : make_kv_map_block(&c.kmap, k_cache, num_blocks, num_kv_heads, head_dim, dtype) &&
-                                   make_kv_map_block(&c.vmap, v_cache, num_blocks, num_kv_heads, head_dim, dtype);
+    const bool maps_ok =
+        cache == Cache::kFp4   ? true
+        : cache == Cache::kFp8 ? make_kv_map_fp8(&c.kmap, k_cache, num_blocks, num_kv_heads) &&
+                                     make_kv_map_fp8(&c.vmap, v_cache, num_blocks, num_kv_heads)
+                               : make_kv_map_block(&c.kmap, k_cache, num_blocks, num_kv_heads, head_dim, dtype) &&
+                                     make_kv_map_block(&c.vmap, v_cache, num_blocks, num_kv_heads, head_dim, dtype);
     if (!maps_ok) return PA_ERR_CUDA;
     pa::DecodeParams& p = c.p;
     p = pa::DecodeParams{};
@@ -334,16 +360,22 @@ static int decode_prepare(DecodeCall& c, void* out, const void* q, const void* k
     p.col_chunks = (cols + chunk - 1) / chunk;
     p.scale_log2 = scale_log2(scale) * k_scale;
     p.v_scale = v_scale;
+    p.k_pool = k_cache;
+    p.v_pool = v_cache;
+    if (mod) p.mod = *mod;
     carve_workspace(p, workspace);
     c.head_dim = head_dim;
     c.dtype = dtype;
-    c.fp8 = fp8;
+    c.cache = cache;
+    c.modified = mod != nullptr;
     return PA_OK;
 }
 
 static int decode_launch(const DecodeCall& c, cudaStream_t stream) {
-    cudaError_t e = c.fp8 ? pa::launch_decode_fp8(c.p, c.kmap, c.vmap, c.dtype, stream)
-                          : pa::launch_decode(c.p, c.kmap, c.vmap, c.head_dim, c.dtype, stream);
+    cudaError_t e = c.cache == Cache::kFp8   ? pa::launch_decode_fp8(c.p, c.kmap, c.vmap, c.dtype, stream)
+                    : c.cache == Cache::kFp4 ? pa::launch_decode_fp4(c.p, c.head_dim, c.dtype, stream)
+                    : c.modified ? pa::launch_decode_mod(c.p, c.kmap, c.vmap, c.head_dim, c.dtype, stream)
+                                 : pa::launch_decode(c.p, c.kmap, c.vmap, c.head_dim, c.dtype, stream);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -352,12 +384,13 @@ static int decode_impl(void* out, const void* q, const void* k_cache, const void
                        const int32_t* cu_q_lens, int num_seqs, int max_seq_len, int num_blocks, float scale,
                        int num_q_heads, int num_kv_heads, int head_dim, int partition_size, void* workspace,
                        size_t workspace_bytes, int dtype, cudaStream_t stream, int max_q, int max_rows,
-                       bool fp8 = false, float k_scale = 1.f, float v_scale = 1.f) {
+                       Cache cache = Cache::k16, float k_scale = 1.f, float v_scale = 1.f,
+                       const pa::ScoreMod* mod = nullptr) {
     DecodeCall c;
     const int rc = decode_prepare(c, out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, cu_q_lens,
                                   num_seqs, max_seq_len, num_blocks, scale, num_q_heads, num_kv_heads, head_dim,
-                                  partition_size, workspace, workspace_bytes, dtype, max_q, max_rows, num_seqs, fp8,
-                                  k_scale, v_scale);
+                                  partition_size, workspace, workspace_bytes, dtype, max_q, max_rows, num_seqs, cache,
+                                  k_scale, v_scale, mod);
     return rc ? rc : decode_launch(c, stream);
 }
 
@@ -431,8 +464,181 @@ int pa_paged_attention_decode_fp8(void* out, const void* q, const void* k_cache,
     if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_INVALID_ARG;
     return decode_impl(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, nullptr, num_seqs,
                        max_seq_len, num_blocks, scale, num_q_heads, num_kv_heads, head_dim, partition_size,
-                       workspace, workspace_bytes, dtype, static_cast<cudaStream_t>(stream), 1, num_seqs, true,
+                       workspace, workspace_bytes, dtype, static_cast<cudaStream_t>(stream), 1, num_seqs,
+                       Cache::kFp8, k_scale, v_scale);
+}
+
+int pa_paged_attention_decode_fp4(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                                  int num_seqs, int max_seq_len, int num_blocks, float scale, float k_scale,
+                                  float v_scale, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                  int partition_size, void* workspace, size_t workspace_bytes, int dtype,
+                                  void* stream) {
+    int rc = check_shape(num_q_heads, num_kv_heads, head_dim, block_size, dtype, num_blocks);
+    if (rc) return rc;
+    if (num_seqs < 0 || num_seqs > kMaxGrid || max_seq_len < 0 || max_blocks_per_seq <= 0) return PA_ERR_INVALID_ARG;
+    if (partition_size < 0 || partition_size % PA_BLOCK_SIZE) return PA_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || !std::isfinite(k_scale) || !std::isfinite(v_scale)) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0) return PA_OK;
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !seq_lens) return PA_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_INVALID_ARG;
+    return decode_impl(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, nullptr, num_seqs,
+                       max_seq_len, num_blocks, scale, num_q_heads, num_kv_heads, head_dim, partition_size,
+                       workspace, workspace_bytes, dtype, static_cast<cudaStream_t>(stream), 1, num_seqs,
+                       Cache::kFp4, k_scale, v_scale);
+}
+
+int pa_paged_attention_decode_mod(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                                  int num_seqs, int max_seq_len, int num_blocks, float scale, float softcap,
+                                  int window, const float* alibi_slopes, int num_q_heads, int num_kv_heads,
+                                  int head_dim, int block_size, int partition_size, void* workspace,
+                                  size_t workspace_bytes, int dtype, void* stream) {
+    int rc = check_shape(num_q_heads, num_kv_heads, head_dim, block_size, dtype, num_blocks);
+    if (rc) return rc;
+    if (num_seqs < 0 || num_seqs > kMaxGrid || max_seq_len < 0 || max_blocks_per_seq <= 0) return PA_ERR_INVALID_ARG;
+    if (partition_size < 0 || partition_size % PA_BLOCK_SIZE) return PA_ERR_INVALID_ARG;
+    pa::ScoreMod mod;
+    if (!std::isfinite(scale) || !score_mod(mod, scale, softcap, window, alibi_slopes)) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0) return PA_OK;
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !seq_lens) return PA_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_INVALID_ARG;
+    return decode_impl(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, nullptr, num_seqs,
+                       max_seq_len, num_blocks, scale, num_q_heads, num_kv_heads, head_dim, partition_size,
+                       workspace, workspace_bytes, dtype, static_cast<cudaStream_t>(stream), 1, num_seqs,
+                       Cache::k16, 1.f, 1.f, &mod);
+}
+
+// Everything an append call does; `cache` says what the pools hold.
+static int append_impl(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, const void* key,
+                       int64_t key_stride, const void* value, int64_t value_stride, void* k_cache, void* v_cache,
+                       const int64_t* slot_mapping, const int64_t* positions, const float* cos_sin,
+                       int max_positions, int num_tokens, int num_blocks, int num_q_heads, int num_kv_heads,
+                       int head_dim, int rot_dim, int interleaved, int block_size, int dtype, void* stream,
+                       Cache cache, float k_scale, float v_scale) {
+    if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+    if (block_size != PA_BLOCK_SIZE) return PA_ERR_UNSUPPORTED;
+    if (head_dim != 128 && (head_dim != 64 || cache == Cache::kFp8)) return PA_ERR_UNSUPPORTED;
+    if (num_tokens < 0 || num_q_heads < 0 || num_kv_heads <= 0 || num_q_heads > kMaxGrid || num_kv_heads > kMaxGrid ||
+        num_blocks <= 0 || num_blocks > kMaxPoolBlocks)
+        return PA_ERR_INVALID_ARG;
+    if (rot_dim < 0 || rot_dim > head_dim || (interleaved != 0 && interleaved != 1)) return PA_ERR_INVALID_ARG;
+    if (rot_dim % 16) return PA_ERR_UNSUPPORTED;
+    if (rot_dim > 0 && max_positions <= 0) return PA_ERR_INVALID_ARG;
+    if (!(k_scale > 0.f) || !(v_scale > 0.f) || !std::isfinite(k_scale) || !std::isfinite(v_scale))
+        return PA_ERR_INVALID_ARG;
+    const float k_inv = 1.0f / k_scale, v_inv = 1.0f / v_scale;   // one fp32 division, as the definition states
+    if (!std::isfinite(k_inv) || !std::isfinite(v_inv)) return PA_ERR_INVALID_ARG;
+    // rows start on 16-byte boundaries and do not overlap within a token
+    const int64_t kv_row = static_cast<int64_t>(num_kv_heads) * head_dim;
+    const int64_t q_row = static_cast<int64_t>(num_q_heads) * head_dim;
+    if (num_tokens > 1 && (key_stride < kv_row || value_stride < kv_row)) return PA_ERR_INVALID_ARG;
+    if (num_tokens > 1 && num_q_heads > 0 && (q_stride < q_row || q_out_stride < q_row)) return PA_ERR_INVALID_ARG;
+    if (key_stride % 8 || value_stride % 8 || (num_q_heads > 0 && (q_stride % 8 || q_out_stride % 8)))
+        return PA_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return PA_OK;
+    if (!key || !value || !k_cache || !v_cache || !slot_mapping) return PA_ERR_INVALID_ARG;
+    if (num_q_heads > 0 && (!q || !q_out || !aligned16(q) || !aligned16(q_out))) return PA_ERR_INVALID_ARG;
+    if (rot_dim > 0 && (!positions || !cos_sin || !aligned16(cos_sin))) return PA_ERR_INVALID_ARG;
+    if (!aligned16(key) || !aligned16(value) || !aligned16(k_cache) || !aligned16(v_cache))
+        return PA_ERR_INVALID_ARG;
+    // in place only as a whole: a row that overlaps another row's source races
+    if (num_q_heads > 0 && q == q_out && q_stride != q_out_stride && num_tokens > 1) return PA_ERR_INVALID_ARG;
+    unsigned int* err = error_word();
+    if (!err) return PA_ERR_CUDA;
+    pa::AppendParams p{};
+    p.q_out = q_out;
+    p.q = q;
+    p.key = key;
+    p.value = value;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.positions = positions;
+    p.cos_sin = cos_sin;
+    p.slots = slot_mapping;
+    p.q_out_stride = q_out_stride;
+    p.q_stride = q_stride;
+    p.key_stride = key_stride;
+    p.value_stride = value_stride;
+    p.num_slots = static_cast<int64_t>(num_blocks) * PA_BLOCK_SIZE;
+    p.num_tokens = num_tokens;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.max_positions = max_positions;
+    p.rot = rot_dim;
+    p.interleaved = interleaved;
+    p.k_inv = k_inv;
+    p.v_inv = v_inv;
+    p.err = err;
+    const cudaError_t e = pa::launch_append(p, head_dim, dtype, static_cast<int>(cache),
+                                            static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+int pa_paged_rope_kv_write(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, const void* key,
+                           int64_t key_stride, const void* value, int64_t value_stride, void* k_cache,
+                           void* v_cache, const int64_t* slot_mapping, const int64_t* positions,
+                           const float* cos_sin, int max_positions, int num_tokens, int num_blocks,
+                           int num_q_heads, int num_kv_heads, int head_dim, int rot_dim, int interleaved,
+                           int block_size, int dtype, void* stream) {
+    if (rot_dim == 0) return PA_ERR_INVALID_ARG;
+    return append_impl(q_out, q_out_stride, q, q_stride, key, key_stride, value, value_stride, k_cache, v_cache,
+                       slot_mapping, positions, cos_sin, max_positions, num_tokens, num_blocks, num_q_heads,
+                       num_kv_heads, head_dim, rot_dim, interleaved, block_size, dtype, stream, Cache::k16, 1.f, 1.f);
+}
+
+int pa_paged_rope_kv_write_fp8(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, const void* key,
+                               int64_t key_stride, const void* value, int64_t value_stride, void* k_cache,
+                               void* v_cache, const int64_t* slot_mapping, const int64_t* positions,
+                               const float* cos_sin, int max_positions, int num_tokens, int num_blocks,
+                               int num_q_heads, int num_kv_heads, int head_dim, int rot_dim, int interleaved,
+                               int block_size, int src_dtype, float k_scale, float v_scale, void* stream) {
+    if (rot_dim == 0) return PA_ERR_INVALID_ARG;
+    return append_impl(q_out, q_out_stride, q, q_stride, key, key_stride, value, value_stride, k_cache, v_cache,
+                       slot_mapping, positions, cos_sin, max_positions, num_tokens, num_blocks, num_q_heads,
+                       num_kv_heads, head_dim, rot_dim, interleaved, block_size, src_dtype, stream, Cache::kFp8,
                        k_scale, v_scale);
+}
+
+int pa_paged_rope_kv_write_fp4(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, const void* key,
+                               int64_t key_stride, const void* value, int64_t value_stride, void* k_cache,
+                               void* v_cache, const int64_t* slot_mapping, const int64_t* positions,
+                               const float* cos_sin, int max_positions, int num_tokens, int num_blocks,
+                               int num_q_heads, int num_kv_heads, int head_dim, int rot_dim, int interleaved,
+                               int block_size, int src_dtype, float k_scale, float v_scale, void* stream) {
+    if (rot_dim == 0) return PA_ERR_INVALID_ARG;
+    return append_impl(q_out, q_out_stride, q, q_stride, key, key_stride, value, value_stride, k_cache, v_cache,
+                       slot_mapping, positions, cos_sin, max_positions, num_tokens, num_blocks, num_q_heads,
+                       num_kv_heads, head_dim, rot_dim, interleaved, block_size, src_dtype, stream, Cache::kFp4,
+                       k_scale, v_scale);
+}
+
+int pa_paged_kv_write_fp4(const void* key, const void* value, void* k_cache, void* v_cache,
+                          const int64_t* slot_mapping, int num_tokens, int num_blocks, int num_kv_heads,
+                          int head_dim, int block_size, int src_dtype, float k_scale, float v_scale, void* stream) {
+    const int64_t row = static_cast<int64_t>(num_kv_heads) * head_dim;
+    return append_impl(nullptr, 0, nullptr, 0, key, row, value, row, k_cache, v_cache, slot_mapping, nullptr, nullptr,
+                       0, num_tokens, num_blocks, 0, num_kv_heads, head_dim, 0, 0, block_size, src_dtype, stream,
+                       Cache::kFp4, k_scale, v_scale);
+}
+
+int pa_fp4_tile_bytes(int head_dim) { return head_dim == 64 || head_dim == 128 ? fp4_tile_bytes(head_dim) : 0; }
+
+int pa_paged_kv_unpack_fp4(void* k_out, void* v_out, const void* k_cache, const void* v_cache, int num_blocks,
+                           int num_kv_heads, int head_dim, int block_size, float k_scale, float v_scale, int dtype,
+                           void* stream) {
+    if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+    if (block_size != PA_BLOCK_SIZE || (head_dim != 64 && head_dim != 128)) return PA_ERR_UNSUPPORTED;
+    if (num_blocks < 0 || num_blocks > kMaxPoolBlocks || num_kv_heads <= 0 || num_kv_heads > kMaxGrid)
+        return PA_ERR_INVALID_ARG;
+    if (!std::isfinite(k_scale) || !std::isfinite(v_scale)) return PA_ERR_INVALID_ARG;
+    if (num_blocks == 0) return PA_OK;
+    if (!k_out || !v_out || !k_cache || !v_cache) return PA_ERR_INVALID_ARG;
+    if (!aligned16(k_out) || !aligned16(v_out) || !aligned16(k_cache) || !aligned16(v_cache))
+        return PA_ERR_INVALID_ARG;
+    const cudaError_t e = pa::launch_unpack_fp4(k_out, v_out, k_cache, v_cache, num_blocks, num_kv_heads, head_dim,
+                                                dtype, k_scale, v_scale, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 size_t pa_prefill_workspace_bytes(int num_seqs, int num_tokens, int num_q_heads, int head_dim, int max_seq_len) {
@@ -478,15 +684,16 @@ static int prefill_impl(void* out, const void* q, const void* k_cache, const voi
                         const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
                         const int32_t* cu_q_lens, int num_seqs, int num_tokens, int max_q_len, int max_seq_len,
                         int num_blocks, float scale, int num_q_heads, int num_kv_heads, int head_dim,
-                        void* workspace, size_t workspace_bytes, int dtype, cudaStream_t s, bool fp8,
-                        float k_scale, float v_scale) {
+                        void* workspace, size_t workspace_bytes, int dtype, cudaStream_t s, Cache cache,
+                        float k_scale, float v_scale, const pa::ScoreMod* mod = nullptr) {
     const size_t pb = plan_bytes(num_seqs, num_tokens);
     const size_t base_bytes = pa_prefill_workspace_bytes(num_seqs, num_tokens, num_q_heads, head_dim, max_seq_len);
     if (!workspace || workspace_bytes < base_bytes) return PA_ERR_WORKSPACE_TOO_SMALL;
     if (!aligned256(workspace)) return PA_ERR_INVALID_ARG;
-    // FP8 chunks: room for the 16-bit copy of at least one block
+    // FP8 or 4-bit chunks: room for the 16-bit copy of at least one block
+    const bool copied = cache != Cache::k16;
     pa::Fp8Copy copy{};
-    if (fp8 && max_q_len > PA_VERIFY_MAX_Q) {
+    if (copied && max_q_len > PA_VERIFY_MAX_Q) {
         const size_t fixed = fp8_copy_fixed_bytes(num_seqs, max_blocks_per_seq);
         const size_t per = fp8_copy_block_bytes(num_kv_heads, head_dim);
         if (workspace_bytes < base_bytes + fixed + per) return PA_ERR_WORKSPACE_TOO_SMALL;
@@ -507,6 +714,7 @@ static int prefill_impl(void* out, const void* q, const void* k_cache, const voi
         copy.v_codes = v_cache;
         copy.src_tables = block_tables;
         copy.src_num_blocks = num_blocks;
+        copy.fp4 = cache == Cache::kFp4;
     }
     int32_t* plan = static_cast<int32_t*>(workspace);
     const int group = num_q_heads / num_kv_heads;
@@ -517,35 +725,36 @@ static int prefill_impl(void* out, const void* q, const void* k_cache, const voi
     int rc = decode_prepare(dc, out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, cu_q_lens,
                             num_seqs, max_seq_len, num_blocks, scale, num_q_heads, num_kv_heads, head_dim, 0,
                             static_cast<uint8_t*>(workspace) + pb, workspace_bytes - pb, dtype, max_q,
-                            verify_rows_bound(num_seqs, num_tokens), num_tokens, fp8, k_scale, v_scale);
+                            verify_rows_bound(num_seqs, num_tokens), num_tokens, cache, k_scale, v_scale, mod);
     if (rc) return rc;
     if (max_q_len <= PA_VERIFY_MAX_Q) return decode_launch(dc, s);
     unsigned int* err = error_word();
     pa::PrefillParams p{};
     p.out = out;
     p.q = q;
-    p.block_tables = fp8 ? copy.table : block_tables;
+    p.block_tables = copied ? copy.table : block_tables;
     p.seq_lens = seq_lens;
     p.cu_q_lens = cu_q_lens;
     p.err = err;
     p.num_seqs = num_seqs;
     p.max_blocks = max_blocks_per_seq;
     p.max_seq_len = max_seq_len;
-    p.num_blocks = fp8 ? copy.cap_blocks : num_blocks;
+    p.num_blocks = copied ? copy.cap_blocks : num_blocks;
     p.num_q_heads = num_q_heads;
     p.num_kv_heads = num_kv_heads;
     p.group = group;
     p.scale_log2 = scale_log2(scale) * k_scale;
     p.v_scale = v_scale;
+    if (mod) p.mod = *mod;
     CUtensorMap kmap, vmap;
     // tiles of 128 / group queries (every supported grouping) on the tcgen05
     // tensor cores, running beside the decode rows: the decode plan and the
     // prefill kernel go first; the decode kernel then starts on the SMs the
     // prefill kernel leaves free.  K comes in one box per 64-dim half of a
-    // block, V in one box per block, from the 16-bit cache or (FP8 cache)
-    // from the chunks' 16-bit copy.
-    const void* kc = fp8 ? copy.k16 : k_cache;
-    const void* vc = fp8 ? copy.v16 : v_cache;
+    // block, V in one box per block, from the 16-bit cache or (FP8 or 4-bit
+    // cache) from the chunks' 16-bit copy.
+    const void* kc = copied ? copy.k16 : k_cache;
+    const void* vc = copied ? copy.v16 : v_cache;
     if (!make_kv_map(&kmap, kc, p.num_blocks, num_kv_heads, head_dim, dtype) ||
         !make_kv_map_block(&vmap, vc, p.num_blocks, num_kv_heads, head_dim, dtype))
         return PA_ERR_CUDA;
@@ -555,10 +764,10 @@ static int prefill_impl(void* out, const void* q, const void* k_cache, const voi
     if (!make_q_map(&qmap, q, num_tokens, num_q_heads, head_dim, group, p.q_per_tile, dtype)) return PA_ERR_CUDA;
     if (pa::launch_decode_plan(dc.p, s) != cudaSuccess) return PA_ERR_CUDA;
     p.decode_units = dc.p.unit_count;
-    p.overlap_ctas = std::max(1, fp8 ? pa::sm_count() * kOverlapPrefillNumFp8 / kOverlapPrefillDenFp8
+    p.overlap_ctas = std::max(1, copied ? pa::sm_count() * kOverlapPrefillNumFp8 / kOverlapPrefillDenFp8
                                      : pa::sm_count() * kOverlapPrefillNum / kOverlapPrefillDen);
     if (pa::launch_prefill_tc(p, plan, kmap, vmap, qmap, head_dim, dtype, max_q_len, num_tokens,
-                              fp8 ? &copy : nullptr, s) !=
+                              copied ? &copy : nullptr, mod != nullptr, s) !=
         cudaSuccess)
         return PA_ERR_CUDA;
     dc.p.overlap = 1;
@@ -582,7 +791,51 @@ int pa_paged_attention_prefill(void* out, const void* q, const void* k_cache, co
     if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_INVALID_ARG;
     return prefill_impl(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, cu_q_lens, num_seqs,
                         num_tokens, max_q_len, max_seq_len, num_blocks, scale, num_q_heads, num_kv_heads, head_dim,
-                        workspace, workspace_bytes, dtype, static_cast<cudaStream_t>(stream), false, 1.f, 1.f);
+                        workspace, workspace_bytes, dtype, static_cast<cudaStream_t>(stream), Cache::k16, 1.f, 1.f);
+}
+
+int pa_paged_attention_prefill_mod(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                                   const int32_t* cu_q_lens, int num_seqs, int num_tokens, int max_q_len,
+                                   int max_seq_len, int num_blocks, float scale, float softcap, int window,
+                                   const float* alibi_slopes, int num_q_heads, int num_kv_heads, int head_dim,
+                                   int block_size, void* workspace, size_t workspace_bytes, int dtype,
+                                   void* stream) {
+    int rc = check_shape(num_q_heads, num_kv_heads, head_dim, block_size, dtype, num_blocks);
+    if (rc) return rc;
+    if (num_seqs < 0 || num_seqs > kMaxGrid || num_tokens < 0 || max_q_len < 0 || max_seq_len < 0 ||
+        max_blocks_per_seq <= 0)
+        return PA_ERR_INVALID_ARG;
+    pa::ScoreMod mod;
+    if (!std::isfinite(scale) || !score_mod(mod, scale, softcap, window, alibi_slopes)) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0 || num_tokens == 0) return PA_OK;
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !seq_lens || !cu_q_lens) return PA_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_INVALID_ARG;
+    return prefill_impl(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, cu_q_lens, num_seqs,
+                        num_tokens, max_q_len, max_seq_len, num_blocks, scale, num_q_heads, num_kv_heads, head_dim,
+                        workspace, workspace_bytes, dtype, static_cast<cudaStream_t>(stream), Cache::k16, 1.f, 1.f,
+                        &mod);
+}
+
+int pa_paged_attention_prefill_fp4(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                                   const int32_t* cu_q_lens, int num_seqs, int num_tokens, int max_q_len,
+                                   int max_seq_len, int num_blocks, float scale, float k_scale, float v_scale,
+                                   int num_q_heads, int num_kv_heads, int head_dim, int block_size, void* workspace,
+                                   size_t workspace_bytes, int dtype, void* stream) {
+    int rc = check_shape(num_q_heads, num_kv_heads, head_dim, block_size, dtype, num_blocks);
+    if (rc) return rc;
+    if (num_seqs < 0 || num_seqs > kMaxGrid || num_tokens < 0 || max_q_len < 0 || max_seq_len < 0 ||
+        max_blocks_per_seq <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || !std::isfinite(k_scale) || !std::isfinite(v_scale)) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0 || num_tokens == 0) return PA_OK;
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !seq_lens || !cu_q_lens) return PA_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_INVALID_ARG;
+    return prefill_impl(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, cu_q_lens, num_seqs,
+                        num_tokens, max_q_len, max_seq_len, num_blocks, scale, num_q_heads, num_kv_heads, head_dim,
+                        workspace, workspace_bytes, dtype, static_cast<cudaStream_t>(stream), Cache::kFp4, k_scale,
+                        v_scale);
 }
 
 int pa_paged_attention_prefill_fp8(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -603,7 +856,7 @@ int pa_paged_attention_prefill_fp8(void* out, const void* q, const void* k_cache
     if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_INVALID_ARG;
     return prefill_impl(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, cu_q_lens, num_seqs,
                         num_tokens, max_q_len, max_seq_len, num_blocks, scale, num_q_heads, num_kv_heads, head_dim,
-                        workspace, workspace_bytes, dtype, static_cast<cudaStream_t>(stream), true, k_scale,
+                        workspace, workspace_bytes, dtype, static_cast<cudaStream_t>(stream), Cache::kFp8, k_scale,
                         v_scale);
 }
 

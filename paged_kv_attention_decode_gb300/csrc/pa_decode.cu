@@ -44,6 +44,7 @@ constexpr unsigned kFull = 0xffffffffu;
 // The tensor-core path keeps a column's reference max until a score exceeds
 // it by this much (log2 units), so softmax weights stay within [0, 2^8].
 constexpr float kLazyRescaleLog2 = 8.f;
+constexpr float kLog2e = 1.4426950408889634f;
 
 // Per-warp shared memory: a ring of kStages (K tile, V tile) slots.  A warp
 // handles one block at a time, so it moves bytes at (tile bytes) / (block
@@ -108,6 +109,21 @@ __device__ __forceinline__ float dot2_mixed(float s, uint32_t q01, uint32_t k01)
     return s;
 }
 
+// First partition that a sequence's rows read: with a window, the one that
+// holds the first key its first query sees.
+__device__ __forceinline__ int first_part(const DecodeParams& p, int n, int qlen) {
+    return p.mod.window > 0 ? max(0, n - qlen + 1 - p.mod.window) / p.partition_tokens : 0;
+}
+
+// raw q . k -> score in log2 units, before the distance bias.
+__device__ __forceinline__ float mod_score(const ScoreMod& mod, float scale_log2, float raw) {
+    if (mod.cap_log2 > 0.f) {
+        const float e = 1.f + fast_exp2(raw * mod.cap_in);   // inf: the reciprocal is 0, the score +cap
+        return fmaf(-2.f * mod.cap_log2, fast_rcp(e), mod.cap_log2);
+    }
+    return raw * scale_log2;
+}
+
 // ---------------------------------------------------------------------------
 // MHA block step: fp32 dot products on the ALU.
 // Lane l owns head dims [l*DPL, (l+1)*DPL).
@@ -121,7 +137,9 @@ __device__ __forceinline__ float dot2_mixed(float s, uint32_t q01, uint32_t k01)
 // (four 16-byte loads of codes, no transpose-reduction), which leaves the
 // scores in the same lanes as the reduction does.
 // ---------------------------------------------------------------------------
-template <typename T, int D, bool kFp8 = false>
+// kMod: the scores are modified (ScoreMod); `skip` tokens at the block's start
+// lie before the window, `dist` is the block's first position less the query's.
+template <typename T, int D, bool kFp8 = false, bool kMod = false>
 struct AluState {
     static constexpr int DPL = D / 32;
     static constexpr bool kMixedK = !kFp8 || std::is_same<T, __half>::value;
@@ -152,7 +170,9 @@ struct AluState {
         }
     }
 
-    __device__ __forceinline__ void step(const uint8_t* kt, const uint8_t* vt, int nvalid, int lane) {
+    __device__ __forceinline__ void step(const uint8_t* kt, const uint8_t* vt, int nvalid, int lane,
+                                         const ScoreMod* mod = nullptr, float slope = 0.f, int skip = 0,
+                                         int dist = 0) {
         float s;
         if constexpr (kTokenK) {
             // lanes 2t and 2t+1 each take one half of token t's 128 dims
@@ -238,9 +258,13 @@ struct AluState {
                 part[0] = keep + __shfl_xor_sync(kFull, send, 2);
             }
             s = part[0] + __shfl_xor_sync(kFull, part[0], 1);
-            if constexpr (kMixedK) s *= qscale;
+            if constexpr (kMixedK && !kMod) s *= qscale;
         }
         const int tok = lane >> 1;
+        if constexpr (kMod) {
+            s = fmaf(slope, static_cast<float>(dist + tok), mod_score(*mod, qscale, s));
+            s = tok < skip ? -INFINITY : s;
+        }
         s = tok < nvalid ? s : -INFINITY;
         float mb = s;
         mb = fmaxf(mb, __shfl_xor_sync(kFull, mb, 2));
@@ -254,7 +278,7 @@ struct AluState {
         l = l * alpha + ((lane & 1) ? 0.f : p);
 #pragma unroll
         for (int j = 0; j < DPL; ++j) acc[j] *= alpha;
-        if (nvalid == 16) {
+        if (nvalid == 16 && (!kMod || skip == 0)) {
 #pragma unroll
             for (int t = 0; t < 16; ++t) {
                 const float pt = __shfl_sync(kFull, p, 2 * t);
@@ -264,7 +288,7 @@ struct AluState {
                 for (int j = 0; j < DPL; ++j) acc[j] = fmaf(pt, v[j], acc[j]);
             }
         } else {
-            for (int t = 0; t < nvalid; ++t) {
+            for (int t = kMod ? skip : 0; t < nvalid; ++t) {
                 const float pt = __shfl_sync(kFull, p, 2 * t);
                 float v[DPL];
                 load_dims(vt, t, lane, v);
@@ -308,7 +332,9 @@ __device__ __forceinline__ uint32_t codes_to(uint16_t codes) {
 // chunk; one byte permute pairs the tokens of each dim, so the m-tile's rows
 // g and g+8 are dims 2g and 2g+1 of the chunk (undone when O^T is written).
 // P and the converted V are fp16 (every E4M3 value is an fp16 value; P <= 2^8).
-template <typename T, int D, int NT, bool kFp8 = false>
+// kMod: the scores are modified (ScoreMod); column j then also has a first
+// visible token lo[nt][e], a slope and its query's position.
+template <typename T, int D, int NT, bool kFp8 = false, bool kMod = false>
 struct MmaState {
     static constexpr int KS = D / 16;
     uint32_t qb[KS][NT][2];   // Q^T as the B operand, per 16-dim k-step and column tile
@@ -316,12 +342,16 @@ struct MmaState {
     float m[NT][2];
     float l[NT][2];
     int lim[NT][2];           // first token the column may not see
+    int lo[kMod ? NT : 1][2];         // first token the column sees
+    int pos[kMod ? NT : 1][2];
+    float slope[kMod ? NT : 1][2];
 
     // `masked`: some column of this block has a limit inside it (else every
     // token of the block is visible to every column).  Rows at or past
-    // `nvalid` lie beyond the partition end.
+    // `nvalid` lie beyond the partition end, rows before `skip` before every
+    // column's first visible token.
     __device__ __forceinline__ void step(uint8_t* kt, uint8_t* vt, int base, int nvalid, bool masked, int lane,
-                                         float scale_log2) {
+                                         float scale_log2, const ScoreMod* mod = nullptr, int skip = 0) {
         const uint32_t ka = smem_addr(kt);
         const uint32_t va = smem_addr(vt);
         float c[NT][4];
@@ -386,10 +416,22 @@ struct MmaState {
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const bool v0 = !masked || base + r0 < lim[nt][e];
-                const bool v8 = !masked || base + r0 + 8 < lim[nt][e];
-                s[nt][e] = v0 ? c[nt][e] * scale_log2 : -INFINITY;
-                s[nt][2 + e] = v8 ? c[nt][2 + e] * scale_log2 : -INFINITY;
+                if constexpr (kMod) {
+                    const int t0 = base + r0, t8 = base + r0 + 8;
+                    const float x0 = fmaf(slope[nt][e], static_cast<float>(t0 - pos[nt][e]),
+                                          mod_score(*mod, scale_log2, c[nt][e]));
+                    const float x8 = fmaf(slope[nt][e], static_cast<float>(t8 - pos[nt][e]),
+                                          mod_score(*mod, scale_log2, c[nt][2 + e]));
+                    const bool v0 = !masked || (t0 < lim[nt][e] && t0 >= lo[nt][e]);
+                    const bool v8 = !masked || (t8 < lim[nt][e] && t8 >= lo[nt][e]);
+                    s[nt][e] = v0 ? x0 : -INFINITY;
+                    s[nt][2 + e] = v8 ? x8 : -INFINITY;
+                } else {
+                    const bool v0 = !masked || base + r0 < lim[nt][e];
+                    const bool v8 = !masked || base + r0 + 8 < lim[nt][e];
+                    s[nt][e] = v0 ? c[nt][e] * scale_log2 : -INFINITY;
+                    s[nt][2 + e] = v8 ? c[nt][2 + e] * scale_log2 : -INFINITY;
+                }
             }
             float mx0 = fmaxf(s[nt][0], s[nt][2]), mx1 = fmaxf(s[nt][1], s[nt][3]);
 #pragma unroll
@@ -463,6 +505,16 @@ struct MmaState {
                 }
             }
             __syncwarp();
+        }
+        if constexpr (kMod) {
+            if (skip > 0) {   // rows before the window, likewise
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h) {
+                    uint4* z = reinterpret_cast<uint4*>(vt + h * TileGeom<D>::kHalfBytes);
+                    for (int i = lane; i < skip * 8; i += 32) z[i] = make_uint4(0, 0, 0, 0);
+                }
+                __syncwarp();
+            }
         }
         if constexpr (kFp8) {
             const int ft = (lane & 7) + ((lane >> 3) & 1) * 8;
@@ -594,13 +646,14 @@ __global__ void __launch_bounds__(1024) decode_plan_kernel(const DecodeParams p)
     __syncthreads();
     for (int base = 0; base < p.num_seqs; base += 1024) {
         const int b = base + tid;
-        int v = 0, vr = 0, qlen = 0;
+        int v = 0, vr = 0, qlen = 0, part0 = 0;
         if (b < p.num_seqs) {
             int n = n0;
             qlen = qlen0;
             if (base > 0) n = row_of(b, true, qlen);
             if (n > 0) {
-                v = n / P;
+                part0 = first_part(p, n, qlen);
+                v = max(0, n / P - part0);
                 vr = n > P ? qlen : 0;
             } else if (qlen > 0) {
                 // an empty (or rejected) sequence gets zero rows here
@@ -612,7 +665,8 @@ __global__ void __launch_bounds__(1024) decode_plan_kernel(const DecodeParams p)
         }
         const int start = block_exclusive_scan(v, warp_tot, &carry_u, chunk_total);
         for (int i = 0; i < v; ++i)
-            p.units[start + i] = static_cast<int32_t>((static_cast<uint32_t>(b) << 16) | static_cast<uint32_t>(i));
+            p.units[start + i] =
+                static_cast<int32_t>((static_cast<uint32_t>(b) << 16) | static_cast<uint32_t>(part0 + i));
         const int rstart = block_exclusive_scan(vr, warp_tot, &carry_r, chunk_total);
         if (vr) {
             p.row_base[b] = rstart;
@@ -657,11 +711,12 @@ __global__ void __launch_bounds__(1024) decode_plan_kernel(const DecodeParams p)
 // the next item as soon as the fetches reach the end of the current one, so
 // the warp's HBM pipeline never drains between items.  Warps never wait for
 // one another.
-template <typename T, int D, bool kMma, bool kFp8, int kMaxNT>
+template <typename T, int D, bool kMma, bool kFp8, int kMaxNT, bool kMod>
 __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeShape<D, kFp8, kMma, kMaxNT>::kMinCtasPerSm)
     decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap) {
     static_assert(kMma || kMaxNT == 1, "the FMA path handles one query per row");
+    static_assert(!kMod || !kFp8, "modified scores read 16-bit caches");
     using Shape = DecodeShape<D, kFp8, kMma, kMaxNT>;
     constexpr int kDecodeStages = Shape::kStages;
     constexpr int kQueue = 8;  // claimed items not yet computed (<= STAGES + 1 in use)
@@ -705,6 +760,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeShape<D, kFp8, kMma, 
 
     struct Item {
         int b, g, part, n, qlen, qrow0, col0, ncols, tok1, lim_min, blk0, nblk;
+        int lo_min, lo_max;   // first visible token of the chunk's first and last column (kMod)
         const int32_t* bt;
     };
     auto load_item = [&](int w, Item& it) {
@@ -731,6 +787,17 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeShape<D, kFp8, kMma, 
         // query q (position n - qlen + q) sees the tokens below n - qlen + q + 1
         it.lim_min = min(it.tok1, n - it.qlen + 1 + it.col0 / G);
         it.blk0 = tok0 >> 4;
+        if constexpr (kMod) {
+            // a window hides the tokens at and before a query's position less
+            // its length: blocks wholly before the first column's are not read
+            // (at least one block stays: the item's partials are always written)
+            it.lo_min = it.lo_max = 0;
+            if (p.mod.window > 0 && n > 0 && it.ncols > 0) {
+                it.lo_min = max(0, n - it.qlen + it.col0 / G - p.mod.window + 1);
+                it.lo_max = max(0, n - it.qlen + (it.col0 + it.ncols - 1) / G - p.mod.window + 1);
+                it.blk0 = max(it.blk0, min(it.lo_min >> 4, ((it.tok1 + 15) >> 4) - 1));
+            }
+        }
         it.nblk = (n > 0 && it.ncols > 0) ? ((it.tok1 + 15) >> 4) - it.blk0 : 0;
         it.bt = p.block_tables + static_cast<int64_t>(it.b) * p.max_blocks + it.blk0;
     };
@@ -849,7 +916,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeShape<D, kFp8, kMma, 
 
     // MHA decode row: fp32 FMA path
     auto run_alu = [&](const Item& it, const uint32_t (&qw)[kQWords]) -> bool {
-        AluState<T, D, kFp8> alu;
+        AluState<T, D, kFp8, kMod> alu;
 #pragma unroll
         for (int j = 0; j < kQWords; ++j) {
             if constexpr (AluState<T, D, kFp8>::kMixedK) {
@@ -875,8 +942,15 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeShape<D, kFp8, kMma, 
         }
         alu.m = -INFINITY;
         alu.l = 0.f;
-        if (!for_each_block(it, [&](uint8_t* kt, uint8_t* vt, int, int nvalid) { alu.step(kt, vt, nvalid, lane); }))
-            return false;
+        float slope = 0.f;
+        if constexpr (kMod) slope = p.mod.slopes ? p.mod.slopes[it.g] * kLog2e : 0.f;
+        const bool done = for_each_block(it, [&](uint8_t* kt, uint8_t* vt, int base, int nvalid) {
+            if constexpr (kMod)
+                alu.step(kt, vt, nvalid, lane, &p.mod, slope, max(0, it.lo_min - base), base - (it.n - 1));
+            else
+                alu.step(kt, vt, nvalid, lane);
+        });
+        if (!done) return false;
         constexpr int DPL = AluState<T, D>::DPL;
 #pragma unroll
         for (int j = 0; j < DPL; ++j) alu.acc[j] *= p.v_scale;
@@ -911,7 +985,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeShape<D, kFp8, kMma, 
     // (query, head) columns of a decode or verify row: tensor-core path
     auto run_mma = [&](auto nt_tag, const Item& it, int w) -> bool {
         constexpr int NT = decltype(nt_tag)::value;
-        MmaState<T, D, NT, kFp8> mma;
+        MmaState<T, D, NT, kFp8, kMod> mma;
         if (kPrefetchQ && NT == 1 && qpre_item == w) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
@@ -933,11 +1007,23 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, DecodeShape<D, kFp8, kMma, 
                 mma.l[nt][e] = 0.f;
                 const int cl = nt * 8 + 2 * (lane & 3) + e;
                 mma.lim[nt][e] = cl < it.ncols ? min(it.tok1, it.n - it.qlen + 1 + (it.col0 + cl) / G) : 0;
+                if constexpr (kMod) {
+                    const int col = it.col0 + (cl < it.ncols ? cl : 0);
+                    const int qi = col / G;
+                    mma.pos[nt][e] = it.n - it.qlen + qi;
+                    mma.lo[nt][e] = p.mod.window > 0 ? max(0, mma.pos[nt][e] - p.mod.window + 1) : 0;
+                    mma.slope[nt][e] = p.mod.slopes ? p.mod.slopes[it.g * G + (col - qi * G)] * kLog2e : 0.f;
+                }
             }
         }
         const bool ok = for_each_block(it, [&](uint8_t* kt, uint8_t* vt, int base, int nvalid) {
-            const bool masked = base + 16 > it.lim_min;
-            mma.step(kt, vt, base, nvalid, masked, lane, p.scale_log2);
+            if constexpr (kMod) {
+                const bool masked = base + 16 > it.lim_min || base < it.lo_max;
+                mma.step(kt, vt, base, nvalid, masked, lane, p.scale_log2, &p.mod, min(16, max(0, it.lo_min - base)));
+            } else {
+                const bool masked = base + 16 > it.lim_min;
+                mma.step(kt, vt, base, nvalid, masked, lane, p.scale_log2);
+            }
         });
         if (!ok) return false;
         const bool split = it.n > P;
@@ -1061,8 +1147,10 @@ __global__ void __launch_bounds__(kReduceWarps * 32) decode_reduce_kernel(const 
         const int qrow = (p.cu_q_lens ? p.cu_q_lens[b] : b) + static_cast<int>(entry & 7u);
         int n = p.seq_lens[b];
         if (n < 0 || n > p.max_seq_len || n > p.max_blocks * 16) n = 0;
-        const int nparts = n > 0 ? (n + P - 1) / P : 1;
-        const int64_t base = (static_cast<int64_t>(k) * p.num_q_heads + hq) * p.max_parts;
+        // (with a window, the partitions before the first live one were not written)
+        const int part0 = first_part(p, n, p.cu_q_lens ? p.cu_q_lens[b + 1] - p.cu_q_lens[b] : 1);
+        const int nparts = (n > 0 ? (n + P - 1) / P : 1) - part0;
+        const int64_t base = (static_cast<int64_t>(k) * p.num_q_heads + hq) * p.max_parts + part0;
         const float* wm = p.ws_m + base;
         const float* wl = p.ws_l + base;
         const float* wa = p.ws_acc + base * D + lane * DPL;
@@ -1145,8 +1233,10 @@ __global__ void __launch_bounds__(D) decode_reduce_cta_kernel(const DecodeParams
         const int qrow = (p.cu_q_lens ? p.cu_q_lens[b] : b) + static_cast<int>(entry & 7u);
         int n = p.seq_lens[b];
         if (n < 0 || n > p.max_seq_len || n > p.max_blocks * 16) n = 0;
-        const int nparts = n > 0 ? (n + P - 1) / P : 1;
-        const int64_t base = (static_cast<int64_t>(k) * p.num_q_heads + hq) * p.max_parts;
+        // (with a window, the partitions before the first live one were not written)
+        const int part0 = first_part(p, n, p.cu_q_lens ? p.cu_q_lens[b + 1] - p.cu_q_lens[b] : 1);
+        const int nparts = (n > 0 ? (n + P - 1) / P : 1) - part0;
+        const int64_t base = (static_cast<int64_t>(k) * p.num_q_heads + hq) * p.max_parts + part0;
         const float* wm = p.ws_m + base;
         const float* wl = p.ws_l + base;
         const float* wa = p.ws_acc + base * D;
@@ -1199,11 +1289,28 @@ __global__ void __launch_bounds__(D) decode_reduce_cta_kernel(const DecodeParams
 }
 
 
-template <typename T, int D, bool kMma, bool kFp8 = false, int kMaxNT = 1>
+template <typename T, int D>
+cudaError_t launch_reduce_t(const DecodeParams& p, cudaStream_t s) {
+    if (p.max_parts <= 1) return cudaSuccess;
+    const long long pairs = static_cast<long long>(p.max_rows) * p.num_q_heads;
+    if (pairs >= kReduceWarpPairsMin) {
+        // persistent: a few waves of 8-warp CTAs, one warp per pair
+        const int rgrid = static_cast<int>(std::max<long long>(
+            1, std::min<long long>((pairs + kReduceWarps - 1) / kReduceWarps, 8LL * sm_count())));
+        // scheduled while the decode grid drains (its CTAs wait on chip);
+        // the CTA-per-pair layout below has too many CTAs for that to pay
+        return launch_pdl(decode_reduce_kernel<T, D>, dim3(rgrid), dim3(kReduceWarps * 32), 0, s, p);
+    }
+    dim3 rgrid(p.num_q_heads, std::min(p.max_rows, kReduceMaxRowsPerLaunch));
+    decode_reduce_cta_kernel<T, D><<<rgrid, D, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T, int D, bool kMma, bool kFp8 = false, int kMaxNT = 1, bool kMod = false>
 cudaError_t launch_decode_t(const DecodeParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
                             cudaStream_t s) {
     constexpr int smem = DecodeShape<D, kFp8, kMma, kMaxNT>::kSmemBytes;
-    auto kern = decode_kernel<T, D, kMma, kFp8, kMaxNT>;
+    auto kern = decode_kernel<T, D, kMma, kFp8, kMaxNT, kMod>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (!p.overlap) {
@@ -1226,22 +1333,7 @@ cudaError_t launch_decode_t(const DecodeParams& p, const CUtensorMap& kmap, cons
         std::max<long long>(1, std::min<long long>(want, static_cast<long long>(ctas_per_sm) * sm_count())));
     e = launch_pdl(kern, dim3(grid), dim3(kDecodeWarps * 32), smem, s, p, kmap, vmap);
     if (e != cudaSuccess) return e;
-    if (p.max_parts > 1) {
-        const long long pairs = static_cast<long long>(p.max_rows) * p.num_q_heads;
-        if (pairs >= kReduceWarpPairsMin) {
-            // persistent: a few waves of 8-warp CTAs, one warp per pair
-            const int rgrid = static_cast<int>(std::max<long long>(
-                1, std::min<long long>((pairs + kReduceWarps - 1) / kReduceWarps, 8LL * sm_count())));
-            // scheduled while the decode grid drains (its CTAs wait on chip);
-            // the CTA-per-pair layout below has too many CTAs for that to pay
-            e = launch_pdl(decode_reduce_kernel<T, D>, dim3(rgrid), dim3(kReduceWarps * 32), 0, s, p);
-        } else {
-            dim3 rgrid(p.num_q_heads, std::min(p.max_rows, kReduceMaxRowsPerLaunch));
-            decode_reduce_cta_kernel<T, D><<<rgrid, D, 0, s>>>(p);
-            e = cudaGetLastError();
-        }
-    }
-    return e;
+    return launch_reduce_t<T, D>(p, s);
 }
 
 }  // namespace
@@ -1258,8 +1350,14 @@ int sm_count() {
     return c;
 }
 
-cudaError_t launch_decode_plan(const DecodeParams& p, cudaStream_t s) {
+cudaError_t launch_decode_reduce(const DecodeParams& p, int head_dim, int dtype, cudaStream_t s) {
+    if (dtype == 0) return head_dim == 128 ? launch_reduce_t<__half, 128>(p, s) : launch_reduce_t<__half, 64>(p, s);
+    return head_dim == 128 ? launch_reduce_t<__nv_bfloat16, 128>(p, s) : launch_reduce_t<__nv_bfloat16, 64>(p, s);
+}
+
+cudaError_t launch_decode_plan(const DecodeParams& p, cudaStream_t s, bool pdl) {
     if (p.num_seqs == 0) return cudaSuccess;
+    if (pdl) return launch_pdl(decode_plan_kernel, dim3(1), dim3(1024), 0, s, p);
     decode_plan_kernel<<<1, 1024, 0, s>>>(p);
     return cudaGetLastError();
 }
@@ -1283,22 +1381,33 @@ cudaError_t launch_decode_fp8(const DecodeParams& p, const CUtensorMap& kmap, co
                       : launch_decode_fp8_t<__nv_bfloat16>(p, kmap, vmap, s);
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kMod = false>
 cudaError_t launch_decode_d(const DecodeParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
                             cudaStream_t s) {
-    if (p.max_q * p.group > 8) return launch_decode_t<T, D, true, false, 2>(p, kmap, vmap, s);
-    if (p.group > 1 || p.max_q > 1) return launch_decode_t<T, D, true, false, 1>(p, kmap, vmap, s);
-    return launch_decode_t<T, D, false, false, 1>(p, kmap, vmap, s);
+    if (p.max_q * p.group > 8) return launch_decode_t<T, D, true, false, 2, kMod>(p, kmap, vmap, s);
+    if (p.group > 1 || p.max_q > 1) return launch_decode_t<T, D, true, false, 1, kMod>(p, kmap, vmap, s);
+    return launch_decode_t<T, D, false, false, 1, kMod>(p, kmap, vmap, s);
+}
+
+template <bool kMod>
+cudaError_t launch_decode_16(const DecodeParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                             int head_dim, int dtype, cudaStream_t s) {
+    if (p.num_seqs == 0) return cudaSuccess;
+    if (dtype == 0)
+        return head_dim == 128 ? launch_decode_d<__half, 128, kMod>(p, kmap, vmap, s)
+                               : launch_decode_d<__half, 64, kMod>(p, kmap, vmap, s);
+    return head_dim == 128 ? launch_decode_d<__nv_bfloat16, 128, kMod>(p, kmap, vmap, s)
+                           : launch_decode_d<__nv_bfloat16, 64, kMod>(p, kmap, vmap, s);
 }
 
 cudaError_t launch_decode(const DecodeParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
                           int head_dim, int dtype, cudaStream_t s) {
-    if (p.num_seqs == 0) return cudaSuccess;
-    if (dtype == 0)
-        return head_dim == 128 ? launch_decode_d<__half, 128>(p, kmap, vmap, s)
-                               : launch_decode_d<__half, 64>(p, kmap, vmap, s);
-    return head_dim == 128 ? launch_decode_d<__nv_bfloat16, 128>(p, kmap, vmap, s)
-                           : launch_decode_d<__nv_bfloat16, 64>(p, kmap, vmap, s);
+    return launch_decode_16<false>(p, kmap, vmap, head_dim, dtype, s);
+}
+
+cudaError_t launch_decode_mod(const DecodeParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                              int head_dim, int dtype, cudaStream_t s) {
+    return launch_decode_16<true>(p, kmap, vmap, head_dim, dtype, s);
 }
 
 }  // namespace pa

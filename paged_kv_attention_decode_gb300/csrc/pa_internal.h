@@ -12,6 +12,7 @@
 #define PA_DEVERR_SEQ_LEN_ 4u
 #define PA_DEVERR_TIMEOUT_ 8u
 #define PA_DEVERR_WORKSPACE_ 16u
+#define PA_DEVERR_POSITION_ 32u
 
 namespace pa {
 
@@ -39,6 +40,19 @@ inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, siz
 // in the prefill kernels.
 #define PA_VERIFY_MAX_Q_ 8
 
+
+// Modified scores (all zero: none).  With raw = q . k:
+//   s = cap > 0 ? cap * tanh(scale * raw / cap) : scale * raw
+//   s += slope[q head] * (key position - query position)
+//   visible: query position - window < key position <= query position
+// `cap_in` and `cap_log2` take raw to s in log2 units: tanh(x) = 1 - 2 / (1 +
+// e^2x), so s log2(e) = cap_log2 - 2 cap_log2 / (1 + 2^(raw * cap_in)).
+struct ScoreMod {
+    float cap_in;                 // 2 log2(e) scale / cap
+    float cap_log2;               // cap * log2(e); 0: no cap
+    int window;                   // 0: no window
+    const float* slopes;          // [Hq] or nullptr
+};
 
 struct DecodeParams {
     void* out;                    // [T, Hq, D] (T = B without cu_q_lens)
@@ -77,6 +91,9 @@ struct DecodeParams {
     // launch; everything the decode kernel reads completed before that
     // prefill kernel started, so it does not wait for it
     int overlap;
+    const void* k_pool;           // 4-bit pools (read without tensor maps)
+    const void* v_pool;
+    ScoreMod mod;
 };
 
 struct PrefillParams {
@@ -101,9 +118,33 @@ struct PrefillParams {
     const int32_t* decode_units;
     int overlap_ctas;
     int pair_cap;                 // pair-list capacity of the plan (num_tokens / 4 + num_seqs)
+    ScoreMod mod;
 };
 
-// FP8 (E4M3) cache: the prefill chunks' blocks widened to a 16-bit copy in
+// Rotation and cache write of new tokens; strides count elements between tokens.
+struct AppendParams {
+    void* q_out;
+    const void* q;                // [T, Hq, D]
+    const void* key;              // [T, Hkv, D]
+    const void* value;
+    void* k_cache;
+    void* v_cache;
+    const int64_t* positions;     // [T]
+    const float* cos_sin;         // [max_positions, rot]: cos | sin
+    const int64_t* slots;         // [T]
+    int64_t q_out_stride, q_stride, key_stride, value_stride;
+    int64_t num_slots;
+    int num_tokens;
+    int num_q_heads;
+    int num_kv_heads;
+    int max_positions;
+    int rot;                      // rotated dims of a head (a multiple of 16), 0: none
+    int interleaved;
+    float k_inv, v_inv;           // 1 / pool scale (quantised caches)
+    unsigned int* err;
+};
+
+// FP8 (E4M3) or 4-bit cache: the prefill chunks' blocks widened to a 16-bit copy in
 // the workspace, which the tensor-core kernel reads like a 16-bit cache.  The
 // plan lists each chunk whose copy fits (`chunk_seq`, with its first copy
 // block in `chunk_base`); sequence b's block i goes to copy block
@@ -116,10 +157,11 @@ struct Fp8Copy {
     void* k16;                    // [cap_blocks, 16, Hkv, D] of the query type
     void* v16;
     int cap_blocks;
-    const void* k_codes;          // the caller's E4M3 pools [num_blocks, Hkv, 16, D]
+    const void* k_codes;          // the caller's E4M3 pools [num_blocks, Hkv, 16, D], or 4-bit pools
     const void* v_codes;
     const int32_t* src_tables;    // the caller's block table [num_seqs, max_blocks]
     int src_num_blocks;
+    int fp4;                      // 1: 4-bit pools
 };
 
 // Launchers (return cudaError_t of the launch).
@@ -131,8 +173,23 @@ cudaError_t launch_kv_write(const void* key, const void* value, void* k_cache, v
                             int head_dim, unsigned int* err, cudaStream_t s);
 cudaError_t launch_decode(const DecodeParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
                           int head_dim, int dtype, cudaStream_t s);
-// The work-list plan alone (for p.overlap launches, which skip it).
-cudaError_t launch_decode_plan(const DecodeParams& p, cudaStream_t s);
+// The work-list plan alone (for p.overlap launches, which skip it; `pdl`: it
+// may start before the preceding kernel of the stream has finished).
+cudaError_t launch_decode_plan(const DecodeParams& p, cudaStream_t s, bool pdl = false);
+// The merge of split sequences' partials (nothing when no sequence can be split).
+cudaError_t launch_decode_reduce(const DecodeParams& p, int head_dim, int dtype, cudaStream_t s);
+// launch_decode with p.mod applied to the scores (16-bit cache).
+cudaError_t launch_decode_mod(const DecodeParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                              int head_dim, int dtype, cudaStream_t s);
+// 4-bit cache (p.k_pool / p.v_pool).
+cudaError_t launch_decode_fp4(const DecodeParams& p, int head_dim, int dtype, cudaStream_t s);
+cudaError_t launch_widen_fp4(const Fp8Copy& c, const int32_t* seq_lens, int max_blocks, int num_kv_heads,
+                             int head_dim, int dtype, cudaStream_t s);
+// cache: 0 the 16-bit type of the tokens, 1 FP8 (E4M3, head-major), 2 4-bit.
+cudaError_t launch_append(const AppendParams& p, int head_dim, int dtype, int cache, cudaStream_t s);
+cudaError_t launch_unpack_fp4(void* k_out, void* v_out, const void* k_cache, const void* v_cache, int num_blocks,
+                              int num_kv_heads, int head_dim, int dtype, float k_scale, float v_scale,
+                              cudaStream_t s);
 int sm_count();
 // FP8 (E4M3) cache, head_dim 128; q/out of `dtype`.
 cudaError_t launch_decode_fp8(const DecodeParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
@@ -154,10 +211,10 @@ cudaError_t launch_wait_selftest(unsigned int* err, cudaStream_t s);
 // `plan` is device scratch of num_seqs + 1 + 2 * pair_cap int32 (the work list
 // of query-tile pairs).  With `copy` (FP8 cache, head_dim 128) the plan also
 // lists the chunks' copy blocks, a kernel widens them, and K and V come from
-// the copy: p.block_tables = copy->table, p.num_blocks = copy->cap_blocks,
-// kmap / vmap over copy->k16 / v16.
+// the copy (4-bit cache likewise, head_dim 64 or 128): p.block_tables = copy->table, p.num_blocks = copy->cap_blocks,
+// kmap / vmap over copy->k16 / v16.  `modified`: apply p.mod (no copy).
 cudaError_t launch_prefill_tc(const PrefillParams& p, int32_t* plan, const CUtensorMap& kmap,
                               const CUtensorMap& vmap, const CUtensorMap& qmap, int head_dim, int dtype,
-                              int max_q_len, int num_tokens, const Fp8Copy* copy, cudaStream_t s);
+                              int max_q_len, int num_tokens, const Fp8Copy* copy, bool modified, cudaStream_t s);
 
 }  // namespace pa

@@ -181,13 +181,17 @@ __device__ __forceinline__ void fma2(float& x, float& y, float s, float a) {
         : "f"(s), "f"(a));
 }
 
-// Key tiles a query-tile pair of a chunk reads: those of its last tile.
+// First key that the query at `pos` sees.
+__device__ __forceinline__ int window_start(int pos, int window) { return window > 0 ? max(0, pos - window + 1) : 0; }
+
+// Key tiles a query-tile pair of a chunk reads: those of its last tile, less
+// those before the window of its first query.
 // Pair pr of a chunk of ql queries on a sequence of n tokens (tiles of qt rows).
-__device__ __forceinline__ int pair_key_tiles(int n, int ql, int qt, int pr) {
+__device__ __forceinline__ int pair_key_tiles(int n, int ql, int qt, int pr, int window) {
     const int ntiles = (ql + qt - 1) / qt;
     const int last = min(2 * pr + 1, ntiles - 1);                 // the pair's last query tile
     const int q_last = min(ql, (last + 1) * qt) - 1;
-    return (n - ql + q_last + kTcKeys) / kTcKeys;
+    return (n - ql + q_last + kTcKeys) / kTcKeys - window_start(n - ql + 2 * pr * qt, window) / kTcKeys;
 }
 
 // One 16-byte run of E4M3 codes (16 elements) widened to 16-bit values of
@@ -213,6 +217,24 @@ __device__ __forceinline__ void widen16(const uint4& in, uint4& lo, uint4& hi) {
     }
     lo = make_uint4(o[0], o[1], o[2], o[3]);
     hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// A row's 128 raw scores of one key tile -> modified scores in log2 units
+// (ScoreMod; `dist` = the tile's first key position less the row's).
+__device__ __forceinline__ void modify_scores(float (&sv)[kTcKeys], const ScoreMod& mod, float scale_log2,
+                                              float slope, int dist) {
+    if (mod.cap_log2 > 0.f) {
+#pragma unroll
+        for (int c = 0; c < kTcKeys; ++c)
+            sv[c] = fmaf(-2.f * mod.cap_log2, fast_rcp(1.f + fast_exp2(sv[c] * mod.cap_in)), mod.cap_log2);
+    } else {
+#pragma unroll
+        for (int c = 0; c < kTcKeys; c += 2) mul2(sv[c], sv[c + 1], scale_log2);
+    }
+    if (mod.slopes) {
+#pragma unroll
+        for (int c = 0; c < kTcKeys; ++c) sv[c] = fmaf(slope, static_cast<float>(dist + c), sv[c]);
+    }
 }
 
 // Exclusive prefix sum of one value per thread over a 1024-thread block, plus
@@ -270,7 +292,7 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
                                                             int num_tokens, int q_per_tile,
                                                             int32_t* __restrict__ offsets, int pair_cap,
                                                             unsigned int* err, const Fp8Copy copy, int max_seq_len,
-                                                            int max_blocks) {
+                                                            int max_blocks, int window) {
     __shared__ int warp_tot[32];
     __shared__ int carry, blk_carry, chunk_carry, blk_end;
     __shared__ int hist[kPlanBuckets];
@@ -296,7 +318,7 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
     };
     auto bucket = [&](int n, int ql, int pr) {
         // a malformed sequence (skipped by the kernel) goes to class 0
-        const int c = (n >= ql && ql > 0) ? pair_key_tiles(n, ql, q_per_tile, pr) : 0;
+        const int c = (n >= ql && ql > 0) ? pair_key_tiles(n, ql, q_per_tile, pr, window) : 0;
         return kPlanBuckets - 1 - max(0, min(c, kPlanBuckets - 1));   // longest first
     };
     for (int base = 0; base < num_seqs; base += 1024) {
@@ -423,7 +445,11 @@ __global__ void __launch_bounds__(kWidenThreads) widen_chunk_blocks_kernel(const
 // k * C + i for even k and k * C + C - 1 - i for odd k, so the CTAs' total
 // costs stay even.  (Beside decode rows: pair w / num_kv_heads of the plan's
 // own order, round-robin.)
-template <typename T, int D>
+// kMod: the scores are modified (ScoreMod).  With a window a pair's key tiles
+// start at the tile of its first query's first key (tile index j0 + j); blocks
+// wholly before that key are not read (their table entries may be anything),
+// their keys are masked and their V rows cleared.
+template <typename T, int D, bool kMod>
 __global__ void __launch_bounds__(kTcThreads, 1)
     prefill_tc_kernel(const PrefillParams p, const int32_t* __restrict__ plan,
                       const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -532,6 +558,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // tiles A (x = 0) and B (x = 1, absent past the chunk's last tile).
     struct Item {
         int g, row0, qlen, n, nkt, pos_pair, nblk_live;
+        int j0, blk_first;   // first key tile and first live block (0 without a window)
         int q0[kTcTiles], nkx[kTcTiles], pos_lo[kTcTiles], pos_hi[kTcTiles];
         const int32_t* bt;
     };
@@ -563,6 +590,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 it.pos_lo[x] = it.pos_hi[x] = 0;
                 it.nkx[x] = 0;
             }
+        }
+        it.j0 = it.blk_first = 0;
+        if constexpr (kMod) {
+            const int first = window_start(it.pos_lo[0], p.mod.window);
+            it.j0 = first / kTcKeys;
+            it.blk_first = first >> 4;
+            it.nkx[0] -= it.j0;
+            if (it.nkx[1]) it.nkx[1] -= it.j0;
         }
         it.nkt = max(it.nkx[0], it.nkx[1]);                          // key tiles of the pair
         it.pos_pair = it.nkx[1] ? it.pos_hi[1] : it.pos_hi[0];      // the pair's last query position
@@ -606,7 +641,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
         const uint32_t s_tm = tmem + lane_base + static_cast<uint32_t>(x * kTcKeys);
         const uint32_t o_tm = tmem + lane_base + static_cast<uint32_t>(kTcTiles * kTcKeys + x * D);
-        const bool fold = p.scale_log2 > 0.f;   // scale folded into the exponent's FMA
+        const bool fold = !kMod && p.scale_log2 > 0.f;   // scale folded into the exponent's FMA
         int n_items_x = 0;   // items of this tile so far (o_done phases)
         for (int k = 0; ok; ++k) {
             const int w0 = item_at(k);
@@ -626,12 +661,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 // does the item's live table hold an id outside the pool?  (One
                 // scan per item keeps table loads off the per-tile path.)
                 bool any_bad = false;
-                for (int blk = lane; blk < it.nblk_live; blk += 32) {
+                for (int blk = it.blk_first + lane; blk < it.nblk_live; blk += 32) {
                     const int id = it.bt[blk];
                     any_bad |= id < 0 || id >= p.num_blocks;
                 }
                 any_bad = __any_sync(kFullMask, any_bad);
                 float m_ref = -INFINITY, l_run = 0.f;
+                float slope = 0.f;
+                if constexpr (kMod) {
+                    if (p.mod.slopes) slope = p.mod.slopes[it.g * G + r % G] * 1.4426950408889634f;
+                }
+                const int lo_row = kMod ? window_start(pos_row, p.mod.window) : 0;
+                const int lo_hi = kMod ? window_start(pos_hi, p.mod.window) : 0;
                 for (int j = 0; j < nk; ++j) {
                     const int Tx = tx0 + j;
                     const int J = kv0 + j;
@@ -641,19 +682,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (any_bad) {
 #pragma unroll
                         for (int jb = 0; jb < kTcBlocks; ++jb) {
-                            const int blk = j * kTcBlocks + jb;
-                            if (blk < it.nblk_live) {
+                            const int blk = (it.j0 + j) * kTcBlocks + jb;
+                            if (blk >= it.blk_first && blk < it.nblk_live) {
                                 const int id = it.bt[blk];
                                 if (id < 0 || id >= p.num_blocks) bad |= 1u << jb;
                             }
                         }
                     }
+                    // (blocks before the window are dead in the same way)
+                    if (kMod && j == 0) bad |= (1u << (it.blk_first % kTcBlocks)) - 1u;
                     if (!__all_sync(kFullMask, wait_or_abort(&s_full[x], Tx & 1, abort_v))) {
                         ok = false;
                         break;
                     }
                     tc_fence_after_sync();
-                    const int key0 = j * kTcKeys;
+                    const int key0 = (it.j0 + j) * kTcKeys;
                     // The row maximum only decides the lazy rescale below, so a
                     // first pass takes the exponentials against the current
                     // reference m_ref without it.  When the tile's sum of P stays
@@ -664,7 +707,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // tensor memory until P is stored, and takes the maximum
                     // first.  Either way P is what taking the maximum every time
                     // gives.  (Warp-wide decisions: tcgen05.ld/st are collective.)
-                    bool need_max = __any_sync(kFullMask, m_ref == -INFINITY);
+                    // (Modified scores cost more than a maximum: it is taken first,
+                    // and there is no second pass.)
+                    bool need_max = kMod || __any_sync(kFullMask, m_ref == -INFINITY);
                     float sv[kTcKeys];
                     float l_tile;
 #pragma unroll 1
@@ -689,14 +734,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         // maximum of the scaled scores is the scaled maximum, as
                         // rounding is monotonic), fused with the subtraction of
                         // the exponent.
-                        if (!fold) {
+                        if constexpr (kMod) modify_scores(sv, p.mod, p.scale_log2, slope, key0 - pos_row);
+                        if (!kMod && !fold) {
 #pragma unroll
                             for (int c = 0; c < kTcKeys; c += 2) mul2(sv[c], sv[c + 1], p.scale_log2);
                         }
-                        if ((key0 + kTcKeys - 1 > pos_lo) || bad) {
+                        if ((key0 + kTcKeys - 1 > pos_lo) || bad || (kMod && key0 < lo_hi)) {
 #pragma unroll
                             for (int c = 0; c < kTcKeys; ++c) {
-                                const bool dead = key0 + c > pos_row || ((bad >> (c >> 4)) & 1u);
+                                const bool dead = key0 + c > pos_row || (kMod && key0 + c < lo_row) ||
+                                                  ((bad >> (c >> 4)) & 1u);
                                 sv[c] = dead ? -INFINITY : sv[c];
                             }
                         }
@@ -981,8 +1028,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const bool do_k = sk % kTcLoaders == li, do_v = sv % kTcLoaders == li;
                 if (!do_k && !do_v) continue;
                 int id = -1;
-                if (lane < kTcBlocks && j * kTcBlocks + lane < it.nblk_live) {
-                    id = it.bt[j * kTcBlocks + lane];
+                const int blk = (it.j0 + j) * kTcBlocks + lane;
+                if (lane < kTcBlocks && blk >= it.blk_first && blk < it.nblk_live) {
+                    id = it.bt[blk];
                     if (id < 0 || id >= p.num_blocks) {
                         if (do_k) record_error(p.err, PA_DEVERR_BLOCK_ID_);
                         id = -1;
@@ -1032,11 +1080,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 
-template <typename T, int D>
+template <typename T, int D, bool kMod = false>
 cudaError_t launch_t(const PrefillParams& p, int32_t* plan, const CUtensorMap& kmap, const CUtensorMap& vmap,
                      const CUtensorMap& qmap, int max_q_len, int num_tokens, const Fp8Copy* copy, cudaStream_t s) {
     constexpr int smem = TcShape<D>::kSmem;
-    auto kern = prefill_tc_kernel<T, D>;
+    auto kern = prefill_tc_kernel<T, D, kMod>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     // the softmax warpgroups' register increase is granted from the pool the
@@ -1048,10 +1096,15 @@ cudaError_t launch_t(const PrefillParams& p, int32_t* plan, const CUtensorMap& k
     if (launch_regs < kTcLaunchRegs) return cudaErrorInvalidConfiguration;
     const Fp8Copy none{};
     prefill_plan_kernel<<<1, 1024, 0, s>>>(p.cu_q_lens, p.seq_lens, p.num_seqs, num_tokens, p.q_per_tile, plan,
-                                           p.pair_cap, p.err, copy ? *copy : none, p.max_seq_len, p.max_blocks);
+                                           p.pair_cap, p.err, copy ? *copy : none, p.max_seq_len, p.max_blocks,
+                                           p.mod.window);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    if (copy && copy->cap_blocks > 0) {
+    if (copy && copy->fp4) {
+        e = launch_widen_fp4(*copy, p.seq_lens, p.max_blocks, p.num_kv_heads, D, std::is_same<T, __half>::value ? 0 : 1,
+                             s);
+        if (e != cudaSuccess) return e;
+    } else if (copy && copy->cap_blocks > 0) {
         // a few CTAs per SM stream the copy blocks (at most cap_blocks of them)
         const int wgrid = std::max(1, std::min(copy->cap_blocks, 8 * sm_count()));
         widen_chunk_blocks_kernel<T><<<wgrid, kWidenThreads, 0, s>>>(*copy, p.seq_lens, p.max_blocks,
@@ -1075,15 +1128,16 @@ cudaError_t launch_t(const PrefillParams& p, int32_t* plan, const CUtensorMap& k
 
 cudaError_t launch_prefill_tc(const PrefillParams& p, int32_t* plan, const CUtensorMap& kmap,
                               const CUtensorMap& vmap, const CUtensorMap& qmap, int head_dim, int dtype,
-                              int max_q_len, int num_tokens, const Fp8Copy* copy, cudaStream_t s) {
+                              int max_q_len, int num_tokens, const Fp8Copy* copy, bool modified, cudaStream_t s) {
     if (p.num_seqs == 0 || max_q_len <= PA_VERIFY_MAX_Q_) return cudaSuccess;
-    if (copy && head_dim != 128) return cudaErrorInvalidValue;
-    if (dtype == 0)
-        return head_dim == 128 ? launch_t<__half, 128>(p, plan, kmap, vmap, qmap, max_q_len, num_tokens, copy, s)
-                               : launch_t<__half, 64>(p, plan, kmap, vmap, qmap, max_q_len, num_tokens, copy, s);
-    return head_dim == 128
-               ? launch_t<__nv_bfloat16, 128>(p, plan, kmap, vmap, qmap, max_q_len, num_tokens, copy, s)
-               : launch_t<__nv_bfloat16, 64>(p, plan, kmap, vmap, qmap, max_q_len, num_tokens, copy, s);
+    if (copy && !copy->fp4 && head_dim != 128) return cudaErrorInvalidValue;
+    auto go = [&](auto launch) { return launch(p, plan, kmap, vmap, qmap, max_q_len, num_tokens, copy, s); };
+    if (modified) {
+        if (dtype == 0) return head_dim == 128 ? go(launch_t<__half, 128, true>) : go(launch_t<__half, 64, true>);
+        return head_dim == 128 ? go(launch_t<__nv_bfloat16, 128, true>) : go(launch_t<__nv_bfloat16, 64, true>);
+    }
+    if (dtype == 0) return head_dim == 128 ? go(launch_t<__half, 128>) : go(launch_t<__half, 64>);
+    return head_dim == 128 ? go(launch_t<__nv_bfloat16, 128>) : go(launch_t<__nv_bfloat16, 64>);
 }
 
 }  // namespace pa

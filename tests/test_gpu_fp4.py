@@ -1,0 +1,223 @@
+"""Attention over a 4-bit cache (decode, verify rows, prefill chunks) against a
+64-bit reference over the values that the cache's bytes stand for."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_attention_decode_gb300 as pa
+from tests import _ref64 as R
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+DT = {"f16": torch.float16, "bf16": torch.bfloat16}
+KS, VS = 1 / 256, 1 / 128
+
+
+def build(lens, qlens, Hq, Hkv, D, dt, seed, qscale=1.0):
+    """Pools of quantised N(0, 1) rows with scattered blocks; slots that no
+    sequence covers (tails of last blocks too) hold random codes and NaN scales."""
+    rng = np.random.default_rng(seed)
+    used = [(int(n) + 15) // 16 for n in lens]
+    NB = sum(used) + 3
+    perm = rng.permutation(NB)
+    tables = rng.integers(-5, NB + 5, (len(lens), max(1, max(used))))
+    live = np.zeros((NB, 16), bool)
+    at = 0
+    for b, u in enumerate(used):
+        tables[b, :u] = perm[at:at + u]
+        at += u
+        for j in range(int(lens[b])):
+            live[tables[b, j // 16], j % 16] = True
+    pools = []
+    for isv, sc in ((False, KS), (True, VS)):
+        codes, s = R.quantise_fp4(rng.standard_normal((NB, 16, Hkv, D)).astype(np.float32), sc)
+        codes[~live] = rng.integers(0, 16, codes[~live].shape)
+        s[~live] = 127
+        pools.append(R.pack_tiles(codes, s, isv))
+    T = int(sum(qlens))
+    q = (torch.randn(T, Hq, D, generator=torch.Generator().manual_seed(seed)) * qscale).to(dt)
+    return q, pools, tables.astype(np.int32)
+
+
+def put(*arrays):
+    return [(a if isinstance(a, torch.Tensor) else torch.from_numpy(np.ascontiguousarray(a))).to(DEV) for a in arrays]
+
+
+def check(out, q, pools, tables, lens, qlens, scale, bad=()):
+    kv = [R.tile_values(p, isv, s) for p, isv, s in zip(pools, (False, True), (KS, VS))]
+    ref, A, smax, cnt = R.attention(q.double().numpy(), *kv, tables, lens, qlens, scale, bad=bad)
+    tol = R.bound(ref, A, smax, cnt, 6 * 448 * VS, q.dtype, torch.float16)
+    got = out.double().cpu().numpy()
+    assert np.all(np.isfinite(got))
+    worst = np.max(np.abs(got - ref) / tol) if got.size else 0
+    assert worst <= 1, worst
+
+
+def decode(q, pools, tables, lens, scale, **kw):
+    qd, kd, vd, td, ld = put(q, *pools, tables, np.asarray(lens, np.int32))
+    out = pa.paged_attention_decode_fp4(qd, kd, vd, td, ld, scale, KS, VS, max_seq_len=int(max(lens)), **kw)
+    torch.cuda.synchronize()
+    return out
+
+
+def step(q, pools, tables, lens, qlens, scale, **kw):
+    cu = np.concatenate([[0], np.cumsum(qlens)]).astype(np.int32)
+    qd, kd, vd, td, ld, cd = put(q, *pools, tables, np.asarray(lens, np.int32), cu)
+    out = pa.paged_attention_prefill_fp4(qd, kd, vd, td, ld, cd, scale, KS, VS, int(max(qlens)), int(max(lens)), **kw)
+    torch.cuda.synchronize()
+    return out
+
+
+LENS = [1, 2, 15, 16, 17, 31, 33, 100, 511, 512, 513, 1025, 700]
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,dn", [(4, 4, 128, "f16"), (4, 4, 128, "bf16"), (3, 3, 64, "f16"), (8, 1, 64, "bf16"),
+                                         (8, 2, 128, "f16"), (16, 2, 128, "bf16"), (10, 2, 64, "bf16"),
+                                         (7, 1, 128, "f16"), (24, 2, 128, "f16"), (64, 1, 128, "bf16"),
+                                         (40, 2, 64, "f16")])
+def test_decode(Hq, Hkv, D, dn):
+    q, pools, tables = build(LENS, [1] * len(LENS), Hq, Hkv, D, DT[dn], seed=Hq + D)
+    out = decode(q, pools, tables, LENS, 1 / math.sqrt(D))
+    check(out, q, pools, tables, LENS, [1] * len(LENS), 1 / math.sqrt(D))
+    assert pa.device_error() == 0
+
+
+@pytest.mark.parametrize("part", [16, 64, 1024])
+def test_decode_partitions(part):
+    q, pools, tables = build(LENS, [1] * len(LENS), 8, 2, 128, torch.bfloat16, seed=part)
+    out = decode(q, pools, tables, LENS, 0.09, partition_size=part)
+    check(out, q, pools, tables, LENS, [1] * len(LENS), 0.09)
+
+
+@pytest.mark.parametrize("qscale", [1e-30, 1e-4, 300.0])
+@pytest.mark.parametrize("scale", [0.09, -0.05, 0.0])
+def test_decode_query_magnitudes(qscale, scale):
+    # bf16 queries far outside fp16's range enter exactly (a power of two per column)
+    lens = [40, 300]
+    q, pools, tables = build(lens, [1, 1], 8, 2, 128, torch.bfloat16, seed=4, qscale=qscale)
+    q[0, 0] = 0
+    q[1, 3, 5] *= 1000
+    out = decode(q, pools, tables, lens, scale)
+    check(out, q, pools, tables, lens, [1, 1], scale)
+
+
+def test_moving_reference():
+    # scores that pass the running reference by more than 2^8 block after block
+    lens = [200]
+    q, pools, tables = build(lens, [1], 4, 1, 64, torch.float16, seed=8)
+    q = torch.ones_like(q)
+    codes, s = R.unpack_tiles(pools[0], False)
+    for j in range(200):
+        codes[tables[0, j // 16], j % 16] = 2 + min(5, j // 33)      # rising keys
+        s[tables[0, j // 16], j % 16] = 0x50
+    pools[0] = R.pack_tiles(codes, s, False)
+    for scale in (2.0, -2.0):
+        out = decode(q, pools, tables, lens, scale)
+        check(out, q, pools, tables, lens, [1], scale)
+
+
+def test_empty_and_bad_rows():
+    lens = [30, 0, 50, 64]
+    q, pools, tables = build(lens, [1] * 4, 8, 4, 128, torch.float16, seed=2)
+    tables[2, 1] = 10 ** 6                    # tokens 16 .. 31 contribute nothing
+    qd, kd, vd, td, ld = put(q, *pools, tables, np.asarray(lens, np.int32))
+    out = torch.full_like(qd, 3.0)
+    pa.paged_attention_decode_fp4(qd, kd, vd, td, ld, 0.1, KS, VS, 64, out=out)
+    assert pa.device_error() == 1
+    check(out, q, pools, tables, lens, [1] * 4, 0.1)
+    assert torch.all(out[1] == 0)
+    tables[2] = -1                            # a row whose every block is bad
+    td = put(tables)[0]
+    pa.paged_attention_decode_fp4(qd, kd, vd, td, ld, 0.1, KS, VS, 64, out=out)
+    assert pa.device_error() == 1
+    assert torch.all(out[2] == 0)
+    # a length above the stated maximum is rejected as in the other decodes
+    pa.paged_attention_decode_fp4(qd, kd, vd, td, ld, 0.1, KS, VS, 50, out=out)
+    assert pa.device_error() & 4 and torch.all(out[3] == 0)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,dn", [(4, 4, 128, "bf16"), (8, 2, 128, "f16"), (16, 1, 64, "bf16"),
+                                         (24, 3, 128, "bf16"), (6, 2, 64, "f16")])
+def test_verify_and_decode_rows(Hq, Hkv, D, dn):
+    lens, qlens = [5, 17, 600, 1024, 33, 2, 1300, 8], [5, 8, 3, 1, 2, 2, 7, 8]
+    q, pools, tables = build(lens, qlens, Hq, Hkv, D, DT[dn], seed=Hq * D)
+    out = step(q, pools, tables, lens, qlens, 1 / math.sqrt(D))
+    check(out, q, pools, tables, lens, qlens, 1 / math.sqrt(D))
+    assert pa.device_error() == 0
+
+
+STEP = [(300, 300), (500, 37), (213, 9), (400, 150), (50, 2), (700, 8), (90, 4), (549, 1), (16, 1), (1, 1), (129, 128)]
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,dn", [(4, 4, 128, "f16"), (8, 2, 128, "bf16"), (6, 2, 64, "bf16"),
+                                         (16, 1, 64, "f16")])
+def test_varlen_step(Hq, Hkv, D, dn):
+    lens, qlens = zip(*STEP)
+    q, pools, tables = build(lens, qlens, Hq, Hkv, D, DT[dn], seed=Hq + Hkv)
+    out = step(q, pools, tables, lens, qlens, 1 / math.sqrt(D))
+    # (chunks: P in the query's type; the fp16 bound of `check` is for verify
+    # and decode rows, so bf16 chunks get the wider one)
+    kv = [R.tile_values(p, isv, s) for p, isv, s in zip(pools, (False, True), (KS, VS))]
+    ref, A, smax, cnt = R.attention(q.double().numpy(), *kv, tables, lens, qlens, 1 / math.sqrt(D))
+    tol = R.bound(ref, A, smax, cnt, 6 * 448 * VS, DT[dn], DT[dn])
+    got = out.double().cpu().numpy()
+    assert np.all(np.isfinite(got)) and np.max(np.abs(got - ref) / tol) <= 1
+    assert pa.device_error() == 0
+    # without a size hint the copy is sized from the arrays: the same bits
+    assert torch.equal(out, step(q, pools, tables, lens, qlens, 1 / math.sqrt(D), chunk_kv_tokens=sum(lens)))
+
+
+def test_chunks_that_do_not_fit_the_copy_are_skipped():
+    lens, qlens = [300, 1000, 50], [300, 37, 1]
+    q, pools, tables = build(lens, qlens, 8, 2, 64, torch.bfloat16, seed=6)
+    cu = np.concatenate([[0], np.cumsum(qlens)]).astype(np.int32)
+    qd, kd, vd, td, ld, cd = put(q, *pools, tables, np.asarray(lens, np.int32), cu)
+    per = 2 * 16 * 2 * 64 * 2
+    n = pa.prefill_fp8_workspace_bytes(3, int(cu[-1]), 8, 2, 64, 1000, tables.shape[1], 300)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)     # 19 + 2 blocks: the first chunk's alone
+    assert n > 21 * per
+    out = torch.full_like(qd, 5.0)
+    pa.paged_attention_prefill_fp4(qd, kd, vd, td, ld, cd, 0.1, KS, VS, 300, 1000, out=out, workspace=ws,
+                                   chunk_kv_tokens=300)
+    assert pa.device_error() == 16
+    assert torch.all(out[300:337] == 5.0)
+    kv = [R.tile_values(p, isv, s) for p, isv, s in zip(pools, (False, True), (KS, VS))]
+    ref, A, smax, cnt = R.attention(q.double().numpy(), *kv, tables, lens, qlens, 0.1)
+    tol = R.bound(ref, A, smax, cnt, 6 * 448 * VS, torch.bfloat16, torch.bfloat16)
+    ok = np.r_[0:300, 337:338]
+    assert np.max((np.abs(out.double().cpu().numpy() - ref) / tol)[ok]) <= 1
+
+
+def test_long_context_many_partitions():
+    lens = [9000, 33000]
+    q, pools, tables = build(lens, [1, 1], 2, 1, 64, torch.bfloat16, seed=12)
+    out = decode(q, pools, tables, lens, 0.125)
+    check(out, q, pools, tables, lens, [1, 1], 0.125)
+
+
+def test_pool_past_4_gib():
+    """Tiles past 2^32 bytes of a pool: the last blocks of a large pool."""
+    Hkv, D = 8, 128
+    tile = pa.fp4_tile_bytes(D)
+    NB = (1 << 32) // (Hkv * tile) + 40
+    lens = [100, 37]
+    q, pools, tables = build(lens, [1, 1], 16, Hkv, D, torch.float16, seed=13)
+    n = pools[0].shape[0]
+    big = []
+    for p in pools:
+        x = torch.full((NB, Hkv, tile), 0x7F, dtype=torch.uint8, device=DEV)
+        x[NB - n:] = torch.from_numpy(p).to(DEV)
+        big.append(x)
+    far = np.where((tables >= 0) & (tables < n), tables + NB - n, tables).astype(np.int32)
+    qd, td, ld = put(q, far, np.asarray(lens, np.int32))
+    out = pa.paged_attention_decode_fp4(qd, *big, td, ld, 0.1, KS, VS, 100)
+    check(out, q, pools, tables, lens, [1, 1], 0.1)
+    # the writer reaches the last slot too
+    k = torch.randn(1, Hkv, D, dtype=torch.float16, device=DEV)
+    pa.paged_kv_write_fp4(k, k, *big, torch.tensor([NB * 16 - 1], device=DEV), KS, VS)
+    c, s = R.quantise_fp4(k.float().cpu().numpy(), KS)
+    got, gs = R.unpack_tiles(big[0][-1:].cpu().numpy(), False)
+    assert np.array_equal(got[0, 15], c[0]) and np.array_equal(gs[0, 15], s[0])
+    assert pa.device_error() == 0
