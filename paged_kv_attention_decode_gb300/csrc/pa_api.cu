@@ -175,7 +175,8 @@ size_t partials_bytes(int num_seqs, int num_q_heads, int head_dim, int parts) {
 }
 
 // Decode workspace:
-//   [header 256 B: unit count @0, partials row count @64, work counter @128]
+//   [header 256 B: unit count @0, partials row count @64, work counter @128,
+//    chunk CTAs of a varlen call @192]
 //   [unit list: num_seqs * parts int32]
 //   when parts > 1: [row_base: num_seqs int32][rows: max_rows int32][partials of max_rows rows]
 size_t decode_ws_bytes(int num_seqs, int max_rows, int num_q_heads, int head_dim, int parts) {
@@ -192,6 +193,7 @@ void carve_workspace(pa::DecodeParams& p, void* ws) {
     p.unit_count = reinterpret_cast<int32_t*>(base);
     p.row_count = reinterpret_cast<int32_t*>(base + 64);
     p.work_counter = reinterpret_cast<int32_t*>(base + 128);
+    p.split = reinterpret_cast<int32_t*>(base + 192);
     p.units = reinterpret_cast<int32_t*>(base + 256);
     base += 256 + align256(static_cast<size_t>(p.num_seqs) * p.max_parts * sizeof(int32_t));
     if (p.max_parts > 1) {
@@ -221,6 +223,8 @@ enum class Cache { k16, kFp8, kFp4 };
 // Bytes of one 4-bit (block, kv head) tile: 16 rows of head_dim / 2 code bytes
 // and head_dim / 16 group scales.
 int fp4_tile_bytes(int head_dim) { return PA_BLOCK_SIZE * (head_dim / 2 + head_dim / 16); }
+
+bool softcapped(const pa::ScoreMod& m) { return m.cap_log2 > 0.f; }
 
 bool score_mod(pa::ScoreMod& m, float scale, float softcap, int window, const float* slopes) {
     if (!std::isfinite(softcap) || softcap < 0.f || window < 0) return false;
@@ -766,6 +770,14 @@ static int prefill_impl(void* out, const void* q, const void* k_cache, const voi
     p.decode_units = dc.p.unit_count;
     p.overlap_ctas = std::max(1, copied ? pa::sm_count() * kOverlapPrefillNumFp8 / kOverlapPrefillDenFp8
                                      : pa::sm_count() * kOverlapPrefillNum / kOverlapPrefillDen);
+    if (mod || cache == Cache::kFp4) {
+        // SMs shared by work.  Measured: a key tile of a pair (two 128 x 128
+        // tiles) takes 2.0 us of one SM at head_dim 128 (capped scores 3.0 us),
+        // a key of a decode row 12 ns (16-bit) or 5 ns (4-bit) of one SM per
+        // column chunk.
+        p.split = dc.p.split;
+        p.decode_weight = (cache == Cache::kFp4 ? 5.f : 12.f) * dc.p.col_chunks / (mod && softcapped(*mod) ? 3000.f : 2000.f);
+    }
     if (pa::launch_prefill_tc(p, plan, kmap, vmap, qmap, head_dim, dtype, max_q_len, num_tokens,
                               copied ? &copy : nullptr, mod != nullptr, s) !=
         cudaSuccess)

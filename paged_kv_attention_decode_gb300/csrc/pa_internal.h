@@ -69,6 +69,7 @@ struct DecodeParams {
     int32_t* row_base;            // [B] first partials row of a split sequence
     int32_t* rows;                // [max_rows] (sequence << 3 | query index) of every partials row
     int32_t* row_count;           // number of entries in `rows` (header of the workspace)
+    int32_t* split;               // varlen calls: CTAs that take chunks (header of the workspace)
     unsigned int* err;            // device error word
     int num_seqs;
     int max_blocks;
@@ -119,6 +120,11 @@ struct PrefillParams {
     int overlap_ctas;
     int pair_cap;                 // pair-list capacity of the plan (num_tokens / 4 + num_seqs)
     ScoreMod mod;
+    // non-null: the plan shares the SMs between chunks and decode rows by their
+    // work and writes the number of CTAs that take chunks here; a key of a
+    // decode row costs decode_weight key tiles of a query-tile pair
+    int32_t* split;
+    float decode_weight;
 };
 
 // Rotation and cache write of new tokens; strides count elements between tokens.

@@ -292,14 +292,19 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
                                                             int num_tokens, int q_per_tile,
                                                             int32_t* __restrict__ offsets, int pair_cap,
                                                             unsigned int* err, const Fp8Copy copy, int max_seq_len,
-                                                            int max_blocks, int window) {
+                                                            int max_blocks, int window, int32_t* split,
+                                                            int split_ctas, float decode_weight) {
     __shared__ int warp_tot[32];
+    __shared__ unsigned long long chunk_cost, row_cost;   // key tiles of pairs; keys of decode and verify rows
     __shared__ int carry, blk_carry, chunk_carry, blk_end;
     __shared__ int hist[kPlanBuckets];
     int32_t* order = offsets + num_seqs + 1;
     int32_t* seq_of_pair = order + pair_cap;
     const int tid = threadIdx.x;
-    if (tid == 0) carry = blk_carry = chunk_carry = blk_end = 0;
+    if (tid == 0) {
+        carry = blk_carry = chunk_carry = blk_end = 0;
+        chunk_cost = row_cost = 0;
+    }
     for (int i = tid; i < kPlanBuckets; i += 1024) hist[i] = 0;
     __syncthreads();
     // the pairs of sequence b: count them (offsets) and their cost classes
@@ -347,6 +352,13 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
         }
         if (b < num_seqs)
             for (int pr = 0; pr < v; ++pr) atomicAdd(&hist[bucket(n, ql, pr)], 1);
+        if (split && b < num_seqs && n >= ql && n <= max_seq_len) {
+            unsigned long long cost = 0;
+            for (int pr = 0; pr < v; ++pr) cost += pair_key_tiles(n, ql, q_per_tile, pr, window);
+            if (cost) atomicAdd(&chunk_cost, cost);
+            if (ql > 0 && ql <= PA_VERIFY_MAX_Q_)
+                atomicAdd(&row_cost, static_cast<unsigned long long>(n - window_start(n - ql, window)));
+        }
         const int start = block_exclusive_scan_1024(v, warp_tot, &carry);
         if (b < num_seqs) {
             offsets[b] = start;
@@ -355,6 +367,12 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
     }
     if (tid == 0) {
         offsets[num_seqs] = carry;
+        if (split) {
+            // the CTAs that take chunks: in proportion to the two kinds' work,
+            // so that they end together
+            const float c = static_cast<float>(chunk_cost), d = static_cast<float>(row_cost) * decode_weight;
+            *split = c + d > 0.f ? min(split_ctas, max(1, static_cast<int>(split_ctas * c / (c + d) + 0.5f))) : split_ctas;
+        }
         if (copy.hdr) {
             copy.hdr[0] = chunk_carry;
             copy.hdr[1] = blk_end;
@@ -499,8 +517,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // (even totals, the kernel ends together).  Beside decode rows, they take
     // them round-robin in plan order: CTAs that finish early hand their SMs to
     // the HBM-bound decode kernel sooner, which shortens the step more.
-    const bool snake = !(p.decode_units && *p.decode_units > 0);
-    if (!snake) ctas = min(ctas, p.overlap_ctas);
+    // (With a split by work (p.split), the CTAs that stay also end together.)
+    const bool snake = p.split || !(p.decode_units && *p.decode_units > 0);
+    if (p.split) ctas = min(ctas, *p.split);
+    else if (!snake) ctas = min(ctas, p.overlap_ctas);
     const int total_items = plan[p.num_seqs] * p.num_kv_heads;
     if (static_cast<int>(blockIdx.x) >= total_items || static_cast<int>(blockIdx.x) >= ctas) return;
 
@@ -1097,7 +1117,7 @@ cudaError_t launch_t(const PrefillParams& p, int32_t* plan, const CUtensorMap& k
     const Fp8Copy none{};
     prefill_plan_kernel<<<1, 1024, 0, s>>>(p.cu_q_lens, p.seq_lens, p.num_seqs, num_tokens, p.q_per_tile, plan,
                                            p.pair_cap, p.err, copy ? *copy : none, p.max_seq_len, p.max_blocks,
-                                           p.mod.window);
+                                           p.mod.window, p.split, sm_count(), p.decode_weight);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if (copy && copy->fp4) {
