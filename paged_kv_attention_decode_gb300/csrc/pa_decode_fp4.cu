@@ -6,29 +6,25 @@
 // 16-bit decode kernel; the block step differs.
 //
 // One warp handles one (sequence partition, kv head) item and streams its
-// (block, kv head) tiles, 9 D bytes each for K and for V.
-//  * The tiles go from memory straight to registers, in the layout of the
-//    tensor-core fragments, one block ahead of the block being computed: no
-//    shared memory, no barriers.  For S^T = K Q^T a lane (g, c) = (lane / 4,
-//    lane % 4) reads its quarter row of dims for two tokens (one 16-byte load
-//    each at head_dim 128); the order of the dims in the contraction is free,
-//    and Q^T is loaded in the same order.  For O^T = V^T P^T it reads 16 dims
-//    (one scale group) of tokens 4c .. 4c + 3; two masks and shifts per word
-//    pair the tokens of each dim, so that one conversion gives an fp16 pair of
-//    consecutive tokens of one dim, which is what the fragment holds.
+// (block, kv head) tiles, 9 D bytes each for K and for V, two blocks a step.
+//  * The warp copies the tiles into its own ring of shared-memory slots with
+//    16-byte cp.async, all lanes at once, and waits for no other warp.
+//  * The tensor-core fragments come from the tiles without a 16-bit copy.  For
+//    S^T = K Q^T a lane (g, c) = (lane / 4, lane % 4) reads its quarter row of
+//    dims for two tokens (one 16-byte load each at head_dim 128); the order of
+//    the dims in the contraction is free, and Q^T is loaded in the same order.
+//    For O^T = V^T P^T it reads 16 dims (one scale group) of tokens 4c .. 4c +
+//    3; two masks and shifts per word pair the tokens of each dim, so that one
+//    conversion gives an fp16 pair of consecutive tokens of one dim, which is
+//    what the fragment holds.
 //  * Codes are widened to fp16 and multiplied by their group's scale (exact,
 //    see group_values), then fed to mma.sync m16n8k16 (fp32 accumulate).  P is
 //    fp16 (at most 2^8, 11 significant bits).  bf16 queries enter as fp16
 //    times a power of two per column, chosen so that the column's largest
 //    magnitude lies in [2^8, 2^9): every element above 2^-22 of it is exact.
 //  * Softmax: a column's reference maximum moves only when some score passes
-//    it by more than 2^8, so most blocks need one vote and no reduction.  P^T
+//    it by more than 2^8, so most steps need one vote and no reduction.  P^T
 //    reaches the second product's layout through movmatrix.
-//
-// Bound: HBM, 4.5 bits per cached value.  A tile pair is 18 D bytes (2304 at
-// head_dim 128), 98 SM clocks at the measured copy rate over 152 SMs; a block
-// step issues about 220 instructions per warp (64 conversions on the 16-lane
-// pipe), 55 clocks per SM when four warps issue side by side.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -49,51 +45,126 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
     return d;
 }
 
-// One block's tile pair as this lane holds it.
+// D = A B (m16n8k16, fp16 operands, fp32 result), without an accumulator to clear.
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// 16 bytes from memory (src + kSrc) to shared memory (dst + kDst), not kept in
+// L1 (each tile is read once).
+template <int kDst, int kSrc>
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(kDst), "n"(kSrc)
+                 : "memory");
+}
+// f(0), f(1) .. f(N - 1) with the index as a compile-time constant.
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        static_for<N, I + 1>(f);
+    }
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {   // until at most N groups are pending
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// W 32-bit words (and 8- or 16-bit ones) of shared memory at `addr` + kOff.
+template <int W, int kOff>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[W]) {
+    if constexpr (W == 4)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4 + %5];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(addr), "n"(kOff));
+    else if constexpr (W == 2)
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2 + %3];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr), "n"(kOff));
+    else
+        asm volatile("ld.shared.u32 %0, [%1 + %2];" : "=r"(w[0]) : "r"(addr), "n"(kOff));
+}
+template <int kOff>
+__device__ __forceinline__ uint16_t lds_u16(uint32_t addr) {
+    uint16_t x;
+    asm volatile("ld.shared.u16 %0, [%1 + %2];" : "=h"(x) : "r"(addr), "n"(kOff));
+    return x;
+}
+template <int kOff>
+__device__ __forceinline__ uint16_t lds_u8x2(uint32_t addr) {   // one byte, twice
+    uint32_t x;
+    asm volatile("ld.shared.u8 %0, [%1 + %2];" : "=r"(x) : "r"(addr), "n"(kOff));
+    return static_cast<uint16_t>(x * 0x0101u);
+}
+
+// One block's tiles as this lane holds them.
 template <int D>
-struct Fp4Frag {
-    static constexpr int KW = D / 32;    // 32-bit words of K codes per token (a quarter row)
-    static constexpr int VW = D / 64;    // 32-bit words of V codes per token
+struct Fp4K {
+    static constexpr int KW = D / 32;    // 32-bit words of codes per token (a quarter row)
     uint32_t k[2][KW];                   // tokens ta, ta + 2
-    uint32_t ks[2];                      // their scales (D / 64 bytes each)
-    uint32_t v[4][VW];                   // tokens 4c .. 4c + 3, dims of this lane
-    uint32_t vs;                         // their four scales
+    uint16_t ks[2];                      // their scales (two groups at head_dim 128, one twice at 64)
+};
+template <int D>
+struct Fp4V {
+    static constexpr int VW = D / 64;    // 32-bit words of codes per token
+    uint32_t v[4][VW];                   // tokens 4c .. 4c + 3 (pairs swapped: flip), dims of this lane
+    uint32_t vs;                         // scales of tokens 4c .. 4c + 3
 };
 
+// Byte offsets of this lane's words within a tile.  The lanes of a V load read
+// 64-byte rows: quarters c = 2, 3 take their token pairs in swapped order, so
+// that a load touches even and odd rows alike (two wavefronts per half warp
+// instead of four); S^T takes its rows in the same order.
 template <int D>
-__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[D]) {
-    if constexpr (D == 4) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
-        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-    } else if constexpr (D == 2) {
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
-        w[0] = x.x; w[1] = x.y;
-    } else {
-        w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-    }
-}
-
-template <int D>
-__device__ __forceinline__ void load_frag(Fp4Frag<D>& f, const uint8_t* kt, const uint8_t* vt, int lane) {
+struct Fp4Lane {
     using Tile = Fp4Tile<D>;
-    const int g = lane >> 2, c = lane & 3;
-    const int ta = 4 * (g >> 1) + (g & 1);            // rows g and g + 8 of S^T
-    const int vg = D == 128 ? g : g >> 1;             // scale group of this lane's V dims
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int t = ta + 2 * i;
-        load_words(kt + t * Tile::kRow + c * (Tile::kRow / 4), f.k[i]);
-        const uint8_t* s = kt + Tile::scale_off(false, t, c * (D / 64));
-        if constexpr (D == 128) f.ks[i] = __ldg(reinterpret_cast<const uint16_t*>(s));
-        else f.ks[i] = __ldg(s);
+    int ta;              // rows g and g + 8 of S^T: tokens ta, ta + 2
+    int k, ks, vs;
+    int va, vb;          // first and second token of a pair
+    uint32_t flip;       // byte order of a word of four scales: this quarter's pairs may be swapped
+    __device__ __forceinline__ explicit Fp4Lane(int lane) {
+        const int g = lane >> 2, c = lane & 3;
+        ta = 4 * (g >> 1) + ((g & 1) ^ (g >> 2));
+        flip = c >> 1 ? 0x2301u : 0x3210u;
+        k = ta * Tile::kRow + c * (Tile::kRow / 4);
+        ks = Tile::scale_off(false, ta, c * (D / 64));
+        va = (4 * c + (c >> 1)) * Tile::kRow + g * (Tile::kRow / 8);
+        vb = (4 * c + 1 - (c >> 1)) * Tile::kRow + g * (Tile::kRow / 8);
+        vs = Tile::scale_off(true, 4 * c, D == 128 ? g : g >> 1);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) load_words(vt + (4 * c + i) * Tile::kRow + g * (Tile::kRow / 8), f.v[i]);
-    f.vs = __ldg(reinterpret_cast<const uint32_t*>(vt + Tile::scale_off(true, 4 * c, vg)));
-}
+    // `slot`: shared address of a slot; kJ: which of its two blocks.
+    template <int kJ>
+    __device__ __forceinline__ void load_k(Fp4K<D>& f, uint32_t slot) const {
+        constexpr int o = 2 * kJ * Tile::kBytes;
+        lds_words<Fp4K<D>::KW, o>(slot + k, f.k[0]);
+        lds_words<Fp4K<D>::KW, o + 2 * Tile::kRow>(slot + k, f.k[1]);
+        if constexpr (D == 128) {
+            f.ks[0] = lds_u16<o>(slot + ks);
+            f.ks[1] = lds_u16<o + 2 * Tile::kGroups>(slot + ks);
+        } else {
+            f.ks[0] = lds_u8x2<o>(slot + ks);
+            f.ks[1] = lds_u8x2<o + 2 * Tile::kGroups>(slot + ks);
+        }
+    }
+    template <int kJ>
+    __device__ __forceinline__ void load_v(Fp4V<D>& f, uint32_t slot) const {
+        constexpr int o = (2 * kJ + 1) * Tile::kBytes;
+        lds_words<Fp4V<D>::VW, o>(slot + va, f.v[0]);
+        lds_words<Fp4V<D>::VW, o>(slot + vb, f.v[1]);
+        lds_words<Fp4V<D>::VW, o + 2 * Tile::kRow>(slot + va, f.v[2]);
+        lds_words<Fp4V<D>::VW, o + 2 * Tile::kRow>(slot + vb, f.v[3]);
+        uint32_t x[1];
+        lds_words<1, o>(slot + vs, x);
+        f.vs = x[0];
+    }
+};
 
-// NT tiles of 8 (query, head) columns of one item.
-template <int D, int NT>
+// NT tiles of 8 (query, head) columns of one item.  E = 1: only one column
+// (single queries without grouped heads), so that a lane's second one is left out.
+template <int D, int NT, int E>
 struct Fp4State {
     static constexpr int KS = D / 16;
     uint32_t qb[KS][NT][2];   // Q^T: k-step kk holds dims c * D/4 + 4 kk + {0, 1 | 2, 3}
@@ -101,62 +172,69 @@ struct Fp4State {
     float m[NT][2], l[NT][2], mul[NT][2];
     int lim[NT][2];           // first token the column may not see
 
-    __device__ __forceinline__ void step(Fp4Frag<D>& f, int base, int nvalid, bool masked, int lane) {
-        const int g = lane >> 2, c = lane & 3;
-        const int ta = 4 * (g >> 1) + (g & 1);
-        float s[NT][4], s2[NT][4];
+    // S^T = K Q^T of one block (raw products).
+    __device__ __forceinline__ void scores(const Fp4K<D>& f, float (&s)[NT][4]) const {
+        uint32_t sc[2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int i = 0; i < 2; ++i) sc[i] = e4m3x2_to_f16x2(f.ks[i]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[nt][e] = s2[nt][e] = 0.f;
-        // S^T = K Q^T, two accumulation chains
-        {
-            uint32_t sc[2];
+        for (int w = 0; w < Fp4K<D>::KW; ++w) {
+            uint32_t x[2][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                sc[i] = e4m3x2_to_f16x2(static_cast<uint16_t>(D == 128 ? f.ks[i] : f.ks[i] * 0x0101u));
+            for (int i = 0; i < 2; ++i) {
+                // words 0, 1 belong to the lane's first group, 2, 3 to its second
+                const uint32_t b = __byte_perm(sc[i], 0u, w < 2 ? 0x1010u : 0x3232u);
+                e2m1x8_to_f16x2(f.k[i][w], x[i]);
 #pragma unroll
-            for (int w = 0; w < Fp4Frag<D>::KW; ++w) {
-                uint32_t x[2][4];
+                for (int j = 0; j < 4; ++j) x[i][j] = hmul2_bits(x[i][j], b);
+            }
+            const uint32_t a0[4] = {x[0][0], x[1][0], x[0][1], x[1][1]};
+            const uint32_t a1[4] = {x[0][2], x[1][2], x[0][3], x[1][3]};
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    // words 0, 1 belong to the lane's first group, 2, 3 to its second
-                    const uint32_t b = __byte_perm(sc[i], 0u, w < 2 ? 0x1010u : 0x3232u);
-                    e2m1x8_to_f16x2(f.k[i][w], x[i]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) x[i][j] = hmul2_bits(x[i][j], b);
-                }
-                const uint32_t a0[4] = {x[0][0], x[1][0], x[0][1], x[1][1]};
-                const uint32_t a1[4] = {x[0][2], x[1][2], x[0][3], x[1][3]};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    Mma<__half>::run(s[nt], a0, qb[2 * w][nt][0], qb[2 * w][nt][1]);
-                    Mma<__half>::run(s2[nt], a1, qb[2 * w + 1][nt][0], qb[2 * w + 1][nt][1]);
-                }
+            for (int nt = 0; nt < NT; ++nt) {
+                if (w == 0) mma_first(s[nt], a0, qb[0][nt][0], qb[0][nt][1]);
+                else Mma<__half>::run(s[nt], a0, qb[2 * w][nt][0], qb[2 * w][nt][1]);
+                Mma<__half>::run(s[nt], a1, qb[2 * w + 1][nt][0], qb[2 * w + 1][nt][1]);
             }
         }
-        bool grow = false;
+    }
+
+    // Tokens at and past the columns' limits (all of them when !ok) get -inf.
+    __device__ __forceinline__ void mask(float (&s)[NT][4], int base, bool ok, int ta) const {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                s[nt][e] = (s[nt][e] + s2[nt][e]) * mul[nt][e];
-                s[nt][2 + e] = (s[nt][2 + e] + s2[nt][2 + e]) * mul[nt][e];
-                if (masked) {
-                    if (base + ta >= lim[nt][e]) s[nt][e] = -INFINITY;
-                    if (base + ta + 2 >= lim[nt][e]) s[nt][2 + e] = -INFINITY;
-                }
-                grow |= fmaxf(s[nt][e], s[nt][2 + e]) > m[nt][e] + kLazyLog2;
+            for (int e = 0; e < E; ++e) {
+                if (!ok || base + ta >= lim[nt][e]) s[nt][e] = -INFINITY;
+                if (!ok || base + ta + 2 >= lim[nt][e]) s[nt][2 + e] = -INFINITY;
             }
         }
+    }
+
+    // Softmax weights of NB blocks' raw scores against the running reference,
+    // as the B operand of the second product (b[block][nt][2]).  mul > 0.
+    template <int NB>
+    __device__ __forceinline__ void weights(const float (&s)[NB][NT][4], uint32_t (&b)[NB][NT][2]) {
+        auto largest = [&](int nt, int e) {
+            float mx = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
+#pragma unroll
+            for (int j = 1; j < NB; ++j) mx = fmaxf(mx, fmaxf(s[j][nt][e], s[j][nt][2 + e]));
+            return mx;
+        };
+        bool grow = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < E; ++e) grow |= largest(nt, e) * mul[nt][e] > m[nt][e] + kLazyLog2;
         if (__any_sync(kAll, grow)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float mx = fmaxf(s[nt][e], s[nt][2 + e]);
+                for (int e = 0; e < E; ++e) {
+                    float mx = largest(nt, e);
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, off));
+                    mx *= mul[nt][e];
                     if (!(mx > m[nt][e] + kLazyLog2)) continue;
                     const float al = fast_exp2(m[nt][e] - mx);   // 0 while the column saw no token yet
                     m[nt][e] = mx;
@@ -169,30 +247,43 @@ struct Fp4State {
                 }
             }
         }
-        uint32_t b0[NT], b1[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             // a column without a visible token yet keeps m = -inf; its weights are 2^(-inf - 0) = 0
-            const float r0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
-            const float r1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-            const float p0 = fast_exp2(s[nt][0] - r0), p1 = fast_exp2(s[nt][1] - r1);
-            const float p2 = fast_exp2(s[nt][2] - r0), p3 = fast_exp2(s[nt][3] - r1);
-            l[nt][0] += p0 + p2;
-            l[nt][1] += p1 + p3;
-            // rows 2c, 2c + 1 of the two 8 x 8 pieces are tokens 4c, 4c + 1 and 4c + 2, 4c + 3
-            b0[nt] = movmatrix_trans(Elem<__half>::pack(p0, p1));
-            b1[nt] = movmatrix_trans(Elem<__half>::pack(p2, p3));
+            float r[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) r[e] = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                float w[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    w[e] = fast_exp2(fmaf(s[j][nt][e], mul[nt][e], -r[e]));
+                    w[2 + e] = fast_exp2(fmaf(s[j][nt][2 + e], mul[nt][e], -r[e]));
+                    l[nt][e] += w[e] + w[2 + e];
+                }
+                // rows 2c, 2c + 1 of the two 8 x 8 pieces are tokens 4c, 4c + 1 and 4c + 2, 4c + 3 (flipped alike)
+                b[j][nt][0] = movmatrix_trans(Elem<__half>::pack(w[0], w[1]));
+                b[j][nt][1] = movmatrix_trans(Elem<__half>::pack(w[2], w[3]));
+            }
         }
+    }
+
+    // O^T += V^T P^T of one block.  Unless `full`, tokens at and past nvalid
+    // count as 0.
+    __device__ __forceinline__ void accumulate(const Fp4V<D>& f, const uint32_t (&b)[NT][2], bool full, int nvalid,
+                                               int c, uint32_t flip) {
         uint32_t vs = f.vs;
-        if (nvalid < 16) {
+        if (!full) {
             // rows past the end may hold anything, a NaN scale too: their scale becomes 0
             const int keep = min(4, max(0, nvalid - 4 * c));
             vs = keep == 4 ? vs : vs & ((1u << (8 * keep)) - 1u);
         }
+        vs = __byte_perm(vs, 0u, flip);
         const uint32_t s01 = e4m3x2_to_f16x2(static_cast<uint16_t>(vs & 0xffffu));
         const uint32_t s23 = e4m3x2_to_f16x2(static_cast<uint16_t>(vs >> 16));
 #pragma unroll
-        for (int w = 0; w < Fp4Frag<D>::VW; ++w) {
+        for (int w = 0; w < Fp4V<D>::VW; ++w) {
             constexpr uint32_t kLow = 0x0f0f0f0fu;
             // byte b: (first, second token) of dim 8w + 2b (even) or 8w + 2b + 1 (odd)
             uint32_t e01[4], o01[4], e23[4], o23[4];
@@ -201,26 +292,54 @@ struct Fp4State {
             e2m1x8_to_f16x2((f.v[2][w] & kLow) | ((f.v[3][w] << 4) & ~kLow), e23);
             e2m1x8_to_f16x2(((f.v[2][w] >> 4) & kLow) | (f.v[3][w] & ~kLow), o23);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const uint32_t a[4] = {hmul2_bits(e01[b], s01), hmul2_bits(o01[b], s01), hmul2_bits(e23[b], s23),
-                                       hmul2_bits(o23[b], s23)};
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t a[4] = {hmul2_bits(e01[i], s01), hmul2_bits(o01[i], s01), hmul2_bits(e23[i], s23),
+                                       hmul2_bits(o23[i], s23)};
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) Mma<__half>::run(o[4 * w + b][nt], a, b0[nt], b1[nt]);
+                for (int nt = 0; nt < NT; ++nt) Mma<__half>::run(o[4 * w + i][nt], a, b[nt][0], b[nt][1]);
             }
         }
     }
 };
 
+// A warp's ring of slots; a slot holds the (K tile, V tile) of a step's blocks.
+// kCols: columns of an item (1, 8 or 16).
+template <int D, int kCols>
+struct Fp4Shape {
+    static constexpr int kTile = Fp4Tile<D>::kBytes;
+    static constexpr int kBlocks = kCols > 8 ? 2 : 4;   // per step
+    static constexpr int kSlot = 2 * kBlocks * kTile;
+    static constexpr int kSlots = kCols > 8 ? 3 : 2;
+    static constexpr int kMinCtas = kCols > 8 ? 2 : 3;
+    static constexpr int kSmem = kFp4Warps * kSlots * kSlot;
+};
+
 // Persistent and warp-granular: a warp takes its first item by its own index
-// and the following ones from the plan's counter, claimed one item ahead.
-template <typename T, int D, int kMaxNT>
-__global__ void __launch_bounds__(kFp4Warps * 32, kMaxNT == 1 ? 4 : 2) decode_fp4_kernel(const DecodeParams p) {
-    using Tile = Fp4Tile<D>;
-    constexpr int kCols = 8 * kMaxNT;
+// and the following ones from the plan's counter, claimed one item ahead.  It
+// fetches kSlots steps ahead of the step being computed and on into its next
+// items.  Each step commits one group of copies (an empty one past the last
+// item), so the oldest of kSlots groups is always the one being waited for.
+template <typename T, int D, int kCols>
+__global__ void __launch_bounds__(kFp4Warps * 32, Fp4Shape<D, kCols>::kMinCtas) decode_fp4_kernel(const DecodeParams p) {
+    using Shape = Fp4Shape<D, kCols>;
+    constexpr int NB = Shape::kBlocks;
+    constexpr int E = kCols == 1 ? 1 : 2;
+    constexpr int kTile = Shape::kTile;
+    constexpr int kSlots = Shape::kSlots;
+    constexpr int kQueue = 8;   // items fetched (in part) and not yet computed: at most kSlots + 1
+    static_assert(kSlots + 1 < kQueue, "the item queue");
+    struct Item {
+        int b, h, part, n, qlen, qrow0, col0, nblk;
+    };
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    __shared__ __align__(16) Item all_queue[kFp4Warps][kQueue];
+    const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
     const int G = p.group, H = p.num_kv_heads, C = p.col_chunks, P = p.partition_tokens;
     const int warps = gridDim.x * kFp4Warps;
+    const uint32_t ring = smem_addr(smem_raw) + warp * kSlots * Shape::kSlot;
+    Item* queue = all_queue[warp];
     // the work list (and, through it, the KV write) is complete; with
     // p.overlap the list was built before the prefill kernel that this one
     // runs beside, and the wait moves to the exit
@@ -228,48 +347,155 @@ __global__ void __launch_bounds__(kFp4Warps * 32, kMaxNT == 1 ? 4 : 2) decode_fp
     pdl_trigger();   // the merge may be scheduled; it waits for this grid
     const int total = *p.unit_count * H * C;
 
-    auto run_item = [&](auto nt_tag, int b, int h, int part, int n, int qlen, int64_t qrow0, int col0, int ncols) {
+    // ---- fetch cursor ----------------------------------------------------
+    uint32_t q_tail = 0, q_head = 0;
+    const int32_t* f_bt = nullptr;
+    // the item's head in block 0, plus this lane's 16 bytes: K, V, and the
+    // tiles' last chunks (lanes 0 .. kTail - 1 of K, the next kTail lanes of V)
+    constexpr int kFull = kTile / 16 / 32, kTail = kTile / 16 % 32;   // 16-byte chunks per lane, and left over
+    const uint8_t *f_k = nullptr, *f_v = nullptr, *f_t = nullptr;
+    const int t_off = lane < kTail ? 0 : kTile - 16 * kTail;          // where a lane's last chunk goes
+    int f_nblk = 0, f_i = 0, ids = -1;
+    const uint32_t block_bytes = static_cast<uint32_t>(H) * kTile;   // below 2^27: H <= 65535
+    // The item after the cursor's is looked up ahead, one dependent load a
+    // step, so that taking it finds everything in registers: its index
+    // (claimed by lane 0), its unit, then its sequence's length and rows.
+    int n_claim = blockIdx.x * kFp4Warps + warp, n_stage = 0;
+    int n_w = 0, n_h = 0, n_col0 = 0, n_len = 0, n_row0 = 0, n_row1 = 0;
+    uint32_t n_unit = 0;
+    auto look_ahead = [&]() {
+        if (n_stage == 0) {
+            n_w = __shfl_sync(kAll, n_claim, 0);
+            if (n_w < total) {
+                const int ug = C == 1 ? n_w : n_w / C;
+                const int u = ug / H;
+                n_h = ug - u * H;
+                n_col0 = (n_w - ug * C) * kCols;
+                n_unit = static_cast<uint32_t>(__ldg(p.units + u));
+            }
+            n_stage = 1;
+        } else if (n_stage == 1) {
+            if (n_w < total) {
+                const int b = static_cast<int>(n_unit >> 16);
+                n_len = __ldg(p.seq_lens + b);
+                n_row0 = b;
+                n_row1 = b + 1;
+                if (p.cu_q_lens) {
+                    n_row0 = __ldg(p.cu_q_lens + b);
+                    n_row1 = __ldg(p.cu_q_lens + b + 1);
+                }
+            }
+            n_stage = 2;
+        }
+    };
+    auto next_item = [&]() {
+        f_nblk = f_i = 0;
+        for (;;) {
+            while (n_stage < 2) look_ahead();
+            if (n_w >= total) return;
+            Item it;
+            it.h = n_h;
+            it.b = static_cast<int>(n_unit >> 16);
+            it.part = static_cast<int>(n_unit & 0xffffu);
+            it.n = n_len;
+            it.qrow0 = n_row0;
+            it.qlen = n_row1 - n_row0;
+            it.col0 = n_col0;
+            if (lane == 0) n_claim = warps + atomicAdd(p.work_counter, 1);
+            n_stage = 0;
+            // (the plan lists valid sequences only; a column chunk past the
+            // row's last (query, head) pair has nothing to do)
+            const bool ok = it.col0 < it.qlen * G && it.n >= it.qlen && it.n <= p.max_seq_len &&
+                            it.n <= p.max_blocks * 16 && it.qlen >= 1 && it.qlen <= p.max_q && it.qrow0 >= 0 &&
+                            it.qrow0 + it.qlen <= p.num_rows;
+            const int tok0 = it.part * P;
+            it.nblk = ok ? ((min(it.n, tok0 + P) + 15) >> 4) - (tok0 >> 4) : 0;
+            if (it.nblk <= 0) continue;
+            if (lane == 0) queue[q_tail % kQueue] = it;
+            ++q_tail;
+            f_bt = p.block_tables + static_cast<int64_t>(it.b) * p.max_blocks + (tok0 >> 4);
+            f_nblk = it.nblk;
+            f_k = static_cast<const uint8_t*>(p.k_pool) + static_cast<int64_t>(it.h) * kTile + 16 * lane;
+            f_v = static_cast<const uint8_t*>(p.v_pool) + static_cast<int64_t>(it.h) * kTile + 16 * lane;
+            f_t = lane < kTail ? f_k : f_v - 16 * kTail;
+            return;
+        }
+    };
+    // NB bits per pending step (newest lowest): its blocks' ids were inside the pool
+    uint32_t loaded = 0;
+    static_assert(NB * kSlots <= 32 && 32 % NB == 0, "the pending steps' bits, the id window");
+    auto fetch_step = [&](uint32_t slot) {
+        loaded <<= NB;
+        if (f_i < f_nblk) {
+            if ((f_i & 31) == 0) {   // the next 32 blocks' ids, one per lane
+                ids = -1;
+                if (f_i + lane < f_nblk) {
+                    ids = __ldg(f_bt + f_i + lane);
+                    if (ids < 0 || ids >= p.num_blocks) {
+                        record_error(p.err, PA_DEVERR_BLOCK_ID_);   // its tokens contribute nothing
+                        ids = -1;
+                    }
+                }
+            }
+            const uint32_t dst = slot + 16 * lane, dst_t = dst + t_off;
+            static_for<NB>([&](auto j) {
+                constexpr int o = 2 * j * kTile;
+                const int id = __shfl_sync(kAll, ids, (f_i + j) & 31);
+                if (id >= 0) {
+                    const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(id)) * block_bytes;
+                    const uint8_t *k = f_k + off, *v = f_v + off;
+                    static_for<kFull>([&](auto i) {
+                        cp_async16<o + 512 * i, 512 * i>(dst, k);
+                        cp_async16<o + kTile + 512 * i, 512 * i>(dst, v);
+                    });
+                    if (lane < 2 * kTail) cp_async16<o + 512 * kFull, 512 * kFull>(dst_t, f_t + off);
+                    loaded |= 1u << j;
+                }
+            });
+            f_i += NB;
+            if (f_i >= f_nblk) next_item();
+            else if (n_stage < 2) look_ahead();
+        }
+        cp_async_commit();
+    };
+    next_item();
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) fetch_step(ring + i * Shape::kSlot);
+
+    // ---- compute: the fetched items in order --------------------------------
+    uint32_t slot = ring;
+    const uint32_t ring_end = ring + kSlots * Shape::kSlot;
+    const Fp4Lane<D> at(lane);
+    auto run_item = [&](auto nt_tag, const Item& it) {
         constexpr int NT = decltype(nt_tag)::value;
-        const int tok0 = part * P, tok1 = min(n, tok0 + P);
-        const int blk0 = tok0 >> 4, nblk = ((tok1 + 15) >> 4) - blk0;
-        const int lim_min = min(tok1, n - qlen + 1 + col0 / G);
-        const int32_t* bt = p.block_tables + static_cast<int64_t>(b) * p.max_blocks + blk0;
-        const uint8_t* kp = static_cast<const uint8_t*>(p.k_pool) + static_cast<int64_t>(h) * Tile::kBytes;
-        const uint8_t* vp = static_cast<const uint8_t*>(p.v_pool) + static_cast<int64_t>(h) * Tile::kBytes;
-        const int64_t block_bytes = static_cast<int64_t>(H) * Tile::kBytes;
-        // ids of 32 blocks at a time, one per lane
-        int ids = lane < nblk ? __ldg(bt + lane) : 0;
-        auto block_id = [&](int i) {
-            if ((i & 31) == 0 && i > 0) ids = i + lane < nblk ? __ldg(bt + i + lane) : 0;
-            return __shfl_sync(kAll, ids, i & 31);
-        };
-        Fp4Frag<D> cur, nxt;
-        bool cur_ok, nxt_ok = false;
-        auto fetch = [&](Fp4Frag<D>& f, int i) {
-            const int id = block_id(i);
-            const bool ok = id >= 0 && id < p.num_blocks;
-            if (ok) load_frag<D>(f, kp + id * block_bytes, vp + id * block_bytes, lane);
-            else if (lane == 0) record_error(p.err, PA_DEVERR_BLOCK_ID_);
-            return ok;
-        };
-        cur_ok = fetch(cur, 0);
-        Fp4State<D, NT> st;
+        const int tok0 = it.part * P, tok1 = min(it.n, tok0 + P);
+        const int ncols = min(kCols, it.qlen * G - it.col0);
+        // query index of a column (one division, skipped for single queries)
+        auto query_of = [&](int col) { return it.qlen == 1 ? 0 : col / G; };
+        const int lim_min = min(tok1, it.n - it.qlen + 1 + query_of(it.col0));
+        const bool parts = it.n > P;
+        const int64_t prow = parts ? __ldg(p.row_base + it.b) : 0;
+        Fp4State<D, NT, E> st;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             // this lane's quarter of column nt * 8 + g's query
             const int cl = nt * 8 + g;
             const bool ok = cl < ncols;
-            const int col = col0 + (ok ? cl : 0);
-            const int qi = col / G;
-            const uint16_t* qq = static_cast<const uint16_t*>(p.q) +
-                                 ((qrow0 + qi) * p.num_q_heads + h * G + (col - qi * G)) * D + c * (D / 4);
+            const int col = it.col0 + (ok ? cl : 0);
+            const int qi = query_of(col);
+            const uint16_t* qq =
+                static_cast<const uint16_t*>(p.q) +
+                (static_cast<int64_t>(it.qrow0 + qi) * p.num_q_heads + it.h * G + (col - qi * G)) * D + c * (D / 4);
             uint32_t w[D / 8];
 #pragma unroll
             for (int j = 0; j < D / 32; ++j) {
                 const uint4 x = ok ? *reinterpret_cast<const uint4*>(qq + 8 * j) : make_uint4(0, 0, 0, 0);
                 w[4 * j] = x.x; w[4 * j + 1] = x.y; w[4 * j + 2] = x.z; w[4 * j + 3] = x.w;
             }
+            // the score scale's sign goes into the query, so that the column's
+            // multiplier is positive (the largest raw score is the largest)
             float undo = 1.f;
+            const bool neg = p.scale_log2 < 0.f;
             if constexpr (std::is_same<T, __nv_bfloat16>::value) {
                 float mx = 0.f;
 #pragma unroll
@@ -282,13 +508,16 @@ __global__ void __launch_bounds__(kFp4Warps * 32, kMaxNT == 1 ? 4 : 2) decode_fp
                 // 2^(8 - e) for mx in [2^e, 2^(e+1)), the exponent kept in fp32's range
                 const int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
                 const int up = mx > 0.f && mx < INFINITY ? min(8 - e, 120) : 0;
-                const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+                const float f = __uint_as_float((neg ? 0x80000000u : 0u) | static_cast<uint32_t>(127 + up) << 23);
                 undo = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
 #pragma unroll
                 for (int j = 0; j < D / 8; ++j) {
                     const float2 x = Elem<T>::to_float2(w[j]);
                     w[j] = Elem<__half>::pack(x.x * f, x.y * f);
                 }
+            } else if (neg) {
+#pragma unroll
+                for (int j = 0; j < D / 8; ++j) w[j] ^= 0x80008000u;
             }
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
@@ -298,42 +527,61 @@ __global__ void __launch_bounds__(kFp4Warps * 32, kMaxNT == 1 ? 4 : 2) decode_fp
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 // the accumulators' columns: 2c + e
-                st.mul[nt][e] = p.scale_log2 * __shfl_sync(kAll, undo, (2 * c + e) * 4);
+                // (at least fp32's smallest normal, so that a masked -inf stays -inf)
+                st.mul[nt][e] = fmaxf(fabsf(p.scale_log2) * __shfl_sync(kAll, undo, (2 * c + e) * 4), 1.17549435e-38f);
                 st.m[nt][e] = -INFINITY;
                 st.l[nt][e] = 0.f;
                 const int ce = nt * 8 + 2 * c + e;
-                st.lim[nt][e] = ce < ncols ? min(tok1, n - qlen + 1 + (col0 + ce) / G) : 0;
+                st.lim[nt][e] = ce < ncols ? min(tok1, it.n - it.qlen + 1 + query_of(it.col0 + ce)) : 0;
 #pragma unroll
                 for (int mt = 0; mt < D / 16; ++mt) st.o[mt][nt][e] = st.o[mt][nt][2 + e] = 0.f;
             }
         }
-        for (int i = 0; i < nblk; ++i) {
-            if (i + 1 < nblk) nxt_ok = fetch(nxt, i + 1);
-            if (cur_ok) {
-                const int base = tok0 + 16 * i;
-                st.step(cur, base, min(16, tok1 - base), base + 16 > lim_min, lane);
+        int base = tok0;
+        for (int i = 0; i < it.nblk; i += NB, base += 16 * NB) {
+            cp_async_wait<kSlots - 1>();
+            __syncwarp();   // every lane's copies of this step are in place
+            const uint32_t have = loaded >> (NB * (kSlots - 1));   // (older steps' bits lie above)
+            float sc[NB][NT][4];
+            uint32_t pb[NB][NT][2];
+            static_for<NB>([&](auto j) {
+                Fp4K<D> f;
+                at.template load_k<j>(f, slot);
+                st.scores(f, sc[j]);
+            });
+            // every column sees all the step's tokens
+            const bool full = base + 16 * NB <= lim_min && (have & ((1u << NB) - 1u)) == (1u << NB) - 1u;
+            if (!full) {
+#pragma unroll
+                for (int j = 0; j < NB; ++j) st.mask(sc[j], base + 16 * j, (have >> j) & 1u, at.ta);
             }
-            cur = nxt;
-            cur_ok = nxt_ok;
+            st.weights(sc, pb);
+            static_for<NB>([&](auto j) {
+                Fp4V<D> f;
+                at.template load_v<j>(f, slot);
+                st.accumulate(f, pb[j], full, (have >> j) & 1u ? tok1 - base - 16 * j : 0, c, at.flip);
+            });
+            __syncwarp();   // every lane has read the slot: refill it
+            fetch_step(slot);
+            slot = slot + Shape::kSlot == ring_end ? ring : slot + Shape::kSlot;
         }
-        const bool parts = n > P;
-        const int64_t prow = parts ? p.row_base[b] : 0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < E; ++e) {
                 float lh = st.l[nt][e];
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) lh += __shfl_xor_sync(kAll, lh, off);
                 const int ce = nt * 8 + 2 * c + e;
                 if (ce >= ncols) continue;
-                const int qi = (col0 + ce) / G;
-                const int hq = h * G + (col0 + ce - qi * G);
+                const int qi = query_of(it.col0 + ce);
+                const int hq = it.h * G + (it.col0 + ce - qi * G);
                 // this lane holds dims g * D/8 .. of the column, in order
                 if (!parts) {
                     const float inv = lh > 0.f ? p.v_scale / lh : 0.f;
-                    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
-                                                                ((qrow0 + qi) * p.num_q_heads + hq) * D + g * (D / 8));
+                    uint32_t* dst = reinterpret_cast<uint32_t*>(
+                        static_cast<uint16_t*>(p.out) +
+                        (static_cast<int64_t>(it.qrow0 + qi) * p.num_q_heads + hq) * D + g * (D / 8));
 #pragma unroll
                     for (int mt = 0; mt < D / 16; mt += 4)
                         *reinterpret_cast<uint4*>(dst + mt) =
@@ -342,7 +590,7 @@ __global__ void __launch_bounds__(kFp4Warps * 32, kMaxNT == 1 ? 4 : 2) decode_fp
                                        Elem<T>::pack(st.o[mt + 2][nt][e] * inv, st.o[mt + 2][nt][2 + e] * inv),
                                        Elem<T>::pack(st.o[mt + 3][nt][e] * inv, st.o[mt + 3][nt][2 + e] * inv));
                 } else {
-                    const int64_t pi = ((prow + qi) * p.num_q_heads + hq) * p.max_parts + part;
+                    const int64_t pi = ((prow + qi) * p.num_q_heads + hq) * p.max_parts + it.part;
                     if (g == 0) {
                         p.ws_m[pi] = st.m[nt][e];
                         p.ws_l[pi] = lh;
@@ -358,51 +606,37 @@ __global__ void __launch_bounds__(kFp4Warps * 32, kMaxNT == 1 ? 4 : 2) decode_fp
         }
     };
 
-    int w = blockIdx.x * kFp4Warps + (threadIdx.x >> 5);
-    while (w < total) {
-        int claim = 0;
-        if (lane == 0) claim = atomicAdd(p.work_counter, 1);
-        const int ug = w / C;
-        const uint32_t unit = static_cast<uint32_t>(p.units[ug / H]);
-        const int h = ug % H;
-        const int b = static_cast<int>(unit >> 16), part = static_cast<int>(unit & 0xffffu);
-        int qlen = 1;
-        int64_t qrow0 = b;
-        if (p.cu_q_lens) {
-            qrow0 = p.cu_q_lens[b];
-            qlen = p.cu_q_lens[b + 1] - static_cast<int>(qrow0);
-        }
-        const int n = p.seq_lens[b];
-        const int col0 = (w % C) * kCols;
-        const int ncols = min(kCols, qlen * G - col0);
-        // (the plan lists valid sequences only; a column chunk past the row's last pair has nothing to do)
-        if (ncols > 0 && n >= qlen && n <= p.max_seq_len && n <= p.max_blocks * 16 && qlen >= 1 && qlen <= p.max_q &&
-            qrow0 >= 0 && qrow0 + qlen <= p.num_rows) {
-            if (kMaxNT == 1 || ncols <= 8)
-                run_item(std::integral_constant<int, 1>{}, b, h, part, n, qlen, qrow0, col0, ncols);
-            else
-                run_item(std::integral_constant<int, kMaxNT>{}, b, h, part, n, qlen, qrow0, col0, ncols);
-        }
-        w = warps + __shfl_sync(kAll, claim, 0);
+    while (q_head != q_tail) {
+        __syncwarp();
+        const Item it = queue[q_head % kQueue];
+        ++q_head;
+        if (kCols <= 8 || it.qlen * G - it.col0 <= 8)
+            run_item(std::integral_constant<int, 1>{}, it);
+        else
+            run_item(std::integral_constant<int, (kCols + 7) / 8>{}, it);
     }
+    cp_async_wait<0>();
     // beside a prefill kernel this grid completes only after it (what the
     // stream runs next is ordered after this grid alone)
     if (p.overlap) pdl_wait();
 }
 
-template <typename T, int D, int kMaxNT>
+template <typename T, int D, int kCols>
 cudaError_t launch_kernel(const DecodeParams& p, cudaStream_t s) {
-    auto kern = decode_fp4_kernel<T, D, kMaxNT>;
+    constexpr int smem = Fp4Shape<D, kCols>::kSmem;
+    auto kern = decode_fp4_kernel<T, D, kCols>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
     static const int ctas_per_sm = [&] {   // once per kernel variant (thread-safe)
         int n = 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kFp4Warps * 32, 0) != cudaSuccess || n < 1) n = 1;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kFp4Warps * 32, smem) != cudaSuccess || n < 1) n = 1;
         return n;
     }();
     const long long items = static_cast<long long>(p.num_seqs) * p.max_parts * p.num_kv_heads * p.col_chunks;
     const long long want = (items + kFp4Warps - 1) / kFp4Warps;
     const int grid = static_cast<int>(
         std::max<long long>(1, std::min<long long>(want, static_cast<long long>(ctas_per_sm) * sm_count())));
-    return launch_pdl(kern, dim3(grid), dim3(kFp4Warps * 32), 0, s, p);
+    return launch_pdl(kern, dim3(grid), dim3(kFp4Warps * 32), smem, s, p);
 }
 
 // Chunks' blocks of a 4-bit cache widened into the 16-bit copy that the
@@ -463,7 +697,9 @@ __global__ void __launch_bounds__(kWidenFp4Threads) widen_chunk_blocks_fp4_kerne
 
 template <typename T, int D>
 cudaError_t launch_d(const DecodeParams& p, cudaStream_t s) {
-    return p.max_q * p.group > 8 ? launch_kernel<T, D, 2>(p, s) : launch_kernel<T, D, 1>(p, s);
+    // columns per item: the row's, at most 16 (p.col_chunks counts chunks of 8, or of 16 past 8)
+    const int cols = p.max_q * p.group;
+    return cols > 8 ? launch_kernel<T, D, 16>(p, s) : cols > 1 ? launch_kernel<T, D, 8>(p, s) : launch_kernel<T, D, 1>(p, s);
 }
 
 }  // namespace
