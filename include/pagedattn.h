@@ -140,6 +140,23 @@ int pa_paged_kv_write(const void* key, const void* value, void* k_cache, void* v
 int pa_decode_partition(int max_seq_len, int partition_size);
 
 /*
+ * A partition length for a decode call of these sizes that also looks at the
+ * number of work items (partitions x kv heads x chunks of 16 (query, head)
+ * pairs): pa_decode_partition(max_seq_len, 0), halved down to PA_MIN_PARTITION
+ * tokens while sequences of max_seq_len tokens would give fewer than
+ * PA_PARTITION_ITEMS items, so that few or few-headed sequences still spread
+ * over the GPU; at most PA_MAX_PARTITIONS_FOR partitions a sequence (the merge
+ * of more takes longer than it saves).  Lengths of at most 2 *
+ * PA_MIN_PARTITION tokens stay in one partition.  Pass the value as partition_size, to the workspace function too
+ * (with a window, max_seq_len of the call is right here as well).  Returns -1
+ * for a negative size, no heads, or num_q_heads not a multiple of num_kv_heads.
+ */
+#define PA_MIN_PARTITION 64
+#define PA_PARTITION_ITEMS 8192
+#define PA_MAX_PARTITIONS_FOR 256
+int pa_decode_partition_for(int num_seqs, int num_q_heads, int num_kv_heads, int max_seq_len);
+
+/*
  * Workspace for pa_paged_attention_decode: the kernel's work list (one entry
  * per sequence partition) and the split-context partials of num_seqs
  * sequences no longer than max_seq_len, cut into partitions of

@@ -10,6 +10,7 @@ from ._binding import (  # noqa: F401
     copy_blocks,
     count_chunk_kv_tokens,
     decode_partition,
+    decode_partition_for,
     decode_workspace_bytes,
     fp4_tile_bytes,
     library_path,

@@ -68,6 +68,7 @@ _SIGNATURES = {
                                               _f32, _f32, _i32, _p, _i32, _i32, _i32, _i32, _p, _sz, _i32, _p]),
     "pa_copy_blocks": (_i32, [_p, _p, _p, _i32, _i32, _i32, _i32, _i32, _p]),
     "pa_decode_partition": (_i32, [_i32, _i32]),
+    "pa_decode_partition_for": (_i32, [_i32, _i32, _i32, _i32]),
     "pa_selftest_wait_timeout": (_i32, [_p]),
     "pa_paged_kv_gather": (_i32, [_p, _p, _p, _p, _p, _i32, _p, _p, _i32, _i32, _i32, _i32, _i32, _i32, _p]),
 }
@@ -108,8 +109,8 @@ def _check(rc: int, what: str) -> None:
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:   # the current stream's handle, without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -179,6 +180,14 @@ def decode_partition(max_seq_len: int, partition_size: int = 0) -> int:
     """Partition length (tokens) a decode call uses; 0 selects the automatic one."""
     n = int(load_library().pa_decode_partition(max_seq_len, partition_size))
     _need(n > 0, "invalid max_seq_len or partition_size")
+    return n
+
+
+def decode_partition_for(num_seqs: int, num_q_heads: int, num_kv_heads: int, max_seq_len: int) -> int:
+    """Partition length that gives a decode call of these sizes enough work
+    items for the GPU (at most that of `decode_partition(max_seq_len)`)."""
+    n = int(load_library().pa_decode_partition_for(num_seqs, num_q_heads, num_kv_heads, max_seq_len))
+    _need(n > 0, "invalid sizes")
     return n
 
 
@@ -419,46 +428,66 @@ def paged_attention_prefill_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
 # Rotation and append; 4-bit (E2M1) cache
 # --------------------------------------------------------------------------
 
-def _on_current(*ts) -> None:
+# These calls check their arguments with one condition on the way (a serving
+# step makes thousands of them) and find out what was wrong only when it fails.
+
+def _on_current(*ts) -> bool:
     """Every tensor on the current device (the library enqueues on its stream)."""
     dev = torch.cuda.current_device()
     for t in ts:
-        if t is not None:
-            _need(t.is_cuda and t.device.index == dev, "tensors must be on the current CUDA device")
+        if t.get_device() != dev:
+            return False
+    return True
 
 
-def _rows(t: torch.Tensor, what: str) -> int:
-    """Token stride (elements) of [T, H, D] rows whose heads are dense within a token."""
+def _rows(t: torch.Tensor) -> int:
+    """Token stride (elements) of [T, H, D] rows whose heads are dense within a
+    token; -1 if they are not."""
     T, H, D = t.shape
-    _need(t.stride(2) == 1 and (H <= 1 or t.stride(1) == D), f"{what}: head rows must be dense within a token")
-    return t.stride(0) if T > 1 else H * D
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != D and H > 1):
+        return -1
+    return s0 if T > 1 else H * D
 
 
 def _rope(name, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin, interleaved, q_out, stream,
           pool, scales):
     """The three rotate-and-append calls; `pool` is (num_blocks, num_kv_heads, head_dim, block_size)."""
-    _on_current(q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin, q_out)
     NB, H, D, bs = pool
-    T, Hq = key.shape[0], q.shape[1]
-    _need(k_cache.is_contiguous() and v_cache.is_contiguous() and v_cache.shape == k_cache.shape, "cache shape")
-    _need(tuple(key.shape) == (T, H, D) and value.shape == key.shape and tuple(q.shape) == (T, Hq, D),
-          "q/key/value shape")
-    _need(q.dtype == key.dtype == value.dtype, "q/key/value dtype")
-    _need(slot_mapping.dtype == torch.int64 and slot_mapping.is_contiguous() and slot_mapping.numel() >= T,
-          "slot_mapping: int64 [num_tokens]")
-    _need(positions.dtype == torch.int64 and positions.is_contiguous() and positions.numel() >= T,
-          "positions: int64 [num_tokens]")
-    _need(cos_sin.dtype == torch.float32 and cos_sin.is_contiguous() and cos_sin.dim() == 2,
-          "cos_sin: float32 [max_positions, rot_dim]")
+    T, H2, D2 = key.shape
+    dtype = q.dtype
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-    _need(q_out.shape == q.shape and q_out.dtype == q.dtype, "q_out shape/dtype")
-    rc = getattr(load_library(), name)(
-        q_out.data_ptr(), _rows(q_out, "q_out"), q.data_ptr(), _rows(q, "q"), key.data_ptr(), _rows(key, "key"),
-        value.data_ptr(), _rows(value, "value"), k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(),
-        positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0], T, NB, Hq, H, D, cos_sin.shape[1],
-        int(bool(interleaved)), bs, _dt(q), *scales, _stream(stream))
-    _check(rc, name)
+        q_out = torch.empty_like(q)
+    qs, ks, vs, os = _rows(q), _rows(key), _rows(value), _rows(q_out)
+    if not (_on_current(q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin, q_out)
+            and H2 == H and D2 == D and value.shape == key.shape and q.shape[0] == T and q.shape[2] == D
+            and q_out.shape == q.shape and key.dtype == dtype and value.dtype == dtype and q_out.dtype == dtype
+            and v_cache.shape == k_cache.shape and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and slot_mapping.dtype == torch.int64 and slot_mapping.is_contiguous() and slot_mapping.numel() >= T
+            and positions.dtype == torch.int64 and positions.is_contiguous() and positions.numel() >= T
+            and cos_sin.dtype == torch.float32 and cos_sin.dim() == 2 and cos_sin.is_contiguous()
+            and qs >= 0 and ks >= 0 and vs >= 0 and os >= 0):
+        _need(_on_current(q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin, q_out),
+              "tensors must be on the current CUDA device")
+        _need(k_cache.is_contiguous() and v_cache.is_contiguous() and v_cache.shape == k_cache.shape, "cache shape")
+        _need(H2 == H and D2 == D and value.shape == key.shape and q.shape[0] == T and q.shape[2] == D,
+              "q/key/value shape")
+        _need(key.dtype == dtype and value.dtype == dtype, "q/key/value dtype")
+        _need(q_out.shape == q.shape and q_out.dtype == dtype, "q_out shape/dtype")
+        _need(slot_mapping.dtype == torch.int64 and slot_mapping.is_contiguous() and slot_mapping.numel() >= T,
+              "slot_mapping: int64 [num_tokens]")
+        _need(positions.dtype == torch.int64 and positions.is_contiguous() and positions.numel() >= T,
+              "positions: int64 [num_tokens]")
+        _need(cos_sin.dtype == torch.float32 and cos_sin.is_contiguous() and cos_sin.dim() == 2,
+              "cos_sin: float32 [max_positions, rot_dim]")
+        _need(False, "q, key, value and q_out: head rows must be dense within a token")
+    maxp, rot = cos_sin.shape
+    rc = getattr(_lib or load_library(), name)(
+        q_out.data_ptr(), os, q.data_ptr(), qs, key.data_ptr(), ks, value.data_ptr(), vs, k_cache.data_ptr(),
+        v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), cos_sin.data_ptr(), maxp, T, NB,
+        q.shape[1], H, D, rot, 1 if interleaved else 0, bs, _dt(q), *scales, _stream(stream))
+    if rc:
+        _check(rc, name)
     return q_out
 
 
@@ -475,7 +504,9 @@ def paged_rope_kv_write(q: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
     [max_positions, rot_dim], cosines then sines; pairs are (i, i + rot_dim/2),
     or (2i, 2i + 1) when interleaved."""
     NB, bs, H, D = k_cache.shape
-    _need(k_cache.dtype == v_cache.dtype == key.dtype, "cache dtype")
+    dtype = key.dtype
+    if k_cache.dtype != dtype or v_cache.dtype != dtype:
+        _need(False, "cache dtype")
     return _rope("pa_paged_rope_kv_write", q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
                  interleaved, q_out, stream, (NB, H, D, bs), ())
 
@@ -500,10 +531,13 @@ def fp4_tile_bytes(head_dim: int) -> int:
 
 
 def _fp4_pool(k_cache: torch.Tensor, v_cache: torch.Tensor, D: int):
-    _need(k_cache.dim() == 3 and k_cache.element_size() == 1 and v_cache.element_size() == 1 and
-          k_cache.shape == v_cache.shape and k_cache.shape[2] == fp4_tile_bytes(D),
-          "4-bit pools: bytes [NB, Hkv, fp4_tile_bytes(head_dim)]")
-    return k_cache.shape[0], k_cache.shape[1]
+    """(num_blocks, num_kv_heads) of a pair of 4-bit pools of head_dim D."""
+    shape = k_cache.shape
+    if not (len(shape) == 3 and shape[2] == 9 * D and (D == 128 or D == 64) and v_cache.shape == shape
+            and k_cache.element_size() == 1 and v_cache.element_size() == 1):
+        _need(D == 128 or D == 64, "4-bit caches hold head_dim 64 or 128")
+        _need(False, "4-bit pools: bytes [NB, Hkv, fp4_tile_bytes(head_dim)]")
+    return shape[0], shape[1]
 
 
 def paged_rope_kv_write_fp4(q: torch.Tensor, key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor,
@@ -521,47 +555,80 @@ def paged_kv_write_fp4(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Te
                        slot_mapping: torch.Tensor, k_scale: float, v_scale: float, stream=None) -> None:
     """In place: E2M1 codes and E4M3 group scales of key/value into the 4-bit
     pools [NB, Hkv, fp4_tile_bytes(D)] (slot < 0: skipped)."""
-    _cuda(key, value, k_cache, v_cache, slot_mapping)
-    _on_current(key, value, k_cache, v_cache, slot_mapping)
     T, H, D = key.shape
     NB, H2 = _fp4_pool(k_cache, v_cache, D)
-    _need(H == H2 and value.shape == key.shape and value.dtype == key.dtype, "key/value/cache shapes")
-    _need(slot_mapping.dtype == torch.int64 and slot_mapping.numel() >= T, "slot_mapping: int64 [num_tokens]")
-    rc = load_library().pa_paged_kv_write_fp4(key.data_ptr(), value.data_ptr(), k_cache.data_ptr(),
-                                              v_cache.data_ptr(), slot_mapping.data_ptr(), T, NB, H, D,
-                                              PA_BLOCK_SIZE, _dt(key), float(k_scale), float(v_scale),
-                                              _stream(stream))
-    _check(rc, "pa_paged_kv_write_fp4")
+    if not (_on_current(key, value, k_cache, v_cache, slot_mapping) and H == H2 and value.shape == key.shape
+            and value.dtype == key.dtype and slot_mapping.dtype == torch.int64 and slot_mapping.numel() >= T
+            and key.is_contiguous() and value.is_contiguous() and k_cache.is_contiguous()
+            and v_cache.is_contiguous() and slot_mapping.is_contiguous()):
+        _cuda(key, value, k_cache, v_cache, slot_mapping)
+        _need(_on_current(key, value, k_cache, v_cache, slot_mapping), "tensors must be on the current CUDA device")
+        _need(H == H2 and value.shape == key.shape and value.dtype == key.dtype, "key/value/cache shapes")
+        _need(False, "slot_mapping: int64 [num_tokens]")
+    rc = (_lib or load_library()).pa_paged_kv_write_fp4(
+        key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), T, NB, H,
+        D, PA_BLOCK_SIZE, _dt(key), k_scale, v_scale, _stream(stream))
+    if rc:
+        _check(rc, "pa_paged_kv_write_fp4")
 
 
 def paged_kv_unpack_fp4(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: float, v_scale: float,
                         dtype: torch.dtype, stream=None):
     """Both 4-bit pools as 16-bit pools [NB, 16, Hkv, D] of `dtype`."""
-    _cuda(k_cache, v_cache)
-    _on_current(k_cache, v_cache)
-    _need(k_cache.dim() == 3 and k_cache.shape[2] % 9 == 0, "4-bit pools: bytes [NB, Hkv, fp4_tile_bytes(head_dim)]")
-    D = k_cache.shape[2] // 9
-    NB, H = _fp4_pool(k_cache, v_cache, D)
-    k_out = torch.empty(NB, PA_BLOCK_SIZE, H, D, dtype=dtype, device=k_cache.device)
+    NB, H, tile = k_cache.shape
+    D = tile // 9
+    _fp4_pool(k_cache, v_cache, D)
+    if not (_on_current(k_cache, v_cache) and k_cache.is_contiguous() and v_cache.is_contiguous()):
+        _cuda(k_cache, v_cache)
+        _need(False, "tensors must be on the current CUDA device")
+    k_out = torch.empty((NB, PA_BLOCK_SIZE, H, D), dtype=dtype, device=k_cache.device)
     v_out = torch.empty_like(k_out)
-    rc = load_library().pa_paged_kv_unpack_fp4(k_out.data_ptr(), v_out.data_ptr(), k_cache.data_ptr(),
-                                               v_cache.data_ptr(), NB, H, D, PA_BLOCK_SIZE, float(k_scale),
-                                               float(v_scale), _dt(k_out), _stream(stream))
-    _check(rc, "pa_paged_kv_unpack_fp4")
+    rc = (_lib or load_library()).pa_paged_kv_unpack_fp4(
+        k_out.data_ptr(), v_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), NB, H, D, PA_BLOCK_SIZE, k_scale,
+        v_scale, _dt(k_out), _stream(stream))
+    if rc:
+        _check(rc, "pa_paged_kv_unpack_fp4")
     return k_out, v_out
 
 
-def _tables(block_tables: torch.Tensor, seq_lens: torch.Tensor, B: int) -> None:
+def _attn_args(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, alibi_slopes, out, workspace) -> None:
+    """What the attention calls below ask of their tensors besides the pools' shape."""
+    ts = [t for t in (q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, alibi_slopes, out, workspace)
+          if t is not None]
+    B = q.shape[0] if cu_q_lens is None else seq_lens.shape[0]
+    ok = (block_tables.dtype == torch.int32 and seq_lens.dtype == torch.int32 and seq_lens.numel() == B
+          and block_tables.dim() == 2 and block_tables.shape[0] >= B)
+    for t in ts:
+        ok = ok and t.is_contiguous()
+    if out is not None:
+        ok = ok and out.shape == q.shape and out.dtype == q.dtype
+    if cu_q_lens is not None:
+        ok = ok and cu_q_lens.dtype == torch.int32 and cu_q_lens.shape[0] == B + 1
+    if alibi_slopes is not None:
+        ok = ok and alibi_slopes.dtype == torch.float32 and alibi_slopes.numel() == q.shape[1]
+    if ok and _on_current(*ts):
+        return
+    _cuda(*ts)
+    _need(_on_current(*ts), "tensors must be on the current CUDA device")
     _need(block_tables.dtype == torch.int32 and seq_lens.dtype == torch.int32, "int32 tables")
     _need(seq_lens.numel() == B and block_tables.dim() == 2 and block_tables.shape[0] >= B, "table shapes")
+    _need(cu_q_lens is None or (cu_q_lens.dtype == torch.int32 and cu_q_lens.shape[0] == B + 1), "cu_q_lens")
+    _need(out is None or (out.shape == q.shape and out.dtype == q.dtype), "out shape/dtype")
+    _need(False, "alibi_slopes: float32 [num_q_heads]")
 
 
-def _out_ws(q, out, nbytes, workspace):
-    if out is None:
-        out = torch.empty_like(q)
-    _need(out.shape == q.shape and out.dtype == q.dtype, "out shape/dtype")
-    workspace = _workspace(nbytes, q.device, workspace)
-    return out, workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+def _pool16(q, k_cache, v_cache):
+    NB, bs, Hkv, D = k_cache.shape
+    if q.shape[2] != D or v_cache.shape != k_cache.shape or k_cache.dtype != q.dtype or v_cache.dtype != q.dtype:
+        _need(False, "cache shape/dtype")
+    return NB, bs, Hkv
+
+
+def _ws(nbytes, q, workspace):
+    """(address, bytes) of the caller's workspace, or of a new one."""
+    if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def paged_attention_decode_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -570,22 +637,25 @@ def paged_attention_decode_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
                                partition_size: int = 0, workspace: torch.Tensor | None = None,
                                stream=None) -> torch.Tensor:
     """Decode attention over 4-bit pools [NB, Hkv, fp4_tile_bytes(D)]:
-    q [B, Hq, D] -> out [B, Hq, D]."""
-    _cuda(q, k_cache, v_cache, block_tables, seq_lens, out, workspace)
-    _on_current(q, k_cache, v_cache, block_tables, seq_lens, out, workspace)
+    q [B, Hq, D] -> out [B, Hq, D].  partition_size 0 takes the length of
+    `decode_partition_for`."""
     B, Hq, D = q.shape
     NB, Hkv = _fp4_pool(k_cache, v_cache, D)
-    _tables(block_tables, seq_lens, B)
+    _attn_args(q, k_cache, v_cache, block_tables, seq_lens, None, None, out, workspace)
     if max_seq_len is None:
         max_seq_len = int(seq_lens.max().item()) if B else 0
-    out, workspace, ws_bytes = _out_ws(q, out, decode_workspace_bytes(B, Hq, D, max_seq_len, partition_size),
-                                       workspace)
-    rc = load_library().pa_paged_attention_decode_fp4(
+    if out is None:
+        out = torch.empty_like(q)
+    lib = _lib or load_library()
+    if partition_size == 0:
+        partition_size = lib.pa_decode_partition_for(B, Hq, Hkv, max_seq_len)
+    workspace, ws_bytes = _ws(lib.pa_decode_workspace_bytes(B, Hq, D, max_seq_len, partition_size), q, workspace)
+    rc = lib.pa_paged_attention_decode_fp4(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-        block_tables.shape[1], seq_lens.data_ptr(), B, max_seq_len, NB, float(scale), float(k_scale),
-        float(v_scale), Hq, Hkv, D, PA_BLOCK_SIZE, partition_size, _ptr(workspace), ws_bytes, _dt(q),
-        _stream(stream))
-    _check(rc, "pa_paged_attention_decode_fp4")
+        block_tables.shape[1], seq_lens.data_ptr(), B, max_seq_len, NB, scale, k_scale, v_scale, Hq, Hkv, D,
+        PA_BLOCK_SIZE, partition_size, workspace.data_ptr(), ws_bytes, _dt(q), _stream(stream))
+    if rc:
+        _check(rc, "pa_paged_attention_decode_fp4")
     return out
 
 
@@ -597,39 +667,33 @@ def paged_attention_prefill_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
     """Causal varlen attention of new query rows over 4-bit pools (decodes,
     speculative-verify rows and prefill chunks in one call).  `chunk_kv_tokens`
     as in `paged_attention_prefill_fp8`."""
-    _cuda(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, out, workspace)
-    _on_current(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, out, workspace)
     T, Hq, D = q.shape
     NB, Hkv = _fp4_pool(k_cache, v_cache, D)
+    _attn_args(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, None, out, workspace)
     B = seq_lens.shape[0]
-    _tables(block_tables, seq_lens, B)
-    _need(cu_q_lens.shape[0] == B + 1 and cu_q_lens.dtype == torch.int32, "cu_q_lens")
+    if out is None:
+        out = torch.empty_like(q)
+    lib = _lib or load_library()
+    max_blocks = block_tables.shape[1]
     if max_q_len > 8 and B > 0 and T > 0:
         if chunk_kv_tokens is None:
             chunk_kv_tokens = count_chunk_kv_tokens(seq_lens, cu_q_lens)
-        nbytes = prefill_fp8_workspace_bytes(B, T, Hq, Hkv, D, max_seq_len, block_tables.shape[1],
-                                             chunk_kv_tokens)
+        nbytes = lib.pa_prefill_fp8_workspace_bytes(B, T, Hq, Hkv, D, max_seq_len, max_blocks, chunk_kv_tokens)
     else:
-        nbytes = prefill_workspace_bytes(B, T, Hq, D, max_seq_len)
-    out, workspace, ws_bytes = _out_ws(q, out, nbytes, workspace)
-    rc = load_library().pa_paged_attention_prefill_fp4(
-        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-        block_tables.shape[1], seq_lens.data_ptr(), cu_q_lens.data_ptr(), B, T, max_q_len, max_seq_len, NB,
-        float(scale), float(k_scale), float(v_scale), Hq, Hkv, D, PA_BLOCK_SIZE, _ptr(workspace), ws_bytes, _dt(q),
-        _stream(stream))
-    _check(rc, "pa_paged_attention_prefill_fp4")
+        nbytes = lib.pa_prefill_workspace_bytes(B, T, Hq, D, max_seq_len)
+    workspace, ws_bytes = _ws(nbytes, q, workspace)
+    rc = lib.pa_paged_attention_prefill_fp4(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), max_blocks,
+        seq_lens.data_ptr(), cu_q_lens.data_ptr(), B, T, max_q_len, max_seq_len, NB, scale, k_scale, v_scale, Hq, Hkv,
+        D, PA_BLOCK_SIZE, workspace.data_ptr(), ws_bytes, _dt(q), _stream(stream))
+    if rc:
+        _check(rc, "pa_paged_attention_prefill_fp4")
     return out
 
 
 # --------------------------------------------------------------------------
 # Modified scores (16-bit cache)
 # --------------------------------------------------------------------------
-
-def _slopes(alibi_slopes, Hq: int) -> None:
-    if alibi_slopes is not None:
-        _need(alibi_slopes.dtype == torch.float32 and alibi_slopes.is_contiguous() and alibi_slopes.numel() == Hq,
-              "alibi_slopes: float32 [num_q_heads]")
-
 
 def paged_attention_decode_mod(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                                block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float,
@@ -639,24 +703,25 @@ def paged_attention_decode_mod(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
                                stream=None) -> torch.Tensor:
     """`paged_attention_decode` with modified scores: softcap * tanh(s / softcap)
     when softcap > 0, plus alibi_slopes[h] * (key - query position), over the
-    last `window` positions when window > 0."""
-    _cuda(q, k_cache, v_cache, block_tables, seq_lens, out, workspace)
-    _on_current(q, k_cache, v_cache, block_tables, seq_lens, out, workspace, alibi_slopes)
+    last `window` positions when window > 0.  partition_size 0 takes the length
+    of `decode_partition_for`."""
     B, Hq, D = q.shape
-    NB, bs, Hkv, D2 = k_cache.shape
-    _need(D2 == D and v_cache.shape == k_cache.shape and k_cache.dtype == v_cache.dtype == q.dtype,
-          "cache shape/dtype")
-    _tables(block_tables, seq_lens, B)
-    _slopes(alibi_slopes, Hq)
+    NB, bs, Hkv = _pool16(q, k_cache, v_cache)
+    _attn_args(q, k_cache, v_cache, block_tables, seq_lens, None, alibi_slopes, out, workspace)
     if max_seq_len is None:
         max_seq_len = int(seq_lens.max().item()) if B else 0
-    out, workspace, ws_bytes = _out_ws(q, out, decode_workspace_bytes(B, Hq, D, max_seq_len, partition_size),
-                                       workspace)
-    rc = load_library().pa_paged_attention_decode_mod(
+    if out is None:
+        out = torch.empty_like(q)
+    lib = _lib or load_library()
+    if partition_size == 0:
+        partition_size = lib.pa_decode_partition_for(B, Hq, Hkv, max_seq_len)
+    workspace, ws_bytes = _ws(lib.pa_decode_workspace_bytes(B, Hq, D, max_seq_len, partition_size), q, workspace)
+    rc = lib.pa_paged_attention_decode_mod(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-        block_tables.shape[1], seq_lens.data_ptr(), B, max_seq_len, NB, float(scale), float(softcap), int(window),
-        _ptr(alibi_slopes), Hq, Hkv, D, bs, partition_size, _ptr(workspace), ws_bytes, _dt(q), _stream(stream))
-    _check(rc, "pa_paged_attention_decode_mod")
+        block_tables.shape[1], seq_lens.data_ptr(), B, max_seq_len, NB, scale, softcap, window, _ptr(alibi_slopes),
+        Hq, Hkv, D, bs, partition_size, workspace.data_ptr(), ws_bytes, _dt(q), _stream(stream))
+    if rc:
+        _check(rc, "pa_paged_attention_decode_mod")
     return out
 
 
@@ -668,21 +733,18 @@ def paged_attention_prefill_mod(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
                                 stream=None) -> torch.Tensor:
     """`paged_attention_prefill` (decode, verify and chunk rows in one call) with
     modified scores, as `paged_attention_decode_mod`."""
-    _cuda(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, out, workspace)
-    _on_current(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, out, workspace, alibi_slopes)
     T, Hq, D = q.shape
-    NB, bs, Hkv, D2 = k_cache.shape
-    _need(D2 == D and v_cache.shape == k_cache.shape and k_cache.dtype == v_cache.dtype == q.dtype,
-          "cache shape/dtype")
+    NB, bs, Hkv = _pool16(q, k_cache, v_cache)
+    _attn_args(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, alibi_slopes, out, workspace)
     B = seq_lens.shape[0]
-    _tables(block_tables, seq_lens, B)
-    _need(cu_q_lens.shape[0] == B + 1 and cu_q_lens.dtype == torch.int32, "cu_q_lens")
-    _slopes(alibi_slopes, Hq)
-    out, workspace, ws_bytes = _out_ws(q, out, prefill_workspace_bytes(B, T, Hq, D, max_seq_len), workspace)
-    rc = load_library().pa_paged_attention_prefill_mod(
+    if out is None:
+        out = torch.empty_like(q)
+    lib = _lib or load_library()
+    workspace, ws_bytes = _ws(lib.pa_prefill_workspace_bytes(B, T, Hq, D, max_seq_len), q, workspace)
+    rc = lib.pa_paged_attention_prefill_mod(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-        block_tables.shape[1], seq_lens.data_ptr(), cu_q_lens.data_ptr(), B, T, max_q_len, max_seq_len, NB,
-        float(scale), float(softcap), int(window), _ptr(alibi_slopes), Hq, Hkv, D, bs, _ptr(workspace), ws_bytes,
-        _dt(q), _stream(stream))
-    _check(rc, "pa_paged_attention_prefill_mod")
+        block_tables.shape[1], seq_lens.data_ptr(), cu_q_lens.data_ptr(), B, T, max_q_len, max_seq_len, NB, scale,
+        softcap, window, _ptr(alibi_slopes), Hq, Hkv, D, bs, workspace.data_ptr(), ws_bytes, _dt(q), _stream(stream))
+    if rc:
+        _check(rc, "pa_paged_attention_prefill_mod")
     return out

@@ -299,6 +299,19 @@ int pa_decode_partition(int max_seq_len, int partition_size) {
     return effective_partition(max_seq_len, partition_size);
 }
 
+int pa_decode_partition_for(int num_seqs, int num_q_heads, int num_kv_heads, int max_seq_len) {
+    if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_seq_len < 0 || num_q_heads % num_kv_heads)
+        return -1;
+    int part = effective_partition(max_seq_len, 0);
+    if (max_seq_len <= 2 * PA_MIN_PARTITION) return part;   // one partition: no merge
+    const int group = num_q_heads / num_kv_heads;
+    const long long per_part = static_cast<long long>(num_seqs) * num_kv_heads * ((group + 15) / 16);
+    while (part > PA_MIN_PARTITION && per_part * parts_for(max_seq_len, part) < PA_PARTITION_ITEMS &&
+           parts_for(max_seq_len, part / 2) <= PA_MAX_PARTITIONS_FOR)
+        part /= 2;
+    return part;
+}
+
 size_t pa_decode_workspace_bytes(int num_seqs, int num_q_heads, int head_dim, int max_seq_len,
                                  int partition_size) {
     if (num_seqs <= 0 || num_q_heads <= 0 || head_dim <= 0 || max_seq_len < 0 || partition_size < 0) return 0;
