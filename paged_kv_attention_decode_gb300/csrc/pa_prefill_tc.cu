@@ -71,6 +71,8 @@ constexpr float kRescaleLog2 = 8.f;
 constexpr float kPLazyMax = 256.f;   // 2^kRescaleLog2: a tile's sum of P below it needs no row maximum
 constexpr unsigned kFullMask = 0xffffffffu;
 
+enum { kPlain = 0, kWindow = 1, kCapped = 2, kBiased = 3 };   // kinds of scores
+
 template <int D>
 struct TcShape {
     static constexpr int kKeyHalf = kTcKeys * 128;          // 128 keys x one 64-dim half
@@ -219,21 +221,64 @@ __device__ __forceinline__ void widen16(const uint4& in, uint4& lo, uint4& hi) {
     hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-// A row's 128 raw scores of one key tile -> modified scores in log2 units
-// (ScoreMod; `dist` = the tile's first key position less the row's).
-__device__ __forceinline__ void modify_scores(float (&sv)[kTcKeys], const ScoreMod& mod, float scale_log2,
-                                              float slope, int dist) {
-    if (mod.cap_log2 > 0.f) {
+// (x, y) <- (x * u, y * v)
+__device__ __forceinline__ void mulp(float& x, float& y, float u, float v) {
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(u), "f"(v));
+}
+
+// The smallest of a row's 128 values: four chains of three-input minima.
+__device__ __forceinline__ float row_min(const float (&sv)[kTcKeys]) {
+    float mq[4] = {INFINITY, INFINITY, INFINITY, INFINITY};
 #pragma unroll
-        for (int c = 0; c < kTcKeys; ++c)
-            sv[c] = fmaf(-2.f * mod.cap_log2, fast_rcp(1.f + fast_exp2(sv[c] * mod.cap_in)), mod.cap_log2);
-    } else {
+    for (int c = 0; c < kTcKeys; c += 8) {
 #pragma unroll
-        for (int c = 0; c < kTcKeys; c += 2) mul2(sv[c], sv[c + 1], scale_log2);
+        for (int u = 0; u < 4; ++u)
+            asm("min.f32 %0, %0, %1, %2;" : "+f"(mq[u]) : "f"(sv[c + 2 * u]), "f"(sv[c + 2 * u + 1]));
     }
-    if (mod.slopes) {
+    return fminf(fminf(mq[0], mq[1]), fminf(mq[2], mq[3]));
+}
+// The smaller of two values; a NaN stays.
+__device__ __forceinline__ float fmin_nan(float a, float b) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// Raw scores -> r = 1 / (1 + 2^(raw * cap_in)), of which the capped score is
+// cap - 2 cap r (ScoreMod).  The special-function unit sets the pace of capped
+// rows (2^x at 32 a clock per SM, reciprocals at 16, and P's own 2^x), so four
+// scores share one reciprocal: with a .. d the four sums, 1 / (ac) = bd / (ac
+// bd) and 1 / a = c / (ac).  The exponent is held at 30 (r = 2^-30, a capped
+// score within 2^-29 of the cap), so that the product of four sums stays below
+// 2^121.  A NaN reaches its group: scores of hidden keys, which may be
+// anything, are cleared before.
+__device__ __forceinline__ void cap_reciprocals(float (&sv)[kTcKeys], float cap_in) {
 #pragma unroll
-        for (int c = 0; c < kTcKeys; ++c) sv[c] = fmaf(slope, static_cast<float>(dist + c), sv[c]);
+    for (int i = 0; i < kTcKeys; i += 4) {
+        float &a = sv[i], &b = sv[i + 1], &c = sv[i + 2], &d = sv[i + 3];
+        mul2(a, b, cap_in);
+        mul2(c, d, cap_in);
+        a = fast_exp2(fmin_nan(a, 30.f));
+        b = fast_exp2(fmin_nan(b, 30.f));
+        c = fast_exp2(fmin_nan(c, 30.f));
+        d = fast_exp2(fmin_nan(d, 30.f));
+        add2(a, b, 1.f, 1.f);
+        add2(c, d, 1.f, 1.f);
+        float ac = a, bd = b;
+        mulp(ac, bd, c, d);
+        const float r = fast_rcp(ac * bd);
+        float iac = bd, ibd = ac;
+        mul2(iac, ibd, r);
+        const float a0 = a, b0 = b;
+        a = c;
+        b = d;
+        mulp(a, b, iac, ibd);
+        c = a0;
+        d = b0;
+        mulp(c, d, iac, ibd);
     }
 }
 
@@ -463,16 +508,22 @@ __global__ void __launch_bounds__(kWidenThreads) widen_chunk_blocks_kernel(const
 // k * C + i for even k and k * C + C - 1 - i for odd k, so the CTAs' total
 // costs stay even.  (Beside decode rows: pair w / num_kv_heads of the plan's
 // own order, round-robin.)
-// kMod: the scores are modified (ScoreMod).  With a window a pair's key tiles
+// kMode: kPlain, or one of the kinds of modified scores (ScoreMod): kWindow
+// alone, kCapped (with or without a window), kBiased (a distance bias, with or
+// without a cap or a window).  They are kernels of their own because the
+// softmax loop has to stay small: with all kinds in one kernel the instruction
+// fetch stalled it (windowed chunks took 255 us instead of 199, capped ones 341
+// instead of 329).  With a window a pair's key tiles
 // start at the tile of its first query's first key (tile index j0 + j); blocks
 // wholly before that key are not read (their table entries may be anything),
 // their keys are masked and their V rows cleared.
-template <typename T, int D, bool kMod>
+template <typename T, int D, int kMode>
 __global__ void __launch_bounds__(kTcThreads, 1)
     prefill_tc_kernel(const PrefillParams p, const int32_t* __restrict__ plan,
                       const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                       const __grid_constant__ CUtensorMap qmap) {
     using Sh = TcShape<D>;
+    constexpr bool kMod = kMode != kPlain;
     constexpr int NK = Sh::kKStages;
     constexpr int NV = Sh::kVStages;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -578,7 +629,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // tiles A (x = 0) and B (x = 1, absent past the chunk's last tile).
     struct Item {
         int g, row0, qlen, n, nkt, pos_pair, nblk_live;
-        int j0, blk_first;   // first key tile and first live block (0 without a window)
+        int j0, key_first;   // first key tile and first key of the pair (0 without a window)
         int q0[kTcTiles], nkx[kTcTiles], pos_lo[kTcTiles], pos_hi[kTcTiles];
         const int32_t* bt;
     };
@@ -611,11 +662,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 it.nkx[x] = 0;
             }
         }
-        it.j0 = it.blk_first = 0;
+        it.j0 = it.key_first = 0;
         if constexpr (kMod) {
-            const int first = window_start(it.pos_lo[0], p.mod.window);
-            it.j0 = first / kTcKeys;
-            it.blk_first = first >> 4;
+            it.key_first = window_start(it.pos_lo[0], p.mod.window);
+            it.j0 = it.key_first / kTcKeys;
             it.nkx[0] -= it.j0;
             if (it.nkx[1]) it.nkx[1] -= it.j0;
         }
@@ -661,7 +711,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
         const uint32_t s_tm = tmem + lane_base + static_cast<uint32_t>(x * kTcKeys);
         const uint32_t o_tm = tmem + lane_base + static_cast<uint32_t>(kTcTiles * kTcKeys + x * D);
-        const bool fold = !kMod && p.scale_log2 > 0.f;   // scale folded into the exponent's FMA
+        // scale folded into the exponent's FMA
+        const bool fold = (kMode == kPlain || kMode == kWindow) && p.scale_log2 > 0.f;
         int n_items_x = 0;   // items of this tile so far (o_done phases)
         for (int k = 0; ok; ++k) {
             const int w0 = item_at(k);
@@ -681,16 +732,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 // does the item's live table hold an id outside the pool?  (One
                 // scan per item keeps table loads off the per-tile path.)
                 bool any_bad = false;
-                for (int blk = it.blk_first + lane; blk < it.nblk_live; blk += 32) {
+                for (int blk = (it.key_first >> 4) + lane; blk < it.nblk_live; blk += 32) {
                     const int id = it.bt[blk];
                     any_bad |= id < 0 || id >= p.num_blocks;
                 }
                 any_bad = __any_sync(kFullMask, any_bad);
                 float m_ref = -INFINITY, l_run = 0.f;
                 float slope = 0.f;
-                if constexpr (kMod) {
-                    if (p.mod.slopes) slope = p.mod.slopes[it.g * G + r % G] * 1.4426950408889634f;
-                }
+                if constexpr (kMode == kBiased) slope = p.mod.slopes[it.g * G + r % G] * 1.4426950408889634f;
                 const int lo_row = kMod ? window_start(pos_row, p.mod.window) : 0;
                 const int lo_hi = kMod ? window_start(pos_hi, p.mod.window) : 0;
                 for (int j = 0; j < nk; ++j) {
@@ -703,14 +752,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                         for (int jb = 0; jb < kTcBlocks; ++jb) {
                             const int blk = (it.j0 + j) * kTcBlocks + jb;
-                            if (blk >= it.blk_first && blk < it.nblk_live) {
+                            if (blk >= it.key_first >> 4 && blk < it.nblk_live) {
                                 const int id = it.bt[blk];
                                 if (id < 0 || id >= p.num_blocks) bad |= 1u << jb;
                             }
                         }
                     }
                     // (blocks before the window are dead in the same way)
-                    if (kMod && j == 0) bad |= (1u << (it.blk_first % kTcBlocks)) - 1u;
+                    if (kMod && j == 0) bad |= (1u << ((it.key_first >> 4) % kTcBlocks)) - 1u;
                     if (!__all_sync(kFullMask, wait_or_abort(&s_full[x], Tx & 1, abort_v))) {
                         ok = false;
                         break;
@@ -727,9 +776,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // tensor memory until P is stored, and takes the maximum
                     // first.  Either way P is what taking the maximum every time
                     // gives.  (Warp-wide decisions: tcgen05.ld/st are collective.)
-                    // (Modified scores cost more than a maximum: it is taken first,
-                    // and there is no second pass.)
-                    bool need_max = kMod || __any_sync(kFullMask, m_ref == -INFINITY);
+                    // (Capped or biased scores cost more than a maximum: it is
+                    // taken first, and there is no second pass.)
+                    bool need_max = kMode == kCapped || kMode == kBiased || __any_sync(kFullMask, m_ref == -INFINITY);
+                    const bool masked = (key0 + kTcKeys - 1 > pos_lo) || bad || (kMod && key0 < lo_hi);
                     float sv[kTcKeys];
                     float l_tile;
 #pragma unroll 1
@@ -754,23 +804,52 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         // maximum of the scaled scores is the scaled maximum, as
                         // rounding is monotonic), fused with the subtraction of
                         // the exponent.
-                        if constexpr (kMod) modify_scores(sv, p.mod, p.scale_log2, slope, key0 - pos_row);
-                        if (!kMod && !fold) {
+                        // P = 2^(sv * mul + off - m_ref).  A capped score stays
+                        // as its reciprocal r (mul = -2 cap, off = cap; the
+                        // hidden keys' is +inf); a biased one is finished here.
+                        float mul = fold ? p.scale_log2 : 1.f, off = 0.f;
+                        if constexpr (kMode == kCapped || kMode == kBiased) {
+                            const bool capped = kMode == kCapped || p.mod.cap_log2 > 0.f;
+                            if (capped) {
+                                if (masked) {
+#pragma unroll
+                                    for (int c = 0; c < kTcKeys; ++c) {
+                                        const bool dead = key0 + c > pos_row || key0 + c < lo_row ||
+                                                          ((bad >> (c >> 4)) & 1u);
+                                        sv[c] = dead ? 0.f : sv[c];
+                                    }
+                                }
+                                cap_reciprocals(sv, p.mod.cap_in);
+                                mul = -2.f * p.mod.cap_log2;
+                                off = p.mod.cap_log2;
+                            }
+                            if constexpr (kMode == kBiased) {
+                                const float f = capped ? mul : p.scale_log2;
+                                const float b0 = fmaf(slope, static_cast<float>(key0 - pos_row), off);
+#pragma unroll
+                                for (int c = 0; c < kTcKeys; ++c)
+                                    sv[c] = fmaf(sv[c], f, fmaf(slope, static_cast<float>(c), b0));
+                                mul = 1.f;
+                                off = 0.f;
+                            }
+                        } else if (!fold) {
 #pragma unroll
                             for (int c = 0; c < kTcKeys; c += 2) mul2(sv[c], sv[c + 1], p.scale_log2);
                         }
-                        if ((key0 + kTcKeys - 1 > pos_lo) || bad || (kMod && key0 < lo_hi)) {
+                        if (masked) {
 #pragma unroll
                             for (int c = 0; c < kTcKeys; ++c) {
                                 const bool dead = key0 + c > pos_row || (kMod && key0 + c < lo_row) ||
                                                   ((bad >> (c >> 4)) & 1u);
-                                sv[c] = dead ? -INFINITY : sv[c];
+                                sv[c] = dead ? (kMode == kCapped ? INFINITY : -INFINITY) : sv[c];
                             }
                         }
                         if (need_max) {
-                            // the row maximum: four chains of three-input maxima
                             float mx;
-                            {
+                            if constexpr (kMode == kCapped) {
+                                mx = fmaf(row_min(sv), mul, off);
+                            } else {
+                                // the row maximum: four chains of three-input maxima
                                 float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                                 for (int c = 0; c < kTcKeys; c += 8) {
@@ -809,9 +888,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         {
                             const float ref = m_ref == -INFINITY ? 0.f : m_ref;
                             // s * 1 + (-ref) rounds once, like s - ref: one loop for both
-                            const float mul = fold ? p.scale_log2 : 1.f;
 #pragma unroll
-                            for (int c = 0; c < kTcKeys; c += 2) fma2(sv[c], sv[c + 1], mul, -ref);
+                            for (int c = 0; c < kTcKeys; c += 2) fma2(sv[c], sv[c + 1], mul, kMode == kCapped ? off - ref : -ref);
 #pragma unroll
                             for (int c = 0; c < kTcKeys; ++c) sv[c] = fast_exp2(sv[c]);
                             float sq[4] = {0.f, 0.f, 0.f, 0.f};
@@ -845,7 +923,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // reads this key tile clears them before its P V (the other
                     // tile's P V is issued after it)
                     const bool clearer = x == 0 || j >= nk_a;
-                    if (clearer && (j == it.nkt - 1 || bad)) {
+                    // (With a window, those before the pair's first key as well.)
+                    if (clearer && (j == it.nkt - 1 || bad || (kMod && key0 < it.key_first))) {
                         if (!__all_sync(kFullMask, wait_or_abort(&v_full[J % NV], (J / NV) & 1, abort_v))) {
                             ok = false;
                             break;
@@ -855,7 +934,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         for (int idx = r; idx < kTcKeys * CPR; idx += kTcSoftmaxWarps * 32) {
                             const int key = idx / CPR;
                             const int c = idx - key * CPR;
-                            if (key0 + key > it.pos_pair || ((bad >> (key >> 4)) & 1u))
+                            if (key0 + key > it.pos_pair || (kMod && key0 + key < it.key_first) ||
+                                ((bad >> (key >> 4)) & 1u))
                                 *reinterpret_cast<uint4*>(vt + (key >> 4) * (D / 64) * 2048 + (c >> 3) * 2048 +
                                                           (key & 15) * 128 + (((c & 7) ^ (key & 7)) << 4)) =
                                     make_uint4(0, 0, 0, 0);
@@ -1049,7 +1129,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (!do_k && !do_v) continue;
                 int id = -1;
                 const int blk = (it.j0 + j) * kTcBlocks + lane;
-                if (lane < kTcBlocks && blk >= it.blk_first && blk < it.nblk_live) {
+                if (lane < kTcBlocks && blk >= it.key_first >> 4 && blk < it.nblk_live) {
                     id = it.bt[blk];
                     if (id < 0 || id >= p.num_blocks) {
                         if (do_k) record_error(p.err, PA_DEVERR_BLOCK_ID_);
@@ -1100,11 +1180,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 
-template <typename T, int D, bool kMod = false>
+template <typename T, int D, int kMode = kPlain>
 cudaError_t launch_t(const PrefillParams& p, int32_t* plan, const CUtensorMap& kmap, const CUtensorMap& vmap,
                      const CUtensorMap& qmap, int max_q_len, int num_tokens, const Fp8Copy* copy, cudaStream_t s) {
     constexpr int smem = TcShape<D>::kSmem;
-    auto kern = prefill_tc_kernel<T, D, kMod>;
+    auto kern = prefill_tc_kernel<T, D, kMode>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     // the softmax warpgroups' register increase is granted from the pool the
@@ -1152,12 +1232,15 @@ cudaError_t launch_prefill_tc(const PrefillParams& p, int32_t* plan, const CUten
     if (p.num_seqs == 0 || max_q_len <= PA_VERIFY_MAX_Q_) return cudaSuccess;
     if (copy && !copy->fp4 && head_dim != 128) return cudaErrorInvalidValue;
     auto go = [&](auto launch) { return launch(p, plan, kmap, vmap, qmap, max_q_len, num_tokens, copy, s); };
-    if (modified) {
-        if (dtype == 0) return head_dim == 128 ? go(launch_t<__half, 128, true>) : go(launch_t<__half, 64, true>);
-        return head_dim == 128 ? go(launch_t<__nv_bfloat16, 128, true>) : go(launch_t<__nv_bfloat16, 64, true>);
-    }
-    if (dtype == 0) return head_dim == 128 ? go(launch_t<__half, 128>) : go(launch_t<__half, 64>);
-    return head_dim == 128 ? go(launch_t<__nv_bfloat16, 128>) : go(launch_t<__nv_bfloat16, 64>);
+    auto of = [&](auto kind) {
+        constexpr int kMode = decltype(kind)::value;
+        if (dtype == 0) return head_dim == 128 ? go(launch_t<__half, 128, kMode>) : go(launch_t<__half, 64, kMode>);
+        return head_dim == 128 ? go(launch_t<__nv_bfloat16, 128, kMode>) : go(launch_t<__nv_bfloat16, 64, kMode>);
+    };
+    if (!modified) return of(std::integral_constant<int, kPlain>{});
+    if (p.mod.slopes) return of(std::integral_constant<int, kBiased>{});
+    if (p.mod.cap_log2 > 0.f) return of(std::integral_constant<int, kCapped>{});
+    return of(std::integral_constant<int, kWindow>{});
 }
 
 }  // namespace pa

@@ -33,8 +33,8 @@ MODS = {
 
 def build(lens, qlens, Hq, Hkv, D, dt, seed, window=0, qscale=3.0):
     """Scattered blocks; every slot that no query of the step may see (tails,
-    unused blocks, blocks wholly before the windows) is NaN, and the table
-    entries of blocks before the windows are garbage."""
+    unused blocks, keys before the windows) is NaN, and the table entries of
+    blocks before the windows are garbage."""
     rng = np.random.default_rng(seed)
     used = [(int(n) + 15) // 16 for n in lens]
     NB = sum(used) + 3
@@ -44,9 +44,10 @@ def build(lens, qlens, Hq, Hkv, D, dt, seed, window=0, qscale=3.0):
     at = 0
     for b, u in enumerate(used):
         n, c = int(lens[b]), int(qlens[b])
-        first = max(0, n - c + 1 - window) // 16 if window else 0
+        lo = max(0, n - c + 1 - window) if window else 0
+        first = lo // 16
         tables[b, first:u] = perm[at + first:at + u]
-        for j in range(16 * first, n):
+        for j in range(lo, n):
             live[perm[at + j // 16], j % 16] = True
         at += u
     g = torch.Generator().manual_seed(seed)
