@@ -787,7 +787,7 @@ static int prefill_impl(void* out, const void* q, const void* k_cache, const voi
         // SMs shared by work: a key tile of a pair (two 128 x 128 tiles) takes
         // 2.0 us of one SM at head_dim 128 (capped scores 2.6 us)
         p.split = dc.p.split;
-        p.decode_weight = (cache == Cache::kFp4 ? 5.f : 12.f) * dc.p.col_chunks / (mod && softcapped(*mod) ? 2600.f : 2000.f);
+        p.decode_weight = (cache == Cache::kFp4 ? 0.5f : 1.2f) * dc.p.col_chunks / (mod && softcapped(*mod) ? 2600.f : 2000.f);
     }
     if (pa::launch_prefill_tc(p, plan, kmap, vmap, qmap, head_dim, dtype, max_q_len, num_tokens,
                               copied ? &copy : nullptr, mod != nullptr, s) !=

@@ -229,16 +229,15 @@ __device__ __forceinline__ void mulp(float& x, float& y, float u, float v) {
         : "f"(u), "f"(v));
 }
 
-// The smallest of a row's 128 values: four chains of three-input minima.
-__device__ __forceinline__ float row_min(const float (&sv)[kTcKeys]) {
-    float mq[4] = {INFINITY, INFINITY, INFINITY, INFINITY};
+// The largest of a row's 128 values: four chains of three-input maxima.
+__device__ __forceinline__ float row_max(const float (&sv)[kTcKeys]) {
+    float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
     for (int c = 0; c < kTcKeys; c += 8) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            asm("min.f32 %0, %0, %1, %2;" : "+f"(mq[u]) : "f"(sv[c + 2 * u]), "f"(sv[c + 2 * u + 1]));
+        for (int u = 0; u < 4; ++u) mq[u] = fmax3(mq[u], sv[c + 2 * u], sv[c + 2 * u + 1]);
     }
-    return fminf(fminf(mq[0], mq[1]), fminf(mq[2], mq[3]));
+    return fmax3(fmaxf(mq[0], mq[1]), mq[2], mq[3]);
 }
 // The smaller of two values; a NaN stays.
 __device__ __forceinline__ float fmin_nan(float a, float b) {
@@ -247,24 +246,21 @@ __device__ __forceinline__ float fmin_nan(float a, float b) {
     return d;
 }
 
-// Raw scores -> r = 1 / (1 + 2^(raw * cap_in)), of which the capped score is
-// cap - 2 cap r (ScoreMod).  The special-function unit sets the pace of capped
-// rows (2^x at 32 a clock per SM, reciprocals at 16, and P's own 2^x), so four
+// x = raw * cap_in -> r = 1 / (1 + 2^x), of which the capped score is cap - 2
+// cap r (ScoreMod).  The special-function unit sets the pace of capped rows
+// (2^x at 32 a clock per SM, reciprocals at 16, and P's own 2^x), so four
 // scores share one reciprocal: with a .. d the four sums, 1 / (ac) = bd / (ac
-// bd) and 1 / a = c / (ac).  The exponent is held at 30 (r = 2^-30, a capped
-// score within 2^-29 of the cap), so that the product of four sums stays below
-// 2^121.  A NaN reaches its group: scores of hidden keys, which may be
-// anything, are cleared before.
-__device__ __forceinline__ void cap_reciprocals(float (&sv)[kTcKeys], float cap_in) {
+// bd) and 1 / a = c / (ac).  x is at most 30, so that the product of four sums
+// stays below 2^121.  A NaN reaches its group: scores of hidden keys, which
+// may be anything, are cleared before.
+__device__ __forceinline__ void cap_reciprocals(float (&sv)[kTcKeys]) {
 #pragma unroll
     for (int i = 0; i < kTcKeys; i += 4) {
         float &a = sv[i], &b = sv[i + 1], &c = sv[i + 2], &d = sv[i + 3];
-        mul2(a, b, cap_in);
-        mul2(c, d, cap_in);
-        a = fast_exp2(fmin_nan(a, 30.f));
-        b = fast_exp2(fmin_nan(b, 30.f));
-        c = fast_exp2(fmin_nan(c, 30.f));
-        d = fast_exp2(fmin_nan(d, 30.f));
+        a = fast_exp2(a);
+        b = fast_exp2(b);
+        c = fast_exp2(c);
+        d = fast_exp2(d);
         add2(a, b, 1.f, 1.f);
         add2(c, d, 1.f, 1.f);
         float ac = a, bd = b;
@@ -776,9 +772,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // tensor memory until P is stored, and takes the maximum
                     // first.  Either way P is what taking the maximum every time
                     // gives.  (Warp-wide decisions: tcgen05.ld/st are collective.)
-                    // (Capped or biased scores cost more than a maximum: it is
-                    // taken first, and there is no second pass.)
-                    bool need_max = kMode == kCapped || kMode == kBiased || __any_sync(kFullMask, m_ref == -INFINITY);
+                    // With modified scores the maximum is taken first, always: a
+                    // second pass costs them more, and it would come often (a
+                    // window's first tile may show a row only a few keys, which
+                    // leaves its reference low).  Windowed chunks 191 us against
+                    // 236, capped ones 310 against 463.
+                    bool need_max = kMod || __any_sync(kFullMask, m_ref == -INFINITY);
                     const bool masked = (key0 + kTcKeys - 1 > pos_lo) || bad || (kMod && key0 < lo_hi);
                     float sv[kTcKeys];
                     float l_tile;
@@ -808,18 +807,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         // as its reciprocal r (mul = -2 cap, off = cap; the
                         // hidden keys' is +inf); a biased one is finished here.
                         float mul = fold ? p.scale_log2 : 1.f, off = 0.f;
+                        float x_max = 0.f;
+                        auto hide = [&](float v) {   // hidden keys get v
+#pragma unroll
+                            for (int c = 0; c < kTcKeys; ++c) {
+                                const bool dead = key0 + c > pos_row || (kMod && key0 + c < lo_row) ||
+                                                  ((bad >> (c >> 4)) & 1u);
+                                sv[c] = dead ? v : sv[c];
+                            }
+                        };
                         if constexpr (kMode == kCapped || kMode == kBiased) {
                             const bool capped = kMode == kCapped || p.mod.cap_log2 > 0.f;
                             if (capped) {
-                                if (masked) {
 #pragma unroll
-                                    for (int c = 0; c < kTcKeys; ++c) {
-                                        const bool dead = key0 + c > pos_row || key0 + c < lo_row ||
-                                                          ((bad >> (c >> 4)) & 1u);
-                                        sv[c] = dead ? 0.f : sv[c];
-                                    }
+                                for (int c = 0; c < kTcKeys; c += 2) mul2(sv[c], sv[c + 1], p.mod.cap_in);
+                                if (masked) hide(-INFINITY);
+                                x_max = row_max(sv);
+                                if (__any_sync(kFullMask, x_max > 30.f)) {   // tanh is 1 to 2^-29 there
+#pragma unroll
+                                    for (int c = 0; c < kTcKeys; ++c) sv[c] = fmin_nan(sv[c], 30.f);
                                 }
-                                cap_reciprocals(sv, p.mod.cap_in);
+                                cap_reciprocals(sv);
                                 mul = -2.f * p.mod.cap_log2;
                                 off = p.mod.cap_log2;
                             }
@@ -836,28 +844,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                             for (int c = 0; c < kTcKeys; c += 2) mul2(sv[c], sv[c + 1], p.scale_log2);
                         }
-                        if (masked) {
-#pragma unroll
-                            for (int c = 0; c < kTcKeys; ++c) {
-                                const bool dead = key0 + c > pos_row || (kMod && key0 + c < lo_row) ||
-                                                  ((bad >> (c >> 4)) & 1u);
-                                sv[c] = dead ? (kMode == kCapped ? INFINITY : -INFINITY) : sv[c];
-                            }
-                        }
+                        if (masked) hide(kMode == kCapped ? INFINITY : -INFINITY);
                         if (need_max) {
                             float mx;
-                            if constexpr (kMode == kCapped) {
-                                mx = fmaf(row_min(sv), mul, off);
+                            if constexpr (kMode == kCapped) {   // (-inf where every key is hidden)
+                                mx = x_max == -INFINITY ? -INFINITY
+                                                        : fmaf(fast_rcp(1.f + fast_exp2(x_max)), mul, off);
                             } else {
-                                // the row maximum: four chains of three-input maxima
-                                float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                                for (int c = 0; c < kTcKeys; c += 8) {
-#pragma unroll
-                                    for (int u = 0; u < 4; ++u)
-                                        mq[u] = fmax3(mq[u], sv[c + 2 * u], sv[c + 2 * u + 1]);
-                                }
-                                mx = fmax3(fmaxf(mq[0], mq[1]), mq[2], mq[3]);
+                                mx = row_max(sv);
                                 if (fold) mx *= p.scale_log2;
                             }
                             // lazy rescale: move the reference only when the
