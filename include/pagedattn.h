@@ -145,15 +145,15 @@ int pa_decode_partition(int max_seq_len, int partition_size);
  * pairs): pa_decode_partition(max_seq_len, 0), halved down to PA_MIN_PARTITION
  * tokens while sequences of max_seq_len tokens would give fewer than
  * PA_PARTITION_ITEMS items, so that few or few-headed sequences still spread
- * over the GPU; at most PA_MAX_PARTITIONS_FOR partitions a sequence (the merge
- * of more takes longer than it saves).  Lengths of at most 2 *
- * PA_MIN_PARTITION tokens stay in one partition.  Pass the value as partition_size, to the workspace function too
+ * over the GPU, but not below the square root of 2 * max_seq_len (walking a
+ * partition takes a time in proportion to its length, merging them one in
+ * proportion to their number).  Lengths of at most 2 * PA_MIN_PARTITION tokens
+ * stay in one partition.  Pass the value as partition_size, to the workspace function too
  * (with a window, max_seq_len of the call is right here as well).  Returns -1
  * for a negative size, no heads, or num_q_heads not a multiple of num_kv_heads.
  */
 #define PA_MIN_PARTITION 64
-#define PA_PARTITION_ITEMS 8192
-#define PA_MAX_PARTITIONS_FOR 256
+#define PA_PARTITION_ITEMS 4096
 int pa_decode_partition_for(int num_seqs, int num_q_heads, int num_kv_heads, int max_seq_len);
 
 /*
@@ -439,9 +439,16 @@ int pa_paged_attention_decode_fp4(void* out, const void* q, const void* k_cache,
                                   void* stream);
 
 /* A continuous-batching step over a 4-bit cache: as
- * pa_paged_attention_prefill_fp8, the chunks' 16-bit copy included
- * (pa_prefill_fp8_workspace_bytes sizes the workspace; its chunk and
- * PA_DEVERR_WORKSPACE rules hold). */
+ * pa_paged_attention_prefill_fp8, the chunks' 16-bit copy included (its chunk
+ * and PA_DEVERR_WORKSPACE rules hold).  Its decode and verify rows use
+ * partitions of pa_decode_partition_for(num_seqs, ..) tokens, so it has a
+ * workspace function of its own, with the arguments of
+ * pa_prefill_fp8_workspace_bytes (pa_prefill_mod_workspace_bytes suffices when
+ * max_q_len <= PA_VERIFY_MAX_Q). */
+size_t pa_prefill_fp4_workspace_bytes(int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads,
+                                      int head_dim, int max_seq_len, int max_blocks_per_seq,
+                                      int64_t chunk_kv_tokens);
+
 int pa_paged_attention_prefill_fp4(void* out, const void* q, const void* k_cache, const void* v_cache,
                                    const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
                                    const int32_t* cu_q_lens, int num_seqs, int num_tokens, int max_q_len,
@@ -451,8 +458,8 @@ int pa_paged_attention_prefill_fp4(void* out, const void* q, const void* k_cache
 
 /*
  * Attention with modified scores over a 16-bit cache: pa_paged_attention_decode
- * and pa_paged_attention_prefill (same arguments, workspaces and error rules)
- * with, for query position i, key position j and query head h,
+ * and pa_paged_attention_prefill (same arguments and error rules; the decode's
+ * workspace too, the varlen call's is pa_prefill_mod_workspace_bytes) with, for query position i, key position j and query head h,
  *   s = scale * q . k
  *   s = softcap * tanh(s / softcap)     when softcap > 0 (at most PA_SOFTCAP_MAX)
  *   s = s + alibi_slopes[h] * (j - i)   when alibi_slopes != NULL (fp32 [num_q_heads], device)
@@ -469,6 +476,13 @@ int pa_paged_attention_decode_mod(void* out, const void* q, const void* k_cache,
                                   int window, const float* alibi_slopes, int num_q_heads, int num_kv_heads,
                                   int head_dim, int block_size, int partition_size, void* workspace,
                                   size_t workspace_bytes, int dtype, void* stream);
+
+/* Workspace of pa_paged_attention_prefill_mod: that of
+ * pa_prefill_workspace_bytes, with decode and verify rows in partitions of
+ * pa_decode_partition_for(num_seqs, num_q_heads, num_kv_heads, max_seq_len)
+ * tokens.  0 for a negative argument or a head grouping that does not divide. */
+size_t pa_prefill_mod_workspace_bytes(int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                      int max_seq_len);
 
 int pa_paged_attention_prefill_mod(void* out, const void* q, const void* k_cache, const void* v_cache,
                                    const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,

@@ -31,7 +31,9 @@ from ._binding import (  # noqa: F401
     paged_rope_kv_write,
     paged_rope_kv_write_fp4,
     paged_rope_kv_write_fp8,
+    prefill_fp4_workspace_bytes,
     prefill_fp8_workspace_bytes,
+    prefill_mod_workspace_bytes,
     prefill_workspace_bytes,
     selftest_wait_timeout,
     slot_mapping,

@@ -62,6 +62,8 @@ _SIGNATURES = {
                                              _i32, _i32, _i32, _i32, _i32, _p, _sz, _i32, _p]),
     "pa_paged_attention_prefill_fp4": (_i32, [_p, _p, _p, _p, _p, _i32, _p, _p, _i32, _i32, _i32, _i32, _i32,
                                               _f32, _f32, _f32, _i32, _i32, _i32, _i32, _p, _sz, _i32, _p]),
+    "pa_prefill_mod_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32]),
+    "pa_prefill_fp4_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_int64]),
     "pa_paged_attention_decode_mod": (_i32, [_p, _p, _p, _p, _p, _i32, _p, _i32, _i32, _i32, _f32, _f32, _i32, _p,
                                              _i32, _i32, _i32, _i32, _i32, _p, _sz, _i32, _p]),
     "pa_paged_attention_prefill_mod": (_i32, [_p, _p, _p, _p, _p, _i32, _p, _p, _i32, _i32, _i32, _i32, _i32,
@@ -209,6 +211,20 @@ def prefill_fp8_workspace_bytes(num_seqs: int, num_tokens: int, num_q_heads: int
     return int(load_library().pa_prefill_fp8_workspace_bytes(num_seqs, num_tokens, num_q_heads, num_kv_heads,
                                                              head_dim, max_seq_len, max_blocks_per_seq,
                                                              chunk_kv_tokens))
+
+
+def prefill_fp4_workspace_bytes(num_seqs: int, num_tokens: int, num_q_heads: int, num_kv_heads: int,
+                                head_dim: int, max_seq_len: int, max_blocks_per_seq: int,
+                                chunk_kv_tokens: int) -> int:
+    return int(load_library().pa_prefill_fp4_workspace_bytes(num_seqs, num_tokens, num_q_heads, num_kv_heads,
+                                                             head_dim, max_seq_len, max_blocks_per_seq,
+                                                             chunk_kv_tokens))
+
+
+def prefill_mod_workspace_bytes(num_seqs: int, num_tokens: int, num_q_heads: int, num_kv_heads: int,
+                                head_dim: int, max_seq_len: int) -> int:
+    return int(load_library().pa_prefill_mod_workspace_bytes(num_seqs, num_tokens, num_q_heads, num_kv_heads,
+                                                             head_dim, max_seq_len))
 
 
 def count_chunk_kv_tokens(seq_lens: torch.Tensor, cu_q_lens: torch.Tensor) -> int:
@@ -678,9 +694,9 @@ def paged_attention_prefill_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
     if max_q_len > 8 and B > 0 and T > 0:
         if chunk_kv_tokens is None:
             chunk_kv_tokens = count_chunk_kv_tokens(seq_lens, cu_q_lens)
-        nbytes = lib.pa_prefill_fp8_workspace_bytes(B, T, Hq, Hkv, D, max_seq_len, max_blocks, chunk_kv_tokens)
+        nbytes = lib.pa_prefill_fp4_workspace_bytes(B, T, Hq, Hkv, D, max_seq_len, max_blocks, chunk_kv_tokens)
     else:
-        nbytes = lib.pa_prefill_workspace_bytes(B, T, Hq, D, max_seq_len)
+        nbytes = lib.pa_prefill_mod_workspace_bytes(B, T, Hq, Hkv, D, max_seq_len)
     workspace, ws_bytes = _ws(nbytes, q, workspace)
     rc = lib.pa_paged_attention_prefill_fp4(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), max_blocks,
@@ -740,7 +756,7 @@ def paged_attention_prefill_mod(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
     if out is None:
         out = torch.empty_like(q)
     lib = _lib or load_library()
-    workspace, ws_bytes = _ws(lib.pa_prefill_workspace_bytes(B, T, Hq, D, max_seq_len), q, workspace)
+    workspace, ws_bytes = _ws(lib.pa_prefill_mod_workspace_bytes(B, T, Hq, Hkv, D, max_seq_len), q, workspace)
     rc = lib.pa_paged_attention_prefill_mod(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         block_tables.shape[1], seq_lens.data_ptr(), cu_q_lens.data_ptr(), B, T, max_q_len, max_seq_len, NB, scale,

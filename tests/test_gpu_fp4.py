@@ -175,7 +175,7 @@ def test_chunks_that_do_not_fit_the_copy_are_skipped():
     cu = np.concatenate([[0], np.cumsum(qlens)]).astype(np.int32)
     qd, kd, vd, td, ld, cd = put(q, *pools, tables, np.asarray(lens, np.int32), cu)
     per = 2 * 16 * 2 * 64 * 2
-    n = pa.prefill_fp8_workspace_bytes(3, int(cu[-1]), 8, 2, 64, 1000, tables.shape[1], 300)
+    n = pa.prefill_fp4_workspace_bytes(3, int(cu[-1]), 8, 2, 64, 1000, tables.shape[1], 300)
     ws = torch.empty(n, dtype=torch.uint8, device=DEV)     # 19 + 2 blocks: the first chunk's alone
     assert n > 21 * per
     out = torch.full_like(qd, 5.0)
