@@ -14,9 +14,12 @@
 // Bound: HBM.  Every q, k and v value is read once and written once, with six
 // operations per pair between; the table rows (512 bytes per token at head_dim
 // 128) are shared by a token's heads.  One CTA owns one token (or a share of
-// its head rows when there are few tokens): a thread keeps the cos / sin of
-// its 16 dims in registers and walks the token's head rows, so the table is
-// read once per thread instead of once per row.
+// its head rows when there are few tokens); eight threads of 16 dims share a
+// head row at head_dim 128.  Measured at 8192 tokens, 32/8 heads of 128, bf16:
+// 35 us for 206 MB (5.8 TB/s, 0.86 of the measured copy rate).  Several rows'
+// loads at once cost occupancy and were slower (two rows 36.2 us, four 40.3),
+// as were 64 or 256 threads (36.2, 43.7) and one row per thread with more CTAs
+// (37.5); reading a row only after its position and table row took 37.2.
 #include <algorithm>
 
 #include "pa_fp4.cuh"
@@ -28,9 +31,13 @@ namespace {
 constexpr int kAppendThreads = 128;
 enum { kSame = 0, kFp8 = 1, kFp4 = 2 };
 
+// Eight 16-bit values.  (Not through the read-only path: q may be rotated in place.)
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
-    const uint4 r = *reinterpret_cast<const uint4*>(p);   // (not the read-only path: q may be rotated in place)
+__device__ __forceinline__ uint4 raw8(const T* p) {
+    return *reinterpret_cast<const uint4*>(p);
+}
+template <typename T>
+__device__ __forceinline__ void widen8(const uint4& r, float (&x)[8]) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -78,69 +85,75 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
     const bool rotated = 16 * u < p.rot;            // this thread's dims are rotated
     const bool split = rotated && !p.interleaved;   // its pairs are half a rotated part apart
     const int d0 = split ? 8 * u : 16 * u;
+    // head rows of a token: queries, then keys, then values
+    const int rows = p.num_q_heads + 2 * p.num_kv_heads;
+    const int step = gridDim.y * kRows;
     const int d1 = split ? half + 8 * u : 16 * u + 8;
     for (int t = blockIdx.x; t < p.num_tokens; t += gridDim.x) {
-        int64_t pos = 0;
-        if (p.rot) {
-            pos = __ldg(p.positions + t);
-            if (pos < 0 || pos >= p.max_positions) {
-                // neither the query row nor the cache row is written
-                if (threadIdx.x == 0 && blockIdx.y == 0) record_error(p.err, PA_DEVERR_POSITION_);
-                continue;
-            }
-        }
-        const int64_t slot = __ldg(p.slots + t);
-        const bool in_pool = slot >= 0 && slot < p.num_slots;
-        if (slot >= p.num_slots && threadIdx.x == 0 && blockIdx.y == 0) record_error(p.err, PA_DEVERR_SLOT_);
-        float cs[8], sn[8];                         // of this thread's 8 pairs
-        if (rotated) {
-            const float* row = p.cos_sin + pos * p.rot + 8 * u;
-            const float4 c0 = __ldg(reinterpret_cast<const float4*>(row));
-            const float4 c1 = __ldg(reinterpret_cast<const float4*>(row + 4));
-            const float4 s0 = __ldg(reinterpret_cast<const float4*>(row + half));
-            const float4 s1 = __ldg(reinterpret_cast<const float4*>(row + half + 4));
-            cs[0] = c0.x; cs[1] = c0.y; cs[2] = c0.z; cs[3] = c0.w;
-            cs[4] = c1.x; cs[5] = c1.y; cs[6] = c1.z; cs[7] = c1.w;
-            sn[0] = s0.x; sn[1] = s0.y; sn[2] = s0.z; sn[3] = s0.w;
-            sn[4] = s1.x; sn[5] = s1.y; sn[6] = s1.z; sn[7] = s1.w;
-        }
-        auto rotate = [&](float (&a)[8], float (&b)[8]) {
-            if (!p.interleaved) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) rotate_pair(a[j], b[j], cs[j], sn[j]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    rotate_pair(a[2 * j], a[2 * j + 1], cs[j], sn[j]);
-                    rotate_pair(b[2 * j], b[2 * j + 1], cs[4 + j], sn[4 + j]);
+        for (int r = blockIdx.y * kRows + threadIdx.x / U; r < rows; r += step) {
+            // the row's loads first: they do not wait for the token's position,
+            // slot and table row
+            const bool is_q = r < p.num_q_heads, is_v = r >= p.num_q_heads + p.num_kv_heads;
+            const int h = is_q ? r : r - p.num_q_heads - (is_v ? p.num_kv_heads : 0);
+            const T* src = (is_q   ? q + static_cast<int64_t>(t) * p.q_stride
+                            : is_v ? value + static_cast<int64_t>(t) * p.value_stride
+                                   : key + static_cast<int64_t>(t) * p.key_stride) +
+                           h * D;
+            // a quantised group is 16 consecutive dims whatever the pairs
+            const bool whole = kCache == kFp4 && !is_q;
+            const uint4 w0 = raw8(src + (whole ? 16 * u : d0));
+            const uint4 w1 = raw8(src + (whole ? 16 * u + 8 : d1));
+            int64_t pos = 0;
+            if (p.rot) {
+                pos = __ldg(p.positions + t);
+                if (pos < 0 || pos >= p.max_positions) {
+                    // neither the query row nor the cache row is written
+                    if (threadIdx.x == 0 && blockIdx.y == 0) record_error(p.err, PA_DEVERR_POSITION_);
+                    break;
                 }
             }
-        };
-        // head rows of the token: queries, then keys, then values
-        const int rows = p.num_q_heads + 2 * p.num_kv_heads;
-        for (int r = blockIdx.y * kRows + threadIdx.x / U; r < rows; r += gridDim.y * kRows) {
+            const int64_t slot = __ldg(p.slots + t);
+            const bool in_pool = slot >= 0 && slot < p.num_slots;
+            if (slot >= p.num_slots && threadIdx.x == 0 && blockIdx.y == 0) record_error(p.err, PA_DEVERR_SLOT_);
+            float cs[8], sn[8];                         // of this thread's 8 pairs
+            if (rotated) {
+                const float* row = p.cos_sin + pos * p.rot + 8 * u;
+                const float4 c0 = __ldg(reinterpret_cast<const float4*>(row));
+                const float4 c1 = __ldg(reinterpret_cast<const float4*>(row + 4));
+                const float4 s0 = __ldg(reinterpret_cast<const float4*>(row + half));
+                const float4 s1 = __ldg(reinterpret_cast<const float4*>(row + half + 4));
+                cs[0] = c0.x; cs[1] = c0.y; cs[2] = c0.z; cs[3] = c0.w;
+                cs[4] = c1.x; cs[5] = c1.y; cs[6] = c1.z; cs[7] = c1.w;
+                sn[0] = s0.x; sn[1] = s0.y; sn[2] = s0.z; sn[3] = s0.w;
+                sn[4] = s1.x; sn[5] = s1.y; sn[6] = s1.z; sn[7] = s1.w;
+            }
+            auto rotate = [&](float (&a)[8], float (&b)[8]) {
+                if (!p.interleaved) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) rotate_pair(a[j], b[j], cs[j], sn[j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        rotate_pair(a[2 * j], a[2 * j + 1], cs[j], sn[j]);
+                        rotate_pair(b[2 * j], b[2 * j + 1], cs[4 + j], sn[4 + j]);
+                    }
+                }
+            };
             float a[8], b[8];
-            if (r < p.num_q_heads) {
-                const T* src = q + static_cast<int64_t>(t) * p.q_stride + r * D;
-                T* dst = q_out + static_cast<int64_t>(t) * p.q_out_stride + r * D;
-                load8(src + d0, a);
-                load8(src + d1, b);
+            widen8<T>(w0, a);
+            widen8<T>(w1, b);
+            if (is_q) {
                 if (rotated) rotate(a, b);
+                T* dst = q_out + static_cast<int64_t>(t) * p.q_out_stride + h * D;
                 store8(dst + d0, a);
                 store8(dst + d1, b);
                 continue;
             }
             if (!in_pool) continue;
-            const bool is_v = r >= p.num_q_heads + p.num_kv_heads;
-            const int h = r - p.num_q_heads - (is_v ? p.num_kv_heads : 0);
-            const T* src = is_v ? value + static_cast<int64_t>(t) * p.value_stride + h * D
-                                : key + static_cast<int64_t>(t) * p.key_stride + h * D;
             void* pool = is_v ? p.v_cache : p.k_cache;
             const int64_t blk = slot >> 4;
             const int off = static_cast<int>(slot & 15);
             if constexpr (kCache != kFp4) {
-                load8(src + d0, a);
-                load8(src + d1, b);
                 if (rotated && !is_v) rotate(a, b);
                 if constexpr (kCache == kSame) {
                     T* dst = static_cast<T*>(pool) + (slot * p.num_kv_heads + h) * D;
@@ -153,21 +166,18 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
                     *reinterpret_cast<uint2*>(dst + d1) = codes8(b, inv);
                 }
             } else {
-                // 16 consecutive dims: the partners of a split pair are read too
-                load8(src + 16 * u, a);
-                load8(src + 16 * u + 8, b);
                 if (rotated && !is_v) {
                     if (p.interleaved) {
                         rotate(a, b);
                     } else {
+                        // the partners of a split pair lie half a rotated part away
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             const int d = 16 * u + 8 * x;
                             const bool first = d < half;      // a' = a c - b s, else b' = b c + a s
-                            const int i = first ? d : d - half;
+                            const float* row = p.cos_sin + pos * p.rot + (first ? d : d - half);
                             float o[8];
-                            load8(src + (first ? d + half : d - half), o);
-                            const float* row = p.cos_sin + pos * p.rot + i;
+                            widen8<T>(raw8(src + (first ? d + half : d - half)), o);
                             float(&y)[8] = x ? b : a;
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
