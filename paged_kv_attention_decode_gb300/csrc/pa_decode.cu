@@ -1213,18 +1213,27 @@ __global__ void __launch_bounds__(kReduceWarps * 32) decode_reduce_kernel(const 
 // launches with few pairs and many partitions (long contexts), where one warp
 // per pair would leave most SMs idle.  The per-partition weights are formed
 // once in shared memory; each thread then streams one head dimension of every
-// partition's accumulator.
+// partition's accumulator.  kGroups > 1: as many groups of D threads share the
+// partitions out (in runs) and add their sums at the end; each thread's chain
+// of loads is that much shorter (118 partitions of 512 (row, head) pairs at
+// head_dim 128: 19 us with one group, 9 with four).  The plain decode keeps
+// one group, and with it the order of its sums.
+constexpr int kWideGroups = 4;   // of the 4-bit and modified-score calls
 constexpr int kReduceMaxParts = 1024;   // partitions staged in shared memory per pass
 constexpr int kReduceMaxRowsPerLaunch = 2048;
 // below this many (row, q head) pairs a whole CTA merges each pair
 constexpr long long kReduceWarpPairsMin = 1024;
 
-template <typename T, int D>
-__global__ void __launch_bounds__(D) decode_reduce_cta_kernel(const DecodeParams p) {
+template <typename T, int D, int kGroups>
+__global__ void __launch_bounds__(D * kGroups) decode_reduce_cta_kernel(const DecodeParams p) {
+    constexpr int kThreads = D * kGroups;
     __shared__ float sc[kReduceMaxParts];
-    __shared__ float red[D / 32];
+    __shared__ float red[kThreads / 32];
+    __shared__ float part[kGroups > 1 ? kThreads : 1];
     const int hq = blockIdx.x;
-    const int d = threadIdx.x;
+    const int t = threadIdx.x;
+    const int d = t % D;
+    const int grp = t / D;
     const int P = p.partition_tokens;
     const int nrows = *p.row_count;
     for (int k = blockIdx.y; k < nrows; k += gridDim.y) {
@@ -1243,14 +1252,14 @@ __global__ void __launch_bounds__(D) decode_reduce_cta_kernel(const DecodeParams
 
         // M = max_p m_p (block reduction)
         float M = -INFINITY;
-        for (int i = d; i < nparts; i += D) M = fmaxf(M, wm[i]);
+        for (int i = t; i < nparts; i += kThreads) M = fmaxf(M, wm[i]);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, off));
-        if ((d & 31) == 0) red[d >> 5] = M;
+        if ((t & 31) == 0) red[t >> 5] = M;
         __syncthreads();
         M = red[0];
 #pragma unroll
-        for (int w = 1; w < D / 32; ++w) M = fmaxf(M, red[w]);
+        for (int w = 1; w < kThreads / 32; ++w) M = fmaxf(M, red[w]);
         __syncthreads();
 
         float L = 0.f, A = 0.f;
@@ -1258,38 +1267,49 @@ __global__ void __launch_bounds__(D) decode_reduce_cta_kernel(const DecodeParams
             for (int p0 = 0; p0 < nparts; p0 += kReduceMaxParts) {
                 const int np = min(kReduceMaxParts, nparts - p0);
                 float lpart = 0.f;
-                for (int i = d; i < np; i += D) {
+                for (int i = t; i < np; i += kThreads) {
                     const float s = fast_exp2(wm[p0 + i] - M);
                     sc[i] = s;
                     lpart = fmaf(wl[p0 + i], s, lpart);
                 }
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) lpart += __shfl_xor_sync(kFull, lpart, off);
-                if ((d & 31) == 0) red[d >> 5] = lpart;
+                if ((t & 31) == 0) red[t >> 5] = lpart;
                 __syncthreads();
 #pragma unroll
-                for (int w = 0; w < D / 32; ++w) L += red[w];
+                for (int w = 0; w < kThreads / 32; ++w) L += red[w];
                 const float* a = wa + static_cast<int64_t>(p0) * D + d;
-                int i = 0;
-                for (; i + 8 <= np; i += 8) {
+                // this group's run of the pass
+                int i = np * grp / kGroups;
+                const int end = np * (grp + 1) / kGroups;
+                for (; i + 8 <= end; i += 8) {
                     float x[8];
 #pragma unroll
                     for (int u = 0; u < 8; ++u) x[u] = a[static_cast<int64_t>(i + u) * D];
 #pragma unroll
                     for (int u = 0; u < 8; ++u) A = fmaf(x[u], sc[i + u], A);
                 }
-                for (; i < np; ++i) A = fmaf(a[static_cast<int64_t>(i) * D], sc[i], A);
+                for (; i < end; ++i) A = fmaf(a[static_cast<int64_t>(i) * D], sc[i], A);
                 __syncthreads();
             }
         }
+        if constexpr (kGroups > 1) {
+            part[t] = A;
+            __syncthreads();
+            A = part[d];
+#pragma unroll
+            for (int w = 1; w < kGroups; ++w) A += part[w * D + d];
+        }
         const float v = L > 0.f ? A / L : 0.f;
-        reinterpret_cast<uint16_t*>(p.out)[(static_cast<int64_t>(qrow) * p.num_q_heads + hq) * D + d] =
-            Elem<T>::from_float(v);
+        if (grp == 0)
+            reinterpret_cast<uint16_t*>(p.out)[(static_cast<int64_t>(qrow) * p.num_q_heads + hq) * D + d] =
+                Elem<T>::from_float(v);
+        if constexpr (kGroups > 1) __syncthreads();   // (part and red are rewritten by the next row)
     }
 }
 
 
-template <typename T, int D>
+template <typename T, int D, int kGroups>
 cudaError_t launch_reduce_t(const DecodeParams& p, cudaStream_t s) {
     if (p.max_parts <= 1) return cudaSuccess;
     const long long pairs = static_cast<long long>(p.max_rows) * p.num_q_heads;
@@ -1302,7 +1322,7 @@ cudaError_t launch_reduce_t(const DecodeParams& p, cudaStream_t s) {
         return launch_pdl(decode_reduce_kernel<T, D>, dim3(rgrid), dim3(kReduceWarps * 32), 0, s, p);
     }
     dim3 rgrid(p.num_q_heads, std::min(p.max_rows, kReduceMaxRowsPerLaunch));
-    decode_reduce_cta_kernel<T, D><<<rgrid, D, 0, s>>>(p);
+    decode_reduce_cta_kernel<T, D, kGroups><<<rgrid, D * kGroups, 0, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -1333,7 +1353,7 @@ cudaError_t launch_decode_t(const DecodeParams& p, const CUtensorMap& kmap, cons
         std::max<long long>(1, std::min<long long>(want, static_cast<long long>(ctas_per_sm) * sm_count())));
     e = launch_pdl(kern, dim3(grid), dim3(kDecodeWarps * 32), smem, s, p, kmap, vmap);
     if (e != cudaSuccess) return e;
-    return launch_reduce_t<T, D>(p, s);
+    return launch_reduce_t<T, D, kMod ? kWideGroups : 1>(p, s);
 }
 
 }  // namespace
@@ -1351,8 +1371,11 @@ int sm_count() {
 }
 
 cudaError_t launch_decode_reduce(const DecodeParams& p, int head_dim, int dtype, cudaStream_t s) {
-    if (dtype == 0) return head_dim == 128 ? launch_reduce_t<__half, 128>(p, s) : launch_reduce_t<__half, 64>(p, s);
-    return head_dim == 128 ? launch_reduce_t<__nv_bfloat16, 128>(p, s) : launch_reduce_t<__nv_bfloat16, 64>(p, s);
+    if (dtype == 0)
+        return head_dim == 128 ? launch_reduce_t<__half, 128, kWideGroups>(p, s)
+                               : launch_reduce_t<__half, 64, kWideGroups>(p, s);
+    return head_dim == 128 ? launch_reduce_t<__nv_bfloat16, 128, kWideGroups>(p, s)
+                           : launch_reduce_t<__nv_bfloat16, 64, kWideGroups>(p, s);
 }
 
 cudaError_t launch_decode_plan(const DecodeParams& p, cudaStream_t s, bool pdl) {

@@ -650,9 +650,13 @@ __global__ void __launch_bounds__(kWidenFp4Threads) widen_chunk_blocks_fp4_kerne
                                                                                   const int32_t* __restrict__ seq_lens,
                                                                                   int max_blocks, int num_kv_heads) {
     using Tile = Fp4Tile<D>;
+    constexpr int kUnroll = 4;
     const int nchunks = c.hdr[0];
     const int used = min(c.hdr[1], c.cap_blocks);
     const int groups = num_kv_heads * 16 * Tile::kGroups;    // groups per block and pool
+    const bool v = blockIdx.y;
+    const uint8_t* codes = static_cast<const uint8_t*>(v ? c.v_codes : c.k_codes);
+    T* out16 = static_cast<T*>(v ? c.v16 : c.k16);
     for (int u = blockIdx.x; u < used && nchunks > 0; u += gridDim.x) {
         int lo = 0, hi = nchunks - 1;
         while (lo < hi) {
@@ -665,21 +669,29 @@ __global__ void __launch_bounds__(kWidenFp4Threads) widen_chunk_blocks_fp4_kerne
         if (i < 0 || i >= ((seq_lens[b] + 15) >> 4)) continue;
         const int src = c.src_tables[static_cast<int64_t>(b) * max_blocks + i];
         const bool ok = src >= 0 && src < c.src_num_blocks;   // else the attention kernel flags and masks it
-        if (threadIdx.x == 0) c.table[static_cast<int64_t>(b) * max_blocks + i] = ok ? u : -1;
+        if (threadIdx.x == 0 && !v) c.table[static_cast<int64_t>(b) * max_blocks + i] = ok ? u : -1;
         if (!ok) continue;
+        const uint8_t* blk = codes + static_cast<int64_t>(src) * num_kv_heads * Tile::kBytes;
+        T* out = out16 + static_cast<int64_t>(u) * 16 * num_kv_heads * D;
+        for (int x0 = threadIdx.x; x0 < groups; x0 += kUnroll * kWidenFp4Threads) {
+            uint2 raw[kUnroll];
+            uint8_t sc[kUnroll];
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            const uint8_t* blk = static_cast<const uint8_t*>(v ? c.v_codes : c.k_codes) +
-                                 static_cast<int64_t>(src) * num_kv_heads * Tile::kBytes;
-            T* out = static_cast<T*>(v ? c.v16 : c.k16) + static_cast<int64_t>(u) * 16 * num_kv_heads * D;
-            for (int x = threadIdx.x; x < groups; x += kWidenFp4Threads) {
+            for (int k = 0; k < kUnroll; ++k) {
                 // source order: head, token, group
-                const int grp = x % Tile::kGroups, row = x / Tile::kGroups;
-                const int h = row >> 4, t = row & 15;
+                const int x = min(x0 + k * kWidenFp4Threads, groups - 1);
+                const int grp = x % Tile::kGroups, t = x / Tile::kGroups & 15, h = x / Tile::kGroups >> 4;
                 const uint8_t* tile = blk + static_cast<int64_t>(h) * Tile::kBytes;
-                const uint2 codes = *reinterpret_cast<const uint2*>(tile + t * Tile::kRow + 8 * grp);
+                raw[k] = __ldcs(reinterpret_cast<const uint2*>(tile + t * Tile::kRow + 8 * grp));
+                sc[k] = tile[Tile::scale_off(v, t, grp)];
+            }
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k) {
+                const int x = x0 + k * kWidenFp4Threads;
+                if (x >= groups) break;
+                const int grp = x % Tile::kGroups, t = x / Tile::kGroups & 15, h = x / Tile::kGroups >> 4;
                 uint32_t w[8];
-                group_values(codes.x, codes.y, tile[Tile::scale_off(v, t, grp)], w);
+                group_values(raw[k].x, raw[k].y, sc[k], w);
                 if constexpr (std::is_same<T, __nv_bfloat16>::value) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
@@ -719,7 +731,7 @@ cudaError_t launch_decode_fp4(const DecodeParams& p, int head_dim, int dtype, cu
 
 cudaError_t launch_widen_fp4(const Fp8Copy& c, const int32_t* seq_lens, int max_blocks, int num_kv_heads, int head_dim,
                              int dtype, cudaStream_t s) {
-    const int grid = std::max(1, std::min(c.cap_blocks, 8 * sm_count()));
+    const dim3 grid(std::max(1, std::min(c.cap_blocks, 8 * sm_count())), 2);   // K and V
     auto go = [&](auto kern) { kern<<<grid, kWidenFp4Threads, 0, s>>>(c, seq_lens, max_blocks, num_kv_heads); };
     if (dtype == 0) {
         if (head_dim == 128) go(widen_chunk_blocks_fp4_kernel<__half, 128>);

@@ -391,23 +391,36 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
                 atomicMax(&blk_end, first + nb);
             }
         }
-        if (b < num_seqs)
-            for (int pr = 0; pr < v; ++pr) atomicAdd(&hist[bucket(n, ql, pr)], 1);
-        if (split && b < num_seqs && n >= ql && n <= max_seq_len) {
-            unsigned long long cost = 0;
-            for (int pr = 0; pr < v; ++pr) cost += pair_key_tiles(n, ql, q_per_tile, pr, window);
-            if (cost) atomicAdd(&chunk_cost, cost);
-            if (ql > 0 && ql <= PA_VERIFY_MAX_Q_)
-                atomicAdd(&row_cost, static_cast<unsigned long long>(n - window_start(n - ql, window)));
-        }
+        if (split && b < num_seqs && n >= ql && n <= max_seq_len && ql > 0 && ql <= PA_VERIFY_MAX_Q_)
+            atomicAdd(&row_cost, static_cast<unsigned long long>(n - window_start(n - ql, window)));
         const int start = block_exclusive_scan_1024(v, warp_tot, &carry);
         if (b < num_seqs) {
             offsets[b] = start;
             for (int pr = 0; pr < v; ++pr) seq_of_pair[start + pr] = b;
         }
     }
+    __syncthreads();   // (offsets and seq_of_pair, read below by other threads)
+    const int total = carry;
+    // one thread per pair: global pair l of sequence b is its pair pr, counted
+    // from the last one
+    auto pair_at = [&](int l, int& n, int& ql) {
+        const int b = seq_of_pair[l];
+        const int c0 = cu_q_lens[b];
+        ql = cu_q_lens[b + 1] - c0;
+        n = seq_lens[b];
+        return offsets[b + 1] - 1 - l;
+    };
+    if (tid == 0) offsets[num_seqs] = total;
+    __syncthreads();
+    for (int l = tid; l < total; l += 1024) {
+        int n, ql;
+        const int pr = pair_at(l, n, ql);
+        const int k = bucket(n, ql, pr);
+        atomicAdd(&hist[k], 1);
+        if (split) atomicAdd(&chunk_cost, static_cast<unsigned long long>(kPlanBuckets - 1 - k));
+    }
+    __syncthreads();
     if (tid == 0) {
-        offsets[num_seqs] = carry;
         if (split) {
             // the CTAs that take chunks: in proportion to the two kinds' work,
             // so that they end together
@@ -431,18 +444,11 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
         hist[2 * tid + 1] = start + h0;
     }
     __syncthreads();
-    // scatter each pair's global index to its class (the pair counts from
-    // offsets: a chunk without copy blocks has none)
-    for (int b = tid; b < num_seqs; b += 1024) {
-        int ql = 0, n = 0;
-        (void)pairs_of(b, ql, n);
-        const int first = offsets[b];
-        const int v = offsets[b + 1] - first;
-        for (int pr = 0; pr < v; ++pr) {
-            // the kernel's pair index l within the sequence counts from the last pair
-            const int l = first + (v - 1 - pr);
-            order[atomicAdd(&hist[bucket(n, ql, pr)], 1)] = l;
-        }
+    // scatter each pair's global index to its class
+    for (int l = tid; l < total; l += 1024) {
+        int n, ql;
+        const int pr = pair_at(l, n, ql);
+        order[atomicAdd(&hist[bucket(n, ql, pr)], 1)] = l;
     }
 }
 
