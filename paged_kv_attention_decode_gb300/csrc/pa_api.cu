@@ -376,8 +376,9 @@ static int decode_prepare(DecodeCall& c, void* out, const void* q, const void* k
     p.max_rows = max_rows;
     p.num_rows = num_rows;
     // (query, head) columns per work item: 8, or 16 once a row can have more
+    // (8 over a 4-bit cache)
     const int cols = max_q * p.group;
-    const int chunk = cols > 8 ? 16 : 8;
+    const int chunk = cols > 8 && cache != Cache::kFp4 ? 16 : 8;
     p.col_chunks = (cols + chunk - 1) / chunk;
     p.scale_log2 = scale_log2(scale) * k_scale;
     p.v_scale = v_scale;

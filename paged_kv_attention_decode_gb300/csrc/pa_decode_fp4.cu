@@ -162,18 +162,18 @@ struct Fp4Lane {
     }
 };
 
-// NT tiles of 8 (query, head) columns of one item.  E = 1: only one column
+// The (at most 8) (query, head) columns of one item.  E = 1: only one column
 // (single queries without grouped heads), so that a lane's second one is left out.
-template <int D, int NT, int E>
+template <int D, int E>
 struct Fp4State {
     static constexpr int KS = D / 16;
-    uint32_t qb[KS][NT][2];   // Q^T: k-step kk holds dims c * D/4 + 4 kk + {0, 1 | 2, 3}
-    float o[KS][NT][4];       // O^T: m-tile mt holds dims g * D/8 + 2 mt + {0 | 1}
-    float m[NT][2], l[NT][2], mul[NT][2];
-    int lim[NT][2];           // first token the column may not see
+    uint32_t qb[KS][2];       // Q^T: k-step kk holds dims c * D/4 + 4 kk + {0, 1 | 2, 3}
+    float o[KS][4];           // O^T: m-tile mt holds dims g * D/8 + 2 mt + {0 | 1}
+    float m[2], l[2], mul[2];
+    int lim[2];               // first token the column may not see
 
     // S^T = K Q^T of one block (raw products).
-    __device__ __forceinline__ void scores(const Fp4K<D>& f, float (&s)[NT][4]) const {
+    __device__ __forceinline__ void scores(const Fp4K<D>& f, float (&s)[4]) const {
         uint32_t sc[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) sc[i] = e4m3x2_to_f16x2(f.ks[i]);
@@ -190,89 +190,75 @@ struct Fp4State {
             }
             const uint32_t a0[4] = {x[0][0], x[1][0], x[0][1], x[1][1]};
             const uint32_t a1[4] = {x[0][2], x[1][2], x[0][3], x[1][3]};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                if (w == 0) mma_first(s[nt], a0, qb[0][nt][0], qb[0][nt][1]);
-                else Mma<__half>::run(s[nt], a0, qb[2 * w][nt][0], qb[2 * w][nt][1]);
-                Mma<__half>::run(s[nt], a1, qb[2 * w + 1][nt][0], qb[2 * w + 1][nt][1]);
-            }
+            if (w == 0) mma_first(s, a0, qb[0][0], qb[0][1]);
+            else Mma<__half>::run(s, a0, qb[2 * w][0], qb[2 * w][1]);
+            Mma<__half>::run(s, a1, qb[2 * w + 1][0], qb[2 * w + 1][1]);
         }
     }
 
     // Tokens at and past the columns' limits (all of them when !ok) get -inf.
-    __device__ __forceinline__ void mask(float (&s)[NT][4], int base, bool ok, int ta) const {
+    __device__ __forceinline__ void mask(float (&s)[4], int base, bool ok, int ta) const {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                if (!ok || base + ta >= lim[nt][e]) s[nt][e] = -INFINITY;
-                if (!ok || base + ta + 2 >= lim[nt][e]) s[nt][2 + e] = -INFINITY;
-            }
+        for (int e = 0; e < E; ++e) {
+            if (!ok || base + ta >= lim[e]) s[e] = -INFINITY;
+            if (!ok || base + ta + 2 >= lim[e]) s[2 + e] = -INFINITY;
         }
     }
 
     // Softmax weights of NB blocks' raw scores against the running reference,
-    // as the B operand of the second product (b[block][nt][2]).  mul > 0.
+    // as the B operand of the second product (b[block][2]).  mul > 0.
     template <int NB>
-    __device__ __forceinline__ void weights(const float (&s)[NB][NT][4], uint32_t (&b)[NB][NT][2]) {
-        auto largest = [&](int nt, int e) {
-            float mx = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
+    __device__ __forceinline__ void weights(const float (&s)[NB][4], uint32_t (&b)[NB][2]) {
+        auto largest = [&](int e) {
+            float mx = fmaxf(s[0][e], s[0][2 + e]);
 #pragma unroll
-            for (int j = 1; j < NB; ++j) mx = fmaxf(mx, fmaxf(s[j][nt][e], s[j][nt][2 + e]));
+            for (int j = 1; j < NB; ++j) mx = fmaxf(mx, fmaxf(s[j][e], s[j][2 + e]));
             return mx;
         };
         bool grow = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < E; ++e) grow |= largest(nt, e) * mul[nt][e] > m[nt][e] + kLazyLog2;
+        for (int e = 0; e < E; ++e) grow |= largest(e) * mul[e] > m[e] + kLazyLog2;
         if (__any_sync(kAll, grow)) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int e = 0; e < E; ++e) {
+                float mx = largest(e);
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    float mx = largest(nt, e);
+                for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, off));
+                mx *= mul[e];
+                if (!(mx > m[e] + kLazyLog2)) continue;
+                const float al = fast_exp2(m[e] - mx);   // 0 while the column saw no token yet
+                m[e] = mx;
+                l[e] *= al;
 #pragma unroll
-                    for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, off));
-                    mx *= mul[nt][e];
-                    if (!(mx > m[nt][e] + kLazyLog2)) continue;
-                    const float al = fast_exp2(m[nt][e] - mx);   // 0 while the column saw no token yet
-                    m[nt][e] = mx;
-                    l[nt][e] *= al;
-#pragma unroll
-                    for (int mt = 0; mt < KS; ++mt) {
-                        o[mt][nt][e] *= al;
-                        o[mt][nt][2 + e] *= al;
-                    }
+                for (int mt = 0; mt < KS; ++mt) {
+                    o[mt][e] *= al;
+                    o[mt][2 + e] *= al;
                 }
             }
         }
+        // a column without a visible token yet keeps m = -inf; its weights are 2^(-inf - 0) = 0
+        float r[E];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            // a column without a visible token yet keeps m = -inf; its weights are 2^(-inf - 0) = 0
-            float r[E];
+        for (int e = 0; e < E; ++e) r[e] = m[e] == -INFINITY ? 0.f : m[e];
 #pragma unroll
-            for (int e = 0; e < E; ++e) r[e] = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+        for (int j = 0; j < NB; ++j) {
+            float w[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                float w[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    w[e] = fast_exp2(fmaf(s[j][nt][e], mul[nt][e], -r[e]));
-                    w[2 + e] = fast_exp2(fmaf(s[j][nt][2 + e], mul[nt][e], -r[e]));
-                    l[nt][e] += w[e] + w[2 + e];
-                }
-                // rows 2c, 2c + 1 of the two 8 x 8 pieces are tokens 4c, 4c + 1 and 4c + 2, 4c + 3 (flipped alike)
-                b[j][nt][0] = movmatrix_trans(Elem<__half>::pack(w[0], w[1]));
-                b[j][nt][1] = movmatrix_trans(Elem<__half>::pack(w[2], w[3]));
+            for (int e = 0; e < E; ++e) {
+                w[e] = fast_exp2(fmaf(s[j][e], mul[e], -r[e]));
+                w[2 + e] = fast_exp2(fmaf(s[j][2 + e], mul[e], -r[e]));
+                l[e] += w[e] + w[2 + e];
             }
+            // rows 2c, 2c + 1 of the two 8 x 8 pieces are tokens 4c, 4c + 1 and 4c + 2, 4c + 3 (flipped alike)
+            b[j][0] = movmatrix_trans(Elem<__half>::pack(w[0], w[1]));
+            b[j][1] = movmatrix_trans(Elem<__half>::pack(w[2], w[3]));
         }
     }
 
     // O^T += V^T P^T of one block.  Unless `full`, tokens at and past nvalid
     // count as 0.
-    __device__ __forceinline__ void accumulate(const Fp4V<D>& f, const uint32_t (&b)[NT][2], bool full, int nvalid,
-                                               int c, uint32_t flip) {
+    __device__ __forceinline__ void accumulate(const Fp4V<D>& f, const uint32_t (&b)[2], bool full, int nvalid, int c,
+                                               uint32_t flip) {
         uint32_t vs = f.vs;
         if (!full) {
             // rows past the end may hold anything, a NaN scale too: their scale becomes 0
@@ -295,22 +281,24 @@ struct Fp4State {
             for (int i = 0; i < 4; ++i) {
                 const uint32_t a[4] = {hmul2_bits(e01[i], s01), hmul2_bits(o01[i], s01), hmul2_bits(e23[i], s23),
                                        hmul2_bits(o23[i], s23)};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) Mma<__half>::run(o[4 * w + i][nt], a, b[nt][0], b[nt][1]);
+                Mma<__half>::run(o[4 * w + i], a, b[0], b[1]);
             }
         }
     }
 };
 
 // A warp's ring of slots; a slot holds the (K tile, V tile) of a step's blocks.
-// kCols: columns of an item (1, 8 or 16).
-template <int D, int kCols>
+// Four blocks a step with two slots and 12 warps per SM: against two blocks
+// (three slots, 12 or 16 warps) 132 us to 136 and 131-143 at B=64 with 32
+// heads, 169 to 175 us at eight contexts of 32K-128K; more warps, or two-block
+// fetches for 16 warps, were slower (137-147 us).
+template <int D>
 struct Fp4Shape {
     static constexpr int kTile = Fp4Tile<D>::kBytes;
-    static constexpr int kBlocks = kCols > 8 ? 2 : 4;   // per step
+    static constexpr int kBlocks = 4;
     static constexpr int kSlot = 2 * kBlocks * kTile;
-    static constexpr int kSlots = kCols > 8 ? 3 : 2;
-    static constexpr int kMinCtas = kCols > 8 ? 2 : 3;
+    static constexpr int kSlots = 2;
+    static constexpr int kMinCtas = 3;
     static constexpr int kSmem = kFp4Warps * kSlots * kSlot;
 };
 
@@ -319,9 +307,14 @@ struct Fp4Shape {
 // fetches kSlots steps ahead of the step being computed and on into its next
 // items.  Each step commits one group of copies (an empty one past the last
 // item), so the oldest of kSlots groups is always the one being waited for.
+// kCols: columns of an item, 1 or 8.  Rows with more columns are cut into
+// chunks of 8, each of which reads the tiles again: against a 16-column kernel
+// that widened each tile once (221 registers, 8 warps per SM), verify rows of
+// 1-4 queries of 4 heads took 66 us instead of 73 and of 1-8 queries 97
+// instead of 120; 32 heads per kv head 49 instead of 48.
 template <typename T, int D, int kCols>
-__global__ void __launch_bounds__(kFp4Warps * 32, Fp4Shape<D, kCols>::kMinCtas) decode_fp4_kernel(const DecodeParams p) {
-    using Shape = Fp4Shape<D, kCols>;
+__global__ void __launch_bounds__(kFp4Warps * 32, Fp4Shape<D>::kMinCtas) decode_fp4_kernel(const DecodeParams p) {
+    using Shape = Fp4Shape<D>;
     constexpr int NB = Shape::kBlocks;
     constexpr int E = kCols == 1 ? 1 : 2;
     constexpr int kTile = Shape::kTile;
@@ -466,8 +459,7 @@ __global__ void __launch_bounds__(kFp4Warps * 32, Fp4Shape<D, kCols>::kMinCtas) 
     uint32_t slot = ring;
     const uint32_t ring_end = ring + kSlots * Shape::kSlot;
     const Fp4Lane<D> at(lane);
-    auto run_item = [&](auto nt_tag, const Item& it) {
-        constexpr int NT = decltype(nt_tag)::value;
+    auto run_item = [&](const Item& it) {
         const int tok0 = it.part * P, tok1 = min(it.n, tok0 + P);
         const int ncols = min(kCols, it.qlen * G - it.col0);
         // query index of a column (one division, skipped for single queries)
@@ -475,13 +467,11 @@ __global__ void __launch_bounds__(kFp4Warps * 32, Fp4Shape<D, kCols>::kMinCtas) 
         const int lim_min = min(tok1, it.n - it.qlen + 1 + query_of(it.col0));
         const bool parts = it.n > P;
         const int64_t prow = parts ? __ldg(p.row_base + it.b) : 0;
-        Fp4State<D, NT, E> st;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            // this lane's quarter of column nt * 8 + g's query
-            const int cl = nt * 8 + g;
-            const bool ok = cl < ncols;
-            const int col = it.col0 + (ok ? cl : 0);
+        Fp4State<D, E> st;
+        {
+            // this lane's quarter of column g's query
+            const bool ok = g < ncols;
+            const int col = it.col0 + (ok ? g : 0);
             const int qi = query_of(col);
             const uint16_t* qq =
                 static_cast<const uint16_t*>(p.q) +
@@ -521,20 +511,20 @@ __global__ void __launch_bounds__(kFp4Warps * 32, Fp4Shape<D, kCols>::kMinCtas) 
             }
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-                st.qb[kk][nt][0] = w[2 * kk];
-                st.qb[kk][nt][1] = w[2 * kk + 1];
+                st.qb[kk][0] = w[2 * kk];
+                st.qb[kk][1] = w[2 * kk + 1];
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 // the accumulators' columns: 2c + e
                 // (at least fp32's smallest normal, so that a masked -inf stays -inf)
-                st.mul[nt][e] = fmaxf(fabsf(p.scale_log2) * __shfl_sync(kAll, undo, (2 * c + e) * 4), 1.17549435e-38f);
-                st.m[nt][e] = -INFINITY;
-                st.l[nt][e] = 0.f;
-                const int ce = nt * 8 + 2 * c + e;
-                st.lim[nt][e] = ce < ncols ? min(tok1, it.n - it.qlen + 1 + query_of(it.col0 + ce)) : 0;
+                st.mul[e] = fmaxf(fabsf(p.scale_log2) * __shfl_sync(kAll, undo, (2 * c + e) * 4), 1.17549435e-38f);
+                st.m[e] = -INFINITY;
+                st.l[e] = 0.f;
+                const int ce = 2 * c + e;
+                st.lim[e] = ce < ncols ? min(tok1, it.n - it.qlen + 1 + query_of(it.col0 + ce)) : 0;
 #pragma unroll
-                for (int mt = 0; mt < D / 16; ++mt) st.o[mt][nt][e] = st.o[mt][nt][2 + e] = 0.f;
+                for (int mt = 0; mt < D / 16; ++mt) st.o[mt][e] = st.o[mt][2 + e] = 0.f;
             }
         }
         int base = tok0;
@@ -542,8 +532,8 @@ __global__ void __launch_bounds__(kFp4Warps * 32, Fp4Shape<D, kCols>::kMinCtas) 
             cp_async_wait<kSlots - 1>();
             __syncwarp();   // every lane's copies of this step are in place
             const uint32_t have = loaded >> (NB * (kSlots - 1));   // (older steps' bits lie above)
-            float sc[NB][NT][4];
-            uint32_t pb[NB][NT][2];
+            float sc[NB][4];
+            uint32_t pb[NB][2];
             static_for<NB>([&](auto j) {
                 Fp4K<D> f;
                 at.template load_k<j>(f, slot);
@@ -566,42 +556,39 @@ __global__ void __launch_bounds__(kFp4Warps * 32, Fp4Shape<D, kCols>::kMinCtas) 
             slot = slot + Shape::kSlot == ring_end ? ring : slot + Shape::kSlot;
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int e = 0; e < E; ++e) {
+            float lh = st.l[e];
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                float lh = st.l[nt][e];
+            for (int off = 4; off < 32; off <<= 1) lh += __shfl_xor_sync(kAll, lh, off);
+            const int ce = 2 * c + e;
+            if (ce >= ncols) continue;
+            const int qi = query_of(it.col0 + ce);
+            const int hq = it.h * G + (it.col0 + ce - qi * G);
+            // this lane holds dims g * D/8 .. of the column, in order
+            if (!parts) {
+                const float inv = lh > 0.f ? p.v_scale / lh : 0.f;
+                uint32_t* dst = reinterpret_cast<uint32_t*>(
+                    static_cast<uint16_t*>(p.out) +
+                    (static_cast<int64_t>(it.qrow0 + qi) * p.num_q_heads + hq) * D + g * (D / 8));
 #pragma unroll
-                for (int off = 4; off < 32; off <<= 1) lh += __shfl_xor_sync(kAll, lh, off);
-                const int ce = nt * 8 + 2 * c + e;
-                if (ce >= ncols) continue;
-                const int qi = query_of(it.col0 + ce);
-                const int hq = it.h * G + (it.col0 + ce - qi * G);
-                // this lane holds dims g * D/8 .. of the column, in order
-                if (!parts) {
-                    const float inv = lh > 0.f ? p.v_scale / lh : 0.f;
-                    uint32_t* dst = reinterpret_cast<uint32_t*>(
-                        static_cast<uint16_t*>(p.out) +
-                        (static_cast<int64_t>(it.qrow0 + qi) * p.num_q_heads + hq) * D + g * (D / 8));
-#pragma unroll
-                    for (int mt = 0; mt < D / 16; mt += 4)
-                        *reinterpret_cast<uint4*>(dst + mt) =
-                            make_uint4(Elem<T>::pack(st.o[mt][nt][e] * inv, st.o[mt][nt][2 + e] * inv),
-                                       Elem<T>::pack(st.o[mt + 1][nt][e] * inv, st.o[mt + 1][nt][2 + e] * inv),
-                                       Elem<T>::pack(st.o[mt + 2][nt][e] * inv, st.o[mt + 2][nt][2 + e] * inv),
-                                       Elem<T>::pack(st.o[mt + 3][nt][e] * inv, st.o[mt + 3][nt][2 + e] * inv));
-                } else {
-                    const int64_t pi = ((prow + qi) * p.num_q_heads + hq) * p.max_parts + it.part;
-                    if (g == 0) {
-                        p.ws_m[pi] = st.m[nt][e];
-                        p.ws_l[pi] = lh;
-                    }
-                    float* a = p.ws_acc + pi * D + g * (D / 8);
-#pragma unroll
-                    for (int mt = 0; mt < D / 16; mt += 2)
-                        *reinterpret_cast<float4*>(a + 2 * mt) =
-                            make_float4(st.o[mt][nt][e] * p.v_scale, st.o[mt][nt][2 + e] * p.v_scale,
-                                        st.o[mt + 1][nt][e] * p.v_scale, st.o[mt + 1][nt][2 + e] * p.v_scale);
+                for (int mt = 0; mt < D / 16; mt += 4)
+                    *reinterpret_cast<uint4*>(dst + mt) =
+                        make_uint4(Elem<T>::pack(st.o[mt][e] * inv, st.o[mt][2 + e] * inv),
+                                   Elem<T>::pack(st.o[mt + 1][e] * inv, st.o[mt + 1][2 + e] * inv),
+                                   Elem<T>::pack(st.o[mt + 2][e] * inv, st.o[mt + 2][2 + e] * inv),
+                                   Elem<T>::pack(st.o[mt + 3][e] * inv, st.o[mt + 3][2 + e] * inv));
+            } else {
+                const int64_t pi = ((prow + qi) * p.num_q_heads + hq) * p.max_parts + it.part;
+                if (g == 0) {
+                    p.ws_m[pi] = st.m[e];
+                    p.ws_l[pi] = lh;
                 }
+                float* a = p.ws_acc + pi * D + g * (D / 8);
+#pragma unroll
+                for (int mt = 0; mt < D / 16; mt += 2)
+                    *reinterpret_cast<float4*>(a + 2 * mt) =
+                        make_float4(st.o[mt][e] * p.v_scale, st.o[mt][2 + e] * p.v_scale,
+                                    st.o[mt + 1][e] * p.v_scale, st.o[mt + 1][2 + e] * p.v_scale);
             }
         }
     };
@@ -610,10 +597,7 @@ __global__ void __launch_bounds__(kFp4Warps * 32, Fp4Shape<D, kCols>::kMinCtas) 
         __syncwarp();
         const Item it = queue[q_head % kQueue];
         ++q_head;
-        if (kCols <= 8 || it.qlen * G - it.col0 <= 8)
-            run_item(std::integral_constant<int, 1>{}, it);
-        else
-            run_item(std::integral_constant<int, (kCols + 7) / 8>{}, it);
+        run_item(it);
     }
     cp_async_wait<0>();
     // beside a prefill kernel this grid completes only after it (what the
@@ -623,7 +607,7 @@ __global__ void __launch_bounds__(kFp4Warps * 32, Fp4Shape<D, kCols>::kMinCtas) 
 
 template <typename T, int D, int kCols>
 cudaError_t launch_kernel(const DecodeParams& p, cudaStream_t s) {
-    constexpr int smem = Fp4Shape<D, kCols>::kSmem;
+    constexpr int smem = Fp4Shape<D>::kSmem;
     auto kern = decode_fp4_kernel<T, D, kCols>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -709,9 +693,7 @@ __global__ void __launch_bounds__(kWidenFp4Threads) widen_chunk_blocks_fp4_kerne
 
 template <typename T, int D>
 cudaError_t launch_d(const DecodeParams& p, cudaStream_t s) {
-    // columns per item: the row's, at most 16 (p.col_chunks counts chunks of 8, or of 16 past 8)
-    const int cols = p.max_q * p.group;
-    return cols > 8 ? launch_kernel<T, D, 16>(p, s) : cols > 1 ? launch_kernel<T, D, 8>(p, s) : launch_kernel<T, D, 1>(p, s);
+    return p.max_q * p.group > 1 ? launch_kernel<T, D, 8>(p, s) : launch_kernel<T, D, 1>(p, s);
 }
 
 }  // namespace
