@@ -446,62 +446,77 @@ def paged_attention_prefill_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
 
 # These calls check their arguments with one condition on the way (a serving
 # step makes thousands of them) and find out what was wrong only when it fails.
-
-def _on_current(*ts) -> bool:
-    """Every tensor on the current device (the library enqueues on its stream)."""
-    dev = torch.cuda.current_device()
-    for t in ts:
-        if t.get_device() != dev:
-            return False
-    return True
+_cuda_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_F16, _BF16, _F32, _I32T, _I64T = torch.float16, torch.bfloat16, torch.float32, torch.int32, torch.int64
 
 
-def _rows(t: torch.Tensor) -> int:
-    """Token stride (elements) of [T, H, D] rows whose heads are dense within a
-    token; -1 if they are not."""
-    T, H, D = t.shape
-    s0, s1, s2 = t.stride()
-    if s2 != 1 or (s1 != D and H > 1):
-        return -1
-    return s0 if T > 1 else H * D
+def _refuse(name: str, *checks) -> None:
+    """Raise for the first (condition, message) that does not hold."""
+    for ok, msg in checks:
+        _need(ok, msg)
+    _need(False, f"{name}: invalid arguments")
+
+
+def _current(dev: int, *ts) -> bool:
+    """Every tensor on CUDA device `dev`, and that one current."""
+    return dev >= 0 and all(t is None or t.get_device() == dev for t in ts) and torch.cuda.current_device() == dev
 
 
 def _rope(name, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin, interleaved, q_out, stream,
           pool, scales):
     """The three rotate-and-append calls; `pool` is (num_blocks, num_kv_heads, head_dim, block_size)."""
     NB, H, D, bs = pool
-    T, H2, D2 = key.shape
+    shape = key.shape
+    T, H2, D2 = shape
+    qshape = q.shape
+    T2, Hq, D3 = qshape
     dtype = q.dtype
+    dev = q.get_device()
+    qs, qh, q1 = q.stride()
+    ks, kh, k1 = key.stride()
+    vs, vh, v1 = value.stride()
     if q_out is None:
-        q_out = torch.empty_like(q)
-    qs, ks, vs, os = _rows(q), _rows(key), _rows(value), _rows(q_out)
-    if not (_on_current(q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin, q_out)
-            and H2 == H and D2 == D and value.shape == key.shape and q.shape[0] == T and q.shape[2] == D
-            and q_out.shape == q.shape and key.dtype == dtype and value.dtype == dtype and q_out.dtype == dtype
+        q_out = torch.empty_like(q) if q.is_contiguous() else torch.empty(qshape, dtype=dtype, device=q.device)
+        os = Hq * D
+        out_ok = True
+    else:
+        os, oh, o1 = q_out.stride()
+        out_ok = (q_out.shape == qshape and q_out.dtype == dtype and q_out.get_device() == dev and o1 == 1
+                  and (oh == D or Hq <= 1))
+    if T <= 1:   # the stride of a single row says nothing
+        qs = os = Hq * D
+        ks = vs = H * D
+    if not (dev >= 0 and _cuda_device() == dev and key.get_device() == dev and value.get_device() == dev
+            and k_cache.get_device() == dev and v_cache.get_device() == dev and slot_mapping.get_device() == dev
+            and positions.get_device() == dev and cos_sin.get_device() == dev
+            and T2 == T and H2 == H and D2 == D and D3 == D and value.shape == shape and out_ok
+            and key.dtype == dtype and value.dtype == dtype and (dtype == _F16 or dtype == _BF16)
+            and q1 == 1 and k1 == 1 and v1 == 1 and (qh == D or Hq <= 1) and ((kh == D and vh == D) or H <= 1)
             and v_cache.shape == k_cache.shape and k_cache.is_contiguous() and v_cache.is_contiguous()
-            and slot_mapping.dtype == torch.int64 and slot_mapping.is_contiguous() and slot_mapping.numel() >= T
-            and positions.dtype == torch.int64 and positions.is_contiguous() and positions.numel() >= T
-            and cos_sin.dtype == torch.float32 and cos_sin.dim() == 2 and cos_sin.is_contiguous()
-            and qs >= 0 and ks >= 0 and vs >= 0 and os >= 0):
-        _need(_on_current(q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin, q_out),
-              "tensors must be on the current CUDA device")
-        _need(k_cache.is_contiguous() and v_cache.is_contiguous() and v_cache.shape == k_cache.shape, "cache shape")
-        _need(H2 == H and D2 == D and value.shape == key.shape and q.shape[0] == T and q.shape[2] == D,
-              "q/key/value shape")
-        _need(key.dtype == dtype and value.dtype == dtype, "q/key/value dtype")
-        _need(q_out.shape == q.shape and q_out.dtype == dtype, "q_out shape/dtype")
-        _need(slot_mapping.dtype == torch.int64 and slot_mapping.is_contiguous() and slot_mapping.numel() >= T,
-              "slot_mapping: int64 [num_tokens]")
-        _need(positions.dtype == torch.int64 and positions.is_contiguous() and positions.numel() >= T,
-              "positions: int64 [num_tokens]")
-        _need(cos_sin.dtype == torch.float32 and cos_sin.is_contiguous() and cos_sin.dim() == 2,
-              "cos_sin: float32 [max_positions, rot_dim]")
-        _need(False, "q, key, value and q_out: head rows must be dense within a token")
+            and slot_mapping.dtype == _I64T and slot_mapping.is_contiguous() and slot_mapping.numel() >= T
+            and positions.dtype == _I64T and positions.is_contiguous() and positions.numel() >= T
+            and cos_sin.dtype == _F32 and cos_sin.dim() == 2 and cos_sin.is_contiguous()):
+        _refuse(name,
+                (_current(dev, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin, q_out),
+                 "tensors must be on the current CUDA device"),
+                (T2 == T and H2 == H and D2 == D and D3 == D and value.shape == shape, "q/key/value shape"),
+                (key.dtype == dtype and value.dtype == dtype, "q/key/value dtype"),
+                (dtype in _DTYPES, f"unsupported dtype {dtype}"),
+                (v_cache.shape == k_cache.shape and k_cache.is_contiguous() and v_cache.is_contiguous(), "cache shape"),
+                (slot_mapping.dtype == _I64T and slot_mapping.is_contiguous() and slot_mapping.numel() >= T,
+                 "slot_mapping: int64 [num_tokens]"),
+                (positions.dtype == _I64T and positions.is_contiguous() and positions.numel() >= T,
+                 "positions: int64 [num_tokens]"),
+                (cos_sin.dtype == _F32 and cos_sin.dim() == 2 and cos_sin.is_contiguous(),
+                 "cos_sin: float32 [max_positions, rot_dim]"),
+                (False, "q, key, value and q_out: head rows must be dense within a token"))
     maxp, rot = cos_sin.shape
     rc = getattr(_lib or load_library(), name)(
         q_out.data_ptr(), os, q.data_ptr(), qs, key.data_ptr(), ks, value.data_ptr(), vs, k_cache.data_ptr(),
-        v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), cos_sin.data_ptr(), maxp, T, NB,
-        q.shape[1], H, D, rot, 1 if interleaved else 0, bs, _dt(q), *scales, _stream(stream))
+        v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), cos_sin.data_ptr(), maxp, T, NB, Hq, H, D,
+        rot, 1 if interleaved else 0, bs, 0 if dtype == _F16 else 1, *scales,
+        _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(rc, name)
     return q_out
@@ -571,19 +586,27 @@ def paged_kv_write_fp4(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Te
                        slot_mapping: torch.Tensor, k_scale: float, v_scale: float, stream=None) -> None:
     """In place: E2M1 codes and E4M3 group scales of key/value into the 4-bit
     pools [NB, Hkv, fp4_tile_bytes(D)] (slot < 0: skipped)."""
-    T, H, D = key.shape
+    shape = key.shape
+    T, H, D = shape
     NB, H2 = _fp4_pool(k_cache, v_cache, D)
-    if not (_on_current(key, value, k_cache, v_cache, slot_mapping) and H == H2 and value.shape == key.shape
-            and value.dtype == key.dtype and slot_mapping.dtype == torch.int64 and slot_mapping.numel() >= T
+    dtype = key.dtype
+    dev = key.get_device()
+    if not (dev >= 0 and _cuda_device() == dev and value.get_device() == dev and k_cache.get_device() == dev
+            and v_cache.get_device() == dev and slot_mapping.get_device() == dev and H == H2
+            and value.shape == shape and value.dtype == dtype and (dtype == _F16 or dtype == _BF16)
+            and slot_mapping.dtype == _I64T and slot_mapping.numel() >= T and slot_mapping.is_contiguous()
             and key.is_contiguous() and value.is_contiguous() and k_cache.is_contiguous()
-            and v_cache.is_contiguous() and slot_mapping.is_contiguous()):
+            and v_cache.is_contiguous()):
         _cuda(key, value, k_cache, v_cache, slot_mapping)
-        _need(_on_current(key, value, k_cache, v_cache, slot_mapping), "tensors must be on the current CUDA device")
-        _need(H == H2 and value.shape == key.shape and value.dtype == key.dtype, "key/value/cache shapes")
-        _need(False, "slot_mapping: int64 [num_tokens]")
+        _refuse("paged_kv_write_fp4",
+                (_current(dev, value, k_cache, v_cache, slot_mapping), "tensors must be on the current CUDA device"),
+                (H == H2 and value.shape == shape and value.dtype == dtype, "key/value/cache shapes"),
+                (dtype in _DTYPES, f"unsupported dtype {dtype}"),
+                (False, "slot_mapping: int64 [num_tokens]"))
     rc = (_lib or load_library()).pa_paged_kv_write_fp4(
         key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), T, NB, H,
-        D, PA_BLOCK_SIZE, _dt(key), k_scale, v_scale, _stream(stream))
+        D, PA_BLOCK_SIZE, 0 if dtype == _F16 else 1, k_scale, v_scale,
+        _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(rc, "pa_paged_kv_write_fp4")
 
@@ -594,43 +617,53 @@ def paged_kv_unpack_fp4(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: f
     NB, H, tile = k_cache.shape
     D = tile // 9
     _fp4_pool(k_cache, v_cache, D)
-    if not (_on_current(k_cache, v_cache) and k_cache.is_contiguous() and v_cache.is_contiguous()):
+    dev = k_cache.get_device()
+    if not (dev >= 0 and _cuda_device() == dev and v_cache.get_device() == dev and (dtype == _F16 or dtype == _BF16)
+            and k_cache.is_contiguous() and v_cache.is_contiguous()):
         _cuda(k_cache, v_cache)
-        _need(False, "tensors must be on the current CUDA device")
+        _refuse("paged_kv_unpack_fp4",
+                (_current(dev, v_cache), "tensors must be on the current CUDA device"),
+                (False, f"unsupported dtype {dtype}"))
     k_out = torch.empty((NB, PA_BLOCK_SIZE, H, D), dtype=dtype, device=k_cache.device)
     v_out = torch.empty_like(k_out)
     rc = (_lib or load_library()).pa_paged_kv_unpack_fp4(
         k_out.data_ptr(), v_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), NB, H, D, PA_BLOCK_SIZE, k_scale,
-        v_scale, _dt(k_out), _stream(stream))
+        v_scale, 0 if dtype == _F16 else 1, _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(rc, "pa_paged_kv_unpack_fp4")
     return k_out, v_out
 
 
-def _attn_args(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, alibi_slopes, out, workspace) -> None:
-    """What the attention calls below ask of their tensors besides the pools' shape."""
-    ts = [t for t in (q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, alibi_slopes, out, workspace)
-          if t is not None]
+def _attn_args(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, alibi_slopes, out, workspace) -> int:
+    """What the attention calls below ask of their tensors besides the pools'
+    shape; returns the device."""
+    dev = q.get_device()
     B = q.shape[0] if cu_q_lens is None else seq_lens.shape[0]
-    ok = (block_tables.dtype == torch.int32 and seq_lens.dtype == torch.int32 and seq_lens.numel() == B
-          and block_tables.dim() == 2 and block_tables.shape[0] >= B)
-    for t in ts:
-        ok = ok and t.is_contiguous()
-    if out is not None:
-        ok = ok and out.shape == q.shape and out.dtype == q.dtype
-    if cu_q_lens is not None:
-        ok = ok and cu_q_lens.dtype == torch.int32 and cu_q_lens.shape[0] == B + 1
-    if alibi_slopes is not None:
-        ok = ok and alibi_slopes.dtype == torch.float32 and alibi_slopes.numel() == q.shape[1]
-    if ok and _on_current(*ts):
-        return
-    _cuda(*ts)
-    _need(_on_current(*ts), "tensors must be on the current CUDA device")
-    _need(block_tables.dtype == torch.int32 and seq_lens.dtype == torch.int32, "int32 tables")
-    _need(seq_lens.numel() == B and block_tables.dim() == 2 and block_tables.shape[0] >= B, "table shapes")
-    _need(cu_q_lens is None or (cu_q_lens.dtype == torch.int32 and cu_q_lens.shape[0] == B + 1), "cu_q_lens")
-    _need(out is None or (out.shape == q.shape and out.dtype == q.dtype), "out shape/dtype")
-    _need(False, "alibi_slopes: float32 [num_q_heads]")
+    if (dev >= 0 and _cuda_device() == dev and k_cache.get_device() == dev and v_cache.get_device() == dev
+            and block_tables.get_device() == dev and seq_lens.get_device() == dev
+            and block_tables.dtype == _I32T and seq_lens.dtype == _I32T and seq_lens.numel() == B
+            and block_tables.dim() == 2 and block_tables.shape[0] >= B
+            and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and block_tables.is_contiguous() and seq_lens.is_contiguous()
+            and (q.dtype == _F16 or q.dtype == _BF16)
+            and (out is None or (out.get_device() == dev and out.shape == q.shape and out.dtype == q.dtype
+                                 and out.is_contiguous()))
+            and (cu_q_lens is None or (cu_q_lens.get_device() == dev and cu_q_lens.dtype == _I32T
+                                       and cu_q_lens.shape[0] == B + 1 and cu_q_lens.is_contiguous()))
+            and (alibi_slopes is None or (alibi_slopes.get_device() == dev and alibi_slopes.dtype == _F32
+                                          and alibi_slopes.numel() == q.shape[1] and alibi_slopes.is_contiguous()))
+            and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous()))):
+        return dev
+    _cuda(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, alibi_slopes, out, workspace)
+    _refuse("paged attention",
+            (_current(dev, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, alibi_slopes, out, workspace),
+             "tensors must be on the current CUDA device"),
+            (q.dtype in _DTYPES, f"unsupported dtype {q.dtype}"),
+            (block_tables.dtype == _I32T and seq_lens.dtype == _I32T, "int32 tables"),
+            (seq_lens.numel() == B and block_tables.dim() == 2 and block_tables.shape[0] >= B, "table shapes"),
+            (cu_q_lens is None or (cu_q_lens.dtype == _I32T and cu_q_lens.shape[0] == B + 1), "cu_q_lens"),
+            (out is None or (out.shape == q.shape and out.dtype == q.dtype), "out shape/dtype"),
+            (False, "alibi_slopes: float32 [num_q_heads]"))
 
 
 def _pool16(q, k_cache, v_cache):
@@ -657,7 +690,7 @@ def paged_attention_decode_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     `decode_partition_for`."""
     B, Hq, D = q.shape
     NB, Hkv = _fp4_pool(k_cache, v_cache, D)
-    _attn_args(q, k_cache, v_cache, block_tables, seq_lens, None, None, out, workspace)
+    dev = _attn_args(q, k_cache, v_cache, block_tables, seq_lens, None, None, out, workspace)
     if max_seq_len is None:
         max_seq_len = int(seq_lens.max().item()) if B else 0
     if out is None:
@@ -669,7 +702,8 @@ def paged_attention_decode_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     rc = lib.pa_paged_attention_decode_fp4(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         block_tables.shape[1], seq_lens.data_ptr(), B, max_seq_len, NB, scale, k_scale, v_scale, Hq, Hkv, D,
-        PA_BLOCK_SIZE, partition_size, workspace.data_ptr(), ws_bytes, _dt(q), _stream(stream))
+        PA_BLOCK_SIZE, partition_size, workspace.data_ptr(), ws_bytes, 0 if q.dtype == _F16 else 1,
+        _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(rc, "pa_paged_attention_decode_fp4")
     return out
@@ -685,7 +719,7 @@ def paged_attention_prefill_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
     as in `paged_attention_prefill_fp8`."""
     T, Hq, D = q.shape
     NB, Hkv = _fp4_pool(k_cache, v_cache, D)
-    _attn_args(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, None, out, workspace)
+    dev = _attn_args(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, None, out, workspace)
     B = seq_lens.shape[0]
     if out is None:
         out = torch.empty_like(q)
@@ -701,7 +735,8 @@ def paged_attention_prefill_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
     rc = lib.pa_paged_attention_prefill_fp4(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), max_blocks,
         seq_lens.data_ptr(), cu_q_lens.data_ptr(), B, T, max_q_len, max_seq_len, NB, scale, k_scale, v_scale, Hq, Hkv,
-        D, PA_BLOCK_SIZE, workspace.data_ptr(), ws_bytes, _dt(q), _stream(stream))
+        D, PA_BLOCK_SIZE, workspace.data_ptr(), ws_bytes, 0 if q.dtype == _F16 else 1,
+        _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(rc, "pa_paged_attention_prefill_fp4")
     return out
@@ -723,7 +758,7 @@ def paged_attention_decode_mod(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     of `decode_partition_for`."""
     B, Hq, D = q.shape
     NB, bs, Hkv = _pool16(q, k_cache, v_cache)
-    _attn_args(q, k_cache, v_cache, block_tables, seq_lens, None, alibi_slopes, out, workspace)
+    dev = _attn_args(q, k_cache, v_cache, block_tables, seq_lens, None, alibi_slopes, out, workspace)
     if max_seq_len is None:
         max_seq_len = int(seq_lens.max().item()) if B else 0
     if out is None:
@@ -735,7 +770,8 @@ def paged_attention_decode_mod(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     rc = lib.pa_paged_attention_decode_mod(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         block_tables.shape[1], seq_lens.data_ptr(), B, max_seq_len, NB, scale, softcap, window, _ptr(alibi_slopes),
-        Hq, Hkv, D, bs, partition_size, workspace.data_ptr(), ws_bytes, _dt(q), _stream(stream))
+        Hq, Hkv, D, bs, partition_size, workspace.data_ptr(), ws_bytes, 0 if q.dtype == _F16 else 1,
+        _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(rc, "pa_paged_attention_decode_mod")
     return out
@@ -751,7 +787,7 @@ def paged_attention_prefill_mod(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
     modified scores, as `paged_attention_decode_mod`."""
     T, Hq, D = q.shape
     NB, bs, Hkv = _pool16(q, k_cache, v_cache)
-    _attn_args(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, alibi_slopes, out, workspace)
+    dev = _attn_args(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, alibi_slopes, out, workspace)
     B = seq_lens.shape[0]
     if out is None:
         out = torch.empty_like(q)
@@ -760,7 +796,8 @@ def paged_attention_prefill_mod(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
     rc = lib.pa_paged_attention_prefill_mod(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         block_tables.shape[1], seq_lens.data_ptr(), cu_q_lens.data_ptr(), B, T, max_q_len, max_seq_len, NB, scale,
-        softcap, window, _ptr(alibi_slopes), Hq, Hkv, D, bs, workspace.data_ptr(), ws_bytes, _dt(q), _stream(stream))
+        softcap, window, _ptr(alibi_slopes), Hq, Hkv, D, bs, workspace.data_ptr(), ws_bytes, 0 if q.dtype == _F16 else 1,
+        _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(rc, "pa_paged_attention_prefill_mod")
     return out

@@ -13,13 +13,14 @@
 //
 // Bound: HBM.  Every q, k and v value is read once and written once, with six
 // operations per pair between; the table rows (512 bytes per token at head_dim
-// 128) are shared by a token's heads.  One CTA owns one token (or a share of
-// its head rows when there are few tokens); eight threads of 16 dims share a
-// head row at head_dim 128.  Measured at 8192 tokens, 32/8 heads of 128, bf16:
-// 35 us for 206 MB (5.8 TB/s, 0.86 of the measured copy rate).  Several rows'
-// loads at once cost occupancy and were slower (two rows 36.2 us, four 40.3),
-// as were 64 or 256 threads (36.2, 43.7) and one row per thread with more CTAs
-// (37.5); reading a row only after its position and table row took 37.2.
+// 128) are shared by a token's heads.  A CTA takes one token at a time (or a
+// share of its head rows when there are few tokens), as many CTAs as are
+// resident stride over the tokens; eight threads of 16 dims share a head row
+// at head_dim 128.  Measured at 8192 tokens, 32/8 heads of 128, bf16: 35 us for
+// 206 MB (5.9 TB/s, 0.87 of the measured copy rate); one CTA per token 37 us.
+// Several rows' loads at once cost occupancy and were slower (two rows 36.2
+// us, four 40.3), as were 64 or 256 threads (36.2, 43.7); the next row's loads
+// in flight during this one's stores: 35.1.
 #include <algorithm>
 
 #include "pa_fp4.cuh"
@@ -258,10 +259,9 @@ cudaError_t launch_append(const AppendParams& p, int head_dim, int dtype, int ca
     const int rows = p.num_q_heads + 2 * p.num_kv_heads;
     const int per_pass = kAppendThreads / (head_dim / 16);
     const int passes = (rows + per_pass - 1) / per_pass;
-    const int gx = std::min(p.num_tokens, 1 << 20);
+    const int gx = std::min(p.num_tokens, 8 * sm_count());   // as many CTAs as are resident
     // few tokens: a token's head rows are shared out over CTAs
-    const int want = 8 * sm_count();
-    const int gy = std::max(1, std::min(passes, want / gx));
+    const int gy = std::max(1, std::min(passes, 8 * sm_count() / gx));
     const dim3 grid(gx, gy);
     if (dtype == 0) {
         if (head_dim == 128) append_t<__half, 128>(p, cache, grid, s);
