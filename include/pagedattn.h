@@ -430,7 +430,9 @@ int pa_paged_kv_unpack_fp4(void* k_out, void* v_out, const void* k_cache, const 
 
 /* Decode attention over a 4-bit cache: as pa_paged_attention_decode, with k_t
  * and v_t the values above; q and out keep `dtype`; the workspace is sized by
- * pa_decode_workspace_bytes. */
+ * pa_decode_workspace_bytes.  This call and those below refuse sizes of more
+ * than 2^30 work items (num_seqs * partitions of max_seq_len * num_kv_heads *
+ * chunks of 8 or 16 columns). */
 int pa_paged_attention_decode_fp4(void* out, const void* q, const void* k_cache, const void* v_cache,
                                   const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
                                   int num_seqs, int max_seq_len, int num_blocks, float scale, float k_scale,

@@ -605,7 +605,7 @@ def paged_kv_write_fp4(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Te
                 (False, "slot_mapping: int64 [num_tokens]"))
     rc = (_lib or load_library()).pa_paged_kv_write_fp4(
         key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), T, NB, H,
-        D, PA_BLOCK_SIZE, 0 if dtype == _F16 else 1, k_scale, v_scale,
+        D, PA_BLOCK_SIZE, 0 if dtype == _F16 else 1, float(k_scale), float(v_scale),
         _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(rc, "pa_paged_kv_write_fp4")
@@ -627,8 +627,8 @@ def paged_kv_unpack_fp4(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: f
     k_out = torch.empty((NB, PA_BLOCK_SIZE, H, D), dtype=dtype, device=k_cache.device)
     v_out = torch.empty_like(k_out)
     rc = (_lib or load_library()).pa_paged_kv_unpack_fp4(
-        k_out.data_ptr(), v_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), NB, H, D, PA_BLOCK_SIZE, k_scale,
-        v_scale, 0 if dtype == _F16 else 1, _raw_stream(dev) if stream is None else _stream(stream))
+        k_out.data_ptr(), v_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), NB, H, D, PA_BLOCK_SIZE,
+        float(k_scale), float(v_scale), 0 if dtype == _F16 else 1, _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(rc, "pa_paged_kv_unpack_fp4")
     return k_out, v_out
@@ -701,7 +701,8 @@ def paged_attention_decode_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     workspace, ws_bytes = _ws(lib.pa_decode_workspace_bytes(B, Hq, D, max_seq_len, partition_size), q, workspace)
     rc = lib.pa_paged_attention_decode_fp4(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-        block_tables.shape[1], seq_lens.data_ptr(), B, max_seq_len, NB, scale, k_scale, v_scale, Hq, Hkv, D,
+        block_tables.shape[1], seq_lens.data_ptr(), B, max_seq_len, NB, float(scale), float(k_scale),
+        float(v_scale), Hq, Hkv, D,
         PA_BLOCK_SIZE, partition_size, workspace.data_ptr(), ws_bytes, 0 if q.dtype == _F16 else 1,
         _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
@@ -734,8 +735,8 @@ def paged_attention_prefill_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
     workspace, ws_bytes = _ws(nbytes, q, workspace)
     rc = lib.pa_paged_attention_prefill_fp4(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), max_blocks,
-        seq_lens.data_ptr(), cu_q_lens.data_ptr(), B, T, max_q_len, max_seq_len, NB, scale, k_scale, v_scale, Hq, Hkv,
-        D, PA_BLOCK_SIZE, workspace.data_ptr(), ws_bytes, 0 if q.dtype == _F16 else 1,
+        seq_lens.data_ptr(), cu_q_lens.data_ptr(), B, T, max_q_len, max_seq_len, NB, float(scale),
+        float(k_scale), float(v_scale), Hq, Hkv, D, PA_BLOCK_SIZE, workspace.data_ptr(), ws_bytes, 0 if q.dtype == _F16 else 1,
         _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(rc, "pa_paged_attention_prefill_fp4")
@@ -769,8 +770,8 @@ def paged_attention_decode_mod(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     workspace, ws_bytes = _ws(lib.pa_decode_workspace_bytes(B, Hq, D, max_seq_len, partition_size), q, workspace)
     rc = lib.pa_paged_attention_decode_mod(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-        block_tables.shape[1], seq_lens.data_ptr(), B, max_seq_len, NB, scale, softcap, window, _ptr(alibi_slopes),
-        Hq, Hkv, D, bs, partition_size, workspace.data_ptr(), ws_bytes, 0 if q.dtype == _F16 else 1,
+        block_tables.shape[1], seq_lens.data_ptr(), B, max_seq_len, NB, float(scale), float(softcap), int(window),
+        _ptr(alibi_slopes), Hq, Hkv, D, bs, partition_size, workspace.data_ptr(), ws_bytes, 0 if q.dtype == _F16 else 1,
         _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(rc, "pa_paged_attention_decode_mod")
@@ -795,8 +796,8 @@ def paged_attention_prefill_mod(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
     workspace, ws_bytes = _ws(lib.pa_prefill_mod_workspace_bytes(B, T, Hq, Hkv, D, max_seq_len), q, workspace)
     rc = lib.pa_paged_attention_prefill_mod(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-        block_tables.shape[1], seq_lens.data_ptr(), cu_q_lens.data_ptr(), B, T, max_q_len, max_seq_len, NB, scale,
-        softcap, window, _ptr(alibi_slopes), Hq, Hkv, D, bs, workspace.data_ptr(), ws_bytes, 0 if q.dtype == _F16 else 1,
+        block_tables.shape[1], seq_lens.data_ptr(), cu_q_lens.data_ptr(), B, T, max_q_len, max_seq_len, NB, float(scale),
+        float(softcap), int(window), _ptr(alibi_slopes), Hq, Hkv, D, bs, workspace.data_ptr(), ws_bytes, 0 if q.dtype == _F16 else 1,
         _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(rc, "pa_paged_attention_prefill_mod")

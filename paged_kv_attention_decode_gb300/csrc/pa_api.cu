@@ -342,6 +342,15 @@ static int decode_prepare(DecodeCall& c, void* out, const void* q, const void* k
     const int part = effective_partition(max_seq_len, partition_size);
     const int parts = parts_for(max_seq_len, part);
     if (parts > 65535) return PA_ERR_INVALID_ARG;   // partition index is a 16-bit field of the work list
+    // (query, head) columns per work item: 8, or 16 once a row can have more
+    // (8 over a 4-bit cache)
+    const int cols = max_q * (num_q_heads / num_kv_heads);
+    const int chunk = cols > 8 && cache != Cache::kFp4 ? 16 : 8;
+    const int col_chunks = (cols + chunk - 1) / chunk;
+    // the kernels count work items in 32 bits
+    if ((mod || cache == Cache::kFp4) &&
+        static_cast<long long>(num_seqs) * parts * num_kv_heads * col_chunks > (1LL << 30))
+        return PA_ERR_INVALID_ARG;
     const size_t need = decode_ws_bytes(num_seqs, max_rows, num_q_heads, head_dim, parts);
     if (!workspace || workspace_bytes < need) return PA_ERR_WORKSPACE_TOO_SMALL;
     if (!aligned256(workspace)) return PA_ERR_INVALID_ARG;
@@ -375,11 +384,7 @@ static int decode_prepare(DecodeCall& c, void* out, const void* q, const void* k
     p.max_q = max_q;
     p.max_rows = max_rows;
     p.num_rows = num_rows;
-    // (query, head) columns per work item: 8, or 16 once a row can have more
-    // (8 over a 4-bit cache)
-    const int cols = max_q * p.group;
-    const int chunk = cols > 8 && cache != Cache::kFp4 ? 16 : 8;
-    p.col_chunks = (cols + chunk - 1) / chunk;
+    p.col_chunks = col_chunks;
     p.scale_log2 = scale_log2(scale) * k_scale;
     p.v_scale = v_scale;
     p.k_pool = k_cache;

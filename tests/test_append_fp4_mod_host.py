@@ -121,6 +121,11 @@ def test_decode_partition_argument(lib):
     assert call(lib, "decode", "mod", part=-16) == INVALID
 
 
+@pytest.mark.parametrize("cache", ["fp4", "mod"])
+def test_too_many_work_items_are_refused(lib, cache):
+    assert call(lib, "decode", cache, B=60000, ml=1000000, part=64, hq=16, hkv=16) == INVALID
+
+
 def test_partition_for(lib):
     assert pa.decode_partition_for(64, 32, 32, 4096) == 512       # plenty of items
     assert pa.decode_partition_for(8, 64, 8, 131072) == 2048      # exactly 4096 items
