@@ -742,6 +742,10 @@ static int prefill_impl(void* out, const void* q, const void* k_cache, const voi
                         int num_blocks, float scale, int num_q_heads, int num_kv_heads, int head_dim,
                         void* workspace, size_t workspace_bytes, int dtype, cudaStream_t s, Cache cache,
                         float k_scale, float v_scale, const pa::ScoreMod* mod = nullptr) {
+    // the chunks' work items are counted in 32 bits
+    if ((mod || cache == Cache::kFp4) &&
+        (static_cast<long long>(num_tokens) / 4 + num_seqs) * num_kv_heads > (1LL << 30))
+        return PA_ERR_INVALID_ARG;
     const size_t pb = plan_bytes(num_seqs, num_tokens);
     // partitions of the decode and verify rows
     const int part = mod || cache == Cache::kFp4

@@ -124,6 +124,7 @@ def test_decode_partition_argument(lib):
 @pytest.mark.parametrize("cache", ["fp4", "mod"])
 def test_too_many_work_items_are_refused(lib, cache):
     assert call(lib, "decode", cache, B=60000, ml=1000000, part=64, hq=16, hkv=16) == INVALID
+    assert call(lib, "prefill", cache, T=2 ** 31 - 1, hq=16, hkv=16, mq=2048) == INVALID
 
 
 def test_partition_for(lib):

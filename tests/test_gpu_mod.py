@@ -193,3 +193,33 @@ def test_large_window_context():
     out = run(q, pools, tables, lens, qlens, 0.125, False, **m)
     check(out, q, pools, tables, lens, qlens, 0.125, **m)
     assert pa.device_error() == 0
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,chunks", [
+    (32, 8, 64, [(1600, 1536)]),                 # 192 items: 40 in the last round of 152
+    (32, 8, 128, [(1000, 640), (640, 640)]),     # 160 items: 8 in the last round
+    (10, 2, 64, [(2048, 2048), (900, 41)]),      # tiles of 25 queries of 5 heads; 84 items: one round
+    (4, 2, 64, [(5000, 4900), (4900, 4900), (333, 130)]),   # 156 items of two heads, a pair of one tile among them
+])
+def test_windowed_chunks_of_several_rounds(Hq, Hkv, D, chunks):
+    """More work items than SMs: every row is written, and a sample of them
+    agrees with one-token calls over the same keys."""
+    lens, qlens = zip(*chunks)
+    for m in (dict(window=150), dict(window=90, softcap=15.0)):
+        q, pools, tables = build(lens, qlens, Hq, Hkv, D, torch.bfloat16, seed=D + Hq, window=m["window"])
+        out = torch.full_like(q, float("nan")).to(DEV)
+        run(q, pools, tables, list(lens), qlens, 0.1, False, out=out, **m)
+        assert torch.all(torch.isfinite(out))
+        # a decode call per sampled row (its own kernel) sees the same keys
+        rows, at = [], 0
+        for b, (n, c) in enumerate(chunks):
+            rows += [(b, at + i, n - c + i + 1) for i in range(0, c, 37)]
+            rows.append((b, at + c - 1, n))
+            at += c
+        sel = torch.tensor([r for _, r, _ in rows])
+        sl = [n for _, _, n in rows]
+        one = run(q[sel], pools, tables[[b for b, _, _ in rows]], sl, [1] * len(rows), 0.1, True, **m)
+        got, ref = out[sel.to(DEV)].float(), one.float()
+        # each kernel rounds its weights to bf16 (2^-8 of sum p |v| <= 2) and its result (2^-8 of it)
+        assert torch.all((got - ref).abs() <= 2.0 ** -6 * ref.abs() + 2.0 ** -6)
+        assert pa.device_error() == 0
