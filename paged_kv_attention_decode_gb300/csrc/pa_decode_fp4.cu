@@ -635,6 +635,7 @@ __global__ void __launch_bounds__(kWidenFp4Threads) widen_chunk_blocks_fp4_kerne
                                                                                   int max_blocks, int num_kv_heads) {
     using Tile = Fp4Tile<D>;
     constexpr int kUnroll = 4;
+    pdl_wait();   // the plan (no early trigger, as in the FP8 kernel)
     const int nchunks = c.hdr[0];
     const int used = min(c.hdr[1], c.cap_blocks);
     const int groups = num_kv_heads * 16 * Tile::kGroups;    // groups per block and pool
@@ -714,15 +715,13 @@ cudaError_t launch_decode_fp4(const DecodeParams& p, int head_dim, int dtype, cu
 cudaError_t launch_widen_fp4(const Fp8Copy& c, const int32_t* seq_lens, int max_blocks, int num_kv_heads, int head_dim,
                              int dtype, cudaStream_t s) {
     const dim3 grid(std::max(1, std::min(c.cap_blocks, 8 * sm_count())), 2);   // K and V
-    auto go = [&](auto kern) { kern<<<grid, kWidenFp4Threads, 0, s>>>(c, seq_lens, max_blocks, num_kv_heads); };
-    if (dtype == 0) {
-        if (head_dim == 128) go(widen_chunk_blocks_fp4_kernel<__half, 128>);
-        else go(widen_chunk_blocks_fp4_kernel<__half, 64>);
-    } else {
-        if (head_dim == 128) go(widen_chunk_blocks_fp4_kernel<__nv_bfloat16, 128>);
-        else go(widen_chunk_blocks_fp4_kernel<__nv_bfloat16, 64>);
-    }
-    return cudaGetLastError();
+    auto go = [&](auto kern) {
+        return launch_pdl(kern, grid, dim3(kWidenFp4Threads), 0, s, c, seq_lens, max_blocks, num_kv_heads);
+    };
+    if (dtype == 0)
+        return head_dim == 128 ? go(widen_chunk_blocks_fp4_kernel<__half, 128>) : go(widen_chunk_blocks_fp4_kernel<__half, 64>);
+    return head_dim == 128 ? go(widen_chunk_blocks_fp4_kernel<__nv_bfloat16, 128>)
+                           : go(widen_chunk_blocks_fp4_kernel<__nv_bfloat16, 64>);
 }
 
 }  // namespace pa

@@ -342,6 +342,10 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
     int32_t* order = offsets + num_seqs + 1;
     int32_t* seq_of_pair = order + pair_cap;
     const int tid = threadIdx.x;
+    // the next kernel may be scheduled; it waits for this grid (the launches of
+    // a varlen call chained like this, and the plans side by side, take 3 to 8
+    // us less than one after another)
+    pdl_trigger();
     if (tid == 0) {
         carry = blk_carry = chunk_carry = blk_end = 0;
         chunk_cost = row_cost = 0;
@@ -450,6 +454,11 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
         const int pr = pair_at(l, n, ql);
         order[atomicAdd(&hist[bucket(n, ql, pr)], 1)] = l;
     }
+    // This kernel runs beside the decode plan, which it was launched after
+    // (each writes its own part of the workspace, and the decode plan starts
+    // only when all earlier work on the stream is complete).  Having waited
+    // for it here, this grid's completion is also the decode plan's.
+    pdl_wait();
 }
 
 // FP8 (E4M3) cache: the blocks of the chunks the plan listed, widened to
@@ -467,6 +476,10 @@ __global__ void __launch_bounds__(kWidenThreads) widen_chunk_blocks_kernel(const
                                                                            const int32_t* __restrict__ seq_lens,
                                                                            int max_blocks, int num_kv_heads) {
     constexpr int D = 128;
+    // the plan.  No early trigger: attention CTAs placed while this grid drains
+    // share the SMs unevenly with the decode kernel (a 4-bit step of four chunks
+    // and 60 rows took 336 us instead of 308).
+    pdl_wait();
     const int nchunks = c.hdr[0];
     const int used = min(c.hdr[1], c.cap_blocks);
     const int runs = num_kv_heads * 16 * (D / 16);   // 16-code runs per block and pool
@@ -521,7 +534,7 @@ __global__ void __launch_bounds__(kWidenThreads) widen_chunk_blocks_kernel(const
 // their keys are masked and their V rows cleared.
 template <typename T, int D, int kMode>
 __global__ void __launch_bounds__(kTcThreads, 1)
-    prefill_tc_kernel(const PrefillParams p, const int32_t* __restrict__ plan,
+    prefill_tc_kernel(const PrefillParams p, const int32_t* plan,
                       const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                       const __grid_constant__ CUtensorMap qmap) {
     using Sh = TcShape<D>;
@@ -561,9 +574,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int lane = tid & 31;
     const int G = p.group;
     const int QT = p.q_per_tile;  // 128 / G
-    // a decode kernel launched after this one may start now (it reads
-    // nothing this kernel writes); when it has work, only overlap_ctas CTAs
-    // stay, so that it gets the other SMs
+    // the plans, and the chunks' 16-bit copy; then a decode kernel launched
+    // after this one may start (it reads the decode plan and nothing that this
+    // kernel writes); when it has work, only overlap_ctas CTAs stay, so that
+    // it gets the other SMs
+    pdl_wait();
     pdl_trigger();
     int ctas = static_cast<int>(gridDim.x);
     // Alone on the GPU, the CTAs take the items in the cost-sorted snake order
@@ -1195,10 +1210,9 @@ cudaError_t launch_t(const PrefillParams& p, int32_t* plan, const CUtensorMap& k
     }();
     if (launch_regs < kTcLaunchRegs) return cudaErrorInvalidConfiguration;
     const Fp8Copy none{};
-    prefill_plan_kernel<<<1, 1024, 0, s>>>(p.cu_q_lens, p.seq_lens, p.num_seqs, num_tokens, p.q_per_tile, plan,
-                                           p.pair_cap, p.err, copy ? *copy : none, p.max_seq_len, p.max_blocks,
-                                           p.mod.window, p.split, sm_count(), p.decode_weight);
-    e = cudaGetLastError();
+    e = launch_pdl(prefill_plan_kernel, dim3(1), dim3(1024), 0, s, p.cu_q_lens, p.seq_lens, p.num_seqs, num_tokens,
+                   p.q_per_tile, plan, p.pair_cap, p.err, copy ? *copy : none, p.max_seq_len, p.max_blocks,
+                   p.mod.window, p.split, sm_count(), p.decode_weight);
     if (e != cudaSuccess) return e;
     if (copy && copy->fp4) {
         e = launch_widen_fp4(*copy, p.seq_lens, p.max_blocks, p.num_kv_heads, D, std::is_same<T, __half>::value ? 0 : 1,
@@ -1207,9 +1221,8 @@ cudaError_t launch_t(const PrefillParams& p, int32_t* plan, const CUtensorMap& k
     } else if (copy && copy->cap_blocks > 0) {
         // a few CTAs per SM stream the copy blocks (at most cap_blocks of them)
         const int wgrid = std::max(1, std::min(copy->cap_blocks, 8 * sm_count()));
-        widen_chunk_blocks_kernel<T><<<wgrid, kWidenThreads, 0, s>>>(*copy, p.seq_lens, p.max_blocks,
-                                                                     p.num_kv_heads);
-        e = cudaGetLastError();
+        e = launch_pdl(widen_chunk_blocks_kernel<T>, dim3(wgrid), dim3(kWidenThreads), 0, s, *copy, p.seq_lens,
+                       p.max_blocks, p.num_kv_heads);
         if (e != cudaSuccess) return e;
     }
     // upper bound on the work items: each listed chunk (length > 8) has at
@@ -1220,8 +1233,7 @@ cudaError_t launch_t(const PrefillParams& p, int32_t* plan, const CUtensorMap& k
                                                           ((max_q_len + p.q_per_tile - 1) / p.q_per_tile));
     const long long items = (bound_tiles + p.num_seqs) / kTcTiles * p.num_kv_heads + p.num_kv_heads;
     const int grid = static_cast<int>(std::max<long long>(1, std::min<long long>(items, sm_count())));
-    kern<<<grid, kTcThreads, smem, s>>>(p, plan, kmap, vmap, qmap);
-    return cudaGetLastError();
+    return launch_pdl(kern, dim3(grid), dim3(kTcThreads), smem, s, p, plan, kmap, vmap, qmap);
 }
 
 }  // namespace

@@ -221,3 +221,50 @@ def test_pool_past_4_gib():
     got, gs = R.unpack_tiles(big[0][-1:].cpu().numpy(), False)
     assert np.array_equal(got[0, 15], c[0]) and np.array_equal(gs[0, 15], s[0])
     assert pa.device_error() == 0
+
+
+def test_steps_back_to_back_on_one_workspace():
+    """Steps that differ in their chunks, queued on one workspace without a
+    pause and replayed from a graph: each gives what it gives alone, bit for
+    bit (the plans of a step may only start once the step before is done)."""
+    Hq, Hkv, D = 8, 2, 128
+    steps = []
+    for i, (lens, qlens) in enumerate((([700, 40, 333], [600, 9, 1]), ([64, 900, 17, 1000], [1, 4, 17, 1]),
+                                       ([1500, 1500], [1400, 1]))):
+        q, pools, tables = build(lens, qlens, Hq, Hkv, D, torch.bfloat16, seed=90 + i)
+        cu = np.concatenate([[0], np.cumsum(qlens)]).astype(np.int32)
+        steps.append(put(q, *pools, tables, np.asarray(lens, np.int32), cu) + [max(qlens), max(lens), sum(lens)])
+    need = max(pa.prefill_fp4_workspace_bytes(s[4].numel(), s[0].shape[0], Hq, Hkv, D, s[7], s[3].shape[1],
+                                              s[8]) for s in steps)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+
+    def go(s, out):
+        pa.paged_attention_prefill_fp4(*s[:6], 0.1, KS, VS, s[6], s[7], out=out, workspace=ws,
+                                       chunk_kv_tokens=s[8])
+
+    alone = []
+    for s in steps:
+        o = torch.empty_like(s[0])
+        go(s, o)
+        torch.cuda.synchronize()
+        alone.append(o)
+    outs = [[torch.full_like(s[0], float("nan")) for s in steps] for _ in range(8)]
+    for row in outs:
+        for s, o in zip(steps, row):
+            go(s, o)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, a) for row in outs for o, a in zip(row, alone))
+    for row in outs:
+        for o in row:
+            o.fill_(float("nan"))
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        for row in outs:
+            for s, o in zip(steps, row):
+                go(s, o)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, a) for row in outs for o, a in zip(row, alone))
+    assert pa.device_error() == 0
