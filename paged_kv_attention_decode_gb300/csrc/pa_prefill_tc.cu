@@ -366,6 +366,15 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
         const int tiles = ql > PA_VERIFY_MAX_Q_ ? (ql + q_per_tile - 1) / q_per_tile : 0;
         return (tiles + kTcTiles - 1) / kTcTiles;
     };
+    // one addition per warp (every thread of it calls): 64-bit additions to
+    // one address of shared memory go one lane after another, and one per pair
+    // made a step of four chunks of 1536 take 305 us instead of 294
+    auto add_cost = [&](unsigned long long* sum, int v) {
+        unsigned long long c = static_cast<unsigned long long>(v);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) c += __shfl_xor_sync(kFullMask, c, off);
+        if ((tid & 31) == 0 && c) atomicAdd(sum, c);
+    };
     auto bucket = [&](int n, int ql, int pr) {
         // a malformed sequence (skipped by the kernel) goes to class 0
         const int c = (n >= ql && ql > 0) ? pair_key_tiles(n, ql, q_per_tile, pr, window) : 0;
@@ -395,8 +404,10 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
                 atomicMax(&blk_end, first + nb);
             }
         }
-        if (split && b < num_seqs && n >= ql && n <= max_seq_len && ql > 0 && ql <= PA_VERIFY_MAX_Q_)
-            atomicAdd(&row_cost, static_cast<unsigned long long>(n - window_start(n - ql, window)));
+        if (split) {
+            const bool row = b < num_seqs && n >= ql && n <= max_seq_len && ql > 0 && ql <= PA_VERIFY_MAX_Q_;
+            add_cost(&row_cost, row ? n - window_start(n - ql, window) : 0);
+        }
         const int start = block_exclusive_scan_1024(v, warp_tot, &carry);
         if (b < num_seqs) {
             offsets[b] = start;
@@ -416,12 +427,18 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
     };
     if (tid == 0) offsets[num_seqs] = total;
     __syncthreads();
-    for (int l = tid; l < total; l += 1024) {
-        int n, ql;
-        const int pr = pair_at(l, n, ql);
-        const int k = bucket(n, ql, pr);
-        atomicAdd(&hist[k], 1);
-        if (split) atomicAdd(&chunk_cost, static_cast<unsigned long long>(kPlanBuckets - 1 - k));
+    int first_class = 0;   // of pair tid
+    for (int base = 0; base < total; base += 1024) {
+        const int l = base + tid;
+        int k = kPlanBuckets - 1;
+        if (l < total) {
+            int n, ql;
+            const int pr = pair_at(l, n, ql);
+            k = bucket(n, ql, pr);
+            atomicAdd(&hist[k], 1);
+            if (base == 0) first_class = k;
+        }
+        if (split) add_cost(&chunk_cost, kPlanBuckets - 1 - k);
     }
     __syncthreads();
     if (tid == 0) {
@@ -450,9 +467,13 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
     __syncthreads();
     // scatter each pair's global index to its class
     for (int l = tid; l < total; l += 1024) {
-        int n, ql;
-        const int pr = pair_at(l, n, ql);
-        order[atomicAdd(&hist[bucket(n, ql, pr)], 1)] = l;
+        int k = first_class;
+        if (l >= 1024) {
+            int n, ql;
+            const int pr = pair_at(l, n, ql);
+            k = bucket(n, ql, pr);
+        }
+        order[atomicAdd(&hist[k], 1)] = l;
     }
     // This kernel runs beside the decode plan, which it was launched after
     // (each writes its own part of the workspace, and the decode plan starts
