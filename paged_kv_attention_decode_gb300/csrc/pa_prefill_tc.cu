@@ -229,6 +229,11 @@ __device__ __forceinline__ void mulp(float& x, float& y, float u, float v) {
         : "f"(u), "f"(v));
 }
 
+// A word with the bits above bit i set (i may be any integer).
+__device__ __forceinline__ uint32_t bits_above(int i) {
+    return i >= 31 ? 0u : i < 0 ? 0xffffffffu : 0xfffffffeu << i;
+}
+
 // The largest of a row's 128 values: four chains of three-input maxima.
 __device__ __forceinline__ float row_max(const float (&sv)[kTcKeys]) {
     float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -850,12 +855,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         // hidden keys' is +inf); a biased one is finished here.
                         float mul = fold ? p.scale_log2 : 1.f, off = 0.f;
                         float x_max = 0.f;
-                        auto hide = [&](float v) {   // hidden keys get v
+                        // Hidden keys get v, from one bit per key (windowed and
+                        // capped chunks 277 -> 249 us, windowed ones 180 -> 167,
+                        // against comparing every key's position).
+                        auto hide = [&](float v) {
 #pragma unroll
-                            for (int c = 0; c < kTcKeys; ++c) {
-                                const bool dead = key0 + c > pos_row || (kMod && key0 + c < lo_row) ||
-                                                  ((bad >> (c >> 4)) & 1u);
-                                sv[c] = dead ? v : sv[c];
+                            for (int w = 0; w < kTcKeys / 32; ++w) {
+                                const int hi = pos_row - key0 - 32 * w, lo = lo_row - key0 - 32 * w;
+                                uint32_t dead = bits_above(hi);
+                                if constexpr (kMod) dead |= ~bits_above(lo - 1);
+                                dead |= (bad >> (2 * w) & 1u ? 0xffffu : 0u) | (bad >> (2 * w + 1) & 1u ? 0xffff0000u : 0u);
+#pragma unroll
+                                for (int c = 0; c < 32; ++c)
+                                    sv[32 * w + c] = (dead >> c) & 1u ? v : sv[32 * w + c];
                             }
                         };
                         if constexpr (kMode == kCapped || kMode == kBiased) {
