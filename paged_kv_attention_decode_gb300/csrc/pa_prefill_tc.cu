@@ -183,6 +183,13 @@ __device__ __forceinline__ void fma2(float& x, float& y, float s, float a) {
         : "f"(s), "f"(a));
 }
 
+__device__ __forceinline__ void fma2(float& x, float& y, float s, float a, float b) {   // (x * s + a, y * s + b)
+    asm("{\n\t.reg .b64 p, q, r, d;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\t"
+        "mov.b64 r, {%3, %4};\n\tfma.rn.f32x2 d, p, q, r;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(s), "f"(a), "f"(b));
+}
+
 // First key that the query at `pos` sees.
 __device__ __forceinline__ int window_start(int pos, int window) { return window > 0 ? max(0, pos - window + 1) : 0; }
 
@@ -889,8 +896,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 const float f = capped ? mul : p.scale_log2;
                                 const float b0 = fmaf(slope, static_cast<float>(key0 - pos_row), off);
 #pragma unroll
-                                for (int c = 0; c < kTcKeys; ++c)
-                                    sv[c] = fmaf(sv[c], f, fmaf(slope, static_cast<float>(c), b0));
+                                for (int c = 0; c < kTcKeys; c += 2) {
+                                    float u = static_cast<float>(c), v = static_cast<float>(c + 1);
+                                    fma2(u, v, slope, b0);
+                                    fma2(sv[c], sv[c + 1], f, u, v);
+                                }
                                 mul = 1.f;
                                 off = 0.f;
                             }
