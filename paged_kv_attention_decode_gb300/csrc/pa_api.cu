@@ -831,16 +831,16 @@ static int prefill_impl(void* out, const void* q, const void* k_cache, const voi
     p.overlap_ctas = std::max(1, copied ? pa::sm_count() * kOverlapPrefillNumFp8 / kOverlapPrefillDenFp8
                                      : pa::sm_count() * kOverlapPrefillNum / kOverlapPrefillDen);
     if (mod || cache == Cache::kFp4) {
-        // SMs shared by work: a key tile of a pair (two 128 x 128 tiles) takes
-        // 2.0 us of one SM at head_dim 128 (capped scores 2.6 us); a key of a
-        // short row is counted at an eighth of its own time (1.2 ns of 10 at 16
-        // bits, 0.5 ns of 5 at 4 bits), because the rows also run on the SMs
-        // that the chunks leave at their end, and because chunks on few SMs
-        // slow down beside a saturated memory.  Four chunks of 1536 beside 12,
-        // 60, 400, 2048 rows (us): 4-bit 282, 297, 462, 1335, with three times
-        // this weight 268, 304, 521, 1623, with nine times 279, 382, 974,
-        // 4018; 16-bit with a distance bias 323, 371, 770, 2818, with three
-        // times 334, 361, 747, 2963, with nine times 352, 469, 1593, 7403.
+        // SMs shared by work: a key tile of a pair (two 128 x 128 tiles) counts
+        // as 2.0 us of one SM (capped scores 2.6 us); a key of a short row is
+        // counted at an eighth of its own time (1.2 ns of 10 at 16 bits, 0.5 ns
+        // of 5 at 4 bits), because the rows also run on the SMs that the chunks
+        // leave at their end, and because chunks on few SMs slow down beside a
+        // saturated memory.  Four chunks of 1536 beside 12, 60, 400, 2048 rows
+        // (us): 4-bit 268, 291, 449, 1253; 16-bit with a distance bias 303,
+        // 355, 740, 2693, with half as much weight again 308, 350, 721, 2687
+        // (over other steps neither wins), with nine times as much, on earlier
+        // kernels that took 323, 371, 770, 2818: 352, 469, 1593, 7403.
         p.split = dc.p.split;
         p.decode_weight = (cache == Cache::kFp4 ? 0.5f : 1.2f) * dc.p.col_chunks / (mod && softcapped(*mod) ? 2600.f : 2000.f);
     }

@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(kWidenThreads) widen_chunk_blocks_kernel(const
 // without a cap or a window).  They are kernels of their own because the
 // softmax loop has to stay small: with all kinds in one kernel the instruction
 // fetch stalled it (windowed chunks took 255 us instead of 199, capped ones 341
-// instead of 329).  With a window a pair's key tiles
+// instead of 329, before hidden keys came from bits).  With a window a pair's key tiles
 // start at the tile of its first query's first key (tile index j0 + j); blocks
 // wholly before that key are not read (their table entries may be anything),
 // their keys are masked and their V rows cleared.
@@ -830,7 +830,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // second pass costs them more, and it would come often (a
                     // window's first tile may show a row only a few keys, which
                     // leaves its reference low).  Windowed chunks 191 us against
-                    // 236, capped ones 310 against 463.
+                    // 236, capped ones 310 against 463 (before hidden keys
+                    // came from bits).
                     bool need_max = kMod || __any_sync(kFullMask, m_ref == -INFINITY);
                     const bool masked = (key0 + kTcKeys - 1 > pos_lo) || bad || (kMod && key0 < lo_hi);
                     float sv[kTcKeys];
