@@ -94,4 +94,12 @@ __device__ __forceinline__ void group_values(uint32_t lo, uint32_t hi, uint8_t s
     }
 }
 
+// The same for 8 values of a group (one half's codes).
+__device__ __forceinline__ void half_group_values(uint32_t codes, uint8_t scale, uint32_t (&h)[4]) {
+    const uint32_t s2 = e4m3x2_to_f16x2(static_cast<uint16_t>(scale * 0x0101u));
+    e2m1x8_to_f16x2(codes, h);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = hmul2_bits(h[j], s2);
+}
+
 }  // namespace pa
