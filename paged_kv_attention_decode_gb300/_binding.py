@@ -301,18 +301,22 @@ def paged_attention_prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
 def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, pairs: torch.Tensor, stream=None) -> None:
     """In place: block pairs[i, 1] of both pools receives block pairs[i, 0]
     (the copy-on-write step; pairs is a device int32 [n, 2] tensor).  Pools of
-    any kind: 16-bit, FP8, or 4-bit tiles [NB, Hkv, bytes]."""
+    any kind: 16-bit [NB, 16, Hkv, D], FP8 [NB, Hkv, 16, D], or 4-bit tiles
+    [NB, Hkv, bytes]."""
     _cuda(k_cache, v_cache, pairs)
     _need(pairs.dtype == torch.int32 and pairs.dim() == 2 and pairs.shape[1] == 2, "pairs: int32 [n, 2]")
     _need(v_cache.shape == k_cache.shape and v_cache.dtype == k_cache.dtype, "cache shape/dtype")
+    shape, elem = k_cache.shape, k_cache.element_size()
+    NB = shape[0]
     if k_cache.dim() == 3:   # 4-bit tiles: 16 rows of codes and scales
-        NB, H, tile = k_cache.shape
-        _need(k_cache.element_size() == 1 and tile % 16 == 0, "4-bit pools: bytes [NB, Hkv, fp4_tile_bytes]")
-        D = tile // 16
-    else:
-        NB, bs, H, D = k_cache.shape
+        _need(elem == 1 and shape[2] % 16 == 0, "4-bit pools: bytes [NB, Hkv, fp4_tile_bytes]")
+        H, D = shape[1], shape[2] // 16
+    else:                    # 16 token rows, before the heads or (one-byte pools) after them
+        _need(k_cache.dim() == 4 and (shape[1] == PA_BLOCK_SIZE or (elem == 1 and shape[2] == PA_BLOCK_SIZE)),
+              "pools: [NB, 16, Hkv, D], or one-byte [NB, Hkv, 16, D]")
+        H, D = shape[1] * shape[2] // PA_BLOCK_SIZE, shape[3]
     rc = load_library().pa_copy_blocks(k_cache.data_ptr(), v_cache.data_ptr(), pairs.data_ptr(), pairs.shape[0],
-                                       NB, H, D, k_cache.element_size(), _stream(stream))
+                                       NB, H, D, elem, _stream(stream))
     _check(rc, "pa_copy_blocks")
 
 

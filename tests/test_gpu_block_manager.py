@@ -132,3 +132,20 @@ def test_manager_driven_steps():
     oracle.kv_write(bits(key), bits(val), kcb, vcb, slots)
     ref = oracle.paged_attention_prefill(bits(q), kcb, vcb, tables, lens, qlens, 0.088, "bf16")
     assert max_err(out, ref) <= TOL["bf16"]
+
+
+@pytest.mark.parametrize("H", [1, 3, 8, 40])
+def test_copy_blocks_of_head_major_fp8_pools(H):
+    """FP8 pools [NB, Hkv, 16, D] with fewer and with more heads than a block has
+    tokens: the named blocks are copied, the last one too, and no other byte."""
+    NB, D = 9, 128
+    g = torch.Generator(device=DEV).manual_seed(H)
+    pools = [torch.randint(0, 256, (NB, H, 16, D), generator=g, device=DEV, dtype=torch.uint8) for _ in range(2)]
+    want = [p.clone() for p in pools]
+    pairs = torch.tensor([[0, NB - 1], [3, 1]], dtype=torch.int32, device=DEV)
+    for w in want:
+        w[[NB - 1, 1]] = w[[0, 3]]
+    pa.copy_blocks(*pools, pairs)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, w) for p, w in zip(pools, want))
+    assert pa.device_error() == 0
