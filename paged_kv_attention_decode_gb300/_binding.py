@@ -3,7 +3,9 @@
 Argument marshalling only: shape/dtype/device checks, ``data_ptr()`` and the
 current CUDA stream go in, a status code comes out.  Every step of the path
 runs in the library's kernels; there is no fallback of any kind.  Scratch
-space is allocated here with torch (caller-owned memory for the library).
+space is allocated here with torch (caller-owned memory for the library), on
+the stream that the call runs on: torch's current one, or the `stream` given
+(a torch stream or a handle; the caller orders it with the inputs' stream).
 """
 from __future__ import annotations
 
@@ -137,11 +139,37 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _given(stream, call, *args, **kw):
+    """`call(*args, **kw)` with the given stream as torch's current one.
+
+    The calls make scratch that is dropped as they return, while their kernels
+    still run; the allocator hands it to the next tensor of the stream it was
+    made on, at once, so that must be the kernels' stream.  What is read on the
+    way (lengths on the host, sums) is ordered with that stream's work too.  A
+    tensor that the call made and returns may be used and dropped on the stream
+    that was current."""
+    before = torch.cuda.current_stream()
+    handle = _stream(stream)
+    if handle == before.cuda_stream:
+        return call(*args, **kw)
+    if not isinstance(stream, torch.cuda.Stream):   # 0 and 1: the legacy default stream
+        stream = torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        made = call(*args, **kw)
+    theirs = (*args, *kw.values())
+    for t in made if isinstance(made, tuple) else (made,):
+        if not any(t is x for x in theirs):
+            t.record_stream(before)
+    return made
+
+
 # --------------------------------------------------------------------------
 
 def slot_mapping(block_tables: torch.Tensor, seq_lens: torch.Tensor, cu_q_lens, num_tokens: int,
                  num_blocks: int, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """int64 slot of every new token (the last q_len positions of each sequence)."""
+    if stream is not None:
+        return _given(stream, slot_mapping, block_tables, seq_lens, cu_q_lens, num_tokens, num_blocks, out)
     _cuda(block_tables, seq_lens, cu_q_lens)
     _need(block_tables.dtype == torch.int32 and seq_lens.dtype == torch.int32, "int32 tables")
     B = seq_lens.shape[0]
@@ -150,7 +178,7 @@ def slot_mapping(block_tables: torch.Tensor, seq_lens: torch.Tensor, cu_q_lens, 
     _cuda(out)
     rc = load_library().pa_slot_mapping(out.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
                                         seq_lens.data_ptr(), _ptr(cu_q_lens), B, num_tokens,
-                                        num_blocks, PA_BLOCK_SIZE, _stream(stream))
+                                        num_blocks, PA_BLOCK_SIZE, _stream(None))
     _check(rc, "pa_slot_mapping")
     return out
 
@@ -249,6 +277,9 @@ def paged_attention_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
                            partition_size: int = 0, workspace: torch.Tensor | None = None,
                            stream=None) -> torch.Tensor:
     """Decode attention: q [B, Hq, D] -> out [B, Hq, D] over the paged cache."""
+    if stream is not None:
+        return _given(stream, paged_attention_decode, q, k_cache, v_cache, block_tables, seq_lens, scale,
+                      max_seq_len, out, partition_size, workspace)
     _cuda(q, k_cache, v_cache, block_tables, seq_lens, out, workspace)
     B, Hq, D = q.shape
     NB, bs, Hkv, D2 = k_cache.shape
@@ -264,7 +295,7 @@ def paged_attention_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
     rc = load_library().pa_paged_attention_decode(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         block_tables.shape[1], seq_lens.data_ptr(), B, max_seq_len, NB, float(scale), Hq, Hkv, D, bs,
-        partition_size, _ptr(workspace), ws_bytes, _dt(q), _stream(stream))
+        partition_size, _ptr(workspace), ws_bytes, _dt(q), _stream(None))
     _check(rc, "pa_paged_attention_decode")
     return out
 
@@ -279,6 +310,9 @@ def paged_attention_prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
     Chunks of at most PA_VERIFY_MAX_Q (8) queries -- decodes and speculative
     verify steps -- run in the decode kernel, longer chunks in the prefill
     kernels."""
+    if stream is not None:
+        return _given(stream, paged_attention_prefill, q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens,
+                      scale, max_q_len, max_seq_len, out, workspace)
     _cuda(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, out, workspace)
     T, Hq, D = q.shape
     NB, bs, Hkv, D2 = k_cache.shape
@@ -293,7 +327,7 @@ def paged_attention_prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
     rc = load_library().pa_paged_attention_prefill(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         block_tables.shape[1], seq_lens.data_ptr(), cu_q_lens.data_ptr(), B, T, max_q_len, max_seq_len,
-        NB, float(scale), Hq, Hkv, D, bs, _ptr(workspace), ws_bytes, _dt(q), _stream(stream))
+        NB, float(scale), Hq, Hkv, D, bs, _ptr(workspace), ws_bytes, _dt(q), _stream(None))
     _check(rc, "pa_paged_attention_prefill")
     return out
 
@@ -325,6 +359,8 @@ def paged_kv_gather(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: 
     """Test support: every sequence's live K/V rows, gathered through its block
     table into contiguous [sum(seq_lens), Hkv, D] tensors.  16-bit pools are
     [NB, 16, Hkv, D]; one-byte (FP8) pools are head-major [NB, Hkv, 16, D]."""
+    if stream is not None:
+        return _given(stream, paged_kv_gather, k_cache, v_cache, block_tables, seq_lens, max_seq_len)
     _cuda(k_cache, v_cache, block_tables, seq_lens)
     _need(block_tables.dtype == torch.int32 and seq_lens.dtype == torch.int32, "int32 tables")
     _need(v_cache.shape == k_cache.shape and v_cache.dtype == k_cache.dtype, "cache shape/dtype")
@@ -341,7 +377,7 @@ def paged_kv_gather(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: 
     rc = load_library().pa_paged_kv_gather(k_out.data_ptr(), v_out.data_ptr(), k_cache.data_ptr(),
                                            v_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
                                            seq_lens.data_ptr(), cu.data_ptr(), B, max_seq_len, NB, H, D,
-                                           k_cache.element_size(), _stream(stream))
+                                           k_cache.element_size(), _stream(None))
     _check(rc, "pa_paged_kv_gather")
     return k_out, v_out
 
@@ -387,6 +423,9 @@ def paged_attention_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
                                stream=None) -> torch.Tensor:
     """Decode attention over head-major FP8 (E4M3) pools [NB, Hkv, 16, 128]:
     q [B, Hq, 128] -> out [B, Hq, 128]."""
+    if stream is not None:
+        return _given(stream, paged_attention_decode_fp8, q, k_cache, v_cache, block_tables, seq_lens, scale,
+                      k_scale, v_scale, max_seq_len, out, partition_size, workspace)
     _cuda(q, k_cache, v_cache, block_tables, seq_lens, out, workspace)
     _u8(k_cache), _u8(v_cache)
     B, Hq, D = q.shape
@@ -402,7 +441,7 @@ def paged_attention_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     rc = load_library().pa_paged_attention_decode_fp8(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         block_tables.shape[1], seq_lens.data_ptr(), B, max_seq_len, NB, float(scale), float(k_scale),
-        float(v_scale), Hq, Hkv, D, bs, partition_size, _ptr(workspace), ws_bytes, _dt(q), _stream(stream))
+        float(v_scale), Hq, Hkv, D, bs, partition_size, _ptr(workspace), ws_bytes, _dt(q), _stream(None))
     _check(rc, "pa_paged_attention_decode_fp8")
     return out
 
@@ -417,6 +456,10 @@ def paged_attention_prefill_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
     chunks in one call).  `chunk_kv_tokens` sizes the chunks' 16-bit copy
     (see `count_chunk_kv_tokens()`); when it is None and a chunk can be longer than
     8 queries, it is computed from host copies of seq_lens and cu_q_lens."""
+    if stream is not None:
+        return _given(stream, paged_attention_prefill_fp8, q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens,
+                      scale, k_scale, v_scale, max_q_len, max_seq_len, out, workspace,
+                      chunk_kv_tokens=chunk_kv_tokens)
     _cuda(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, out, workspace)
     _u8(k_cache), _u8(v_cache)
     T, Hq, D = q.shape
@@ -439,7 +482,7 @@ def paged_attention_prefill_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         block_tables.shape[1], seq_lens.data_ptr(), cu_q_lens.data_ptr(), B, T, max_q_len, max_seq_len, NB,
         float(scale), float(k_scale), float(v_scale), Hq, Hkv, D, bs, _ptr(workspace), ws_bytes, _dt(q),
-        _stream(stream))
+        _stream(None))
     _check(rc, "pa_paged_attention_prefill_fp8")
     return out
 
@@ -467,8 +510,7 @@ def _current(dev: int, *ts) -> bool:
     return dev >= 0 and all(t is None or t.get_device() == dev for t in ts) and torch.cuda.current_device() == dev
 
 
-def _rope(name, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin, interleaved, q_out, stream,
-          pool, scales):
+def _rope(name, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin, interleaved, q_out, pool, scales):
     """The three rotate-and-append calls; `pool` is (num_blocks, num_kv_heads, head_dim, block_size)."""
     NB, H, D, bs = pool
     shape = key.shape
@@ -520,7 +562,7 @@ def _rope(name, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_si
         q_out.data_ptr(), os, q.data_ptr(), qs, key.data_ptr(), ks, value.data_ptr(), vs, k_cache.data_ptr(),
         v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), cos_sin.data_ptr(), maxp, T, NB, Hq, H, D,
         rot, 1 if interleaved else 0, bs, 0 if dtype == _F16 else 1, *scales,
-        _raw_stream(dev) if stream is None else _stream(stream))
+        _raw_stream(dev))
     if rc:
         _check(rc, name)
     return q_out
@@ -538,12 +580,15 @@ def paged_rope_kv_write(q: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
     (any token stride that is a multiple of 8 elements).  cos_sin is float32
     [max_positions, rot_dim], cosines then sines; pairs are (i, i + rot_dim/2),
     or (2i, 2i + 1) when interleaved."""
+    if stream is not None:
+        return _given(stream, paged_rope_kv_write, q, key, value, k_cache, v_cache, slot_mapping, positions,
+                      cos_sin, interleaved, q_out)
     NB, bs, H, D = k_cache.shape
     dtype = key.dtype
     if k_cache.dtype != dtype or v_cache.dtype != dtype:
         _need(False, "cache dtype")
     return _rope("pa_paged_rope_kv_write", q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
-                 interleaved, q_out, stream, (NB, H, D, bs), ())
+                 interleaved, q_out, (NB, H, D, bs), ())
 
 
 def paged_rope_kv_write_fp8(q: torch.Tensor, key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor,
@@ -551,10 +596,13 @@ def paged_rope_kv_write_fp8(q: torch.Tensor, key: torch.Tensor, value: torch.Ten
                             cos_sin: torch.Tensor, k_scale: float, v_scale: float, interleaved: bool = False,
                             q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """`paged_rope_kv_write` into head-major FP8 (E4M3) pools [NB, Hkv, 16, 128]."""
+    if stream is not None:
+        return _given(stream, paged_rope_kv_write_fp8, q, key, value, k_cache, v_cache, slot_mapping, positions,
+                      cos_sin, k_scale, v_scale, interleaved, q_out)
     _u8(k_cache), _u8(v_cache)
     NB, H, bs, D = k_cache.shape
     return _rope("pa_paged_rope_kv_write_fp8", q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
-                 interleaved, q_out, stream, (NB, H, D, bs), (float(k_scale), float(v_scale)))
+                 interleaved, q_out, (NB, H, D, bs), (float(k_scale), float(v_scale)))
 
 
 def fp4_tile_bytes(head_dim: int) -> int:
@@ -580,10 +628,13 @@ def paged_rope_kv_write_fp4(q: torch.Tensor, key: torch.Tensor, value: torch.Ten
                             cos_sin: torch.Tensor, k_scale: float, v_scale: float, interleaved: bool = False,
                             q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """`paged_rope_kv_write` into 4-bit pools [NB, Hkv, fp4_tile_bytes(D)]."""
+    if stream is not None:
+        return _given(stream, paged_rope_kv_write_fp4, q, key, value, k_cache, v_cache, slot_mapping, positions,
+                      cos_sin, k_scale, v_scale, interleaved, q_out)
     D = key.shape[2]
     NB, H = _fp4_pool(k_cache, v_cache, D)
     return _rope("pa_paged_rope_kv_write_fp4", q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
-                 interleaved, q_out, stream, (NB, H, D, PA_BLOCK_SIZE), (float(k_scale), float(v_scale)))
+                 interleaved, q_out, (NB, H, D, PA_BLOCK_SIZE), (float(k_scale), float(v_scale)))
 
 
 def paged_kv_write_fp4(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -618,6 +669,8 @@ def paged_kv_write_fp4(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Te
 def paged_kv_unpack_fp4(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: float, v_scale: float,
                         dtype: torch.dtype, stream=None):
     """Both 4-bit pools as 16-bit pools [NB, 16, Hkv, D] of `dtype`."""
+    if stream is not None:
+        return _given(stream, paged_kv_unpack_fp4, k_cache, v_cache, k_scale, v_scale, dtype)
     NB, H, tile = k_cache.shape
     D = tile // 9
     _fp4_pool(k_cache, v_cache, D)
@@ -632,7 +685,7 @@ def paged_kv_unpack_fp4(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: f
     v_out = torch.empty_like(k_out)
     rc = (_lib or load_library()).pa_paged_kv_unpack_fp4(
         k_out.data_ptr(), v_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), NB, H, D, PA_BLOCK_SIZE,
-        float(k_scale), float(v_scale), 0 if dtype == _F16 else 1, _raw_stream(dev) if stream is None else _stream(stream))
+        float(k_scale), float(v_scale), 0 if dtype == _F16 else 1, _raw_stream(dev))
     if rc:
         _check(rc, "pa_paged_kv_unpack_fp4")
     return k_out, v_out
@@ -692,6 +745,9 @@ def paged_attention_decode_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     """Decode attention over 4-bit pools [NB, Hkv, fp4_tile_bytes(D)]:
     q [B, Hq, D] -> out [B, Hq, D].  partition_size 0 takes the length of
     `decode_partition_for`."""
+    if stream is not None:
+        return _given(stream, paged_attention_decode_fp4, q, k_cache, v_cache, block_tables, seq_lens, scale,
+                      k_scale, v_scale, max_seq_len, out, partition_size, workspace)
     B, Hq, D = q.shape
     NB, Hkv = _fp4_pool(k_cache, v_cache, D)
     dev = _attn_args(q, k_cache, v_cache, block_tables, seq_lens, None, None, out, workspace)
@@ -708,7 +764,7 @@ def paged_attention_decode_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
         block_tables.shape[1], seq_lens.data_ptr(), B, max_seq_len, NB, float(scale), float(k_scale),
         float(v_scale), Hq, Hkv, D,
         PA_BLOCK_SIZE, partition_size, workspace.data_ptr(), ws_bytes, 0 if q.dtype == _F16 else 1,
-        _raw_stream(dev) if stream is None else _stream(stream))
+        _raw_stream(dev))
     if rc:
         _check(rc, "pa_paged_attention_decode_fp4")
     return out
@@ -722,6 +778,10 @@ def paged_attention_prefill_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
     """Causal varlen attention of new query rows over 4-bit pools (decodes,
     speculative-verify rows and prefill chunks in one call).  `chunk_kv_tokens`
     as in `paged_attention_prefill_fp8`."""
+    if stream is not None:
+        return _given(stream, paged_attention_prefill_fp4, q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens,
+                      scale, k_scale, v_scale, max_q_len, max_seq_len, out, workspace,
+                      chunk_kv_tokens=chunk_kv_tokens)
     T, Hq, D = q.shape
     NB, Hkv = _fp4_pool(k_cache, v_cache, D)
     dev = _attn_args(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, None, out, workspace)
@@ -741,7 +801,7 @@ def paged_attention_prefill_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), max_blocks,
         seq_lens.data_ptr(), cu_q_lens.data_ptr(), B, T, max_q_len, max_seq_len, NB, float(scale),
         float(k_scale), float(v_scale), Hq, Hkv, D, PA_BLOCK_SIZE, workspace.data_ptr(), ws_bytes, 0 if q.dtype == _F16 else 1,
-        _raw_stream(dev) if stream is None else _stream(stream))
+        _raw_stream(dev))
     if rc:
         _check(rc, "pa_paged_attention_prefill_fp4")
     return out
@@ -761,6 +821,9 @@ def paged_attention_decode_mod(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     when softcap > 0, plus alibi_slopes[h] * (key - query position), over the
     last `window` positions when window > 0.  partition_size 0 takes the length
     of `decode_partition_for`."""
+    if stream is not None:
+        return _given(stream, paged_attention_decode_mod, q, k_cache, v_cache, block_tables, seq_lens, scale,
+                      max_seq_len, softcap, window, alibi_slopes, out, partition_size, workspace)
     B, Hq, D = q.shape
     NB, bs, Hkv = _pool16(q, k_cache, v_cache)
     dev = _attn_args(q, k_cache, v_cache, block_tables, seq_lens, None, alibi_slopes, out, workspace)
@@ -776,7 +839,7 @@ def paged_attention_decode_mod(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         block_tables.shape[1], seq_lens.data_ptr(), B, max_seq_len, NB, float(scale), float(softcap), int(window),
         _ptr(alibi_slopes), Hq, Hkv, D, bs, partition_size, workspace.data_ptr(), ws_bytes, 0 if q.dtype == _F16 else 1,
-        _raw_stream(dev) if stream is None else _stream(stream))
+        _raw_stream(dev))
     if rc:
         _check(rc, "pa_paged_attention_decode_mod")
     return out
@@ -790,6 +853,9 @@ def paged_attention_prefill_mod(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
                                 stream=None) -> torch.Tensor:
     """`paged_attention_prefill` (decode, verify and chunk rows in one call) with
     modified scores, as `paged_attention_decode_mod`."""
+    if stream is not None:
+        return _given(stream, paged_attention_prefill_mod, q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens,
+                      scale, max_q_len, max_seq_len, softcap, window, alibi_slopes, out, workspace)
     T, Hq, D = q.shape
     NB, bs, Hkv = _pool16(q, k_cache, v_cache)
     dev = _attn_args(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, alibi_slopes, out, workspace)
@@ -802,7 +868,7 @@ def paged_attention_prefill_mod(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         block_tables.shape[1], seq_lens.data_ptr(), cu_q_lens.data_ptr(), B, T, max_q_len, max_seq_len, NB, float(scale),
         float(softcap), int(window), _ptr(alibi_slopes), Hq, Hkv, D, bs, workspace.data_ptr(), ws_bytes, 0 if q.dtype == _F16 else 1,
-        _raw_stream(dev) if stream is None else _stream(stream))
+        _raw_stream(dev))
     if rc:
         _check(rc, "pa_paged_attention_prefill_mod")
     return out

@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import paged_kv_attention_decode_gb300 as pa
-from tests._stand_in import StandIn, dev
+from tests._stand_in import StandIn, Stream, dev
 
 
 @pytest.fixture
@@ -38,3 +38,104 @@ def test_copy_blocks_refuses_other_pools(lib, shape, dtype):
     with pytest.raises(pa.PagedAttnError):
         pa.copy_blocks(k, v, dev(torch.zeros(2, 2, dtype=torch.int32)))
     assert not lib.calls
+
+
+# ---- calls on a stream that is not the current one -------------------------
+
+NB, HKV, HQ, D, B, T = 8, 2, 4, 128, 3, 3
+SIDE = 0x7000
+
+
+def z(*shape, dtype=torch.float16):
+    return dev(torch.zeros(shape, dtype=dtype))
+
+
+def pools(kind):
+    shape = {"16": (NB, 16, HKV, D), "fp8": (NB, HKV, 16, D), "fp4": (NB, HKV, 9 * D)}[kind]
+    return tuple(z(*shape, dtype=torch.float16 if kind == "16" else torch.uint8) for _ in range(2))
+
+
+def wrappers():
+    """name -> call(**kw) of every wrapper that makes tensors of its own."""
+    q, key = z(T, HQ, D), z(T, HKV, D)
+    bt, sl = z(B, 4, dtype=torch.int32), dev(torch.full((B,), 20, dtype=torch.int32))
+    cu = dev(torch.arange(B + 1, dtype=torch.int32))
+    slots, pos, cs = z(T, dtype=torch.int64), z(T, dtype=torch.int64), z(30, D, dtype=torch.float32)
+    p16, p8, p4 = pools("16"), pools("fp8"), pools("fp4")
+    rope = (slots, pos, cs)
+    return {
+        "slot_mapping": lambda **kw: pa.slot_mapping(bt, sl, None, B, NB, **kw),
+        "decode": lambda **kw: pa.paged_attention_decode(q, *p16, bt, sl, 0.1, **kw),
+        "prefill": lambda **kw: pa.paged_attention_prefill(q, *p16, bt, sl, cu, 0.1, 1, 20, **kw),
+        "decode_fp8": lambda **kw: pa.paged_attention_decode_fp8(q, *p8, bt, sl, 0.1, 1.0, 1.0, **kw),
+        "prefill_fp8": lambda **kw: pa.paged_attention_prefill_fp8(q, *p8, bt, sl, cu, 0.1, 1.0, 1.0, 9, 20, **kw),
+        "decode_fp4": lambda **kw: pa.paged_attention_decode_fp4(q, *p4, bt, sl, 0.1, 1.0, 1.0, **kw),
+        "prefill_fp4": lambda **kw: pa.paged_attention_prefill_fp4(q, *p4, bt, sl, cu, 0.1, 1.0, 1.0, 9, 20, **kw),
+        "decode_mod": lambda **kw: pa.paged_attention_decode_mod(q, *p16, bt, sl, 0.1, window=5, **kw),
+        "prefill_mod": lambda **kw: pa.paged_attention_prefill_mod(q, *p16, bt, sl, cu, 0.1, 9, 20, window=5, **kw),
+        "rope": lambda **kw: pa.paged_rope_kv_write(q, key, key, *p16, *rope, **kw),
+        "rope_fp8": lambda **kw: pa.paged_rope_kv_write_fp8(q, key, key, *p8, *rope, 1.0, 1.0, **kw),
+        "rope_fp4": lambda **kw: pa.paged_rope_kv_write_fp4(q, key, key, *p4, *rope, 1.0, 1.0, **kw),
+        "unpack_fp4": lambda **kw: pa.paged_kv_unpack_fp4(*p4, 1.0, 1.0, torch.float16, **kw),
+        "gather": lambda **kw: pa.paged_kv_gather(*p16, bt, sl, 20, **kw),
+    }
+
+
+NAMES = ["slot_mapping", "decode", "prefill", "decode_fp8", "prefill_fp8", "decode_fp4", "prefill_fp4", "decode_mod",
+         "prefill_mod", "rope", "rope_fp8", "rope_fp4", "unpack_fp4", "gather"]
+
+
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_a_given_stream_owns_what_the_call_makes(lib, name, as_handle):
+    """Scratch belongs to the stream that the kernels run on: the allocator hands
+    a freed block to the next tensor of the stream it was made on, at once."""
+    call = wrappers()[name]
+    lib.made.clear()
+    out = call(stream=SIDE if as_handle else Stream(SIDE))
+    assert lib.made and {s for _, _, s in lib.made} == {SIDE}
+    (_, args), = lib.calls
+    assert args[-1] == SIDE                                     # where the kernels run
+    assert lib.now.cuda_stream == 0                             # the caller's stream is current again
+    # the result may be used, and dropped, on the caller's stream
+    for t in out if isinstance(out, tuple) else (out,):
+        assert t.recorded == [0]
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_without_a_stream_the_current_one_serves(lib, name):
+    call = wrappers()[name]
+    for kw in ({}, {"stream": SIDE}):                           # (given, but the current one)
+        lib.made.clear(), lib.calls.clear()
+        lib.now = Stream(SIDE)
+        out = call(**kw)
+        assert {s for _, _, s in lib.made} == {SIDE} and lib.calls[0][1][-1] == SIDE
+        for t in out if isinstance(out, tuple) else (out,):
+            assert not hasattr(t, "recorded")
+
+
+@pytest.mark.parametrize("handle", [0, 1])
+def test_the_default_streams_handles(lib, handle):
+    """0 and 1 both name the legacy default stream."""
+    lib.now = Stream(SIDE)
+    call = wrappers()["decode_mod"]
+    lib.made.clear()
+    call(stream=handle)
+    assert {s for _, _, s in lib.made} == {0} and lib.calls[0][1][-1] == 0
+
+
+@pytest.mark.parametrize("name", ["decode", "prefill_fp8", "prefill_fp4", "decode_mod"])
+def test_given_outputs_and_workspaces_stay_the_callers(lib, name):
+    call = wrappers()[name]
+    out, ws = z(T, HQ, D), z(8192, dtype=torch.uint8)
+    lib.made.clear()
+    assert call(stream=Stream(SIDE), out=out, workspace=ws) is out
+    assert not lib.made and not hasattr(out, "recorded") and not hasattr(ws, "recorded")
+    assert ws.data_ptr() in lib.calls[0][1] and lib.calls[0][1][-1] == SIDE
+
+
+def test_a_query_rotated_in_place_on_a_given_stream(lib):
+    q, key = z(T, HQ, D), z(T, HKV, D)
+    res = pa.paged_rope_kv_write(q, key, key, *pools("16"), z(T, dtype=torch.int64), z(T, dtype=torch.int64),
+                                 z(30, D, dtype=torch.float32), q_out=q, stream=Stream(SIDE))
+    assert res is q and not hasattr(q, "recorded") and lib.calls[0][1][-1] == SIDE
