@@ -364,7 +364,9 @@ __global__ void __launch_bounds__(kFp4Warps * 32, Fp4Shape<D>::kMinCtas) decode_
                 const int u = ug / H;
                 n_h = ug - u * H;
                 n_col0 = (n_w - ug * C) * kCols;
-                n_unit = static_cast<uint32_t>(__ldg(p.units + u));
+                // (a plain load, like row_base below: the plan may have
+                // been writing the list when this kernel started)
+                n_unit = static_cast<uint32_t>(p.units[u]);
             }
             n_stage = 1;
         } else if (n_stage == 1) {
@@ -466,7 +468,7 @@ __global__ void __launch_bounds__(kFp4Warps * 32, Fp4Shape<D>::kMinCtas) decode_
         auto query_of = [&](int col) { return it.qlen == 1 ? 0 : col / G; };
         const int lim_min = min(tok1, it.n - it.qlen + 1 + query_of(it.col0));
         const bool parts = it.n > P;
-        const int64_t prow = parts ? __ldg(p.row_base + it.b) : 0;
+        const int64_t prow = parts ? p.row_base[it.b] : 0;
         Fp4State<D, E> st;
         {
             // this lane's quarter of column g's query

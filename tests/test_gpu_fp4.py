@@ -268,3 +268,57 @@ def test_steps_back_to_back_on_one_workspace():
     torch.cuda.synchronize()
     assert all(torch.equal(o, a) for row in outs for o, a in zip(row, alone))
     assert pa.device_error() == 0
+
+
+@pytest.mark.parametrize("verify", [False, True])
+def test_decode_and_verify_calls_back_to_back_on_one_workspace(verify):
+    """Calls without chunks, whose plan starts while the call before still runs:
+    other lengths, batch sizes and partitions each time, one workspace, queued
+    without a pause and replayed from a graph.  Each gives what it gives alone."""
+    Hq, Hkv, D = 8, 2, 128
+    rng = np.random.default_rng(17)
+    calls = []
+    for i, (B, hi, part) in enumerate(((40, 900, 64), (3, 3000, 16), (70, 60, 0), (1, 2500, 128), (25, 1500, 64))):
+        lens = [int(n) for n in rng.integers(8, hi, B)]
+        qlens = [int(c) for c in rng.integers(1, 9, B)] if verify else [1] * B
+        q, pools, tables = build(lens, qlens, Hq, Hkv, D, torch.bfloat16, seed=200 + i)
+        cu = np.concatenate([[0], np.cumsum(qlens)]).astype(np.int32)
+        d = put(q, *pools, tables, np.asarray(lens, np.int32), cu)
+        mx = max(lens)
+        need = pa.prefill_mod_workspace_bytes(B, int(cu[-1]), Hq, Hkv, D, mx) if verify else \
+            pa.decode_workspace_bytes(B, Hq, D, mx, part or pa.decode_partition_for(B, Hq, Hkv, mx))
+        calls.append((d, mx, part, need))
+    ws = torch.empty(max(c[3] for c in calls), dtype=torch.uint8, device=DEV)
+
+    def go(c, out):
+        d, mx, part, _ = c
+        if verify:
+            pa.paged_attention_prefill_fp4(*d, 0.1, KS, VS, 8, mx, out=out, workspace=ws)
+        else:
+            pa.paged_attention_decode_fp4(*d[:5], 0.1, KS, VS, mx, out=out, partition_size=part, workspace=ws)
+
+    alone = []
+    for c in calls:
+        o = torch.empty_like(c[0][0])
+        go(c, o)
+        torch.cuda.synchronize()
+        alone.append(o)
+    outs = [[torch.full_like(c[0][0], float("nan")) for c in calls] for _ in range(12)]
+    for row in outs:
+        for c, o in zip(calls, row):
+            go(c, o)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, a) for row in outs for o, a in zip(row, alone))
+    for row in outs:
+        for o in row:
+            o.fill_(float("nan"))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for row in outs:
+            for c, o in zip(calls, row):
+                go(c, o)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, a) for row in outs for o, a in zip(row, alone))
+    assert pa.device_error() == 0
