@@ -549,13 +549,15 @@ def _rope(name, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_si
                 (T2 == T and H2 == H and D2 == D and D3 == D and value.shape == shape, "q/key/value shape"),
                 (key.dtype == dtype and value.dtype == dtype, "q/key/value dtype"),
                 (dtype in _DTYPES, f"unsupported dtype {dtype}"),
-                (v_cache.shape == k_cache.shape and k_cache.is_contiguous() and v_cache.is_contiguous(), "cache shape"),
+                (v_cache.shape == k_cache.shape and k_cache.is_contiguous() and v_cache.is_contiguous(),
+                 "k_cache and v_cache: contiguous, of one shape"),
                 (slot_mapping.dtype == _I64T and slot_mapping.is_contiguous() and slot_mapping.numel() >= T,
                  "slot_mapping: int64 [num_tokens]"),
                 (positions.dtype == _I64T and positions.is_contiguous() and positions.numel() >= T,
                  "positions: int64 [num_tokens]"),
                 (cos_sin.dtype == _F32 and cos_sin.dim() == 2 and cos_sin.is_contiguous(),
                  "cos_sin: float32 [max_positions, rot_dim]"),
+                (q_out.shape == qshape and q_out.dtype == dtype, "q_out: the shape and dtype of q"),
                 (False, "q, key, value and q_out: head rows must be dense within a token"))
     maxp, rot = cos_sin.shape
     rc = getattr(_lib or load_library(), name)(

@@ -139,3 +139,113 @@ def test_a_query_rotated_in_place_on_a_given_stream(lib):
     res = pa.paged_rope_kv_write(q, key, key, *pools("16"), z(T, dtype=torch.int64), z(T, dtype=torch.int64),
                                  z(30, D, dtype=torch.float32), q_out=q, stream=Stream(SIDE))
     assert res is q and not hasattr(q, "recorded") and lib.calls[0][1][-1] == SIDE
+
+
+# ---- what a refusal names ---------------------------------------------------
+
+def strided(t):
+    """The same shape and values, not contiguous."""
+    return dev(torch.stack([t.as_subclass(torch.Tensor)] * 2, -1)[..., 0])
+
+
+class Elsewhere(type(dev(torch.zeros(1)))):
+    """A tensor of another device than the current one."""
+
+    def get_device(self):
+        return 1
+
+
+def elsewhere(t):
+    return t.as_subclass(Elsewhere)
+
+
+def args_of(call):
+    q, key = z(T, HQ, D), z(T, HKV, D)
+    kind = "fp4" if "fp4" in call else "fp8" if "fp8" in call else "16"
+    k, v = pools(kind)
+    tables = dict(block_tables=z(B, 4, dtype=torch.int32), seq_lens=z(B, dtype=torch.int32))
+    scales = {} if kind == "16" else dict(k_scale=1.0, v_scale=1.0)
+    if "rope" in call:
+        return dict(q=q, key=key, value=z(T, HKV, D), k_cache=k, v_cache=v, slot_mapping=z(T, dtype=torch.int64),
+                    positions=z(T, dtype=torch.int64), cos_sin=z(30, D, dtype=torch.float32), q_out=z(T, HQ, D),
+                    **scales)
+    if "kv_write" in call:
+        return dict(key=key, value=z(T, HKV, D), k_cache=k, v_cache=v, slot_mapping=z(T, dtype=torch.int64), **scales)
+    if "unpack" in call:
+        return dict(k_cache=k, v_cache=v, dtype=torch.float16, **scales)
+    a = dict(q=q, k_cache=k, v_cache=v, scale=0.1, max_seq_len=20, out=z(T, HQ, D),
+             workspace=z(8192, dtype=torch.uint8), **tables, **scales)
+    if "prefill" in call:
+        a.update(cu_q_lens=z(B + 1, dtype=torch.int32), max_q_len=1)
+    if "mod" in call:
+        a.update(alibi_slopes=z(HQ, dtype=torch.float32))
+    return a
+
+
+CALLS = ["paged_rope_kv_write", "paged_rope_kv_write_fp8", "paged_rope_kv_write_fp4", "paged_kv_write_fp4",
+         "paged_kv_unpack_fp4", "paged_attention_decode_fp4", "paged_attention_prefill_fp4",
+         "paged_attention_decode_mod", "paged_attention_prefill_mod"]
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_good_arguments_are_taken(lib, call):
+    getattr(pa, call)(**args_of(call))
+    assert len(lib.calls) == 1
+
+
+def as_type(dtype):
+    return lambda t: dev(t.as_subclass(torch.Tensor).to(dtype))
+
+
+def fewer(t):
+    return dev(t.as_subclass(torch.Tensor)[:-1].clone())
+
+
+ROPE, ATTN = CALLS[:3], CALLS[5:]
+REFUSALS = [
+    # calls, argument, what is wrong with it, words of the message
+    (CALLS[:3] + CALLS[4:], "k_cache", elsewhere, "current CUDA device"),
+    (CALLS, "v_cache", elsewhere, "current CUDA device"),
+    (ROPE + CALLS[3:4], "slot_mapping", elsewhere, "current CUDA device"),
+    (ATTN, "workspace", elsewhere, "current CUDA device"),
+    (ROPE, "k_cache", strided, "k_cache and v_cache: contiguous"),
+    (ROPE[:2], "v_cache", fewer, "k_cache and v_cache: contiguous, of one shape"),
+    (CALLS[3:], "k_cache", strided, "contiguous"),
+    (CALLS[3:4], "key", strided, "contiguous"),
+    (ATTN, "q", strided, "contiguous"),
+    (ATTN, "workspace", strided, "contiguous"),
+    (ATTN, "block_tables", strided, "contiguous"),
+    (CALLS[7:], "alibi_slopes", strided, "contiguous"),
+    (ROPE, "q", strided, "head rows"),
+    (ROPE, "value", strided, "head rows"),
+    (ROPE, "q_out", strided, "head rows"),
+    (ROPE, "q_out", as_type(torch.bfloat16), "q_out: the shape and dtype of q"),
+    (ROPE, "q_out", fewer, "q_out: the shape and dtype of q"),
+    (ROPE, "q", fewer, "q/key/value shape"),
+    (ROPE, "key", as_type(torch.bfloat16), "dtype"),
+    (ROPE + CALLS[3:4], "slot_mapping", fewer, "slot_mapping: int64"),
+    (ROPE + CALLS[3:4], "slot_mapping", as_type(torch.int32), "slot_mapping: int64"),
+    (ROPE, "positions", fewer, "positions: int64"),
+    (ROPE, "positions", strided, "positions: int64"),
+    (ROPE, "cos_sin", as_type(torch.float64), "cos_sin: float32"),
+    (ROPE, "cos_sin", strided, "cos_sin: float32"),
+    (CALLS[3:4], "value", fewer, "key/value/cache shapes"),
+    (ATTN, "seq_lens", as_type(torch.int64), "int32 tables"),
+    (ATTN, "block_tables", fewer, "table shapes"),
+    (ATTN, "out", fewer, "out shape/dtype"),
+    (ATTN, "out", as_type(torch.float32), "out shape/dtype"),
+    (CALLS[6:9:2], "cu_q_lens", fewer, "cu_q_lens"),
+    (CALLS[7:], "alibi_slopes", fewer, "alibi_slopes: float32"),
+    (CALLS[7:], "alibi_slopes", as_type(torch.float16), "alibi_slopes: float32"),
+    (CALLS[7:], "v_cache", fewer, "cache shape/dtype"),
+    (CALLS[5:7], "v_cache", fewer, "4-bit pools"),
+    (CALLS[5:7], "k_cache", as_type(torch.float16), "4-bit pools"),
+]
+
+
+@pytest.mark.parametrize("call,arg,change,words", [(c, a, f, w) for cs, a, f, w in REFUSALS for c in cs])
+def test_refusals_name_what_is_wrong(lib, call, arg, change, words):
+    good = args_of(call)
+    with pytest.raises(pa.PagedAttnError) as e:
+        getattr(pa, call)(**dict(good, **{arg: change(good[arg])}))
+    assert words in str(e.value) and not lib.calls
