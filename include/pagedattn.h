@@ -413,6 +413,13 @@ int pa_paged_kv_write_fp4(const void* key, const void* value, void* k_cache, voi
                           const int64_t* slot_mapping, int num_tokens, int num_blocks, int num_kv_heads,
                           int head_dim, int block_size, int src_dtype, float k_scale, float v_scale, void* stream);
 
+/* The same for rows that lie key_stride and value_stride elements apart (as in
+ * pa_paged_rope_kv_write: slices of a fused projection's rows). */
+int pa_paged_kv_write_fp4_strided(const void* key, int64_t key_stride, const void* value, int64_t value_stride,
+                                  void* k_cache, void* v_cache, const int64_t* slot_mapping, int num_tokens,
+                                  int num_blocks, int num_kv_heads, int head_dim, int block_size, int src_dtype,
+                                  float k_scale, float v_scale, void* stream);
+
 /* pa_paged_rope_kv_write into 4-bit pools. */
 int pa_paged_rope_kv_write_fp4(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, const void* key,
                                int64_t key_stride, const void* value, int64_t value_stride, void* k_cache,

@@ -59,6 +59,7 @@ _SIGNATURES = {
     "pa_paged_rope_kv_write_fp4": (_i32, _ROPE + [_i32, _f32, _f32, _p]),
     "pa_fp4_tile_bytes": (_i32, [_i32]),
     "pa_paged_kv_write_fp4": (_i32, [_p, _p, _p, _p, _p, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _f32, _p]),
+    "pa_paged_kv_write_fp4_strided": (_i32, [_p, _i64, _p, _i64, _p, _p, _p] + [_i32] * 6 + [_f32, _f32, _p]),
     "pa_paged_kv_unpack_fp4": (_i32, [_p, _p, _p, _p, _i32, _i32, _i32, _i32, _f32, _f32, _i32, _p]),
     "pa_paged_attention_decode_fp4": (_i32, [_p, _p, _p, _p, _p, _i32, _p, _i32, _i32, _i32, _f32, _f32, _f32,
                                              _i32, _i32, _i32, _i32, _i32, _p, _sz, _i32, _p]),
@@ -642,7 +643,9 @@ def paged_rope_kv_write_fp4(q: torch.Tensor, key: torch.Tensor, value: torch.Ten
 def paged_kv_write_fp4(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                        slot_mapping: torch.Tensor, k_scale: float, v_scale: float, stream=None) -> None:
     """In place: E2M1 codes and E4M3 group scales of key/value into the 4-bit
-    pools [NB, Hkv, fp4_tile_bytes(D)] (slot < 0: skipped)."""
+    pools [NB, Hkv, fp4_tile_bytes(D)] (slot < 0: skipped).  key/value
+    [T, Hkv, D] may be slices of fused projection rows, as in
+    `paged_rope_kv_write`."""
     shape = key.shape
     T, H, D = shape
     NB, H2 = _fp4_pool(k_cache, v_cache, D)
@@ -652,17 +655,22 @@ def paged_kv_write_fp4(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Te
             and v_cache.get_device() == dev and slot_mapping.get_device() == dev and H == H2
             and value.shape == shape and value.dtype == dtype and (dtype == _F16 or dtype == _BF16)
             and slot_mapping.dtype == _I64T and slot_mapping.numel() >= T and slot_mapping.is_contiguous()
-            and key.is_contiguous() and value.is_contiguous() and k_cache.is_contiguous()
-            and v_cache.is_contiguous()):
-        _cuda(key, value, k_cache, v_cache, slot_mapping)
+            and k_cache.is_contiguous() and v_cache.is_contiguous()):
+        _cuda(k_cache, v_cache, slot_mapping)
         _refuse("paged_kv_write_fp4",
                 (_current(dev, value, k_cache, v_cache, slot_mapping), "tensors must be on the current CUDA device"),
                 (H == H2 and value.shape == shape and value.dtype == dtype, "key/value/cache shapes"),
                 (dtype in _DTYPES, f"unsupported dtype {dtype}"),
                 (False, "slot_mapping: int64 [num_tokens]"))
-    rc = (_lib or load_library()).pa_paged_kv_write_fp4(
-        key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), T, NB, H,
-        D, PA_BLOCK_SIZE, 0 if dtype == _F16 else 1, float(k_scale), float(v_scale),
+    ks, kh, k1 = key.stride()
+    vs, vh, v1 = value.stride()
+    if not (k1 == 1 and v1 == 1 and ((kh == D and vh == D) or H <= 1)):
+        _need(False, "key and value: head rows must be dense within a token")
+    if T <= 1:   # the stride of a single row says nothing
+        ks = vs = H * D
+    rc = (_lib or load_library()).pa_paged_kv_write_fp4_strided(
+        key.data_ptr(), ks, value.data_ptr(), vs, k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), T,
+        NB, H, D, PA_BLOCK_SIZE, 0 if dtype == _F16 else 1, float(k_scale), float(v_scale),
         _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(rc, "pa_paged_kv_write_fp4")

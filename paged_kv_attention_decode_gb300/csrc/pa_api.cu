@@ -640,13 +640,21 @@ int pa_paged_rope_kv_write_fp4(void* q_out, int64_t q_out_stride, const void* q,
                        k_scale, v_scale);
 }
 
+int pa_paged_kv_write_fp4_strided(const void* key, int64_t key_stride, const void* value, int64_t value_stride,
+                                  void* k_cache, void* v_cache, const int64_t* slot_mapping, int num_tokens,
+                                  int num_blocks, int num_kv_heads, int head_dim, int block_size, int src_dtype,
+                                  float k_scale, float v_scale, void* stream) {
+    return append_impl(nullptr, 0, nullptr, 0, key, key_stride, value, value_stride, k_cache, v_cache, slot_mapping,
+                       nullptr, nullptr, 0, num_tokens, num_blocks, 0, num_kv_heads, head_dim, 0, 0, block_size,
+                       src_dtype, stream, Cache::kFp4, k_scale, v_scale);
+}
+
 int pa_paged_kv_write_fp4(const void* key, const void* value, void* k_cache, void* v_cache,
                           const int64_t* slot_mapping, int num_tokens, int num_blocks, int num_kv_heads,
                           int head_dim, int block_size, int src_dtype, float k_scale, float v_scale, void* stream) {
     const int64_t row = static_cast<int64_t>(num_kv_heads) * head_dim;
-    return append_impl(nullptr, 0, nullptr, 0, key, row, value, row, k_cache, v_cache, slot_mapping, nullptr, nullptr,
-                       0, num_tokens, num_blocks, 0, num_kv_heads, head_dim, 0, 0, block_size, src_dtype, stream,
-                       Cache::kFp4, k_scale, v_scale);
+    return pa_paged_kv_write_fp4_strided(key, row, value, row, k_cache, v_cache, slot_mapping, num_tokens, num_blocks,
+                                         num_kv_heads, head_dim, block_size, src_dtype, k_scale, v_scale, stream);
 }
 
 int pa_fp4_tile_bytes(int head_dim) { return head_dim == 64 || head_dim == 128 ? fp4_tile_bytes(head_dim) : 0; }

@@ -211,3 +211,13 @@ def test_reference_attention_by_hand():
     out, _, _, _ = R.attention(q, k, v, np.zeros((1, 1), np.int32), [2], [1], 1.0, softcap=2.0)
     p = math.exp(2) / (math.exp(2) + 1)
     assert np.allclose(out[0, 0], p * v[0, 0, 0] + (1 - p) * v[0, 1, 0])
+
+
+def test_strided_4bit_write_refusals(lib):
+    w = lib.pa_paged_kv_write_fp4_strided
+    a = dict(key=F, ks=1024, value=F, vs=1024, kc=F, vc=F, slots=F, T=4, nb=8, hkv=8, d=128, bs=16, dt=0, a=1.0, b=1.0)
+    for kw, status in ((dict(ks=1020), INVALID), (dict(vs=0), INVALID), (dict(ks=1028), UNSUPPORTED),
+                       (dict(vs=2052), UNSUPPORTED), (dict(key=F + 8), INVALID), (dict(value=None), INVALID),
+                       (dict(T=-1), INVALID), (dict(d=96, ks=768, vs=768), UNSUPPORTED), (dict(a=0.0), INVALID),
+                       (dict(T=0), 0)):
+        assert w(*dict(a, **kw).values(), None) == status

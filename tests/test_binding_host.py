@@ -187,6 +187,19 @@ CALLS = ["paged_rope_kv_write", "paged_rope_kv_write_fp8", "paged_rope_kv_write_
          "paged_attention_decode_mod", "paged_attention_prefill_mod"]
 
 
+def test_a_4bit_write_takes_slices_of_fused_rows(lib):
+    """As the rotating writes do: the rows' stride goes to the library."""
+    fused = z(T, (HQ + 2 * HKV) * D)
+    k, v = (fused[:, (HQ + i * HKV) * D:(HQ + (i + 1) * HKV) * D].unflatten(1, (HKV, D)) for i in (0, 1))
+    p = pools("fp4")
+    for a, b, ks, vs in ((k, v, fused.shape[1], fused.shape[1]), (k, v.contiguous(), fused.shape[1], HKV * D),
+                         (k[:1], v[:1], HKV * D, HKV * D)):
+        lib.calls.clear()
+        pa.paged_kv_write_fp4(a, b, *p, z(T, dtype=torch.int64), 1.0, 1.0)
+        (_, args), = lib.calls
+        assert args[:4] == (a.data_ptr(), ks, b.data_ptr(), vs)
+
+
 @pytest.mark.parametrize("call", CALLS)
 def test_good_arguments_are_taken(lib, call):
     getattr(pa, call)(**args_of(call))
@@ -211,7 +224,8 @@ REFUSALS = [
     (ROPE, "k_cache", strided, "k_cache and v_cache: contiguous"),
     (ROPE[:2], "v_cache", fewer, "k_cache and v_cache: contiguous, of one shape"),
     (CALLS[3:], "k_cache", strided, "contiguous"),
-    (CALLS[3:4], "key", strided, "contiguous"),
+    (CALLS[3:4], "key", strided, "head rows"),
+    (CALLS[3:4], "slot_mapping", strided, "contiguous"),
     (ATTN, "q", strided, "contiguous"),
     (ATTN, "workspace", strided, "contiguous"),
     (ATTN, "block_tables", strided, "contiguous"),

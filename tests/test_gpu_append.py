@@ -258,3 +258,23 @@ def test_empty_step():
     out = pa.paged_rope_kv_write_fp4(q, k, v, *pools, none, none, torch.zeros(4, 64, device=DEV), 1.0, 1.0)
     torch.cuda.synchronize()
     assert out.shape == q.shape and all(torch.equal(a, b) for a, b in zip(pools, before))
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D,dn", [(1, 4, 1, 64, "f16"), (23, 6, 2, 64, "bf16"), (600, 12, 4, 128, "f16")])
+def test_write_fp4_of_fused_rows(T, Hq, Hkv, D, dn):
+    """Rows that are slices of a fused projection (and one side of them dense)."""
+    _, k, v = tokens(T, Hq, Hkv, D, DT[dn], seed=T, fused=True)
+    NB = (T + 15) // 16 + 2
+    slots = slots_for(T, NB, T)
+    for a, b in ((k, v), (k, v.contiguous()), (k.contiguous(), v)):
+        pools = fp4_pools(NB, Hkv, D, 2)
+        before = [x.cpu().numpy().copy() for x in pools]
+        pa.paged_kv_write_fp4(a, b, *pools, torch.from_numpy(slots).to(DEV), 1 / 256, 0.003)
+        torch.cuda.synchronize()
+        for i, (x, scale) in enumerate(((k, 1 / 256), (v, 0.003))):
+            live, isv = slots >= 0, bool(i)
+            codes, sc = (y.copy() for y in R.unpack_tiles(before[i], isv))
+            codes[slots[live] // 16, slots[live] % 16], sc[slots[live] // 16, slots[live] % 16] = \
+                R.quantise_fp4(np32(x)[live], scale)
+            assert np.array_equal(pools[i].cpu().numpy(), R.pack_tiles(codes, sc, isv))
+    assert pa.device_error() == 0
