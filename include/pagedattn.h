@@ -48,6 +48,17 @@
  * table entry and slot they use against the pool; an out-of-range entry is
  * skipped (its tokens contribute nothing, its write is dropped) and recorded
  * in a device error word that pa_get_device_error reads.
+ *
+ * Values: what lies at or past a sequence's length, before every window of its
+ * queries, or in a block that is skipped may hold anything, NaN too.  The cached
+ * v of the other positions has to be finite: a query gives the positions that it
+ * may not see (later ones of its own chunk or verify row) a weight of 0, and 0
+ * times NaN or infinity is NaN.
+ *
+ * Order: the first kernel of an attention call may read seq_lens and cu_q_lens
+ * while the preceding kernel of the stream still runs, if that kernel allows it
+ * (programmatic dependent launch).  A caller's kernel that writes these arrays
+ * must not signal that its dependents may launch before it has written them.
  */
 #ifndef PAGEDATTN_H
 #define PAGEDATTN_H
@@ -148,9 +159,19 @@ int pa_decode_partition(int max_seq_len, int partition_size);
  * over the GPU, but not below the square root of 2 * max_seq_len (walking a
  * partition takes a time in proportion to its length, merging them one in
  * proportion to their number).  Lengths of at most 2 * PA_MIN_PARTITION tokens
- * stay in one partition.  Pass the value as partition_size, to the workspace function too
- * (with a window, max_seq_len of the call is right here as well).  Returns -1
- * for a negative size, no heads, or num_q_heads not a multiple of num_kv_heads.
+ * stay in one partition.  Pass the value as partition_size, to the workspace
+ * function too.  Returns -1 for a negative size, no heads, or num_q_heads not a
+ * multiple of num_kv_heads.
+ * The rule is one for every cache and knows no window; where that matters the
+ * caller may pass a length of its own:
+ *  - a 4-bit call's items hold 8 pairs, so with 9 and more query heads per kv
+ *    head it has more items than are counted here, and longer partitions can
+ *    be faster (16 heads per kv head: 4 x 32768 tokens, 32/2 heads, 256 tokens
+ *    42 us, 512 tokens 36; 16 x 8192, 64/4 heads, 128 tokens 67 us, 1024 48);
+ *  - a window leaves few partitions of a long sequence, so that few sequences
+ *    want the length that the window's own length gives (one sequence of
+ *    131072 tokens, 32/8 heads, window 1024: 512 tokens 44 us, 64 tokens 22;
+ *    four of them: 1024 tokens 71 us, 64 tokens 24).
  */
 #define PA_MIN_PARTITION 64
 #define PA_PARTITION_ITEMS 4096

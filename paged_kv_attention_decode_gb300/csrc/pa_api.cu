@@ -849,6 +849,10 @@ static int prefill_impl(void* out, const void* q, const void* k_cache, const voi
         // 355, 740, 2693, with half as much weight again 308, 350, 721, 2687
         // (over other steps neither wins), with nine times as much, on earlier
         // kernels that took 323, 371, 770, 2818: 352, 469, 1593, 7403.
+        // All of these are steps of 32/8 heads of 128.  col_chunks counts a verify
+        // row's most columns, so a single query weighs 1, 4 and 8 at 1, 4 and 8
+        // heads per kv head (4-bit) for the same bytes: with many heads the rows
+        // get more of the SMs than by their own work.
         p.split = dc.p.split;
         p.decode_weight = (cache == Cache::kFp4 ? 0.5f : 1.2f) * dc.p.col_chunks / (mod && softcapped(*mod) ? 2600.f : 2000.f);
     }

@@ -14,8 +14,9 @@
 // Bound: HBM.  Every q, k and v value is read once and written once, with six
 // operations per pair between; the table rows (512 bytes per token at head_dim
 // 128) are shared by a token's heads.  A CTA takes one token at a time (or a
-// share of its head rows when there are few tokens), as many CTAs as are
-// resident stride over the tokens; eight threads of 16 dims share a head row
+// share of its head rows when there are few tokens), eight CTAs per SM stride
+// over the tokens (as many as are resident for 16-bit and FP8 caches; the 4-bit
+// kernel's 80 registers let six be resident, and the others follow); eight threads of 16 dims share a head row
 // at head_dim 128.  Measured at 8192 tokens, 32/8 heads of 128, bf16: 35 us for
 // 206 MB (5.9 TB/s, 0.87 of the measured copy rate); one CTA per token 37 us.
 // Several rows' loads at once cost occupancy and were slower (two rows 36.2
@@ -259,7 +260,7 @@ cudaError_t launch_append(const AppendParams& p, int head_dim, int dtype, int ca
     const int rows = p.num_q_heads + 2 * p.num_kv_heads;
     const int per_pass = kAppendThreads / (head_dim / 16);
     const int passes = (rows + per_pass - 1) / per_pass;
-    const int gx = std::min(p.num_tokens, 8 * sm_count());   // as many CTAs as are resident
+    const int gx = std::min(p.num_tokens, 8 * sm_count());   // (six of eight are resident over a 4-bit cache)
     // few tokens: a token's head rows are shared out over CTAs
     const int gy = std::max(1, std::min(passes, 8 * sm_count() / gx));
     const dim3 grid(gx, gy);
