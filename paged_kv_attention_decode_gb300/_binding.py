@@ -733,6 +733,11 @@ def _attn_args(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, alibi_slo
             (False, "alibi_slopes: float32 [num_q_heads]"))
 
 
+def _window(window) -> int:
+    """As a C int: past its range, the longest window (no limit) or a negative one (refused)."""
+    return max(-2 ** 31, min(int(window), 2 ** 31 - 1))
+
+
 def _pool16(q, k_cache, v_cache):
     NB, bs, Hkv, D = k_cache.shape
     if q.shape[2] != D or v_cache.shape != k_cache.shape or k_cache.dtype != q.dtype or v_cache.dtype != q.dtype:
@@ -847,7 +852,7 @@ def paged_attention_decode_mod(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     workspace, ws_bytes = _ws(lib.pa_decode_workspace_bytes(B, Hq, D, max_seq_len, partition_size), q, workspace)
     rc = lib.pa_paged_attention_decode_mod(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-        block_tables.shape[1], seq_lens.data_ptr(), B, max_seq_len, NB, float(scale), float(softcap), int(window),
+        block_tables.shape[1], seq_lens.data_ptr(), B, max_seq_len, NB, float(scale), float(softcap), _window(window),
         _ptr(alibi_slopes), Hq, Hkv, D, bs, partition_size, workspace.data_ptr(), ws_bytes, 0 if q.dtype == _F16 else 1,
         _raw_stream(dev))
     if rc:
@@ -877,7 +882,7 @@ def paged_attention_prefill_mod(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
     rc = lib.pa_paged_attention_prefill_mod(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         block_tables.shape[1], seq_lens.data_ptr(), cu_q_lens.data_ptr(), B, T, max_q_len, max_seq_len, NB, float(scale),
-        float(softcap), int(window), _ptr(alibi_slopes), Hq, Hkv, D, bs, workspace.data_ptr(), ws_bytes, 0 if q.dtype == _F16 else 1,
+        float(softcap), _window(window), _ptr(alibi_slopes), Hq, Hkv, D, bs, workspace.data_ptr(), ws_bytes, 0 if q.dtype == _F16 else 1,
         _raw_stream(dev))
     if rc:
         _check(rc, "pa_paged_attention_prefill_mod")

@@ -263,3 +263,17 @@ def test_refusals_name_what_is_wrong(lib, call, arg, change, words):
     with pytest.raises(pa.PagedAttnError) as e:
         getattr(pa, call)(**dict(good, **{arg: change(good[arg])}))
     assert words in str(e.value) and not lib.calls
+
+
+@pytest.mark.parametrize("call", ["paged_attention_decode_mod", "paged_attention_prefill_mod"])
+@pytest.mark.parametrize("window,passed", [(0, 0), (7, 7), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1),
+                                           (2 ** 32, 2 ** 31 - 1), (2 ** 32 + 5, 2 ** 31 - 1),
+                                           (2 ** 63 - 1, 2 ** 31 - 1), (-3, -3), (-2 ** 32, -2 ** 31),
+                                           (-2 ** 32 + 9, -2 ** 31)])
+def test_a_window_past_32_bits_is_no_other_window(lib, call, window, passed):
+    """(a C int would take its low bits: a window of 2^32 + 5 would be one of 5)"""
+    import ctypes
+    getattr(pa, call)(**dict(args_of(call), window=window))
+    (name, args), = lib.calls
+    at = 12 if "decode" in call else 15     # behind scale and softcap
+    assert args[at - 2:at] == (0.1, 0.0) and ctypes.c_int(args[at]).value == passed
