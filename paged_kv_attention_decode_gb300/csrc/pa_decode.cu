@@ -603,15 +603,16 @@ __global__ void __launch_bounds__(1024) decode_plan_kernel(const DecodeParams p)
     // before it reads the list
     pdl_trigger();
     const int P = p.partition_tokens;
+    bool overlap = false;   // cu_q_lens falls somewhere: chunks may share rows
     // (length, queries) of row b; queries = 0 when the row is not handled here
     auto row_of = [&](int b, bool record, int& qlen) -> int {
         qlen = 1;
         if (p.cu_q_lens) {
             const int c0 = p.cu_q_lens[b], c1 = p.cu_q_lens[b + 1];
             qlen = c1 - c0;
-            if (c0 < 0 || c1 > p.num_rows) {
-                // rows outside q / out: none of them is read or written
-                if (record && qlen >= 1 && qlen <= PA_VERIFY_MAX_Q_) record_error(p.err, PA_DEVERR_SEQ_LEN_);
+            if (c0 < 0 || c1 < c0 || c1 > p.num_rows || (overlap && !rows_in_order(p.cu_q_lens, b))) {
+                // rows outside q / out, or of another sequence: none of them is read or written
+                if (record && qlen != 0 && qlen <= PA_VERIFY_MAX_Q_) record_error(p.err, PA_DEVERR_SEQ_LEN_);
                 qlen = 0;
                 return 0;
             }
@@ -630,20 +631,23 @@ __global__ void __launch_bounds__(1024) decode_plan_kernel(const DecodeParams p)
         return n;
     };
     int chunk_total = 0;
-    // Only inputs are read before the wait: the first 1024 rows' lengths.
+    // Only inputs are read before the wait: the first 1024 rows' lengths, and
+    // cu_q_lens for its order.
     // Every global write comes after it, because the preceding kernel of the
     // stream may still be running -- a previous decode call's kernel allows
     // dependent launch as soon as it starts, and it reads the work list, the
     // counter and the output rows that this plan is about to rewrite.
     int qlen0 = 0;
-    const int n0 = tid < p.num_seqs ? row_of(tid, true, qlen0) : 0;
+    int n0 = tid < p.num_seqs ? row_of(tid, true, qlen0) : 0;
+    const bool falls = p.cu_q_lens && falls_anywhere(p.cu_q_lens, p.num_seqs);
     pdl_wait();
     // pass 1: full partitions, partials rows (and the zero rows of empty sequences)
     if (tid == 0) {
         carry_u = 0;
         carry_r = 0;
     }
-    __syncthreads();
+    overlap = __syncthreads_or(falls);
+    if (overlap && tid < p.num_seqs) n0 = row_of(tid, true, qlen0);
     for (int base = 0; base < p.num_seqs; base += 1024) {
         const int b = base + tid;
         int v = 0, vr = 0, qlen = 0, part0 = 0;

@@ -338,4 +338,19 @@ __device__ __forceinline__ float fast_rcp(float x) {
     return y;
 }
 
+// Whether rows cu[b] .. cu[b + 1] - 1 of a varlen batch lie behind those of every
+// sequence before b.  The plans ask only when some entry of cu is below the one
+// before it; the rows of the sequences that pass do not overlap, so that what a
+// plan lists stays within the room that num_tokens and num_seqs give it.
+__device__ __forceinline__ bool rows_in_order(const int32_t* cu, int b) {
+    for (int i = 0; i < b; ++i)
+        if (cu[i] > cu[b]) return false;
+    return true;
+}
+__device__ __forceinline__ bool falls_anywhere(const int32_t* cu, int num_seqs) {   // this thread's share
+    bool falls = false;
+    for (int b = threadIdx.x; b < num_seqs; b += blockDim.x) falls |= cu[b + 1] < cu[b];
+    return falls;
+}
+
 }  // namespace pa

@@ -363,15 +363,15 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
         chunk_cost = row_cost = 0;
     }
     for (int i = tid; i < kPlanBuckets; i += 1024) hist[i] = 0;
-    __syncthreads();
+    const bool overlap = __syncthreads_or(falls_anywhere(cu_q_lens, num_seqs));
     // the pairs of sequence b: count them (offsets) and their cost classes
-    // (a chunk outside the num_tokens query rows has none: its rows cannot be
-    // written, and the pair list stays within num_tokens / 4 + num_seqs)
+    // (a chunk outside the num_tokens query rows, or on rows of another one, has
+    // none: the pair list stays within num_tokens / 4 + num_seqs)
     auto pairs_of = [&](int b, int& ql, int& n) {
         const int c0 = cu_q_lens[b], c1 = cu_q_lens[b + 1];
         ql = c1 - c0;
         n = seq_lens[b];
-        if (c0 < 0 || c1 < c0 || c1 > num_tokens) {
+        if (c0 < 0 || c1 < c0 || c1 > num_tokens || (overlap && !rows_in_order(cu_q_lens, b))) {
             ql = 0;
             return 0;
         }
