@@ -117,7 +117,9 @@ const char* pa_status_string(int status);
  * Rows of a sequence whose table entry is out of range get slot -1 and set
  * PA_DEVERR_BLOCK_ID; rows of a sequence whose seq_len is below its new-token
  * count (or above the table's capacity) get slot -1 and set
- * PA_DEVERR_SEQ_LEN.  A decode row (cu_q_lens NULL) with seq_len 0 is a
+ * PA_DEVERR_SEQ_LEN.  A sequence whose rows fall outside 0 .. num_tokens - 1 sets
+ * it too and has no row written.  Rows behind the last sequence's (a batch
+ * padded to num_tokens rows) get slot -1.  A decode row (cu_q_lens NULL) with seq_len 0 is a
  * padding row (a batch padded to a fixed size, e.g. a captured graph's
  * bucket): slot -1, nothing flagged; decode attention gives it a zero row.
  */

@@ -168,7 +168,8 @@ def _given(stream, call, *args, **kw):
 
 def slot_mapping(block_tables: torch.Tensor, seq_lens: torch.Tensor, cu_q_lens, num_tokens: int,
                  num_blocks: int, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """int64 slot of every new token (the last q_len positions of each sequence)."""
+    """int64 slot of every new token (the last q_len positions of each sequence);
+    -1 for rows behind the last sequence's."""
     if stream is not None:
         return _given(stream, slot_mapping, block_tables, seq_lens, cu_q_lens, num_tokens, num_blocks, out)
     _cuda(block_tables, seq_lens, cu_q_lens)
@@ -176,7 +177,12 @@ def slot_mapping(block_tables: torch.Tensor, seq_lens: torch.Tensor, cu_q_lens, 
     B = seq_lens.shape[0]
     if out is None:
         out = torch.empty(num_tokens, dtype=torch.int64, device=seq_lens.device)
+        if B == 0:   # (the library returns at once)
+            out.fill_(-1)
     _cuda(out)
+    _need(out.dtype == torch.int64 and out.numel() >= num_tokens, "out: int64 [num_tokens]")
+    _need(block_tables.dim() == 2 and block_tables.shape[0] >= B
+          and (cu_q_lens is None or (cu_q_lens.dtype == torch.int32 and cu_q_lens.numel() == B + 1)), "table shapes")
     rc = load_library().pa_slot_mapping(out.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
                                         seq_lens.data_ptr(), _ptr(cu_q_lens), B, num_tokens,
                                         num_blocks, PA_BLOCK_SIZE, _stream(None))

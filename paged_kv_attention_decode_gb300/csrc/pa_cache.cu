@@ -12,15 +12,23 @@
 
 namespace pa {
 
-// One warp per sequence; lanes stride over the sequence's new tokens.
+// One warp per sequence; lanes stride over the sequence's new tokens.  Rows
+// behind the last sequence's (a batch padded to num_tokens rows) get -1.
 __global__ void __launch_bounds__(128) slot_mapping_kernel(int64_t* __restrict__ slots,
                                                            const int32_t* __restrict__ block_tables,
                                                            int max_blocks, const int32_t* __restrict__ seq_lens,
                                                            const int32_t* __restrict__ cu_q_lens, int num_seqs,
-                                                           int num_blocks, unsigned int* err) {
+                                                           int num_tokens, int num_blocks, unsigned int* err) {
     pdl_trigger();
     const int warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     const int lane = threadIdx.x & 31;
+    if (cu_q_lens) {
+        const int64_t end = cu_q_lens[num_seqs];
+        if (end >= 0)
+            for (int64_t r = end + blockIdx.x * blockDim.x + threadIdx.x; r < num_tokens;
+                 r += static_cast<int64_t>(gridDim.x) * blockDim.x)
+                slots[r] = -1;
+    }
     if (warp >= num_seqs) return;
     const int b = warp;
     const int n = seq_lens[b];
@@ -33,6 +41,11 @@ __global__ void __launch_bounds__(128) slot_mapping_kernel(int64_t* __restrict__
         ql = 1;
     }
     if (ql <= 0) return;
+    if (row0 < 0 || row0 > num_tokens - ql) {
+        // rows outside slots (cu_q_lens inconsistent with num_tokens): none of them is written
+        if (lane == 0) record_error(err, PA_DEVERR_SEQ_LEN_);
+        return;
+    }
     const bool seq_ok = n >= ql && n <= max_blocks * 16;
     // a decode row of length 0 pads a batch (to a captured bucket size): it
     // has no token to place, so its slot is -1 and nothing is flagged
@@ -161,12 +174,11 @@ cudaError_t launch_kv_write_fp8(const void* key, const void* value, void* k_cach
 cudaError_t launch_slot_mapping(int64_t* slots, const int32_t* block_tables, int max_blocks,
                                 const int32_t* seq_lens, const int32_t* cu_q_lens, int num_seqs,
                                 int num_tokens, int num_blocks, unsigned int* err, cudaStream_t s) {
-    (void)num_tokens;
     if (num_seqs == 0) return cudaSuccess;
     const int threads = 128;
     const int blocks = (num_seqs * 32 + threads - 1) / threads;
     slot_mapping_kernel<<<blocks, threads, 0, s>>>(slots, block_tables, max_blocks, seq_lens, cu_q_lens,
-                                                   num_seqs, num_blocks, err);
+                                                   num_seqs, num_tokens, num_blocks, err);
     return cudaGetLastError();
 }
 

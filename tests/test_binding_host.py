@@ -277,3 +277,18 @@ def test_a_window_past_32_bits_is_no_other_window(lib, call, window, passed):
     (name, args), = lib.calls
     at = 12 if "decode" in call else 15     # behind scale and softcap
     assert args[at - 2:at] == (0.1, 0.0) and ctypes.c_int(args[at]).value == passed
+
+
+@pytest.mark.parametrize("change,words", [
+    (dict(out=z(2, dtype=torch.int64)), "out: int64"), (dict(out=z(3, dtype=torch.int32)), "out: int64"),
+    (dict(block_tables=z(2, 4, dtype=torch.int32)), "table shapes"),
+    (dict(cu_q_lens=z(3, dtype=torch.int32)), "table shapes"), (dict(cu_q_lens=z(4, dtype=torch.int64)), "table shapes"),
+])
+def test_slot_mapping_refuses_short_arrays(lib, change, words):
+    good = dict(block_tables=z(3, 4, dtype=torch.int32), seq_lens=z(3, dtype=torch.int32),
+                cu_q_lens=z(4, dtype=torch.int32), num_tokens=3, num_blocks=8, out=z(3, dtype=torch.int64))
+    pa.slot_mapping(**good)
+    assert len(lib.calls) == 1
+    with pytest.raises(pa.PagedAttnError, match=words):
+        pa.slot_mapping(**dict(good, **change))
+    assert len(lib.calls) == 1

@@ -79,3 +79,50 @@ def test_overlapping_rows_are_dropped_and_flagged(kind, name):
     assert torch.equal(out[keep], ref[keep]) and torch.all(torch.isfinite(out[keep]))
     lost = np.setdiff1d(np.arange(T), keep)
     assert torch.all(out[lost] == 3.0)
+
+
+def test_slots_of_rows_outside_and_behind():
+    """Slots of a batch padded to more rows than its sequences have (-1 behind
+    them), and of sequences past the rows (flagged, nothing written)."""
+    bt = torch.arange(12, dtype=torch.int32, device=DEV).view(3, 4)
+    sl = torch.tensor([40, 20, 64], dtype=torch.int32, device=DEV)
+
+    def slots(cu, T):
+        buf = torch.full((T + 300,), 77, dtype=torch.int64, device=DEV)
+        pa.device_error()
+        pa.slot_mapping(bt, sl, torch.tensor(cu, dtype=torch.int32, device=DEV), T, 12, out=buf[:T])
+        torch.cuda.synchronize()
+        assert torch.all(buf[T:] == 77)
+        return buf[:T].tolist(), pa.device_error()
+
+    want = [*range(38, 40), 64 + 19, *range(2 * 64 + 60, 2 * 64 + 64)]
+    assert slots([0, 2, 3, 7], 7) == (want, 0)
+    assert slots([0, 2, 3, 7], 500) == (want + [-1] * 493, 0)
+    assert slots([0, 2, 3, 7], 5) == (want[:3] + [77] * 2, 4)       # the last sequence's rows end past the buffer
+    assert slots([0, 0, 0, 0], 300) == ([-1] * 300, 0)
+    made = pa.slot_mapping(bt, sl, torch.tensor([0, 2, 3, 7], dtype=torch.int32, device=DEV), 90, 12)
+    assert made.tolist() == want + [-1] * 83
+    assert pa.slot_mapping(bt[:0], sl[:0], torch.zeros(1, dtype=torch.int32, device=DEV), 9, 12).tolist() == [-1] * 9
+
+
+def test_a_padded_step_appends_nothing_behind_its_sequences():
+    """Slot mapping, rotate-and-append and attention of a step padded to a fixed
+    number of rows: the caches hold the sequences' tokens and nothing else."""
+    T, pad = 7, 64
+    g = torch.Generator(device=DEV).manual_seed(2)
+    bt = torch.arange(12, dtype=torch.int32, device=DEV).view(3, 4)
+    sl, cu = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([2, 1, 4], [0, 2, 3, 7]))
+    q, k, v = (torch.randn(pad, h, D, generator=g, device=DEV).to(torch.bfloat16) for h in (HQ, HKV, HKV))
+    pos = torch.zeros(pad, dtype=torch.int64, device=DEV)
+    cs = torch.cat([torch.ones(4, D // 2), torch.zeros(4, D // 2)], 1).to(DEV)
+    junk = torch.arange(pad, device=DEV)                  # (the next tensor of this size may be this memory)
+    del junk
+    pools = [torch.zeros(12, 16, HKV, D, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    slots = pa.slot_mapping(bt, sl, cu, pad, 12)
+    pa.paged_rope_kv_write(q, k, v, *pools, slots, pos, cs)
+    torch.cuda.synchronize()
+    flat = pools[1].view(-1, HKV, D)
+    held = torch.tensor([0, 1, 64, *range(128, 132)], device=DEV)
+    assert torch.equal(flat[held], v[:T])
+    flat[held] = 0
+    assert torch.all(flat == 0) and pa.device_error() == 0
