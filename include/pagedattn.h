@@ -82,7 +82,7 @@ extern "C" {
  * run in the decode kernel inside pa_paged_attention_prefill. */
 #define PA_VERIFY_MAX_Q 8
 
-typedef enum { PA_F16 = 0, PA_BF16 = 1 } pa_dtype;
+typedef enum { PA_F16 = 0, PA_BF16 = 1, PA_F32 = 2 /* logits only */ } pa_dtype;
 
 typedef enum {
     PA_OK = 0,
@@ -99,6 +99,7 @@ typedef enum {
 #define PA_DEVERR_TIMEOUT 8    /* a bounded wait for a TMA copy ran out (the work was abandoned) */
 #define PA_DEVERR_WORKSPACE 16 /* an FP8 or 4-bit prefill chunk's 16-bit copy did not fit (its rows were skipped) */
 #define PA_DEVERR_POSITION 32  /* a rotation position outside the cos/sin table (the row was skipped) */
+#define PA_DEVERR_BEAM 64      /* a request's beams cannot be reordered (left as they were; see pa_beam_reorder) */
 
 /* Library ABI version (major * 100 + minor). */
 int pa_version(void);
@@ -583,6 +584,107 @@ int pa_selftest_wait_timeout(void* stream);
  * This call synchronises the stream.
  */
 int pa_get_device_error(int* code, int clear, void* stream);
+
+/*
+ * Cross attention to an encoder's states, held in a paged cache of their own
+ * (written once per request with pa_paged_kv_write).  Sequence b has enc_lens[b]
+ * states (0 or more) and any number of query rows, each of which sees every
+ * state: out[r, h] = sum_t softmax_t(scale * q[r, h] . k_t) v_t over t = 0 ..
+ * enc_lens[b] - 1.  The beams of a request, or the tokens of a decoder prompt,
+ * are rows of one sequence, so that its states are read once for all of them.
+ *   out, q        [num_tokens, num_q_heads, head_dim]
+ *   enc_lens      int32 [num_seqs]; 0 gives rows of zeros.
+ *   cu_q_lens     int32 [num_seqs + 1]: sequence b owns rows cu_q_lens[b] ..
+ *                 cu_q_lens[b+1]-1 (it must not fall); or NULL: num_tokens /
+ *                 num_seqs rows each (max_q_len is then ignored).
+ *   max_q_len, max_enc_len  host-side upper bounds.
+ *   workspace     pa_cross_workspace_bytes(...) bytes, 256-byte aligned; none
+ *                 (NULL) while no sequence has more than PA_VERIFY_MAX_Q rows.
+ * Sequences of at most PA_VERIFY_MAX_Q rows take one launch that splits long
+ * states over a cluster of CTAs; longer chunks run in the tensor-core prefill
+ * kernel.  Rows of no sequence are left as they were.  Errors on the device: an
+ * enc_len below 0, above max_enc_len or past the table sets PA_DEVERR_SEQ_LEN and
+ * gives rows of zeros; so does a sequence with rows outside 0 .. num_tokens - 1
+ * or more of them than max_q_len, which are not written; blocks outside the pool
+ * set PA_DEVERR_BLOCK_ID and contribute nothing.
+ */
+int pa_paged_cross_attention(void* out, const void* q, const void* k_cache, const void* v_cache,
+                             const int32_t* block_tables, int max_blocks_per_seq, const int32_t* enc_lens,
+                             const int32_t* cu_q_lens, int num_seqs, int num_tokens, int max_q_len,
+                             int max_enc_len, int num_blocks, float scale, int num_q_heads, int num_kv_heads,
+                             int head_dim, int block_size, void* workspace, size_t workspace_bytes, int dtype,
+                             void* stream);
+size_t pa_cross_workspace_bytes(int num_seqs, int num_tokens, int max_q_len);
+
+/*
+ * Beam search: the num_out best continuations of every request.  Candidate
+ * (beam w, token v) of request s scores scores[s, w] + x - log(sum of exp) of row
+ * w's logits x (a log-softmax); the best come first, ties go to the lowest
+ * w * vocab + v.  Scores are compared in 64 bits and rounded once (within a beam
+ * the order is that of its logits, also where 64 bits do not tell them apart).
+ *   out_scores, out_parents, out_tokens  fp32, int32, int32 [num_seqs, num_out];
+ *                 a parent is a beam of the request, 0 .. num_beams - 1.
+ *   logits        [num_seqs * num_beams, vocab] of `dtype` (fp16, bf16 or fp32),
+ *                 rows logits_stride elements apart, on any boundary.  NaN counts
+ *                 as -inf, +inf as the type's largest value.
+ *   scores        fp32 [num_seqs, num_beams]; -inf (or NaN) is a beam without
+ *                 candidates (all but one before the first step), +inf the largest.
+ *   finished      uint8 [num_seqs, num_beams], or NULL: where it is not 0, the beam
+ *                 has ended, and its only candidate is end_token at its own score
+ *                 (its logits are not read).
+ *   end_token     -1: none (finished is then NULL).
+ *   out_finished  uint8 [num_seqs, num_out], or NULL: the parent had ended, or the
+ *                 token is end_token.
+ * A request with fewer than num_out candidates above -inf fills up with its lowest
+ * other w * vocab + v, at -inf.  num_beams <= PA_MAX_BEAMS, num_out <=
+ * PA_MAX_BEAM_OUT and num_beams * vocab, vocab <= PA_MAX_VOCAB.  The outputs must
+ * not overlap the inputs.  workspace: pa_beam_select_workspace_bytes(...) bytes,
+ * 256-byte aligned.
+ */
+#define PA_MAX_BEAMS 32
+#define PA_MAX_BEAM_OUT 64
+#define PA_MAX_VOCAB (1 << 20)
+int pa_beam_select(float* out_scores, int32_t* out_parents, int32_t* out_tokens, uint8_t* out_finished,
+                   const void* logits, int64_t logits_stride, const float* scores, const uint8_t* finished,
+                   int end_token, int num_seqs, int num_beams, int vocab, int num_out, int dtype, void* workspace,
+                   size_t workspace_bytes, void* stream);
+size_t pa_beam_select_workspace_bytes(int num_seqs, int num_beams, int vocab, int num_out, int dtype);
+
+typedef enum { PA_CACHE_16BIT = 0, PA_CACHE_FP8 = 1, PA_CACHE_FP4 = 2 } pa_cache_kind;
+
+/*
+ * Beam search: the block tables and caches after a selection.  Row j of request
+ * s (row s * num_beams + j of the tables) goes on from row parents[s, j] of the
+ * same request.  With n = 16 f + t tokens in every row of the request:
+ *   - entries 0 .. f - 1 become the parent's: whole blocks are shared;
+ *   - if t > 0, entry f is a block that each row has to itself.  The lowest child
+ *     of a parent takes over the parent's; the other children take, in ascending
+ *     order, the blocks of the rows without a child, in ascending order, and the
+ *     parent's t tokens are copied there, in every layer (whole tiles in a 4-bit
+ *     cache);
+ *   - later entries stay with their row (blocks allotted in advance).
+ * No block is allocated or freed: the request's rows go on with the blocks that
+ * they had together, and these are freed together.  Before the first call every
+ * row must have a last block of its own (one of them filled, if only one beam
+ * lives; the prompt's whole blocks may be shared).
+ *   tables_out    int32 [num_seqs * num_beams, max_blocks_per_seq]: block_tables
+ *                 itself (in place) or an array apart from it.
+ *   seq_lens      int32 [num_seqs * num_beams]: tokens cached, one length for all
+ *                 rows of a request.
+ *   parents       int32 [num_seqs, num_beams], as pa_beam_select gives them.
+ *   k_caches, v_caches  host arrays of num_layers device pointers (0 or more
+ *                 layers), pools of num_blocks blocks of cache_kind: 16-bit
+ *                 [num_blocks, 16, num_kv_heads, head_dim], FP8 [num_blocks,
+ *                 num_kv_heads, 16, 128] or 4-bit tiles.
+ * A request whose rows differ in length, whose length is past the table or that
+ * names a parent outside 0 .. num_beams - 1 sets PA_DEVERR_BEAM, one in which two
+ * rows have the same last block too; a last block outside the pool sets
+ * PA_DEVERR_BLOCK_ID.  Such a request's tables and caches stay as they were.
+ */
+int pa_beam_reorder(int32_t* tables_out, const int32_t* block_tables, int max_blocks_per_seq,
+                    const int32_t* seq_lens, const int32_t* parents, int num_seqs, int num_beams,
+                    void* const* k_caches, void* const* v_caches, int num_layers, int num_blocks,
+                    int num_kv_heads, int head_dim, int block_size, int cache_kind, void* stream);
 
 #ifdef __cplusplus
 }

@@ -7,8 +7,12 @@ fails loudly if the library has not been built.
 """
 from ._binding import (  # noqa: F401
     PagedAttnError,
+    beam_reorder,
+    beam_select,
+    beam_select_workspace_bytes,
     copy_blocks,
     count_chunk_kv_tokens,
+    cross_workspace_bytes,
     decode_partition,
     decode_partition_for,
     decode_workspace_bytes,
@@ -23,6 +27,7 @@ from ._binding import (  # noqa: F401
     paged_attention_prefill_fp4,
     paged_attention_prefill_fp8,
     paged_attention_prefill_mod,
+    paged_cross_attention,
     paged_kv_gather,
     paged_kv_unpack_fp4,
     paged_kv_write,

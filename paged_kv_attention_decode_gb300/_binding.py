@@ -71,6 +71,12 @@ _SIGNATURES = {
                                              _i32, _i32, _i32, _i32, _i32, _p, _sz, _i32, _p]),
     "pa_paged_attention_prefill_mod": (_i32, [_p, _p, _p, _p, _p, _i32, _p, _p, _i32, _i32, _i32, _i32, _i32,
                                               _f32, _f32, _i32, _p, _i32, _i32, _i32, _i32, _p, _sz, _i32, _p]),
+    "pa_cross_workspace_bytes": (_sz, [_i32, _i32, _i32]),
+    "pa_paged_cross_attention": (_i32, [_p, _p, _p, _p, _p, _i32, _p, _p, _i32, _i32, _i32, _i32, _i32, _f32,
+                                        _i32, _i32, _i32, _i32, _p, _sz, _i32, _p]),
+    "pa_beam_select_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32]),
+    "pa_beam_select": (_i32, [_p, _p, _p, _p, _p, _i64, _p, _p, _i32, _i32, _i32, _i32, _i32, _i32, _p, _sz, _p]),
+    "pa_beam_reorder": (_i32, [_p, _p, _i32, _p, _p, _i32, _i32, _p, _p, _i32, _i32, _i32, _i32, _i32, _i32, _p]),
     "pa_copy_blocks": (_i32, [_p, _p, _p, _i32, _i32, _i32, _i32, _i32, _p]),
     "pa_decode_partition": (_i32, [_i32, _i32]),
     "pa_decode_partition_for": (_i32, [_i32, _i32, _i32, _i32]),
@@ -707,11 +713,12 @@ def paged_kv_unpack_fp4(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: f
     return k_out, v_out
 
 
-def _attn_args(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, alibi_slopes, out, workspace) -> int:
+def _attn_args(q, k_cache, v_cache, block_tables, seq_lens, cu_q_lens, alibi_slopes, out, workspace, B=None) -> int:
     """What the attention calls below ask of their tensors besides the pools'
-    shape; returns the device."""
+    shape (B: the number of sequences, where q does not tell); returns the device."""
     dev = q.get_device()
-    B = q.shape[0] if cu_q_lens is None else seq_lens.shape[0]
+    if B is None:
+        B = q.shape[0] if cu_q_lens is None else seq_lens.shape[0]
     if (dev >= 0 and _cuda_device() == dev and k_cache.get_device() == dev and v_cache.get_device() == dev
             and block_tables.get_device() == dev and seq_lens.get_device() == dev
             and block_tables.dtype == _I32T and seq_lens.dtype == _I32T and seq_lens.numel() == B
@@ -892,4 +899,193 @@ def paged_attention_prefill_mod(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
         _raw_stream(dev))
     if rc:
         _check(rc, "pa_paged_attention_prefill_mod")
+    return out
+
+
+# --------------------------------------------------------------------------
+# Cross attention (16-bit cache)
+# --------------------------------------------------------------------------
+
+def cross_workspace_bytes(num_seqs: int, num_tokens: int, max_q_len: int) -> int:
+    return int(load_library().pa_cross_workspace_bytes(num_seqs, num_tokens, max_q_len))
+
+
+def paged_cross_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                          block_tables: torch.Tensor, enc_lens: torch.Tensor, scale: float,
+                          max_enc_len: int | None = None, cu_q_lens: torch.Tensor | None = None,
+                          max_q_len: int | None = None, out: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of decoder rows q [T, Hq, D] to an encoder's states in a paged
+    cache: every row of sequence b sees its enc_lens[b] states (none: a row of
+    zeros).  The beams of a request, or a prompt's tokens, are rows of one
+    sequence: T / B rows each, or, with cu_q_lens, rows cu_q_lens[b] ..
+    cu_q_lens[b + 1] - 1 (at most max_q_len; both lengths are read from the
+    device when they are not given)."""
+    if stream is not None:
+        return _given(stream, paged_cross_attention, q, k_cache, v_cache, block_tables, enc_lens, scale, max_enc_len,
+                      cu_q_lens, max_q_len, out, workspace)
+    T, Hq, D = q.shape
+    NB, bs, Hkv = _pool16(q, k_cache, v_cache)
+    B = enc_lens.shape[0]
+    dev = _attn_args(q, k_cache, v_cache, block_tables, enc_lens, cu_q_lens, None, out, workspace, B)
+    if cu_q_lens is None:
+        if B == 0 or T % B:
+            _need(B > 0 and T % B == 0, "without cu_q_lens, q holds the same number of rows for every sequence")
+        max_q_len = T // B
+    elif max_q_len is None:
+        max_q_len = int((cu_q_lens[1:] - cu_q_lens[:-1]).max().item()) if B else 0
+    if max_enc_len is None:
+        max_enc_len = int(enc_lens.max().item()) if B else 0
+    if out is None:
+        out = torch.empty_like(q)
+    lib = _lib or load_library()
+    ws, ws_bytes = None, 0
+    if max_q_len > 8:
+        workspace, ws_bytes = _ws(lib.pa_cross_workspace_bytes(B, T, max_q_len), q, workspace)
+        ws = workspace.data_ptr()
+    rc = lib.pa_paged_cross_attention(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+        block_tables.shape[1], enc_lens.data_ptr(), None if cu_q_lens is None else cu_q_lens.data_ptr(), B, T,
+        max_q_len, max_enc_len, NB, float(scale), Hq, Hkv, D, bs, ws, ws_bytes, 0 if q.dtype == _F16 else 1,
+        _raw_stream(dev))
+    if rc:
+        _check(rc, "pa_paged_cross_attention")
+    return out
+
+
+# --------------------------------------------------------------------------
+# Beam search
+# --------------------------------------------------------------------------
+
+_LOGITS = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+
+def beam_select_workspace_bytes(num_seqs: int, num_beams: int, vocab: int, num_out: int, dtype: torch.dtype) -> int:
+    return int(load_library().pa_beam_select_workspace_bytes(num_seqs, num_beams, vocab, num_out, _LOGITS[dtype]))
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int, finished: torch.Tensor | None = None,
+                end_token: int = -1, out=None, workspace: torch.Tensor | None = None, stream=None):
+    """The num_out best continuations of every request: candidate (beam w, token
+    v) scores scores[s, w] + log_softmax(logits[s * W + w])[v], best first, ties to
+    the lowest w * V + v.
+
+    logits [S * W, V] (or [S, W, V]; fp16, bf16 or fp32; rows may be strided),
+    scores float32 [S, W] (-inf: a beam without candidates).  `finished` uint8 or
+    bool [S, W]: an ended beam's only candidate is end_token, at its own score.
+    Returns (scores float32, parents int32, tokens int32), each [S, num_out], and
+    with `finished` a fourth like it: the parent had ended, or the token is
+    end_token.  `out`: these tensors, to write to."""
+    if stream is not None:
+        return _given(stream, beam_select, logits, scores, num_out, finished, end_token, out, workspace)
+    S, W = scores.shape
+    V = logits.shape[-1]
+    rows = logits
+    if logits.dim() == 3 and logits.shape[:2] == (S, W) and (
+            S == 1 or W == 1 or logits.stride(0) == W * logits.stride(1)):
+        rows = logits[:, 0] if W == 1 else logits[0] if S == 1 else logits.flatten(0, 1)
+    dev = logits.get_device()
+    code = _LOGITS.get(logits.dtype)
+    num_out, end_token = int(num_out), int(end_token)
+    shape = (S, num_out)
+    if not (dev >= 0 and _cuda_device() == dev and code is not None and rows.dim() == 2 and rows.shape[0] == S * W
+            and (V <= 1 or rows.stride(1) == 1)
+            and scores.get_device() == dev and scores.dtype == _F32 and scores.is_contiguous()
+            and (finished is None or (finished.get_device() == dev and finished.shape == scores.shape
+                                      and finished.dtype in (torch.uint8, torch.bool) and finished.is_contiguous()
+                                      and 0 <= end_token < V))
+            and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous()))):
+        _refuse("beam_select",
+                (_current(dev, scores, finished, workspace), "tensors must be on the current CUDA device"),
+                (code is not None, f"unsupported dtype {logits.dtype}"),
+                (rows.dim() == 2 and rows.shape[0] == S * W and (V <= 1 or rows.stride(1) == 1),
+                 "logits: [S * W, V], or [S, W, V] with evenly spaced rows, dense within a row"),
+                (scores.dtype == _F32 and scores.is_contiguous(), "scores: contiguous float32 [S, W]"),
+                (finished is None or (finished.shape == scores.shape and finished.dtype in (torch.uint8, torch.bool)
+                                      and finished.is_contiguous()), "finished: contiguous uint8 or bool [S, W]"),
+                (False, "end_token: a token, with finished"))
+    kinds = (_F32, _I32T, _I32T, finished.dtype) if finished is not None else (_F32, _I32T, _I32T)
+    if out is None:
+        _need(num_out > 0, "num_out: at least 1")
+        out = tuple(torch.empty(shape, dtype=t, device=logits.device) for t in kinds)
+    else:
+        out = tuple(out)
+        _need(len(out) == len(kinds) and all(t.get_device() == dev and t.shape == shape and t.dtype == d
+                                             and t.is_contiguous() for t, d in zip(out, kinds)),
+              "out: contiguous tensors [S, num_out] of the results' types")
+    lib = _lib or load_library()
+    nbytes = lib.pa_beam_select_workspace_bytes(S, W, V, num_out, code)
+    workspace, ws_bytes = _ws(nbytes, logits, workspace)
+    rc = lib.pa_beam_select(
+        out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr() if finished is not None else None,
+        rows.data_ptr(), rows.stride(0) if S * W > 1 else V, scores.data_ptr(),
+        None if finished is None else finished.data_ptr(), end_token, S, W, V, num_out, code, workspace.data_ptr(),
+        ws_bytes, _raw_stream(dev))
+    if rc:
+        _check(rc, "pa_beam_select")
+    return out
+
+
+def _pool_kind(t: torch.Tensor):
+    """(kind, num_blocks, num_kv_heads, head_dim) of a pool of any kind."""
+    shape = t.shape
+    if t.dim() == 3 and t.element_size() == 1 and shape[2] % 9 == 0:      # 4-bit tiles
+        return 2, shape[0], shape[1], shape[2] // 9
+    if t.dim() == 4 and t.element_size() == 1 and shape[2] == PA_BLOCK_SIZE:
+        return 1, shape[0], shape[1], shape[3]
+    if t.dim() == 4 and t.element_size() == 2 and shape[1] == PA_BLOCK_SIZE:
+        return 0, shape[0], shape[2], shape[3]
+    _need(False, "pools: 16-bit [NB, 16, Hkv, D], FP8 [NB, Hkv, 16, D] or 4-bit tiles [NB, Hkv, bytes]")
+
+
+def beam_reorder(block_tables: torch.Tensor, seq_lens: torch.Tensor, parents: torch.Tensor, k_caches, v_caches,
+                 out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Block tables and caches after a selection: row j of request s goes on from
+    row parents[s, j] of the same request.
+
+    block_tables int32 [S * W, max_blocks], seq_lens int32 [S * W] (one length for
+    all rows of a request), parents int32 [S, W].  Whole blocks are shared; the
+    last, partly filled block of every row is its own (also before the call): the
+    lowest child of a parent takes over the parent's, the others take those of
+    the rows without a child, and the parent's tokens are copied there in every
+    pool of k_caches and v_caches (a tensor, or one for each layer; of any kind).
+    Entries behind the last token stay with their row.  Returns the new tables,
+    in `out`, by default block_tables itself."""
+    if stream is not None:
+        return _given(stream, beam_reorder, block_tables, seq_lens, parents, k_caches, v_caches, out)
+    ks = [k_caches] if isinstance(k_caches, torch.Tensor) else list(k_caches)
+    vs = [v_caches] if isinstance(v_caches, torch.Tensor) else list(v_caches)
+    if out is None:
+        out = block_tables
+    S, W = parents.shape
+    dev = block_tables.get_device()
+    kind, NB, H, D = _pool_kind(ks[0]) if ks else (0, 2 ** 27 - 1, 1, 64)
+    if not (dev >= 0 and _cuda_device() == dev and block_tables.dtype == _I32T and block_tables.dim() == 2
+            and block_tables.shape[0] == S * W and block_tables.is_contiguous()
+            and out.get_device() == dev and out.shape == block_tables.shape and out.dtype == _I32T
+            and out.is_contiguous()
+            and seq_lens.get_device() == dev and seq_lens.dtype == _I32T and seq_lens.numel() == S * W
+            and seq_lens.is_contiguous()
+            and parents.get_device() == dev and parents.dtype == _I32T and parents.is_contiguous()
+            and len(vs) == len(ks) and all(t.get_device() == dev and t.shape == ks[0].shape
+                                           and t.dtype == ks[0].dtype and t.is_contiguous() for t in ks + vs)):
+        _refuse("beam_reorder",
+                (_current(dev, block_tables, seq_lens, parents, out, *ks, *vs),
+                 "tensors must be on the current CUDA device"),
+                (block_tables.dtype == _I32T and block_tables.dim() == 2 and block_tables.shape[0] == S * W
+                 and block_tables.is_contiguous(), "block_tables: contiguous int32 [S * W, max_blocks]"),
+                (out.shape == block_tables.shape and out.dtype == _I32T and out.is_contiguous(),
+                 "out: the shape and dtype of block_tables"),
+                (seq_lens.dtype == _I32T and seq_lens.numel() == S * W and seq_lens.is_contiguous(),
+                 "seq_lens: int32 [S * W]"),
+                (parents.dtype == _I32T and parents.is_contiguous(), "parents: contiguous int32 [S, W]"),
+                (False, "k_caches and v_caches: as many, contiguous, of one shape and dtype"))
+    n = len(ks)
+    ptrs = _p * n
+    rc = (_lib or load_library()).pa_beam_reorder(
+        out.data_ptr(), block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(), parents.data_ptr(), S, W,
+        ptrs(*[t.data_ptr() for t in ks]), ptrs(*[t.data_ptr() for t in vs]), n, NB, H, D, PA_BLOCK_SIZE, kind,
+        _raw_stream(dev))
+    if rc:
+        _check(rc, "pa_beam_reorder")
     return out

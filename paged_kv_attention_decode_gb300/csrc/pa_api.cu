@@ -123,6 +123,7 @@ bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) 
 size_t align256(size_t x) { return (x + 255u) & ~static_cast<size_t>(255u); }
 
 constexpr int kMaxGrid = 65535;
+static_assert(PA_MAX_BEAMS == pa::kMaxBeams && PA_MAX_BEAM_OUT == pa::kMaxBeamOut, "one limit");
 // Share of the SMs the tcgen05 prefill keeps while decode rows run beside it.
 #ifndef PA_OVERLAP_NUM
 #define PA_OVERLAP_NUM 1
@@ -948,6 +949,224 @@ int pa_paged_attention_prefill_fp8(void* out, const void* q, const void* k_cache
                         num_tokens, max_q_len, max_seq_len, num_blocks, scale, num_q_heads, num_kv_heads, head_dim,
                         workspace, workspace_bytes, dtype, static_cast<cudaStream_t>(stream), Cache::kFp8, k_scale,
                         v_scale);
+}
+
+// Cross attention's workspace, for chunks only: [rows of every sequence (without
+// cu_q_lens) | tile plan].
+size_t pa_cross_workspace_bytes(int num_seqs, int num_tokens, int max_q_len) {
+    if (num_seqs <= 0 || num_tokens < 0 || max_q_len <= PA_VERIFY_MAX_Q) return 0;
+    return align256((static_cast<size_t>(num_seqs) + 1) * sizeof(int32_t)) + plan_bytes(num_seqs, num_tokens);
+}
+
+int pa_paged_cross_attention(void* out, const void* q, const void* k_cache, const void* v_cache,
+                             const int32_t* block_tables, int max_blocks_per_seq, const int32_t* enc_lens,
+                             const int32_t* cu_q_lens, int num_seqs, int num_tokens, int max_q_len, int max_enc_len,
+                             int num_blocks, float scale, int num_q_heads, int num_kv_heads, int head_dim,
+                             int block_size, void* workspace, size_t workspace_bytes, int dtype, void* stream) {
+    int rc = check_shape(num_q_heads, num_kv_heads, head_dim, block_size, dtype, num_blocks);
+    if (rc) return rc;
+    if (num_seqs < 0 || num_seqs > kMaxGrid || num_tokens < 0 || max_q_len < 0 || max_enc_len < 0 ||
+        max_blocks_per_seq <= 0 || max_blocks_per_seq > kMaxPoolBlocks)
+        return PA_ERR_INVALID_ARG;
+    if (!std::isfinite(scale)) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0 || num_tokens == 0) return PA_OK;
+    if (!cu_q_lens) {
+        if (num_tokens % num_seqs) return PA_ERR_INVALID_ARG;
+        max_q_len = num_tokens / num_seqs;
+    }
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !enc_lens) return PA_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_INVALID_ARG;
+    const size_t need = pa_cross_workspace_bytes(num_seqs, num_tokens, max_q_len);
+    if (need) {
+        if (!workspace || workspace_bytes < need) return PA_ERR_WORKSPACE_TOO_SMALL;
+        if (!aligned256(workspace)) return PA_ERR_INVALID_ARG;
+    }
+    const int group = num_q_heads / num_kv_heads;
+    const int max_q = std::min(max_q_len, PA_VERIFY_MAX_Q);
+    const int cols = std::max(1, max_q * group), chunk = cols > 8 ? 16 : 8;
+    const int col_chunks = (cols + chunk - 1) / chunk;
+    // CTAs (up to 8 an item) and query-tile pairs are counted in 32 bits
+    if (static_cast<long long>(num_seqs) * num_kv_heads * col_chunks > (1LL << 27) ||
+        (static_cast<long long>(num_tokens) / 4 + num_seqs) * num_kv_heads > (1LL << 30))
+        return PA_ERR_INVALID_ARG;
+    unsigned int* err = error_word();
+    if (!err) return PA_ERR_CUDA;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    CUtensorMap kbmap, vmap;   // one box per (block, head) tile
+    if (!make_kv_map_block(&kbmap, k_cache, num_blocks, num_kv_heads, head_dim, dtype) ||
+        !make_kv_map_block(&vmap, v_cache, num_blocks, num_kv_heads, head_dim, dtype))
+        return PA_ERR_CUDA;
+    pa::CrossParams c{};
+    c.out = out;
+    c.q = q;
+    c.block_tables = block_tables;
+    c.seq_lens = enc_lens;
+    c.cu_q_lens = cu_q_lens;
+    c.err = err;
+    c.num_seqs = num_seqs;
+    c.num_rows = num_tokens;
+    c.q_per_seq = cu_q_lens ? 0 : max_q_len;
+    c.max_q = max_q;
+    c.max_blocks = max_blocks_per_seq;
+    c.max_len = max_enc_len;
+    c.num_blocks = num_blocks;
+    c.num_q_heads = num_q_heads;
+    c.num_kv_heads = num_kv_heads;
+    c.group = group;
+    c.col_chunks = col_chunks;
+    c.scale_log2 = scale_log2(scale);
+    if (max_q_len > PA_VERIFY_MAX_Q) {
+        uint8_t* ws = static_cast<uint8_t*>(workspace);
+        const int32_t* cu = cu_q_lens;
+        if (!cu) {
+            int32_t* rows = reinterpret_cast<int32_t*>(ws);
+            if (pa::launch_uniform_rows(rows, num_seqs, max_q_len, s) != cudaSuccess) return PA_ERR_CUDA;
+            cu = rows;
+        }
+        pa::PrefillParams p{};
+        p.out = out;
+        p.q = q;
+        p.block_tables = block_tables;
+        p.seq_lens = enc_lens;
+        p.cu_q_lens = cu;
+        p.err = err;
+        p.num_seqs = num_seqs;
+        p.max_blocks = max_blocks_per_seq;
+        p.max_seq_len = max_enc_len;
+        p.num_blocks = num_blocks;
+        p.num_q_heads = num_q_heads;
+        p.num_kv_heads = num_kv_heads;
+        p.group = group;
+        p.scale_log2 = c.scale_log2;
+        p.v_scale = 1.f;
+        p.q_per_tile = 128 / group;
+        p.pair_cap = num_tokens / 4 + num_seqs;
+        p.cross = 1;
+        CUtensorMap kmap, qmap;
+        if (!make_kv_map(&kmap, k_cache, num_blocks, num_kv_heads, head_dim, dtype) ||
+            !make_q_map(&qmap, q, num_tokens, num_q_heads, head_dim, group, p.q_per_tile, dtype))
+            return PA_ERR_CUDA;
+        int32_t* plan = reinterpret_cast<int32_t*>(ws + align256((static_cast<size_t>(num_seqs) + 1) * sizeof(int32_t)));
+        if (pa::launch_prefill_tc(p, plan, kmap, vmap, qmap, head_dim, dtype, max_q_len, num_tokens, nullptr, false,
+                                  s) != cudaSuccess)
+            return PA_ERR_CUDA;
+        if (!cu_q_lens) return PA_OK;   // every sequence is a chunk
+        c.chunks_follow = 1;
+        c.overlap = 1;
+    }
+    return pa::launch_cross(c, kbmap, vmap, head_dim, dtype, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// Pieces of a row of logits, a CTA's each.
+static int select_pieces(int vocab, int dtype) {
+    const int per = pa::beam_chunk_elems(dtype);
+    return (vocab + per - 1) / per;
+}
+
+size_t pa_beam_select_workspace_bytes(int num_seqs, int num_beams, int vocab, int num_out, int dtype) {
+    if (num_seqs <= 0 || num_beams <= 0 || num_beams > PA_MAX_BEAMS || vocab <= 0 || vocab > PA_MAX_VOCAB ||
+        num_out <= 0 || num_out > PA_MAX_BEAM_OUT || dtype < PA_F16 || dtype > PA_F32)
+        return 0;
+    const size_t n = static_cast<size_t>(num_seqs) * num_beams * select_pieces(vocab, dtype);
+    return align256(n * sizeof(uint4)) + n * num_out * sizeof(unsigned long long);
+}
+
+int pa_beam_select(float* out_scores, int32_t* out_parents, int32_t* out_tokens, uint8_t* out_finished,
+                   const void* logits, int64_t logits_stride, const float* scores, const uint8_t* finished,
+                   int end_token, int num_seqs, int num_beams, int vocab, int num_out, int dtype, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+    if (dtype != PA_F16 && dtype != PA_BF16 && dtype != PA_F32) return PA_ERR_UNSUPPORTED;
+    if (num_seqs < 0 || num_seqs > kMaxGrid || num_beams <= 0 || vocab <= 0 || num_out <= 0) return PA_ERR_INVALID_ARG;
+    if (num_beams > PA_MAX_BEAMS || vocab > PA_MAX_VOCAB || num_out > PA_MAX_BEAM_OUT) return PA_ERR_UNSUPPORTED;
+    if (num_out > static_cast<long long>(num_beams) * vocab) return PA_ERR_INVALID_ARG;
+    if (end_token < -1 || end_token >= vocab || (finished && end_token < 0)) return PA_ERR_INVALID_ARG;
+    if (logits_stride < vocab && num_seqs * num_beams > 1) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0) return PA_OK;
+    if (!out_scores || !out_parents || !out_tokens || !logits || !scores) return PA_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(logits) % (dtype == PA_F32 ? 4 : 2)) return PA_ERR_INVALID_ARG;
+    const size_t need = pa_beam_select_workspace_bytes(num_seqs, num_beams, vocab, num_out, dtype);
+    if (!workspace || workspace_bytes < need) return PA_ERR_WORKSPACE_TOO_SMALL;
+    if (!aligned256(workspace)) return PA_ERR_INVALID_ARG;
+    pa::BeamSelectParams p{};
+    p.out_scores = out_scores;
+    p.out_parents = out_parents;
+    p.out_tokens = out_tokens;
+    p.out_finished = out_finished;
+    p.logits = logits;
+    p.scores = scores;
+    p.finished = finished;
+    p.stride = logits_stride;
+    p.num_seqs = num_seqs;
+    p.beams = num_beams;
+    p.vocab = vocab;
+    p.k = num_out;
+    p.end_token = end_token;
+    p.chunks = select_pieces(vocab, dtype);
+    const size_t n = static_cast<size_t>(num_seqs) * num_beams * p.chunks;
+    if (n > (1u << 30)) return PA_ERR_INVALID_ARG;
+    p.piece = static_cast<uint4*>(workspace);
+    p.best = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(workspace) + align256(n * sizeof(uint4)));
+    return pa::launch_beam_select(p, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+int pa_beam_reorder(int32_t* tables_out, const int32_t* block_tables, int max_blocks_per_seq,
+                    const int32_t* seq_lens, const int32_t* parents, int num_seqs, int num_beams,
+                    void* const* k_caches, void* const* v_caches, int num_layers, int num_blocks, int num_kv_heads,
+                    int head_dim, int block_size, int cache_kind, void* stream) {
+    if (block_size != PA_BLOCK_SIZE || num_beams > PA_MAX_BEAMS) return PA_ERR_UNSUPPORTED;
+    if (cache_kind != PA_CACHE_16BIT && cache_kind != PA_CACHE_FP8 && cache_kind != PA_CACHE_FP4)
+        return PA_ERR_UNSUPPORTED;
+    if (head_dim != 128 && (head_dim != 64 || cache_kind == PA_CACHE_FP8)) return PA_ERR_UNSUPPORTED;
+    if (num_seqs < 0 || num_seqs > kMaxGrid || num_beams <= 0 || max_blocks_per_seq <= 0 || num_layers < 0 ||
+        num_blocks <= 0 || num_blocks > kMaxPoolBlocks || num_kv_heads <= 0 || num_kv_heads > kMaxGrid)
+        return PA_ERR_INVALID_ARG;
+    // a request's table entries are counted in 32 bits
+    if (static_cast<long long>(num_beams) * max_blocks_per_seq > (1LL << 30)) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0) return PA_OK;
+    if (!tables_out || !block_tables || !seq_lens || !parents) return PA_ERR_INVALID_ARG;
+    // in place as a whole, or apart
+    const size_t bytes = static_cast<size_t>(num_seqs) * num_beams * max_blocks_per_seq * sizeof(int32_t);
+    const uintptr_t a = reinterpret_cast<uintptr_t>(tables_out), b = reinterpret_cast<uintptr_t>(block_tables);
+    if (a != b && a < b + bytes && b < a + bytes) return PA_ERR_INVALID_ARG;
+    if (num_layers > 0 && (!k_caches || !v_caches)) return PA_ERR_INVALID_ARG;
+    for (int i = 0; i < num_layers; ++i)
+        if (!k_caches[i] || !v_caches[i] || !aligned16(k_caches[i]) || !aligned16(v_caches[i])) return PA_ERR_INVALID_ARG;
+    unsigned int* err = error_word();
+    if (!err) return PA_ERR_CUDA;
+    pa::BeamReorderParams p{};
+    p.tables = block_tables;
+    p.tables_out = tables_out;
+    p.seq_lens = seq_lens;
+    p.parents = parents;
+    p.err = err;
+    p.num_seqs = num_seqs;
+    p.beams = num_beams;
+    p.max_blocks = max_blocks_per_seq;
+    p.num_blocks = num_blocks;
+    if (cache_kind == PA_CACHE_FP4) {   // codes and scales of a token lie apart: whole tiles
+        p.block_bytes = static_cast<int64_t>(num_kv_heads) * fp4_tile_bytes(head_dim);
+    } else if (cache_kind == PA_CACHE_FP8) {
+        p.block_bytes = static_cast<int64_t>(PA_BLOCK_SIZE) * num_kv_heads * head_dim;
+        p.runs = num_kv_heads;
+        p.run_stride = PA_BLOCK_SIZE * head_dim;
+        p.token_bytes = head_dim;
+    } else {
+        p.block_bytes = static_cast<int64_t>(PA_BLOCK_SIZE) * num_kv_heads * head_dim * 2;
+        p.runs = 1;
+        p.token_bytes = num_kv_heads * head_dim * 2;
+    }
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    for (int first = 0; first == 0 || first < num_layers; first += pa::kReorderLayers) {
+        p.first = first == 0;
+        p.layers = std::min(num_layers - first, pa::kReorderLayers);
+        for (int i = 0; i < p.layers; ++i) {
+            p.k[i] = k_caches[first + i];
+            p.v[i] = v_caches[first + i];
+        }
+        if (pa::launch_beam_copy(p, s) != cudaSuccess) return PA_ERR_CUDA;
+    }
+    if (tables_out == block_tables && pa::launch_beam_tables(p, s) != cudaSuccess) return PA_ERR_CUDA;
+    return PA_OK;
 }
 
 int pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* pairs, int num_pairs, int num_blocks,

@@ -1,0 +1,459 @@
+// Cross attention of short rows (decoder steps, beams) over an encoder's states
+// in the paged cache.
+//
+// Sequence b has n encoder states (keys) and c query rows, and every row sees
+// every state: out[r, h] = sum_t softmax_t(scale q[r, h] . k_t) v_t, t < n.  The
+// beams of one request are rows of one sequence, so its states are read once
+// for all of them.  Rows and query heads of a KV head together are columns of
+// two products, S^T = K Q^T and O^T += V^T P^T (mma.sync m16n8k16: 16 states, one
+// block, are the M dimension and 8 or 16 columns the N; with so few columns the
+// work is bound by the states' bytes).  Longer chunks take the tcgen05 kernel.
+//
+// One launch, no plan and no second kernel: a cluster of `splits` CTAs (1 to 8)
+// takes one (sequence, KV head, chunk of columns), its 4 * splits warps take the
+// blocks in turn, each with its own ring of TMA tiles and its own running
+// maximum, sum and accumulator.  The warps of a CTA join theirs in shared
+// memory, the CTAs of a cluster through distributed shared memory, each CTA
+// writing its share of the output.
+#include <algorithm>
+#include <type_traits>
+
+#include "pa_device.cuh"
+
+namespace pa {
+
+namespace {
+
+constexpr int kCrossWarps = 4;
+constexpr int kMaxSplits = 8;         // CTAs of a cluster (the portable limit)
+constexpr unsigned kFull = 0xffffffffu;
+constexpr float kLazyRescaleLog2 = 8.f;   // a column's reference maximum moves only when it has grown by this much
+
+template <int D, int NT>
+struct CrossShape {
+    static constexpr int kCols = 8 * NT;
+    static constexpr int kTileBytes = 16 * D * 2;
+    static constexpr int kStageBytes = 2 * kTileBytes;   // K and V of one block
+    static constexpr int kStages = (NT > 1 ? 3 : 2) * (128 / D);
+    static constexpr int kMinCtas = NT > 1 ? 2 : 3;
+    static constexpr int kRingBytes = kCrossWarps * kStages * kStageBytes;
+    // the join: one fp32 accumulator [column][D] per warp, over the rings
+    static constexpr int kPitch = D + 4;
+    static constexpr int kAccBytes = kCols * kPitch * 4;
+    static_assert(kCrossWarps * kAccBytes <= kRingBytes, "the accumulators are joined where the rings were");
+    static constexpr int kSmemBytes = kRingBytes + 1024;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+// Every thread of every CTA of the cluster; orders shared-memory accesses.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Address of `local` in the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_rank(uint32_t local, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(local), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+    float x;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+    return x;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+    float4 x;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                 : "r"(addr)
+                 : "memory");
+    return x;
+}
+
+// One warp's columns: the fragments of S^T and O^T share column ownership (lane
+// l: columns 8 nt + 2 (l % 4) + {0, 1}), so rescaling moves no data.
+template <typename T, int D, int NT>
+struct CrossState {
+    static constexpr int KS = D / 16;
+    uint32_t qb[KS][NT][2];   // Q^T as the B operand
+    float o[KS][NT][4];       // O^T
+    float m[NT][2], l[NT][2];
+
+    // One block: tiles of 16 states, of which the first nvalid are the sequence's.
+    __device__ __forceinline__ void step(uint8_t* kt, uint8_t* vt, int nvalid, int lane, float scale_log2) {
+        const uint32_t ka = smem_addr(kt), va = smem_addr(vt);
+        float c[NT][4], c2[NT][4];   // two chains: even and odd k-steps
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[nt][e] = c2[nt][e] = 0.f;
+        {
+            const int tok = (lane & 7) + ((lane >> 3) & 1) * 8, dsub = ((lane >> 4) & 1) * 8;
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk) {
+                uint32_t a[4];
+                ldsm_x4(ka + tile_off<D>(tok, kk * 16 + dsub), a[0], a[1], a[2], a[3]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) Mma<T>::run(kk & 1 ? c2[nt] : c[nt], a, qb[kk][nt][0], qb[kk][nt][1]);
+            }
+        }
+        const int r0 = lane >> 2;   // this lane's states: r0 and r0 + 8
+        float mx[NT][2];
+        bool grow = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                c[nt][e] = (c[nt][e] + c2[nt][e]) * scale_log2;
+                if (r0 + (e >> 1) * 8 >= nvalid) c[nt][e] = -INFINITY;
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float x = fmaxf(c[nt][e], c[nt][2 + e]);
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, off));
+                mx[nt][e] = x;
+                grow |= x > m[nt][e] + kLazyRescaleLog2;
+            }
+        }
+        if (__any_sync(kFull, grow)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (!(mx[nt][e] > m[nt][e] + kLazyRescaleLog2)) continue;
+                    const float al = fast_exp2(m[nt][e] - mx[nt][e]);   // (0 at first: m = -inf)
+                    m[nt][e] = mx[nt][e];
+                    l[nt][e] *= al;
+#pragma unroll
+                    for (int mt = 0; mt < KS; ++mt) {
+                        o[mt][nt][e] *= al;
+                        o[mt][nt][2 + e] *= al;
+                    }
+                }
+        }
+        // P, rounded to T for the product with V (weights of 0 to 2^8), its sum kept in fp32
+        uint32_t b0[NT], b1[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            // (a column whose scores are all -inf, or NaN, has no reference yet)
+            const float mu0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], mu1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+            const float p0 = fast_exp2(c[nt][0] - mu0), p1 = fast_exp2(c[nt][1] - mu1);
+            const float p2 = fast_exp2(c[nt][2] - mu0), p3 = fast_exp2(c[nt][3] - mu1);
+            l[nt][0] += p0 + p2;
+            l[nt][1] += p1 + p3;
+            // the B operand wants P[state 2 (l % 4) + e (+ 8)][column l / 4]
+            const uint32_t lo = Elem<T>::pack(p0, p1), hi = Elem<T>::pack(p2, p3);
+            const int src = ((lane & 3) << 3) + (lane >> 3);
+            const uint32_t x0 = __shfl_sync(kFull, lo, src), x1 = __shfl_sync(kFull, lo, src + 4);
+            const uint32_t y0 = __shfl_sync(kFull, hi, src), y1 = __shfl_sync(kFull, hi, src + 4);
+            const uint32_t sel = ((lane >> 2) & 1) ? 0x7632u : 0x5410u;
+            b0[nt] = __byte_perm(x0, x1, sel);
+            b1[nt] = __byte_perm(y0, y1, sel);
+        }
+        if (nvalid < 16) {
+            // rows behind the last state may hold anything: 0 * NaN must not reach O
+            const int n16 = (16 - nvalid) * 8;
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) {
+                uint4* z = reinterpret_cast<uint4*>(vt + h * TileGeom<D>::kHalfBytes + nvalid * 128);
+                for (int i = lane; i < n16; i += 32) z[i] = make_uint4(0, 0, 0, 0);
+            }
+            __syncwarp();
+        }
+        const int tok = (lane & 7) + ((lane >> 4) & 1) * 8, dsub = ((lane >> 3) & 1) * 8;
+#pragma unroll
+        for (int mt = 0; mt < KS; ++mt) {
+            uint32_t a[4];
+            ldsm_x4_t(va + tile_off<D>(tok, mt * 16 + dsub), a[0], a[1], a[2], a[3]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) Mma<T>::run(o[mt][nt], a, b0[nt], b1[nt]);
+        }
+    }
+};
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kCrossWarps * 32, CrossShape<D, NT>::kMinCtas)
+    cross_step_kernel(const CrossParams p, const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap) {
+    using Sh = CrossShape<D, NT>;
+    constexpr int kCols = Sh::kCols;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t bars[kCrossWarps][Sh::kStages];
+    __shared__ float s_m[kCrossWarps][kCols];   // the warps' maxima, then [0]: the CTA's
+    __shared__ float s_l[kCrossWarps][kCols];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    pdl_trigger();
+    // (the same offset in every CTA of the cluster: the accumulators are read across it)
+    uint8_t* smem = smem_raw + (((smem_addr(smem_raw) + 1023u) & ~1023u) - smem_addr(smem_raw));
+    uint8_t* ring = smem + warp * Sh::kStages * Sh::kStageBytes;
+    uint64_t* bar = bars[warp];
+    if (lane == 0) {
+        for (int s = 0; s < Sh::kStages; ++s) mbar_init(&bar[s], 1);
+        fence_barrier_init();
+        prefetch_tensormap(&kmap);
+        prefetch_tensormap(&vmap);
+    }
+    __syncwarp();
+
+    const int S = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+    const int G = p.group;
+    int item = static_cast<int>(blockIdx.x) / S;
+    const int chunk = item % p.col_chunks;
+    item /= p.col_chunks;
+    const int g = item % p.num_kv_heads, b = item / p.num_kv_heads;
+    if (!p.overlap) pdl_wait();
+
+    int row0 = b * p.q_per_seq, qlen = p.q_per_seq;
+    if (p.cu_q_lens) {
+        row0 = p.cu_q_lens[b];
+        qlen = p.cu_q_lens[b + 1] - row0;
+    }
+    const int col0 = chunk * kCols;
+    const int ncols = min(kCols, qlen * G - col0);
+    const bool rows_ok = qlen >= 0 && row0 >= 0 && row0 <= p.num_rows - qlen;
+    // none of the chunk's rows is here: longer chunks are another kernel's
+    // (the same for the whole cluster)
+    if (!rows_ok || qlen > p.max_q || ncols <= 0) {
+        const bool theirs = qlen > PA_VERIFY_MAX_Q_ && p.chunks_follow;
+        if ((!rows_ok || qlen > p.max_q) && !theirs && g == 0 && chunk == 0 && rank == 0 && tid == 0)
+            record_error(p.err, PA_DEVERR_SEQ_LEN_);
+        if (p.overlap) pdl_wait();
+        return;
+    }
+    int n = p.seq_lens[b];
+    if (n < 0 || n > p.max_len || n > p.max_blocks * 16) {   // rows of zeros, as for no states
+        if (g == 0 && chunk == 0 && rank == 0 && tid == 0) record_error(p.err, PA_DEVERR_SEQ_LEN_);
+        n = 0;
+    }
+    const int nblk = (n + 15) >> 4;
+
+    // this warp's blocks: first, first + stride, ...
+    const int first = rank * kCrossWarps + warp, stride = S * kCrossWarps;
+    const int count = nblk > first ? (nblk - first + stride - 1) / stride : 0;
+    const int32_t* table = p.block_tables + static_cast<int64_t>(b) * p.max_blocks + first;
+    int at = 0, issued = 0, ids = 0;
+    bool partial = false;   // the last block issued is the sequence's last, and not full
+    auto fetch = [&]() {    // the next block whose id is in the pool (others contribute nothing)
+        while (at < count) {
+            if ((at & 31) == 0) ids = at + lane < count ? table[static_cast<int64_t>(at + lane) * stride] : 0;
+            const int id = __shfl_sync(kFull, ids, at & 31);
+            const int blk = first + at * stride;
+            ++at;
+            if (id < 0 || id >= p.num_blocks) {
+                if (lane == 0) record_error(p.err, PA_DEVERR_BLOCK_ID_);
+                continue;
+            }
+            if (lane == 0) {
+                const int slot = issued % Sh::kStages;
+                uint8_t* dst = ring + slot * Sh::kStageBytes;
+                mbar_arrive_expect_tx(&bar[slot], Sh::kStageBytes);
+                tma_load_4d(dst, &kmap, &bar[slot], 0, id * 16, 0, g);
+                tma_load_4d(dst + Sh::kTileBytes, &vmap, &bar[slot], 0, id * 16, 0, g);
+            }
+            ++issued;
+            partial = blk == nblk - 1 && (n & 15);
+            return;
+        }
+    };
+    for (int s = 0; s < Sh::kStages; ++s) fetch();
+
+    CrossState<T, D, NT> st;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int cl = nt * 8 + (lane >> 2);
+        const bool live = cl < ncols;
+        const int c = col0 + (live ? cl : 0);
+        const int qi = c / G, h = c - qi * G;
+        const uint16_t* q = static_cast<const uint16_t*>(p.q) +
+                            (static_cast<int64_t>(row0 + qi) * p.num_q_heads + g * G + h) * D + 2 * (lane & 3);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            st.qb[kk][nt][0] = live ? *reinterpret_cast<const uint32_t*>(q + kk * 16) : 0u;
+            st.qb[kk][nt][1] = live ? *reinterpret_cast<const uint32_t*>(q + kk * 16 + 8) : 0u;
+        }
+        st.m[nt][0] = st.m[nt][1] = -INFINITY;
+        st.l[nt][0] = st.l[nt][1] = 0.f;
+    }
+#pragma unroll
+    for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) st.o[mt][nt][e] = 0.f;
+
+    int done = 0;
+    bool ok = true;
+    while (done < issued) {
+        const int slot = done % Sh::kStages;
+        ok = __all_sync(kFull, mbar_wait(&bar[slot], (done / Sh::kStages) & 1));
+        if (!ok) break;
+        uint8_t* t = ring + slot * Sh::kStageBytes;
+        st.step(t, t + Sh::kTileBytes, partial && done + 1 == issued ? n & 15 : 16, lane, p.scale_log2);
+        ++done;
+        __syncwarp();
+        fetch();
+    }
+    if (!ok) {
+        // give up: the copies still in flight first (another bounded wait each)
+        if (lane == 0) {
+            record_error(p.err, PA_DEVERR_TIMEOUT_);
+            for (int i = done + 1; i < issued; ++i) (void)mbar_wait(&bar[i % Sh::kStages], (i / Sh::kStages) & 1);
+        }
+        __syncwarp();
+    }
+
+    // the CTA's warps: every accumulator relative to the CTA's maximum, summed in warp order
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float l = st.l[nt][e];
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(kFull, l, off);
+            st.l[nt][e] = l;
+            if (lane < 4) s_m[warp][nt * 8 + 2 * lane + e] = st.m[nt][e];
+        }
+    __syncthreads();   // (and every ring is read)
+    float* acc = reinterpret_cast<float*>(smem);
+    float mc[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int col = nt * 8 + 2 * (lane & 3) + e;
+            float m = s_m[0][col];
+#pragma unroll
+            for (int w = 1; w < kCrossWarps; ++w) m = fmaxf(m, s_m[w][col]);
+            mc[nt][e] = m;
+            const float f = st.m[nt][e] == -INFINITY ? 0.f : fast_exp2(st.m[nt][e] - m);
+            if (lane < 4) s_l[warp][col] = st.l[nt][e] * f;
+            float* dst = acc + warp * (Sh::kAccBytes / 4) + col * Sh::kPitch + (lane >> 2);
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt) {
+                dst[mt * 16] = st.o[mt][nt][e] * f;
+                dst[mt * 16 + 8] = st.o[mt][nt][2 + e] * f;
+            }
+        }
+    __syncthreads();
+    if (warp == 0 && lane < 4) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int col = nt * 8 + 2 * lane + e;
+                s_m[0][col] = mc[nt][e];
+                float l = s_l[0][col];
+#pragma unroll
+                for (int w = 1; w < kCrossWarps; ++w) l += s_l[w][col];
+                s_l[0][col] = l;
+            }
+    }
+    for (int i = tid; i < ncols * (D / 4); i += kCrossWarps * 32) {
+        float4* x = reinterpret_cast<float4*>(acc + (i / (D / 4)) * Sh::kPitch) + i % (D / 4);
+        float4 sum = *x;
+#pragma unroll
+        for (int w = 1; w < kCrossWarps; ++w) {
+            const float4 y = x[w * (Sh::kAccBytes / 16)];
+            sum.x += y.x; sum.y += y.y; sum.z += y.z; sum.w += y.w;
+        }
+        *x = sum;
+    }
+    // the cluster's CTAs: each joins a share of the columns' 8-dim pieces
+    if (S > 1) cluster_sync();
+    else __syncthreads();
+    const uint32_t a_acc = smem_addr(acc), a_m = smem_addr(&s_m[0][0]), a_l = smem_addr(&s_l[0][0]);
+    for (int i = rank * kCrossWarps * 32 + tid; i < ncols * (D / 8); i += S * kCrossWarps * 32) {
+        const int col = i / (D / 8), piece = i % (D / 8);
+        const uint32_t off = static_cast<uint32_t>((col * Sh::kPitch + piece * 8) * 4);
+        float m = -INFINITY;
+        for (int r = 0; r < S; ++r) m = fmaxf(m, ld_cluster(map_rank(a_m + col * 4, r)));
+        float l = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int r = 0; r < S; ++r) {
+            const float mr = ld_cluster(map_rank(a_m + col * 4, r));
+            const float f = mr == -INFINITY ? 0.f : fast_exp2(mr - m);
+            const uint32_t base = map_rank(a_acc + off, r);
+            const float4 u = ld_cluster4(base), v = ld_cluster4(base + 16);
+            l += f * ld_cluster(map_rank(a_l + col * 4, r));
+            x[0] += f * u.x; x[1] += f * u.y; x[2] += f * u.z; x[3] += f * u.w;
+            x[4] += f * v.x; x[5] += f * v.y; x[6] += f * v.z; x[7] += f * v.w;
+        }
+        const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;   // (a NaN stays)
+        const int c = col0 + col, qi = c / G, h = c - qi * G;
+        uint4 o;
+        o.x = Elem<T>::pack(x[0] * inv, x[1] * inv);
+        o.y = Elem<T>::pack(x[2] * inv, x[3] * inv);
+        o.z = Elem<T>::pack(x[4] * inv, x[5] * inv);
+        o.w = Elem<T>::pack(x[6] * inv, x[7] * inv);
+        reinterpret_cast<uint4*>(static_cast<T*>(p.out) +
+                                 (static_cast<int64_t>(row0 + qi) * p.num_q_heads + g * G + h) * D)[piece] = o;
+    }
+    if (S > 1) cluster_sync();   // no CTA leaves while its accumulators are read
+    if (p.overlap) pdl_wait();
+}
+
+template <typename T, int D, int NT>
+cudaError_t launch_t(const CrossParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int splits,
+                     cudaStream_t s) {
+    constexpr int smem = CrossShape<D, NT>::kSmemBytes;
+    auto kern = cross_step_kernel<T, D, NT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.num_seqs) * p.num_kv_heads * p.col_chunks * splits);
+    cfg.blockDim = dim3(kCrossWarps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = splits;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, p, kmap, vmap);
+}
+
+__global__ void __launch_bounds__(256) uniform_rows_kernel(int32_t* cu, int num_seqs, int per) {
+    pdl_trigger();
+    pdl_wait();
+    for (int i = blockIdx.x * 256 + threadIdx.x; i <= num_seqs; i += gridDim.x * 256) cu[i] = i * per;
+}
+
+}  // namespace
+
+cudaError_t launch_uniform_rows(int32_t* cu, int num_seqs, int per, cudaStream_t s) {
+    return launch_pdl(uniform_rows_kernel, dim3(std::min(num_seqs / 256 + 1, 64)), dim3(256), 0, s, cu, num_seqs, per);
+}
+
+cudaError_t launch_cross(const CrossParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int head_dim,
+                         int dtype, cudaStream_t s) {
+    // CTAs for one item: more while the items alone do not fill the GPU and every
+    // warp still has a few blocks
+    const long long items = static_cast<long long>(p.num_seqs) * p.num_kv_heads * p.col_chunks;
+    const int blocks = (p.max_len + 15) / 16;
+    int splits = 1;
+    while (splits < kMaxSplits && items * splits < 6LL * sm_count() && blocks >= splits * kCrossWarps * 4) splits *= 2;
+    const bool wide = p.max_q * p.group > 8;
+    auto go = [&](auto t, auto d) {
+        using T = decltype(t);
+        constexpr int D = decltype(d)::value;
+        return wide ? launch_t<T, D, 2>(p, kmap, vmap, splits, s) : launch_t<T, D, 1>(p, kmap, vmap, splits, s);
+    };
+    auto of = [&](auto t) {
+        return head_dim == 128 ? go(t, std::integral_constant<int, 128>{}) : go(t, std::integral_constant<int, 64>{});
+    };
+    return dtype == 0 ? of(__half{}) : of(__nv_bfloat16{});
+}
+
+}  // namespace pa

@@ -13,6 +13,7 @@
 #define PA_DEVERR_TIMEOUT_ 8u
 #define PA_DEVERR_WORKSPACE_ 16u
 #define PA_DEVERR_POSITION_ 32u
+#define PA_DEVERR_BEAM_ 64u
 
 namespace pa {
 
@@ -125,6 +126,70 @@ struct PrefillParams {
     // decode row costs decode_weight key tiles of a query-tile pair
     int32_t* split;
     float decode_weight;
+    int cross;                    // 1: cross attention (seq_lens count the keys, which every query sees)
+};
+
+// Cross attention of short rows (at most PA_VERIFY_MAX_Q_ queries a sequence).
+struct CrossParams {
+    void* out;                    // [T, Hq, D]
+    const void* q;
+    const int32_t* block_tables;  // [B, max_blocks]
+    const int32_t* seq_lens;      // [B] keys of every sequence
+    const int32_t* cu_q_lens;     // [B + 1], or nullptr: q_per_seq rows each
+    unsigned int* err;
+    int num_seqs;
+    int num_rows;                 // T
+    int q_per_seq;                // without cu_q_lens
+    int max_q;                    // most queries of a sequence handled here
+    int chunks_follow;            // 1: sequences of more than PA_VERIFY_MAX_Q_ queries are another kernel's
+    int max_blocks;
+    int max_len;
+    int num_blocks;
+    int num_q_heads;
+    int num_kv_heads;
+    int group;
+    int col_chunks;               // chunks of 8 or 16 (query, head) columns
+    float scale_log2;
+    // 1: launched right behind a prefill kernel that allows dependent launch;
+    // what this one reads was complete before that one started
+    int overlap;
+};
+
+// Selection of the best continuations (see pa_beam.cu).
+constexpr int kMaxBeams = 32, kMaxBeamOut = 64;
+struct BeamSelectParams {
+    float* out_scores;            // [S, k]
+    int32_t* out_parents;
+    int32_t* out_tokens;
+    uint8_t* out_finished;        // or nullptr
+    const void* logits;           // [S * W, V], row stride in elements
+    const float* scores;          // [S, W]
+    const uint8_t* finished;      // [S, W] or nullptr
+    int64_t stride;
+    int num_seqs, beams, vocab, k, end_token;
+    int chunks;                   // pieces of a row
+    uint4* piece;                 // [S * W, chunks]: maximum, sum (fp32 bits), entries
+    unsigned long long* best;     // [S * W, chunks, k] keys, best first
+};
+
+// Reordering of beams: kinds of pool are runs of `run_bytes` per token, `runs`
+// of them `run_stride` bytes apart, or whole blocks (token_bytes 0).
+constexpr int kReorderLayers = 64;   // pools of one launch
+struct BeamReorderParams {
+    const int32_t* tables;        // [S * W, max_blocks]
+    int32_t* tables_out;          // the same, or another array
+    const int32_t* seq_lens;      // [S * W]
+    const int32_t* parents;       // [S, W]
+    unsigned int* err;
+    int num_seqs, beams, max_blocks, num_blocks;
+    int64_t block_bytes;
+    int runs;
+    int run_stride;               // bytes between the runs of a block
+    int token_bytes;              // bytes of a token in a run; 0: the whole block
+    int layers;                   // of this launch
+    int first;                    // the launch that reports errors (and writes tables_out, if not in place)
+    void* k[kReorderLayers];
+    void* v[kReorderLayers];
 };
 
 // Rotation and cache write of new tokens; strides count elements between tokens.
@@ -189,6 +254,15 @@ cudaError_t launch_decode_mod(const DecodeParams& p, const CUtensorMap& kmap, co
                               int head_dim, int dtype, cudaStream_t s);
 // 4-bit cache (p.k_pool / p.v_pool).
 cudaError_t launch_decode_fp4(const DecodeParams& p, int head_dim, int dtype, cudaStream_t s);
+// cu[i] = i * per, i <= num_seqs
+cudaError_t launch_uniform_rows(int32_t* cu, int num_seqs, int per, cudaStream_t s);
+cudaError_t launch_cross(const CrossParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int head_dim,
+                         int dtype, cudaStream_t s);
+// dtype: 0 fp16, 1 bf16, 2 fp32
+int beam_chunk_elems(int dtype);
+cudaError_t launch_beam_select(const BeamSelectParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_beam_copy(const BeamReorderParams& p, cudaStream_t s);
+cudaError_t launch_beam_tables(const BeamReorderParams& p, cudaStream_t s);   // in place, behind the copies
 cudaError_t launch_widen_fp4(const Fp8Copy& c, const int32_t* seq_lens, int max_blocks, int num_kv_heads,
                              int head_dim, int dtype, cudaStream_t s);
 // cache: 0 the 16-bit type of the tokens, 1 FP8 (E4M3, head-major), 2 4-bit.

@@ -71,7 +71,8 @@ constexpr float kRescaleLog2 = 8.f;
 constexpr float kPLazyMax = 256.f;   // 2^kRescaleLog2: a tile's sum of P below it needs no row maximum
 constexpr unsigned kFullMask = 0xffffffffu;
 
-enum { kPlain = 0, kWindow = 1, kCapped = 2, kBiased = 3 };   // kinds of scores
+// kinds of scores; kCross: every query sees all of the sequence's keys
+enum { kPlain = 0, kWindow = 1, kCapped = 2, kBiased = 3, kCross = 4 };
 
 template <int D>
 struct TcShape {
@@ -202,6 +203,8 @@ __device__ __forceinline__ int pair_key_tiles(int n, int ql, int qt, int pr, int
     const int q_last = min(ql, (last + 1) * qt) - 1;
     return (n - ql + q_last + kTcKeys) / kTcKeys - window_start(n - ql + 2 * pr * qt, window) / kTcKeys;
 }
+// The same with cross attention: every pair reads all of the sequence's keys.
+__device__ __forceinline__ int cross_key_tiles(int n) { return (n + kTcKeys - 1) / kTcKeys; }
 
 // One 16-byte run of E4M3 codes (16 elements) widened to 16-bit values of
 // type T: two 16-byte runs (exact: every E4M3 value is an fp16 and a bf16
@@ -346,7 +349,7 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
                                                             int32_t* __restrict__ offsets, int pair_cap,
                                                             unsigned int* err, const Fp8Copy copy, int max_seq_len,
                                                             int max_blocks, int window, int32_t* split,
-                                                            int split_ctas, float decode_weight) {
+                                                            int split_ctas, float decode_weight, int cross) {
     __shared__ int warp_tot[32];
     __shared__ unsigned long long chunk_cost, row_cost;   // key tiles of pairs; keys of decode and verify rows
     __shared__ int carry, blk_carry, chunk_carry, blk_end;
@@ -389,7 +392,8 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
     };
     auto bucket = [&](int n, int ql, int pr) {
         // a malformed sequence (skipped by the kernel) goes to class 0
-        const int c = (n >= ql && ql > 0) ? pair_key_tiles(n, ql, q_per_tile, pr, window) : 0;
+        const int c = cross ? (n > 0 && n <= max_seq_len ? cross_key_tiles(n) : 0)
+                            : (n >= ql && ql > 0) ? pair_key_tiles(n, ql, q_per_tile, pr, window) : 0;
         return kPlanBuckets - 1 - max(0, min(c, kPlanBuckets - 1));   // longest first
     };
     for (int base = 0; base < num_seqs; base += 1024) {
@@ -564,14 +568,17 @@ __global__ void __launch_bounds__(kWidenThreads) widen_chunk_blocks_kernel(const
 // instead of 329, before hidden keys came from bits).  With a window a pair's key tiles
 // start at the tile of its first query's first key (tile index j0 + j); blocks
 // wholly before that key are not read (their table entries may be anything),
-// their keys are masked and their V rows cleared.
+// their keys are masked and their V rows cleared.  kCross (cross attention):
+// every query sits at the last key, so that all tiles of a chunk read all keys
+// and only the last key tile is masked; a sequence without keys gets rows of
+// zeros.
 template <typename T, int D, int kMode>
 __global__ void __launch_bounds__(kTcThreads, 1)
     prefill_tc_kernel(const PrefillParams p, const int32_t* plan,
                       const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                       const __grid_constant__ CUtensorMap qmap) {
     using Sh = TcShape<D>;
-    constexpr bool kMod = kMode != kPlain;
+    constexpr bool kMod = kMode != kPlain && kMode != kCross;
     constexpr int NK = Sh::kKStages;
     constexpr int NV = Sh::kVStages;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -694,15 +701,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int npairs = (ntiles + kTcTiles - 1) / kTcTiles;
         const int pr = npairs - 1 - (l - plan[b]);
         it.n = p.seq_lens[b];
-        if (it.n < it.qlen || it.n > p.max_seq_len || it.n > p.max_blocks * 16) {
+        const int least = kMode == kCross ? 0 : it.qlen;
+        if (it.n < least || it.n > p.max_seq_len || it.n > p.max_blocks * 16) {
             if (pr == npairs - 1 && it.g == 0 && tid == 0) record_error(p.err, PA_DEVERR_SEQ_LEN_);
+            it.n = 0;
+            if constexpr (kMode == kCross) it.q0[0] = pr * kTcTiles * QT;
             return false;
+        }
+        if constexpr (kMode == kCross) {
+            it.q0[0] = pr * kTcTiles * QT;
+            if (it.n == 0) return false;   // (its rows of zeros: zero_rows)
         }
 #pragma unroll
         for (int x = 0; x < kTcTiles; ++x) {
             const int qt = pr * kTcTiles + x;
             it.q0[x] = qt * QT;
-            if (qt < ntiles) {
+            if (kMode == kCross && qt < ntiles) {
+                it.pos_lo[x] = it.pos_hi[x] = it.n - 1;
+                it.nkx[x] = cross_key_tiles(it.n);
+            } else if (qt < ntiles) {
                 const int q_last = min(it.qlen, it.q0[x] + QT) - 1;
                 it.pos_lo[x] = it.n - it.qlen + it.q0[x];
                 it.pos_hi[x] = it.n - it.qlen + q_last;
@@ -724,6 +741,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         it.nblk_live = (it.pos_pair + 16) >> 4;
         it.bt = p.block_tables + static_cast<int64_t>(b) * p.max_blocks;
         return true;
+    };
+
+    // cross attention without keys: the pair's rows of zeros, by the softmax warps
+    auto zero_rows = [&](const Item& it) {
+        const int rows = min(kTcTiles * QT, it.qlen - it.q0[0]);   // queries of the pair
+        constexpr int CPR = D / 8;
+        for (int i = tid; i < rows * G * CPR; i += kTcMmaWarp * 32) {
+            const int row = i / (G * CPR), c = i - row * G * CPR;
+            reinterpret_cast<uint4*>(static_cast<T*>(p.out) +
+                                     (static_cast<int64_t>(it.row0 + it.q0[0] + row) * p.num_q_heads + it.g * G) *
+                                         D)[c] = make_uint4(0, 0, 0, 0);
+        }
     };
 
     // the CTA's k-th item: kNoMoreItems past the end, -1 when round k has
@@ -762,13 +791,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t s_tm = tmem + lane_base + static_cast<uint32_t>(x * kTcKeys);
         const uint32_t o_tm = tmem + lane_base + static_cast<uint32_t>(kTcTiles * kTcKeys + x * D);
         // scale folded into the exponent's FMA
-        const bool fold = (kMode == kPlain || kMode == kWindow) && p.scale_log2 > 0.f;
+        const bool fold = (kMode == kPlain || kMode == kWindow || kMode == kCross) && p.scale_log2 > 0.f;
         int n_items_x = 0;   // items of this tile so far (o_done phases)
         for (int k = 0; ok; ++k) {
             const int w0 = item_at(k);
             if (w0 == kNoMoreItems) break;
             Item it;
-            if (w0 < 0 || !decode_item(w0, it)) continue;
+            if (w0 < 0) continue;
+            if (!decode_item(w0, it)) {
+                if constexpr (kMode == kCross) zero_rows(it);
+                continue;
+            }
             const int nk = x ? it.nkx[1] : it.nkx[0];
             const int nk_a = it.nkx[0];
             const int q0 = x ? it.q0[1] : it.q0[0];
@@ -778,7 +811,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (nk > 0) {
                 const int qi_row = q0 + r / G;
                 const bool row_ok = r < QT * G && qi_row < it.qlen;
-                const int pos_row = row_ok ? it.n - it.qlen + qi_row : pos_hi;
+                const int pos_row = kMode != kCross && row_ok ? it.n - it.qlen + qi_row : pos_hi;
                 // does the item's live table hold an id outside the pool?  (One
                 // scan per item keeps table loads off the per-tile path.)
                 bool any_bad = false;
@@ -1254,9 +1287,18 @@ cudaError_t launch_t(const PrefillParams& p, int32_t* plan, const CUtensorMap& k
     }();
     if (launch_regs < kTcLaunchRegs) return cudaErrorInvalidConfiguration;
     const Fp8Copy none{};
-    e = launch_pdl(prefill_plan_kernel, dim3(1), dim3(1024), 0, s, p.cu_q_lens, p.seq_lens, p.num_seqs, num_tokens,
-                   p.q_per_tile, plan, p.pair_cap, p.err, copy ? *copy : none, p.max_seq_len, p.max_blocks,
-                   p.mod.window, p.split, sm_count(), p.decode_weight);
+    // The plan reads its inputs at once: behind a decode plan, which starts when all
+    // earlier work is complete, it may run early; on its own it may not.
+    auto plan_args = [&](auto launch) {
+        return launch(p.cu_q_lens, p.seq_lens, p.num_seqs, num_tokens, p.q_per_tile, plan, p.pair_cap, p.err,
+                      copy ? *copy : none, p.max_seq_len, p.max_blocks, p.mod.window, p.split, sm_count(),
+                      p.decode_weight, p.cross);
+    };
+    e = p.cross ? plan_args([&](auto... a) {
+        prefill_plan_kernel<<<1, 1024, 0, s>>>(a...);
+        return cudaGetLastError();
+    })
+                : plan_args([&](auto... a) { return launch_pdl(prefill_plan_kernel, dim3(1), dim3(1024), 0, s, a...); });
     if (e != cudaSuccess) return e;
     if (copy && copy->fp4) {
         e = launch_widen_fp4(*copy, p.seq_lens, p.max_blocks, p.num_kv_heads, D, std::is_same<T, __half>::value ? 0 : 1,
@@ -1293,6 +1335,7 @@ cudaError_t launch_prefill_tc(const PrefillParams& p, int32_t* plan, const CUten
         if (dtype == 0) return head_dim == 128 ? go(launch_t<__half, 128, kMode>) : go(launch_t<__half, 64, kMode>);
         return head_dim == 128 ? go(launch_t<__nv_bfloat16, 128, kMode>) : go(launch_t<__nv_bfloat16, 64, kMode>);
     };
+    if (p.cross) return of(std::integral_constant<int, kCross>{});
     if (!modified) return of(std::integral_constant<int, kPlain>{});
     if (p.mod.slopes) return of(std::integral_constant<int, kBiased>{});
     if (p.mod.cap_log2 > 0.f) return of(std::integral_constant<int, kCapped>{});
