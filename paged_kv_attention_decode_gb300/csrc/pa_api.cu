@@ -1057,17 +1057,12 @@ int pa_paged_cross_attention(void* out, const void* q, const void* k_cache, cons
     return pa::launch_cross(c, kbmap, vmap, head_dim, dtype, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-// Pieces of a row of logits, a CTA's each.
-static int select_pieces(int vocab, int dtype) {
-    const int per = pa::beam_chunk_elems(dtype);
-    return (vocab + per - 1) / per;
-}
 
 size_t pa_beam_select_workspace_bytes(int num_seqs, int num_beams, int vocab, int num_out, int dtype) {
-    if (num_seqs <= 0 || num_beams <= 0 || num_beams > PA_MAX_BEAMS || vocab <= 0 || vocab > PA_MAX_VOCAB ||
+    if (num_seqs <= 0 || num_seqs > kMaxGrid || num_beams <= 0 || num_beams > PA_MAX_BEAMS || vocab <= 0 || vocab > PA_MAX_VOCAB ||
         num_out <= 0 || num_out > PA_MAX_BEAM_OUT || dtype < PA_F16 || dtype > PA_F32)
         return 0;
-    const size_t n = static_cast<size_t>(num_seqs) * num_beams * select_pieces(vocab, dtype);
+    const size_t n = static_cast<size_t>(num_seqs) * num_beams * pa::beam_pieces(num_seqs * num_beams, vocab, dtype);
     return align256(n * sizeof(uint4)) + n * num_out * sizeof(unsigned long long);
 }
 
@@ -1101,7 +1096,7 @@ int pa_beam_select(float* out_scores, int32_t* out_parents, int32_t* out_tokens,
     p.vocab = vocab;
     p.k = num_out;
     p.end_token = end_token;
-    p.chunks = select_pieces(vocab, dtype);
+    p.chunks = pa::beam_pieces(num_seqs * num_beams, vocab, dtype);
     const size_t n = static_cast<size_t>(num_seqs) * num_beams * p.chunks;
     if (n > (1u << 30)) return PA_ERR_INVALID_ARG;
     p.piece = static_cast<uint4*>(workspace);

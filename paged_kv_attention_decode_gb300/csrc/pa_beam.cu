@@ -19,8 +19,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 // ---------------------------------------------------------------------------
 // Candidate (beam w, token v) of a request scores score[w] + x[w, v] - lse(x[w]);
 // the k best of its W * V candidates are wanted, ties to the lowest w * V + v.
-// Two kernels.  The first reads every logit once: a CTA holds 16 KB of a row in
-// registers, sums its exponentials and lists its k largest logits in order.
+// Two kernels.  The first reads every logit once: a CTA holds 16 or 32 KB of a row
+// in registers, sums its exponentials and lists its k largest logits in order.
 // The second joins a row's pieces and a request's rows.
 //
 // Within a row the order of scores is the order of logits, so the first kernel
@@ -34,10 +34,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 // -inf (and NaN, which counts as -inf) never enters a list: a request with
 // fewer than k finite candidates fills up with the lowest other indices.
 constexpr int kSelThreads = 256;
-constexpr int kSelVecs = 4;                     // 16-byte pieces of a row per thread
-constexpr int kSelGroups = 64;                  // groups of 4 threads, >= kMaxBeamOut
+constexpr int kSelGroups = kSelThreads / 4;     // groups of 4 threads
 constexpr int kSelCap = 512;                    // candidates ranked at once
-static_assert(kSelGroups >= kMaxBeamOut && kSelThreads == 4 * kSelGroups, "k groups give k candidates");
+static_assert(kSelGroups >= kMaxBeamOut, "k groups give k candidates");
 
 using u64 = unsigned long long;
 
@@ -53,61 +52,77 @@ __device__ __forceinline__ u64 key_of(float x, int index) {
     // (-0 and +0 are one value)
     return static_cast<u64>(ordered(x + 0.f)) << 32 | static_cast<uint32_t>(~index);
 }
-__device__ __forceinline__ u64 shfl_xor64(u64 x, int off) { return __shfl_xor_sync(kFull, x, off); }
 
-// A 16-byte piece of a row: values as fp32, NaN as -inf, +inf as the type's largest.
+// (x, y) <- (x + a, y + b) and (x * f, y * f), one instruction each
+__device__ __forceinline__ void add_pair(float& x, float& y, float a, float b) {
+    asm("{\n\t.reg .b64 p, q, d;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+        "add.rn.f32x2 d, p, q;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void mul_pair(float& x, float& y, float f) {
+    asm("{\n\t.reg .b64 p, q, d;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\t"
+        "mul.rn.f32x2 d, p, q;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(f));
+}
+
+// 16-byte words of a row.
 template <typename T> struct Logits;
 template <> struct Logits<float> {
     static constexpr int kPer = 4;
-    static __device__ __forceinline__ uint4 clean(uint4 v) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w[i] = __float_as_uint(fminf(fmaxf(__uint_as_float(w[i]), -INFINITY), FLT_MAX));
-        return v;
+    static constexpr float kTop = FLT_MAX;
+    // NaN as -inf, +inf as the type's largest
+    static __device__ __forceinline__ uint32_t clean(uint32_t w) {
+        return __float_as_uint(fminf(fmaxf(__uint_as_float(w), -INFINITY), FLT_MAX));
     }
-    static __device__ __forceinline__ float most(const uint4& v) {
-        return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)),
-                     fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
-    }
-    static __device__ __forceinline__ float get(const uint4& v, int i) {
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
-        return __uint_as_float(w[i]);
-    }
-    static __device__ __forceinline__ void put(uint4& v, int i, const float* src) {
-        reinterpret_cast<uint32_t*>(&v)[i] = src ? __float_as_uint(*src) : 0xff800000u;
+    struct Most {
+        float m = -INFINITY;
+        __device__ __forceinline__ void take(uint32_t w) { m = fmaxf(m, __uint_as_float(w)); }
+        __device__ __forceinline__ float get() const { return m; }
+    };
+    static __device__ __forceinline__ float value(const float* x) { return *x; }
+    static __device__ __forceinline__ void put(uint32_t* w, int i, const float* src) {
+        w[i] = src ? __float_as_uint(*src) : 0xff800000u;
     }
 };
 template <typename T2, typename T> struct Logits16 {
     static constexpr int kPer = 8;
+    static constexpr bool kHalf = std::is_same<T, __half>::value;
+    static constexpr float kTop = kHalf ? 65504.f : 3.3895313892515355e38f;
+    static constexpr uint32_t kLow2 = kHalf ? 0xfc00fc00u : 0xff80ff80u;   // -inf twice
+    static constexpr uint32_t kTop2 = kHalf ? 0x7bff7bffu : 0x7f7f7f7fu;
     static __device__ __forceinline__ T2 two(uint32_t w) { return *reinterpret_cast<T2*>(&w); }
-    static __device__ __forceinline__ uint4 clean(uint4 v) {
-        constexpr uint32_t kLow = std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
-        constexpr uint32_t kTop = std::is_same<T, __half>::value ? 0x7bff7bffu : 0x7f7f7f7fu;
-        uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const T2 x = __hmin2(__hmax2(two(w[i]), two(kLow)), two(kTop));   // (max drops a NaN)
-            w[i] = *reinterpret_cast<const uint32_t*>(&x);
+    static __device__ __forceinline__ uint32_t bits(T2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
+    static __device__ __forceinline__ uint32_t clean(uint32_t w) {
+        return bits(__hmin2(__hmax2(two(w), two(kLow2)), two(kTop2)));   // (a maximum drops a NaN)
+    }
+    struct Most {
+        uint32_t m = kLow2;
+        __device__ __forceinline__ void take(uint32_t w) { m = bits(__hmax2(two(m), two(w))); }
+        __device__ __forceinline__ float get() const {
+            const float2 f = Elem<T>::to_float2(m);
+            return fmaxf(f.x, f.y);
         }
-        return v;
+    };
+    static __device__ __forceinline__ float value(const T* x) {
+        return Elem<T>::to_float2(*reinterpret_cast<const uint16_t*>(x)).x;
     }
-    static __device__ __forceinline__ float most(const uint4& v) {
-        const T2 x = __hmax2(__hmax2(two(v.x), two(v.y)), __hmax2(two(v.z), two(v.w)));
-        const float2 f = Elem<T>::to_float2(*reinterpret_cast<const uint32_t*>(&x));
-        return fmaxf(f.x, f.y);
-    }
-    static __device__ __forceinline__ float get(const uint4& v, int i) {
-        const float2 f = Elem<T>::to_float2(reinterpret_cast<const uint32_t*>(&v)[i >> 1]);
-        return i & 1 ? f.y : f.x;
-    }
-    static __device__ __forceinline__ void put(uint4& v, int i, const T* src) {
-        constexpr uint16_t kLow = std::is_same<T, __half>::value ? 0xfc00u : 0xff80u;
-        reinterpret_cast<uint16_t*>(&v)[i] = src ? *reinterpret_cast<const uint16_t*>(src) : kLow;
+    static __device__ __forceinline__ void put(uint32_t* w, int i, const T* src) {
+        const uint32_t h = src ? *reinterpret_cast<const uint16_t*>(src) : kLow2 & 0xffffu;
+        w[i >> 1] = i & 1 ? (w[i >> 1] & 0xffffu) | h << 16 : h;
     }
 };
 template <> struct Logits<__half> : Logits16<__half2, __half> {};
 template <> struct Logits<__nv_bfloat16> : Logits16<__nv_bfloat162, __nv_bfloat16> {};
+
+// Two fp32 values of a pair of register words: words a and b of fp32, or the
+// halves of word a.
+template <typename T>
+__device__ __forceinline__ float2 pair_of(uint32_t a, uint32_t b) {
+    if constexpr (std::is_same<T, float>::value) return make_float2(__uint_as_float(a), __uint_as_float(b));
+    else return Elem<T>::to_float2(a);
+}
 
 // Bytes `from` .. `from` + 15 of two words (0 < from < 16, the same for the CTA).
 __device__ __forceinline__ uint4 bytes_from(const uint4& a, const uint4& b, uint32_t from) {
@@ -134,11 +149,13 @@ __device__ __forceinline__ bool reads_row(const BeamSelectParams& p, int row) {
     return s > -INFINITY;   // (NaN counts as -inf)
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kSelThreads) beam_pieces_kernel(const BeamSelectParams p) {
+// kVecs: 16-byte words per thread.
+template <typename T, int kVecs>
+__global__ void __launch_bounds__(kSelThreads, kVecs > 4 ? 4 : 6) beam_pieces_kernel(const BeamSelectParams p) {
     using L = Logits<T>;
-    constexpr int kPer = L::kPer;
-    __shared__ float s_group[kSelGroups];
+    constexpr int kPer = L::kPer, kWords = kVecs * 4;
+    constexpr bool kWide = std::is_same<T, float>::value;   // one logit a word
+    __shared__ __align__(16) float s_group[kSelGroups];
     __shared__ float s_m[kSelThreads / 32], s_s[kSelThreads / 32];
     __shared__ float s_tau;
     __shared__ int s_count;
@@ -150,95 +167,143 @@ __global__ void __launch_bounds__(kSelThreads) beam_pieces_kernel(const BeamSele
     pdl_wait();
     if (!reads_row(p, row)) return;
     const T* x = static_cast<const T*>(p.logits) + row * p.stride;
-    // Pieces count from the row's first element, wherever that lies, so that equal
+    const int k = p.k;
+    // index of the first element of this thread's word j
+    auto at = [&](int j) { return ((piece * kVecs + j) * kSelThreads + tid) * kPer; };
+
+    // Words count from the row's first element, wherever that lies, so that equal
     // rows have equal sums: off a 16-byte boundary a thread takes its 16 bytes from
     // the two aligned words that hold them.
+    uint32_t v[kWords];
     const uint32_t lead = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(x) & 15u);
-    const int before = static_cast<int>(lead / sizeof(T));   // elements of the first word in front of a piece
-    const int k = p.k;
-
-    uint4 v[kSelVecs];
-    int at[kSelVecs];   // index of a piece's first element
-#pragma unroll
-    for (int j = 0; j < kSelVecs; ++j) at[j] = ((piece * kSelVecs + j) * kSelThreads + tid) * kPer;
+    const int before = static_cast<int>(lead / sizeof(T));   // elements of the first of them in front of ours
     auto one_by_one = [&](int j) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) L::put(v[j], i, at[j] + i < p.vocab ? x + at[j] + i : nullptr);
+        for (int i = 0; i < kPer; ++i) L::put(v + 4 * j, i, at(j) + i < p.vocab ? x + at(j) + i : nullptr);
     };
-    if (lead == 0) {
+    auto keep = [&](int j, const uint4& w) {
+        v[4 * j] = w.x;
+        v[4 * j + 1] = w.y;
+        v[4 * j + 2] = w.z;
+        v[4 * j + 3] = w.w;
+    };
+    const int end = (piece + 1) * kVecs * kSelThreads * kPer;   // of the CTA's piece
+    if (lead == 0 && end <= p.vocab) {
 #pragma unroll
-        for (int j = 0; j < kSelVecs; ++j) {
-            if (at[j] <= p.vocab - kPer) v[j] = __ldcs(reinterpret_cast<const uint4*>(x + at[j]));
+        for (int j = 0; j < kVecs; ++j) keep(j, __ldcs(reinterpret_cast<const uint4*>(x + at(j))));
+    } else if (lead == 0) {
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            if (at(j) <= p.vocab - kPer) keep(j, __ldcs(reinterpret_cast<const uint4*>(x + at(j))));
             else one_by_one(j);
         }
     } else {
-        uint4 next[kSelVecs];
-        auto inside = [&](int j) { return at[j] >= before && at[j] - before + 2 * kPer <= p.vocab; };
 #pragma unroll
-        for (int j = 0; j < kSelVecs; ++j) {
-            if (inside(j)) {
-                const uint4* w = reinterpret_cast<const uint4*>(x + at[j] - before);
-                v[j] = w[0];
-                next[j] = w[1];
+        for (int j = 0; j < kVecs; ++j) {
+            if (at(j) >= before && at(j) - before + 2 * kPer <= p.vocab) {
+                const uint4* w = reinterpret_cast<const uint4*>(x + at(j) - before);
+                keep(j, bytes_from(w[0], w[1], lead));
+            } else {
+                one_by_one(j);
             }
         }
+    }
+
+    // this thread's, its group's and its warp's largest, and the warp's sum of
+    // 2^((x - wm) log2 e); a NaN or +inf makes that NaN, and only then are the
+    // words cleaned and the sum taken again
+    float tm, gm, wm, sum;
+    bool cleaned = false;
+#pragma unroll 1
+    for (;;) {
+        typename L::Most most;
 #pragma unroll
-        for (int j = 0; j < kSelVecs; ++j) {
-            if (inside(j)) v[j] = bytes_from(v[j], next[j], lead);
-            else one_by_one(j);
+        for (int i = 0; i < kWords; ++i) most.take(v[i]);
+        tm = most.get();
+        gm = fmaxf(tm, __shfl_xor_sync(kFull, tm, 1));
+        gm = fmaxf(gm, __shfl_xor_sync(kFull, gm, 2));
+        wm = gm;
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) wm = fmaxf(wm, __shfl_xor_sync(kFull, wm, off));
+        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+        if (wm > -INFINITY) {
+#pragma unroll
+            for (int i = 0; i < kWords; i += 2) {
+                float2 a, b;
+                if constexpr (kWide) {
+                    a = pair_of<T>(v[i], v[i + 1]);
+                } else {
+                    a = pair_of<T>(v[i], 0u);
+                    b = pair_of<T>(v[i + 1], 0u);
+                    add_pair(b.x, b.y, -wm, -wm);
+                    mul_pair(b.x, b.y, kLog2e);
+                    add_pair(s2, s3, fast_exp2(b.x), fast_exp2(b.y));
+                }
+                add_pair(a.x, a.y, -wm, -wm);
+                mul_pair(a.x, a.y, kLog2e);
+                add_pair(s0, s1, fast_exp2(a.x), fast_exp2(a.y));
+            }
         }
-    }
-    float tm = -INFINITY;
+        sum = (s0 + s1) + (s2 + s3);
+        if (cleaned || !__any_sync(kFull, !(sum < INFINITY))) break;
 #pragma unroll
-    for (int j = 0; j < kSelVecs; ++j) {
-        v[j] = L::clean(v[j]);
-        tm = fmaxf(tm, L::most(v[j]));
-    }
-    float gm = fmaxf(tm, __shfl_xor_sync(kFull, tm, 1));
-    gm = fmaxf(gm, __shfl_xor_sync(kFull, gm, 2));
-    if ((lane & 3) == 0) s_group[tid >> 2] = gm;
-    float wm = gm;
-#pragma unroll
-    for (int off = 4; off < 32; off <<= 1) wm = fmaxf(wm, __shfl_xor_sync(kFull, wm, off));
-    // the warp's sum of 2^((x - wm) log2 e)
-    float sum = 0.f;
-    if (wm > -INFINITY) {
-#pragma unroll
-        for (int j = 0; j < kSelVecs; ++j)
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) sum += fast_exp2((L::get(v[j], i) - wm) * kLog2e);
+        for (int i = 0; i < kWords; ++i) v[i] = L::clean(v[i]);
+        cleaned = true;
     }
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) sum += __shfl_xor_sync(kFull, sum, off);
+    if ((lane & 3) == 0) s_group[tid >> 2] = gm;
     if (lane == 0) {
         s_m[warp] = wm;
         s_s[warp] = sum;
     }
     __syncthreads();
     // tau: the k-th largest of the groups' maxima.  k groups hold an element at
-    // least as large, so the k best are not below it; with 64 groups they are few.
-    if (tid < kSelGroups) {
-        const float mine = s_group[tid];
+    // least as large, so the k best are not below it; with 64 groups they are few
+    // (8 of 8192 logits: 8 or 9 pass; 64: about 300).  A group's four threads
+    // count a quarter of the others each.
+    {
         int better = 0;
-#pragma unroll 8
-        for (int i = 0; i < kSelGroups; ++i) {
-            const float o = s_group[i];
-            better += o > mine || (o == mine && i < tid);
+        const int mine = tid >> 2, first = (tid & 3) * (kSelGroups / 4);
+#pragma unroll
+        for (int i = 0; i < kSelGroups / 4; i += 4) {
+            const float4 o = *reinterpret_cast<const float4*>(s_group + first + i);
+            better += o.x > gm || (o.x == gm && first + i < mine);
+            better += o.y > gm || (o.y == gm && first + i + 1 < mine);
+            better += o.z > gm || (o.z == gm && first + i + 2 < mine);
+            better += o.w > gm || (o.w == gm && first + i + 3 < mine);
         }
-        if (better == k - 1) s_tau = mine;
+        better += __shfl_xor_sync(kFull, better, 1);
+        better += __shfl_xor_sync(kFull, better, 2);
+        if (better == k - 1) s_tau = gm;
     }
     __syncthreads();
-    const float tau = s_tau;
-    if (tm >= tau && tm > -INFINITY) {
+    const float tau = fmaxf(s_tau, -L::kTop);   // (-inf is no candidate)
+    if (tm >= tau) {
+        // a bit for each logit that passes; their values come from memory again
+        // (registers have no index): few of a thread's do
+        constexpr int kMasks = kWide ? (kWords + 31) / 32 : (kWords + 15) / 16;
+        uint32_t mask[kMasks];
 #pragma unroll
-        for (int j = 0; j < kSelVecs; ++j) {
+        for (int b = 0; b < kMasks; ++b) mask[b] = 0u;
+        if constexpr (kWide) {
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const float f = L::get(v[j], i);
-                if (f >= tau && f > -INFINITY) {
-                    const int c = atomicAdd(&s_count, 1);
-                    if (c < kSelCap) s_key[c] = key_of(f, at[j] + i);
-                }
+            for (int i = 0; i < kWords; ++i) mask[i >> 5] |= __uint_as_float(v[i]) >= tau ? 1u << (i & 31) : 0u;
+        } else {
+            const uint32_t t2 = Elem<T>::pack(tau, tau);
+#pragma unroll
+            for (int i = 0; i < kWords; ++i)
+                mask[i >> 4] |= __hge2_mask(L::two(v[i]), L::two(t2)) & (0x00010001u << (i & 15));
+        }
+#pragma unroll
+        for (int b = 0; b < kMasks; ++b) {
+            while (mask[b]) {
+                const int bit = __ffs(mask[b]) - 1;
+                mask[b] &= mask[b] - 1u;
+                const int i = kWide ? 32 * b + bit : 16 * b + (bit & 15);
+                const int e = at(i >> 2) + (kWide ? i & 3 : (i & 3) * 2 + (bit >> 4));
+                const int c = atomicAdd(&s_count, 1);
+                if (c < kSelCap) s_key[c] = key_of(fminf(L::value(x + e), L::kTop), e);
             }
         }
     }
@@ -246,7 +311,6 @@ __global__ void __launch_bounds__(kSelThreads) beam_pieces_kernel(const BeamSele
     const int found = s_count;
     const int64_t slot = static_cast<int64_t>(row) * p.chunks + piece;
     u64* best = p.best + slot * k;
-    int listed = min(found, k);
     if (found <= kSelCap) {
         // rank them against one another
         for (int i = tid; i < found; i += kSelThreads) {
@@ -256,21 +320,23 @@ __global__ void __launch_bounds__(kSelThreads) beam_pieces_kernel(const BeamSele
             if (better < k) best[better] = mine;
         }
     } else {
-        // many equal logits: the largest key below the last one, k times
+        // many equal logits: the largest key below the last one, k times (read again:
+        // kept in registers as keys they would not fit)
         u64 last = ~0ull;
         for (int r = 0; r < k; ++r) {
             u64 top = 0;
-#pragma unroll
-            for (int j = 0; j < kSelVecs; ++j) {
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    const float f = L::get(v[j], i);
-                    const u64 key = f > -INFINITY ? key_of(f, at[j] + i) : 0;
+#pragma unroll 1
+            for (int j = 0; j < kVecs; ++j) {
+                const int stop = min(at(j) + kPer, p.vocab);
+#pragma unroll 1
+                for (int e = at(j); e < stop; ++e) {
+                    const float f = L::value(x + e);   // (NaN and -inf pass by)
+                    const u64 key = f >= -L::kTop ? key_of(fminf(f, L::kTop), e) : 0;
                     if (key < last && key > top) top = key;
                 }
             }
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) top = max(top, shfl_xor64(top, off));
+            for (int off = 1; off < 32; off <<= 1) top = max(top, __shfl_xor_sync(kFull, top, off));
             __syncthreads();
             if (lane == 0) s_key[warp] = top;
             __syncthreads();
@@ -290,143 +356,207 @@ __global__ void __launch_bounds__(kSelThreads) beam_pieces_kernel(const BeamSele
 #pragma unroll
             for (int w = 0; w < kSelThreads / 32; ++w) s += s_s[w] * fast_exp2((s_m[w] - m) * kLog2e);
         }
-        p.piece[slot] = make_uint4(__float_as_uint(m), __float_as_uint(s), static_cast<uint32_t>(listed), 0u);
+        p.piece[slot] = make_uint4(__float_as_uint(m), __float_as_uint(s), static_cast<uint32_t>(min(found, k)), 0u);
     }
 }
 
-// A 64-bit maximum over the warp's lanes, in two 32-bit steps.
-__device__ __forceinline__ u64 warp_max64(u64 x) {
-    const uint32_t hi = __reduce_max_sync(kFull, static_cast<uint32_t>(x >> 32));
-    const uint32_t lo = __reduce_max_sync(kFull, static_cast<uint32_t>(x >> 32) == hi ? static_cast<uint32_t>(x) : 0u);
-    return static_cast<u64>(hi) << 32 | lo;
-}
 __device__ __forceinline__ u64 ordered64(double x) {
     const u64 b = static_cast<u64>(__double_as_longlong(x));
     return b ^ (b >> 63 ? ~0ull : 1ull << 63);
 }
+__device__ __forceinline__ double unordered64(u64 o) {
+    return __longlong_as_double(static_cast<long long>(o ^ (o >> 63 ? 1ull << 63 : ~0ull)));
+}
 
-constexpr int kJoinWarps = 8;
-constexpr int kMaxPieces = 256;   // of a row (vocabularies of 2^20)
+constexpr int kJoinThreads = 256;
+constexpr int kMaxPieces = 256;   // of a row
+constexpr int kJoinCap = 512;     // candidates ranked at once
 
-// One CTA per request.  A warp merges the ordered lists of a row's pieces (one
-// head a lane, the largest leaves k times), then one warp merges the rows' by
-// their scores (one beam a lane).
-__global__ void __launch_bounds__(kJoinWarps * 32) beam_join_kernel(const BeamSelectParams p) {
-    __shared__ u64 s_best[kMaxBeams][kMaxBeamOut];
-    __shared__ int s_n[kMaxBeams];
+// A candidate: its score, then the lower beam, then its row's order (0 score: none).
+struct Cand {
+    u64 score, key;
+    int beam;
+};
+__device__ __forceinline__ bool better_than(const Cand& a, const Cand& b) {
+    if (a.score != b.score) return a.score > b.score;
+    return a.beam != b.beam ? a.beam < b.beam : a.key > b.key;
+}
+
+// One CTA per request: the sums of its rows' pieces, then, of the ordered lists of
+// all pieces, the entries that can be among the k best, ranked against one another.
+__global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelectParams p) {
     // score, the row's largest logit and the logarithm of its sum: a candidate is
     // score + ((x - largest) - logarithm), in this order, as the largest may be huge
     __shared__ float s_score[kMaxBeams], s_most[kMaxBeams];
     __shared__ double s_log[kMaxBeams];
-    __shared__ uint8_t s_pos[kJoinWarps][kMaxPieces];
+    __shared__ int8_t s_kind[kMaxBeams];              // 0: no candidates, 1: a row of logits, 2: ended
+    __shared__ __align__(16) float s_probe[kJoinThreads];
+    __shared__ float s_tau;
+    __shared__ int s_count;
+    __shared__ u64 s_cs[kJoinCap], s_ck[kJoinCap];
+    __shared__ int s_cb[kJoinCap];
+    __shared__ uint8_t s_pos[kMaxBeams * kMaxPieces];
     __shared__ int s_flat[kMaxBeamOut];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int s = static_cast<int>(blockIdx.x);
-    const int W = p.beams, k = p.k, C = p.chunks;
+    const int W = p.beams, k = p.k, C = p.chunks, lists = W * C;
+    if (tid == 0) s_count = 0;
     pdl_trigger();
     pdl_wait();
-    for (int w = warp; w < W; w += kJoinWarps) {
+    const int64_t slot0 = static_cast<int64_t>(s) * lists;
+    for (int w = warp; w < W; w += kJoinThreads / 32) {
         const int row = s * W + w;
         const float score = fminf(p.scores[row], FLT_MAX);
         if (!reads_row(p, row)) {
+            // an ended beam goes on as it is, with its one candidate
+            const bool ended = p.finished && p.finished[row] && p.scores[row] > -INFINITY;
             if (lane == 0) {
-                // an ended beam goes on as it is, with its one candidate
-                const bool ended = p.finished && p.finished[row] && p.scores[row] > -INFINITY;
-                s_n[w] = ended ? 1 : 0;
+                s_kind[w] = ended ? 2 : 0;
                 s_score[w] = score;
                 s_most[w] = 0.f;
                 s_log[w] = 0.0;
-                s_best[w][0] = key_of(0.f, p.end_token);
             }
             continue;
         }
-        const int64_t slot = static_cast<int64_t>(row) * C;
+        const int64_t slot = slot0 + w * C;
         float m = -INFINITY;
         for (int c = lane; c < C; c += 32) m = fmaxf(m, __uint_as_float(p.piece[slot + c].x));
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
-        // this lane's lists: c = lane, lane + 32, ...; its best head
         float sum = 0.f;
-        u64 head = 0;
-        int mine = 0;
-        for (int c = lane; c < C; c += 32) {
-            const uint4 d = p.piece[slot + c];
-            if (m > -INFINITY) sum += __uint_as_float(d.y) * fast_exp2((__uint_as_float(d.x) - m) * kLog2e);
-            s_pos[warp][c] = 0;
-            const u64 h = d.z > 0 ? p.best[(slot + c) * k] : 0;
-            if (h > head) {
-                head = h;
-                mine = c;
+        if (m > -INFINITY)
+            for (int c = lane; c < C; c += 32) {
+                const uint4 d = p.piece[slot + c];
+                sum += __uint_as_float(d.y) * fast_exp2((__uint_as_float(d.x) - m) * kLog2e);
             }
-        }
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) sum += __shfl_xor_sync(kFull, sum, off);
         if (lane == 0) {
+            s_kind[w] = 1;
             s_score[w] = score;
             s_most[w] = m;
             s_log[w] = log(static_cast<double>(sum));
         }
-        int n = 0;
-        for (; n < k; ++n) {
-            const u64 top = warp_max64(head);
-            if (top == 0) break;
-            if (lane == 0) s_best[w][n] = top;
-            if (head == top) {   // (keys are distinct: one lane)
-                ++s_pos[warp][mine];
-                head = 0;
-                for (int c = lane; c < C; c += 32) {
-                    const int at = s_pos[warp][c];
-                    const u64 h = at < static_cast<int>(p.piece[slot + c].z) ? p.best[(slot + c) * k + at] : 0;
-                    if (h > head) {
-                        head = h;
-                        mine = c;
-                    }
-                }
-            }
+    }
+    // Every list gives its d-th entry, d the smallest with lists * d >= k.  The
+    // ceil(k / d)-th largest of these (of a thread's, the largest) has k entries
+    // not below it.
+    const int d = (k + lists - 1) / lists, q = (k + d - 1) / d;
+    auto count_of = [&](int l) -> int {   // entries of list l
+        const int w = l / C;
+        if (s_kind[w] != 1) return s_kind[w] == 2 && l == w * C ? 1 : 0;
+        return static_cast<int>(p.piece[slot0 + l].z);
+    };
+    auto entry = [&](int l, int i) {      // entry i < count_of(l) of list l
+        Cand c;
+        c.beam = l / C;
+        c.key = s_kind[c.beam] == 2 ? key_of(0.f, p.end_token) : p.best[(slot0 + l) * k + i];
+        const double x = unordered(static_cast<uint32_t>(c.key >> 32));
+        c.score = ordered64(s_score[c.beam] + ((x - s_most[c.beam]) - s_log[c.beam]));
+        return c;
+    };
+    __syncthreads();
+    float probe = -INFINITY;   // (rounding is monotonic: no candidate is lost by comparing in fp32)
+    for (int l = tid; l < lists; l += kJoinThreads)
+        if (count_of(l) >= d) probe = fmaxf(probe, static_cast<float>(unordered64(entry(l, d - 1).score)));
+    s_probe[tid] = probe;
+    __syncthreads();
+    {
+        const int n = min(lists, kJoinThreads);
+        int better = 0;
+        for (int i = 0; i < n; i += 4) {
+            const float4 o = *reinterpret_cast<const float4*>(s_probe + i);   // (-inf behind the last)
+            better += o.x > probe || (o.x == probe && i < tid);
+            better += o.y > probe || (o.y == probe && i + 1 < tid);
+            better += o.z > probe || (o.z == probe && i + 2 < tid);
+            better += o.w > probe || (o.w == probe && i + 3 < tid);
         }
-        if (lane == 0) s_n[w] = n;
-        __syncwarp();
+        if (better == q - 1) s_tau = probe;
     }
     __syncthreads();
-    if (warp > 0) return;
-
-    // beams: a lane each, heads compared by score, ties to the lower beam
-    const int n = lane < W ? s_n[lane] : 0;
-    const double cum = n > 0 ? s_score[lane] : 0.0, most = n > 0 ? s_most[lane] : 0.0, lg = n > 0 ? s_log[lane] : 0.0;
-    int at = 0;
-    double score = 0.0;
-    u64 key = 0;
-    auto load = [&]() {
-        if (at < n) {
-            score = cum + ((static_cast<double>(unordered(static_cast<uint32_t>(s_best[lane][at] >> 32))) - most) - lg);
-            key = ordered64(score);
-        } else {
-            key = 0;
-        }
-    };
-    load();
-    const int64_t o = static_cast<int64_t>(s) * k;
-    int r = 0;
-    for (; r < k; ++r) {
-        const u64 top = warp_max64(key);
-        if (top == 0) break;
-        const int win = __ffs(__ballot_sync(kFull, key == top)) - 1;
-        if (lane == win) {
-            const int token = static_cast<int>(~static_cast<uint32_t>(s_best[lane][at]));
-            p.out_scores[o + r] = static_cast<float>(score);
-            p.out_parents[o + r] = lane;
-            p.out_tokens[o + r] = token;
-            s_flat[r] = lane * p.vocab + token;
-            if (p.out_finished)
-                p.out_finished[o + r] = (p.finished && p.finished[s * W + lane]) || token == p.end_token;
-            ++at;
-            load();
+    const float tau = s_tau;
+    for (int l = tid; l < lists; l += kJoinThreads) {
+        const int n = count_of(l);
+        for (int i = 0; i < n; ++i) {
+            const Cand c = entry(l, i);
+            if (!(static_cast<float>(unordered64(c.score)) >= tau)) break;
+            const int at = atomicAdd(&s_count, 1);
+            if (at < kJoinCap) {
+                s_cs[at] = c.score;
+                s_ck[at] = c.key;
+                s_cb[at] = c.beam;
+            }
         }
     }
-    __syncwarp();
+    __syncthreads();
+    const int64_t o = static_cast<int64_t>(s) * k;
+    auto put = [&](int r, const Cand& c) {
+        const int token = static_cast<int>(~static_cast<uint32_t>(c.key));
+        p.out_scores[o + r] = static_cast<float>(unordered64(c.score));
+        p.out_parents[o + r] = c.beam;
+        p.out_tokens[o + r] = token;
+        s_flat[r] = c.beam * p.vocab + token;
+        if (p.out_finished) p.out_finished[o + r] = s_kind[c.beam] == 2 || token == p.end_token;
+    };
+    int found = s_count;
+    if (found <= kJoinCap) {
+        for (int i = tid; i < found; i += kJoinThreads) {
+            const Cand mine{s_cs[i], s_ck[i], s_cb[i]};
+            int better = 0;
+            for (int j = 0; j < found; ++j) {
+                const u64 other = s_cs[j];
+                better += other > mine.score || (other == mine.score && better_than({other, s_ck[j], s_cb[j]}, mine));
+            }
+            if (better < k) put(better, mine);
+        }
+        found = min(found, k);
+    } else {
+        // many equal scores: the best of the lists' heads, k times
+        for (int l = tid; l < lists; l += kJoinThreads) s_pos[l] = 0;
+        for (found = 0; found < k; ++found) {
+            Cand top{0, 0, 0};
+            int from = -1;
+            for (int l = tid; l < lists; l += kJoinThreads) {
+                if (s_pos[l] >= count_of(l)) continue;
+                const Cand c = entry(l, s_pos[l]);
+                if (better_than(c, top)) {
+                    top = c;
+                    from = l;
+                }
+            }
+            const Cand mine = top;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                Cand c;
+                c.score = __shfl_xor_sync(kFull, top.score, off);
+                c.key = __shfl_xor_sync(kFull, top.key, off);
+                c.beam = __shfl_xor_sync(kFull, top.beam, off);
+                if (better_than(c, top)) top = c;
+            }
+            __syncthreads();
+            if (lane == 0) {
+                s_cs[warp] = top.score;
+                s_ck[warp] = top.key;
+                s_cb[warp] = top.beam;
+            }
+            __syncthreads();
+            top = {s_cs[0], s_ck[0], s_cb[0]};
+#pragma unroll
+            for (int w = 1; w < kJoinThreads / 32; ++w) {
+                const Cand c{s_cs[w], s_ck[w], s_cb[w]};
+                if (better_than(c, top)) top = c;
+            }
+            // (candidates are distinct: one thread)
+            if (from >= 0 && mine.score == top.score && mine.key == top.key && mine.beam == top.beam) {
+                put(found, mine);
+                ++s_pos[from];
+            }
+        }
+    }
+    __syncthreads();
     // fewer than k finite candidates: the lowest others, all of score -inf
-    const int found = r;
-    for (int flat = 0; r < k; ++flat) {
+    if (warp > 0) return;
+    for (int r = found, flat = 0; r < k; ++flat) {
         const bool taken = (lane < found && s_flat[lane] == flat) || (lane + 32 < found && s_flat[lane + 32] == flat);
         if (__any_sync(kFull, taken)) continue;
         if (lane == 0) {
@@ -615,15 +745,28 @@ __global__ void __launch_bounds__(kCopyThreads) beam_tables_kernel(const __grid_
 
 }  // namespace
 
-int beam_chunk_elems(int dtype) { return kSelThreads * kSelVecs * (dtype == 2 ? 4 : 8); }
+// 16-byte words per thread
+static int select_vecs(int rows, int vocab, int dtype) {
+    const long long bytes = static_cast<long long>(vocab) * (dtype == 2 ? 4 : 2);
+    return rows * ((bytes + 32767) / 32768) >= 4LL * 152 ? 8 : 4;
+}
+
+int beam_pieces(int rows, int vocab, int dtype) {
+    const int per = kSelThreads * select_vecs(rows, vocab, dtype) * (dtype == 2 ? 4 : 8);
+    return (vocab + per - 1) / per;
+}
 
 cudaError_t launch_beam_select(const BeamSelectParams& p, int dtype, cudaStream_t s) {
-    const dim3 grid(static_cast<unsigned>(p.chunks) * p.num_seqs * p.beams);
-    auto kern = dtype == 0 ? beam_pieces_kernel<__half> : dtype == 1 ? beam_pieces_kernel<__nv_bfloat16>
-                                                                     : beam_pieces_kernel<float>;
-    cudaError_t e = launch_pdl(kern, grid, dim3(kSelThreads), 0, s, p);
+    const int rows = p.num_seqs * p.beams;
+    const dim3 grid(static_cast<unsigned>(p.chunks) * rows);
+    const bool wide = select_vecs(rows, p.vocab, dtype) == 8;
+    auto go = [&](auto t) {
+        using T = decltype(t);
+        return launch_pdl(wide ? beam_pieces_kernel<T, 8> : beam_pieces_kernel<T, 4>, grid, dim3(kSelThreads), 0, s, p);
+    };
+    const cudaError_t e = dtype == 0 ? go(__half{}) : dtype == 1 ? go(__nv_bfloat16{}) : go(0.f);
     if (e != cudaSuccess) return e;
-    return launch_pdl(beam_join_kernel, dim3(p.num_seqs), dim3(kJoinWarps * 32), 0, s, p);
+    return launch_pdl(beam_join_kernel, dim3(p.num_seqs), dim3(kJoinThreads), 0, s, p);
 }
 
 cudaError_t launch_beam_copy(const BeamReorderParams& p, cudaStream_t s) {

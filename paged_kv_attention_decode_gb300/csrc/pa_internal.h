@@ -259,7 +259,7 @@ cudaError_t launch_uniform_rows(int32_t* cu, int num_seqs, int per, cudaStream_t
 cudaError_t launch_cross(const CrossParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int head_dim,
                          int dtype, cudaStream_t s);
 // dtype: 0 fp16, 1 bf16, 2 fp32
-int beam_chunk_elems(int dtype);
+int beam_pieces(int rows, int vocab, int dtype);   // CTAs for a row of logits
 cudaError_t launch_beam_select(const BeamSelectParams& p, int dtype, cudaStream_t s);
 cudaError_t launch_beam_copy(const BeamReorderParams& p, cudaStream_t s);
 cudaError_t launch_beam_tables(const BeamReorderParams& p, cudaStream_t s);   // in place, behind the copies
