@@ -27,9 +27,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 // needs no sum.  A candidate is a 64-bit key, the logit's bits in an order-
 // preserving form above the complement of its index: keys are distinct, larger
 // is better, and ties go to the lower index.  Across rows, scores are compared
-// in 64 bits: a sum of fp32 exponentials is good to about 2^-27 (the terms'
-// errors are independent), but a score of magnitude 16 rounded to fp32 only to
-// 2^-21, and the k best lie close together.
+// as sums of two fp32 numbers: a sum of fp32 exponentials is good to 2^-24 (the
+// terms' errors are independent), but a score of magnitude 16 rounded to fp32 only
+// to 2^-21, and the k best lie close together.
 //
 // -inf (and NaN, which counts as -inf) never enters a list: a request with
 // fewer than k finite candidates fills up with the lowest other indices.
@@ -53,18 +53,18 @@ __device__ __forceinline__ u64 key_of(float x, int index) {
     return static_cast<u64>(ordered(x + 0.f)) << 32 | static_cast<uint32_t>(~index);
 }
 
-// (x, y) <- (x + a, y + b) and (x * f, y * f), one instruction each
+// (x, y) <- (x + a, y + b) and (x * f + a, y * f + a), one instruction each
 __device__ __forceinline__ void add_pair(float& x, float& y, float a, float b) {
     asm("{\n\t.reg .b64 p, q, d;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
         "add.rn.f32x2 d, p, q;\n\tmov.b64 {%0, %1}, d;\n\t}"
         : "+f"(x), "+f"(y)
         : "f"(a), "f"(b));
 }
-__device__ __forceinline__ void mul_pair(float& x, float& y, float f) {
-    asm("{\n\t.reg .b64 p, q, d;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\t"
-        "mul.rn.f32x2 d, p, q;\n\tmov.b64 {%0, %1}, d;\n\t}"
+__device__ __forceinline__ void fma_pair(float& x, float& y, float f, float a) {
+    asm("{\n\t.reg .b64 p, q, r, d;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\tmov.b64 r, {%3, %3};\n\t"
+        "fma.rn.f32x2 d, p, q, r;\n\tmov.b64 {%0, %1}, d;\n\t}"
         : "+f"(x), "+f"(y)
-        : "f"(f));
+        : "f"(f), "f"(a));
 }
 
 // 16-byte words of a row.
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kSelThreads, kVecs > 4 ? 4 : 6) beam_pieces_ke
     using L = Logits<T>;
     constexpr int kPer = L::kPer, kWords = kVecs * 4;
     constexpr bool kWide = std::is_same<T, float>::value;   // one logit a word
-    __shared__ __align__(16) float s_group[kSelGroups];
+    __shared__ __align__(16) uint32_t s_group[kSelGroups];
     __shared__ float s_m[kSelThreads / 32], s_s[kSelThreads / 32];
     __shared__ float s_tau;
     __shared__ int s_count;
@@ -209,50 +209,64 @@ __global__ void __launch_bounds__(kSelThreads, kVecs > 4 ? 4 : 6) beam_pieces_ke
         }
     }
 
-    // this thread's, its group's and its warp's largest, and the warp's sum of
-    // 2^((x - wm) log2 e); a NaN or +inf makes that NaN, and only then are the
-    // words cleaned and the sum taken again
+    // This thread's, its group's and its warp's largest, and the warp's sum of
+    // 2^((x - wm) log2 e), as 2^(x log2 e - c) with c = wm log2 e rounded, and that
+    // rounding taken back from the sum.  A NaN or +inf makes the sum NaN, and from
+    // logits of some 100,000 on c is too coarse: only then are the words cleaned and
+    // the sum taken from the differences.
     float tm, gm, wm, sum;
-    bool cleaned = false;
-#pragma unroll 1
-    for (;;) {
+    auto largest = [&]() {
         typename L::Most most;
 #pragma unroll
         for (int i = 0; i < kWords; ++i) most.take(v[i]);
         tm = most.get();
         gm = fmaxf(tm, __shfl_xor_sync(kFull, tm, 1));
         gm = fmaxf(gm, __shfl_xor_sync(kFull, gm, 2));
-        wm = gm;
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) wm = fmaxf(wm, __shfl_xor_sync(kFull, wm, off));
+        wm = unordered(__reduce_max_sync(kFull, ordered(gm)));
+    };
+    largest();
+    {
+        const float c = wm * kLog2e;
         float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-        if (wm > -INFINITY) {
 #pragma unroll
-            for (int i = 0; i < kWords; i += 2) {
-                float2 a, b;
-                if constexpr (kWide) {
-                    a = pair_of<T>(v[i], v[i + 1]);
-                } else {
-                    a = pair_of<T>(v[i], 0u);
-                    b = pair_of<T>(v[i + 1], 0u);
-                    add_pair(b.x, b.y, -wm, -wm);
-                    mul_pair(b.x, b.y, kLog2e);
-                    add_pair(s2, s3, fast_exp2(b.x), fast_exp2(b.y));
-                }
-                add_pair(a.x, a.y, -wm, -wm);
-                mul_pair(a.x, a.y, kLog2e);
-                add_pair(s0, s1, fast_exp2(a.x), fast_exp2(a.y));
+        for (int i = 0; i < kWords; i += 2) {
+            float2 a;
+            if constexpr (kWide) {
+                a = pair_of<T>(v[i], v[i + 1]);
+            } else {
+                a = pair_of<T>(v[i], 0u);
+                float2 b = pair_of<T>(v[i + 1], 0u);
+                fma_pair(b.x, b.y, kLog2e, -c);
+                add_pair(s2, s3, fast_exp2(b.x), fast_exp2(b.y));
             }
+            fma_pair(a.x, a.y, kLog2e, -c);
+            add_pair(s0, s1, fast_exp2(a.x), fast_exp2(a.y));
         }
         sum = (s0 + s1) + (s2 + s3);
-        if (cleaned || !__any_sync(kFull, !(sum < INFINITY))) break;
+        const float e = 0.6931471805599453f * fmaf(wm, kLog2e, -c);   // times 1 - e + e^2 / 2
+        sum = fmaf(sum, fmaf(0.5f * e, e, -e), sum);
+        if (!(fabsf(e) < 0.0078125f)) sum = INFINITY;
+    }
+    if (__any_sync(kFull, !(sum < INFINITY))) {   // (also where all of the warp's are -inf)
 #pragma unroll
         for (int i = 0; i < kWords; ++i) v[i] = L::clean(v[i]);
-        cleaned = true;
+        largest();
+        sum = 0.f;
+        if (wm > -INFINITY) {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                const float2 f = pair_of<T>(v[i], v[i]);
+                sum += fast_exp2((f.x - wm) * kLog2e);
+                if constexpr (!kWide) sum += fast_exp2((f.y - wm) * kLog2e);
+            }
+        }
     }
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) sum += __shfl_xor_sync(kFull, sum, off);
-    if ((lane & 3) == 0) s_group[tid >> 2] = gm;
+    // (a group's number in the lowest bits makes its maximum distinct; a tau that is
+    // lower by them is one as well)
+    const uint32_t gkey = (ordered(gm) & ~(kSelGroups - 1u)) | static_cast<uint32_t>(tid >> 2);
+    if ((lane & 3) == 0) s_group[tid >> 2] = gkey;
     if (lane == 0) {
         s_m[warp] = wm;
         s_s[warp] = sum;
@@ -264,18 +278,14 @@ __global__ void __launch_bounds__(kSelThreads, kVecs > 4 ? 4 : 6) beam_pieces_ke
     // count a quarter of the others each.
     {
         int better = 0;
-        const int mine = tid >> 2, first = (tid & 3) * (kSelGroups / 4);
 #pragma unroll
         for (int i = 0; i < kSelGroups / 4; i += 4) {
-            const float4 o = *reinterpret_cast<const float4*>(s_group + first + i);
-            better += o.x > gm || (o.x == gm && first + i < mine);
-            better += o.y > gm || (o.y == gm && first + i + 1 < mine);
-            better += o.z > gm || (o.z == gm && first + i + 2 < mine);
-            better += o.w > gm || (o.w == gm && first + i + 3 < mine);
+            const uint4 o = *reinterpret_cast<const uint4*>(s_group + (tid & 3) * (kSelGroups / 4) + i);
+            better += (o.x > gkey) + (o.y > gkey) + (o.z > gkey) + (o.w > gkey);
         }
         better += __shfl_xor_sync(kFull, better, 1);
         better += __shfl_xor_sync(kFull, better, 2);
-        if (better == k - 1) s_tau = gm;
+        if (better == k - 1) s_tau = unordered(gkey & ~(kSelGroups - 1u));
     }
     __syncthreads();
     const float tau = fmaxf(s_tau, -L::kTop);   // (-inf is no candidate)
@@ -360,19 +370,57 @@ __global__ void __launch_bounds__(kSelThreads, kVecs > 4 ? 4 : 6) beam_pieces_ke
     }
 }
 
-__device__ __forceinline__ u64 ordered64(double x) {
-    const u64 b = static_cast<u64>(__double_as_longlong(x));
-    return b ^ (b >> 63 ? ~0ull : 1ull << 63);
+// Sums of two fp32 numbers, about 48 bits: fp64 runs at a small fraction of their
+// rate here (the join took 23 us with it, 64 requests of 8 beams).
+struct Two {
+    float hi, lo;   // |lo| at most half a unit of hi's last place
+};
+// a + b and its rounding error (Knuth)
+__device__ __forceinline__ Two two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), t = __fadd_rn(s, -a);
+    return {s, __fadd_rn(__fadd_rn(a, -__fadd_rn(s, -t)), __fadd_rn(b, -t))};
 }
-__device__ __forceinline__ double unordered64(u64 o) {
-    return __longlong_as_double(static_cast<long long>(o ^ (o >> 63 ? 1ull << 63 : ~0ull)));
+__device__ __forceinline__ Two two_add(Two a, Two b) {
+    const Two s = two_sum(a.hi, b.hi);
+    const float e = __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)), h = __fadd_rn(s.hi, e);
+    return {h, __fadd_rn(e, -__fadd_rn(h, -s.hi))};
+}
+// In the numbers' order, to compare: hi's bits, then lo's.
+__device__ __forceinline__ u64 order_of(Two x) {
+    return static_cast<u64>(ordered(x.hi + 0.f)) << 32 | ordered(x.lo + 0.f);
+}
+
+// log((65 + 2 i) / 64), as sums of two
+__device__ const float kLogTable[32][2] = {
+    {0.015504186972975731f, -4.3701048335620385e-10f}, {0.045809537172317505f, -1.1410232758635175e-09f}, {0.0752234235405922f, -2.303004675852094e-09f}, {0.10379679501056671f, -1.328923193710807e-09f},
+    {0.13157635927200317f, -1.4832839401179854e-09f}, {0.15860502421855927f, 5.9580793632108e-09f}, {0.18492233753204346f, 9.619685048534166e-10f}, {0.2105647623538971f, 6.753452463925669e-09f},
+    {0.23556606471538544f, 6.597381307926753e-09f}, {0.25995752215385437f, 2.283071731667974e-09f}, {0.2837681770324707f, -3.9018259734291405e-09f}, {0.3070250451564789f, -9.86156667437399e-09f},
+    {0.3297532796859741f, 6.686494025132106e-09f}, {0.3519764244556427f, -1.2984644470748208e-09f}, {0.37371641397476196f, -4.181178070439273e-09f}, {0.3949938118457794f, -3.604910370214043e-09f},
+    {0.4158279001712799f, -5.027569027760137e-09f}, {0.43623676896095276f, -2.1860346866020564e-09f}, {0.45623743534088135f, -1.8592938300088235e-09f}, {0.47584590315818787f, 1.7117760542362248e-09f},
+    {0.4950772523880005f, 1.4409851090135817e-08f}, {0.5139457583427429f, -7.2405086370963545e-09f}, {0.5324648022651672f, -3.395695280516975e-09f}, {0.5506471395492554f, -2.1596592958417204e-08f},
+    {0.5685047507286072f, -1.5375938744455198e-08f}, {0.5860490202903748f, 2.4713203927717586e-08f}, {0.603290855884552f, -4.446467638530294e-09f}, {0.6202403903007507f, 1.9451107391432743e-08f},
+    {0.6369074583053589f, 3.931710068627581e-09f}, {0.6533012986183167f, -2.660557107958539e-08f}, {0.669430673122406f, -1.9179775989641712e-08f}, {0.6853039860725403f, 1.702637852929456e-08f},
+};
+// The logarithm of a positive normal x, to about 2^-30 absolute: x = 2^e m, m in [1, 2)
+// near c = (65 + 2 i) / 64, log m = log c + log(1 + (m - c) / c).
+__device__ __forceinline__ Two two_log(float x) {
+    const uint32_t b = __float_as_uint(x);
+    const float e = static_cast<float>(static_cast<int>(b >> 23) - 127);
+    const int i = static_cast<int>(b >> 18) & 31;
+    const float m = __uint_as_float((b & 0x7fffffu) | 0x3f800000u), c = (65 + 2 * i) * 0.015625f;
+    const float u = (m - c) / c;   // |u| <= 1 / 65
+    // u - u^2 / 2 + ... : the next term, u^6 / 6, is below 2^-38
+    const float v = u * u * fmaf(u, fmaf(u, fmaf(u, 0.2f, -0.25f), 0.33333333f), -0.5f);
+    Two r = {kLogTable[i][0], kLogTable[i][1]};
+    r = two_add(r, two_sum(u, v));
+    return two_add(r, {e * 0.693115234375f, e * 3.194618329871446e-05f});   // (the first product is exact)
 }
 
 constexpr int kJoinThreads = 256;
 constexpr int kMaxPieces = 256;   // of a row
 constexpr int kJoinCap = 512;     // candidates ranked at once
 
-// A candidate: its score, then the lower beam, then its row's order (0 score: none).
+// A candidate: its score, then the lower beam, then its row's order (key 0: none).
 struct Cand {
     u64 score, key;
     int beam;
@@ -388,10 +436,10 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
     // score, the row's largest logit and the logarithm of its sum: a candidate is
     // score + ((x - largest) - logarithm), in this order, as the largest may be huge
     __shared__ float s_score[kMaxBeams], s_most[kMaxBeams];
-    __shared__ double s_log[kMaxBeams];
+    __shared__ Two s_log[kMaxBeams];
     __shared__ int8_t s_kind[kMaxBeams];              // 0: no candidates, 1: a row of logits, 2: ended
-    __shared__ __align__(16) float s_probe[kJoinThreads];
-    __shared__ float s_tau;
+    __shared__ __align__(16) uint32_t s_probe[kJoinThreads];
+    __shared__ uint32_t s_tau;
     __shared__ int s_count;
     __shared__ u64 s_cs[kJoinCap], s_ck[kJoinCap];
     __shared__ int s_cb[kJoinCap];
@@ -400,13 +448,24 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int s = static_cast<int>(blockIdx.x);
     const int W = p.beams, k = p.k, C = p.chunks, lists = W * C;
+    // Every list gives its d-th entry, d the smallest with lists * d >= k.  The
+    // ceil(k / d)-th largest of these (of a thread's, the largest) has k entries
+    // not below it.
+    const int d = (k + lists - 1) / lists, q = (k + d - 1) / d;
     if (tid == 0) s_count = 0;
     pdl_trigger();
     pdl_wait();
     const int64_t slot0 = static_cast<int64_t>(s) * lists;
+    // this thread's first list: asked for before the rows' sums are needed
+    // (a row that was not read has whatever the workspace holds)
+    const bool has = tid < lists;
+    const int n_first = has ? static_cast<int>(p.piece[slot0 + tid].z) : 0;
+    const u64 k_first = has ? p.best[(slot0 + tid) * k] : 0, k_probe = has && d > 1 ? p.best[(slot0 + tid) * k + d - 1] : k_first;
     for (int w = warp; w < W; w += kJoinThreads / 32) {
         const int row = s * W + w;
         const float score = fminf(p.scores[row], FLT_MAX);
+        const int64_t slot = slot0 + w * C;
+        uint4 mine = lane < C ? p.piece[slot + lane] : make_uint4(0xff800000u, 0u, 0u, 0u);
         if (!reads_row(p, row)) {
             // an ended beam goes on as it is, with its one candidate
             const bool ended = p.finished && p.finished[row] && p.scores[row] > -INFINITY;
@@ -414,20 +473,18 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
                 s_kind[w] = ended ? 2 : 0;
                 s_score[w] = score;
                 s_most[w] = 0.f;
-                s_log[w] = 0.0;
+                s_log[w] = {0.f, 0.f};
             }
             continue;
         }
-        const int64_t slot = slot0 + w * C;
-        float m = -INFINITY;
-        for (int c = lane; c < C; c += 32) m = fmaxf(m, __uint_as_float(p.piece[slot + c].x));
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
+        float m = __uint_as_float(mine.x);
+        for (int c = lane + 32; c < C; c += 32) m = fmaxf(m, __uint_as_float(p.piece[slot + c].x));
+        m = unordered(__reduce_max_sync(kFull, ordered(m)));
         float sum = 0.f;
         if (m > -INFINITY)
             for (int c = lane; c < C; c += 32) {
-                const uint4 d = p.piece[slot + c];
-                sum += __uint_as_float(d.y) * fast_exp2((__uint_as_float(d.x) - m) * kLog2e);
+                if (c != lane) mine = p.piece[slot + c];
+                sum += __uint_as_float(mine.y) * fast_exp2((__uint_as_float(mine.x) - m) * kLog2e);
             }
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) sum += __shfl_xor_sync(kFull, sum, off);
@@ -435,37 +492,42 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
             s_kind[w] = 1;
             s_score[w] = score;
             s_most[w] = m;
-            s_log[w] = log(static_cast<double>(sum));
+            s_log[w] = two_log(sum);   // (at least 1, where the row has candidates)
         }
     }
-    // Every list gives its d-th entry, d the smallest with lists * d >= k.  The
-    // ceil(k / d)-th largest of these (of a thread's, the largest) has k entries
-    // not below it.
-    const int d = (k + lists - 1) / lists, q = (k + d - 1) / d;
-    auto count_of = [&](int l) -> int {   // entries of list l
-        const int w = l / C;
-        if (s_kind[w] != 1) return s_kind[w] == 2 && l == w * C ? 1 : 0;
-        return static_cast<int>(p.piece[slot0 + l].z);
+    __syncthreads();
+    auto count_of = [&](int l, int n) -> int {   // entries of list l, n those of its piece
+        const int kind = s_kind[l / C];
+        return kind == 1 ? n : kind == 2 && l % C == 0 ? 1 : 0;
     };
-    auto entry = [&](int l, int i) {      // entry i < count_of(l) of list l
+    auto cand_of = [&](int l, u64 key) {
         Cand c;
         c.beam = l / C;
-        c.key = s_kind[c.beam] == 2 ? key_of(0.f, p.end_token) : p.best[(slot0 + l) * k + i];
-        const double x = unordered(static_cast<uint32_t>(c.key >> 32));
-        c.score = ordered64(s_score[c.beam] + ((x - s_most[c.beam]) - s_log[c.beam]));
+        c.key = s_kind[c.beam] == 2 ? key_of(0.f, p.end_token) : key;
+        const float x = unordered(static_cast<uint32_t>(c.key >> 32));
+        const Two lg = s_log[c.beam];
+        const Two lp = two_add(two_sum(x, -s_most[c.beam]), {-lg.hi, -lg.lo});
+        Two t = two_add({s_score[c.beam], 0.f}, lp);
+        if (!(t.hi >= -FLT_MAX && t.hi <= FLT_MAX)) t = {__fadd_rn(s_score[c.beam], lp.hi >= -FLT_MAX ? lp.hi : -FLT_MAX), 0.f};
+        c.score = order_of(t);
         return c;
     };
-    __syncthreads();
-    float probe = -INFINITY;   // (rounding is monotonic: no candidate is lost by comparing in fp32)
-    for (int l = tid; l < lists; l += kJoinThreads)
-        if (count_of(l) >= d) probe = fmaxf(probe, static_cast<float>(unordered64(entry(l, d - 1).score)));
+    auto entry = [&](int l, int i) { return cand_of(l, p.best[(slot0 + l) * k + i]); };
+    // (scores are compared by hi alone here: the order of both is never the other way)
+    uint32_t probe = 0;
+    const int n0 = has ? count_of(tid, n_first) : 0;
+    const Cand first = n0 > 0 ? cand_of(tid, k_first) : Cand{0, 0, 0};
+    if (n0 >= d) probe = static_cast<uint32_t>((d > 1 ? cand_of(tid, k_probe) : first).score >> 32);
+    for (int l = tid + kJoinThreads; l < lists; l += kJoinThreads)
+        if (count_of(l, static_cast<int>(p.piece[slot0 + l].z)) >= d)
+            probe = max(probe, static_cast<uint32_t>(entry(l, d - 1).score >> 32));
     s_probe[tid] = probe;
     __syncthreads();
-    {
+    if (tid < lists) {
         const int n = min(lists, kJoinThreads);
         int better = 0;
         for (int i = 0; i < n; i += 4) {
-            const float4 o = *reinterpret_cast<const float4*>(s_probe + i);   // (-inf behind the last)
+            const uint4 o = *reinterpret_cast<const uint4*>(s_probe + i);   // (0 behind the last)
             better += o.x > probe || (o.x == probe && i < tid);
             better += o.y > probe || (o.y == probe && i + 1 < tid);
             better += o.z > probe || (o.z == probe && i + 2 < tid);
@@ -474,12 +536,12 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
         if (better == q - 1) s_tau = probe;
     }
     __syncthreads();
-    const float tau = s_tau;
+    const uint32_t tau = s_tau;
     for (int l = tid; l < lists; l += kJoinThreads) {
-        const int n = count_of(l);
+        const int n = l == tid ? n0 : count_of(l, static_cast<int>(p.piece[slot0 + l].z));
         for (int i = 0; i < n; ++i) {
-            const Cand c = entry(l, i);
-            if (!(static_cast<float>(unordered64(c.score)) >= tau)) break;
+            const Cand c = l == tid && i == 0 ? first : entry(l, i);
+            if (static_cast<uint32_t>(c.score >> 32) < tau) break;
             const int at = atomicAdd(&s_count, 1);
             if (at < kJoinCap) {
                 s_cs[at] = c.score;
@@ -492,7 +554,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
     const int64_t o = static_cast<int64_t>(s) * k;
     auto put = [&](int r, const Cand& c) {
         const int token = static_cast<int>(~static_cast<uint32_t>(c.key));
-        p.out_scores[o + r] = static_cast<float>(unordered64(c.score));
+        p.out_scores[o + r] = unordered(static_cast<uint32_t>(c.score >> 32));
         p.out_parents[o + r] = c.beam;
         p.out_tokens[o + r] = token;
         s_flat[r] = c.beam * p.vocab + token;
@@ -517,7 +579,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
             Cand top{0, 0, 0};
             int from = -1;
             for (int l = tid; l < lists; l += kJoinThreads) {
-                if (s_pos[l] >= count_of(l)) continue;
+                if (s_pos[l] >= count_of(l, static_cast<int>(p.piece[slot0 + l].z))) continue;
                 const Cand c = entry(l, s_pos[l]);
                 if (better_than(c, top)) {
                     top = c;

@@ -65,17 +65,16 @@ def candidate_scores(logits, scores, finished=None, end_token=-1, top=None):
 
 def select(logits, scores, k, finished=None, end_token=-1, top=None):
     """(scores, parents, tokens, finished) [S, k] of the k best candidates, ties to
-    the lowest w V + v.  (Scores so large that 64 bits do not tell a beam's
-    logits apart, 3e38 less 5 say, tie by rounding only: within a beam the order
-    is that of its logits.)"""
+    the lowest w V + v.  (Beside a score so large that 64 bits swallow a log
+    probability, 3e38 say, what they swallow still orders the candidates.)"""
     S, W, V = logits.shape
     c = candidate_scores(logits, scores, finished, end_token, top).reshape(S, W * V)
-    x = logits.astype(np.float64).reshape(S, W * V)
-    x = np.where(np.isfinite(c), x if top is None else np.minimum(x, top), 0.0)
-    if finished is not None:
-        x = np.where(np.repeat(finished.astype(bool), V, 1), 0.0, x)
-    beam, token = np.divmod(np.arange(W * V), V)
-    at = np.stack([np.lexsort((token, -x[s], beam, -c[s]))[:k] for s in range(S)])
+    cum = np.nan_to_num(scores.astype(np.float64), nan=0.0, posinf=float(np.finfo(np.float32).max), neginf=0.0)
+    lp = candidate_scores(logits, np.where(scores > -np.inf, 0.0, scores), finished, end_token, top).reshape(S, W * V)
+    with np.errstate(invalid="ignore"):
+        big = np.repeat(np.abs(cum), V, 1) > 2.0 ** 60
+        rest = np.where(big & np.isfinite(c), lp, 0.0)
+    at = np.stack([np.lexsort((np.arange(W * V), -rest[s], -c[s]))[:k] for s in range(S)])
     parents, tokens = at // V, at % V
     fin = np.zeros((S, W), bool) if finished is None else finished.astype(bool)
     return (np.take_along_axis(c, at, 1), parents, tokens,
