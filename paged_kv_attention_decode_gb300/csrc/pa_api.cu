@@ -1062,8 +1062,8 @@ size_t pa_beam_select_workspace_bytes(int num_seqs, int num_beams, int vocab, in
     if (num_seqs <= 0 || num_seqs > kMaxGrid || num_beams <= 0 || num_beams > PA_MAX_BEAMS || vocab <= 0 || vocab > PA_MAX_VOCAB ||
         num_out <= 0 || num_out > PA_MAX_BEAM_OUT || dtype < PA_F16 || dtype > PA_F32)
         return 0;
-    const size_t n = static_cast<size_t>(num_seqs) * num_beams * pa::beam_pieces(num_seqs * num_beams, vocab, dtype);
-    return align256(n * sizeof(uint4)) + n * num_out * sizeof(unsigned long long);
+    const size_t n = static_cast<size_t>(num_seqs) * num_beams * pa::beam_pieces(vocab, dtype);
+    return align256(n * sizeof(float2)) + n * 8 * sizeof(float);
 }
 
 int pa_beam_select(float* out_scores, int32_t* out_parents, int32_t* out_tokens, uint8_t* out_finished,
@@ -1096,11 +1096,11 @@ int pa_beam_select(float* out_scores, int32_t* out_parents, int32_t* out_tokens,
     p.vocab = vocab;
     p.k = num_out;
     p.end_token = end_token;
-    p.chunks = pa::beam_pieces(num_seqs * num_beams, vocab, dtype);
-    const size_t n = static_cast<size_t>(num_seqs) * num_beams * p.chunks;
+    p.pieces = pa::beam_pieces(vocab, dtype);
+    const size_t n = static_cast<size_t>(num_seqs) * num_beams * p.pieces;
     if (n > (1u << 30)) return PA_ERR_INVALID_ARG;
-    p.piece = static_cast<uint4*>(workspace);
-    p.best = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(workspace) + align256(n * sizeof(uint4)));
+    p.sums = static_cast<float2*>(workspace);
+    p.groups = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256(n * sizeof(float2)));
     return pa::launch_beam_select(p, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

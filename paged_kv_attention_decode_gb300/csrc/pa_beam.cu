@@ -19,24 +19,27 @@ constexpr float kLog2e = 1.4426950408889634f;
 // ---------------------------------------------------------------------------
 // Candidate (beam w, token v) of a request scores score[w] + x[w, v] - lse(x[w]);
 // the k best of its W * V candidates are wanted, ties to the lowest w * V + v.
-// Two kernels.  The first reads every logit once: a CTA holds 16 or 32 KB of a row
-// in registers, sums its exponentials and lists its k largest logits in order.
-// The second joins a row's pieces and a request's rows.
+// Two kernels.  The first reads every logit once and keeps almost nothing: a warp
+// takes 4 KB of a row in registers and leaves the sum of its exponentials and the
+// largest logit of every 512 bytes (a group).  The second, a CTA per request, joins
+// the sums and looks for the k best groups: the k best candidates lie in them, as
+// the groups' largest are k candidates that are not worse than any outside.  Their
+// logits are read again, k * 512 bytes.
+// Bound by the logits' bytes; each logit costs a conversion, half a multiply-add, a
+// 2^x, half an addition and half a maximum.  (Listing the k best of every 16 KB in
+// the first kernel took three times as many instructions: 64 requests of 8 beams,
+// 131072 tokens, 16 bits, 49 us.)
 //
 // Within a row the order of scores is the order of logits, so the first kernel
-// needs no sum.  A candidate is a 64-bit key, the logit's bits in an order-
-// preserving form above the complement of its index: keys are distinct, larger
-// is better, and ties go to the lower index.  Across rows, scores are compared
-// as sums of two fp32 numbers: a sum of fp32 exponentials is good to 2^-24 (the
-// terms' errors are independent), but a score of magnitude 16 rounded to fp32 only
-// to 2^-21, and the k best lie close together.
+// needs no sum.  Across rows, scores are compared as sums of two fp32 numbers: a sum
+// of fp32 exponentials is good to 2^-24 (the terms' errors are independent), but a
+// score of magnitude 16 rounded to fp32 only to 2^-21, and the k best lie close
+// together.
 //
-// -inf (and NaN, which counts as -inf) never enters a list: a request with
-// fewer than k finite candidates fills up with the lowest other indices.
+// -inf (and NaN, which counts as -inf) is no candidate: a request with fewer than k
+// finite ones fills up with the lowest other indices.
 constexpr int kSelThreads = 256;
-constexpr int kSelGroups = kSelThreads / 4;     // groups of 4 threads
-constexpr int kSelCap = 512;                    // candidates ranked at once
-static_assert(kSelGroups >= kMaxBeamOut, "k groups give k candidates");
+constexpr int kSelVecs = 8;                     // 16-byte words per thread
 
 using u64 = unsigned long long;
 
@@ -48,6 +51,7 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 __device__ __forceinline__ float unordered(uint32_t o) {
     return __uint_as_float(o ^ (o >> 31 ? 0x80000000u : 0xffffffffu));
 }
+// Order of a row's logits: larger first, then the lower index.
 __device__ __forceinline__ u64 key_of(float x, int index) {
     // (-0 and +0 are one value)
     return static_cast<u64>(ordered(x + 0.f)) << 32 | static_cast<uint32_t>(~index);
@@ -67,49 +71,46 @@ __device__ __forceinline__ void fma_pair(float& x, float& y, float f, float a) {
         : "f"(f), "f"(a));
 }
 
-// 16-byte words of a row.
+// Register words of a row: one fp32 logit, or two of 16 bits.  `clean` takes NaN to
+// -inf and +inf to the type's largest; a maximum drops a NaN.
 template <typename T> struct Logits;
 template <> struct Logits<float> {
-    static constexpr int kPer = 4;
+    static constexpr int kPer = 4;   // logits of 16 bytes
     static constexpr float kTop = FLT_MAX;
-    // NaN as -inf, +inf as the type's largest
-    static __device__ __forceinline__ uint32_t clean(uint32_t w) {
-        return __float_as_uint(fminf(fmaxf(__uint_as_float(w), -INFINITY), FLT_MAX));
+    static constexpr uint32_t kLow = 0xff800000u;
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
     }
-    struct Most {
-        float m = -INFINITY;
-        __device__ __forceinline__ void take(uint32_t w) { m = fmaxf(m, __uint_as_float(w)); }
-        __device__ __forceinline__ float get() const { return m; }
-    };
+    static __device__ __forceinline__ uint32_t clean(uint32_t w) {
+        return __float_as_uint(fminf(__uint_as_float(larger(w, kLow)), kTop));
+    }
+    static __device__ __forceinline__ float most(uint32_t w) { return __uint_as_float(w); }
     static __device__ __forceinline__ float value(const float* x) { return *x; }
     static __device__ __forceinline__ void put(uint32_t* w, int i, const float* src) {
-        w[i] = src ? __float_as_uint(*src) : 0xff800000u;
+        w[i] = src ? __float_as_uint(*src) : kLow;
     }
 };
 template <typename T2, typename T> struct Logits16 {
     static constexpr int kPer = 8;
     static constexpr bool kHalf = std::is_same<T, __half>::value;
     static constexpr float kTop = kHalf ? 65504.f : 3.3895313892515355e38f;
-    static constexpr uint32_t kLow2 = kHalf ? 0xfc00fc00u : 0xff80ff80u;   // -inf twice
+    static constexpr uint32_t kLow = kHalf ? 0xfc00fc00u : 0xff80ff80u;   // -inf twice
     static constexpr uint32_t kTop2 = kHalf ? 0x7bff7bffu : 0x7f7f7f7fu;
     static __device__ __forceinline__ T2 two(uint32_t w) { return *reinterpret_cast<T2*>(&w); }
     static __device__ __forceinline__ uint32_t bits(T2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return bits(__hmax2(two(a), two(b))); }
     static __device__ __forceinline__ uint32_t clean(uint32_t w) {
-        return bits(__hmin2(__hmax2(two(w), two(kLow2)), two(kTop2)));   // (a maximum drops a NaN)
+        return bits(__hmin2(two(larger(w, kLow)), two(kTop2)));
     }
-    struct Most {
-        uint32_t m = kLow2;
-        __device__ __forceinline__ void take(uint32_t w) { m = bits(__hmax2(two(m), two(w))); }
-        __device__ __forceinline__ float get() const {
-            const float2 f = Elem<T>::to_float2(m);
-            return fmaxf(f.x, f.y);
-        }
-    };
+    static __device__ __forceinline__ float most(uint32_t w) {
+        const float2 f = Elem<T>::to_float2(w);
+        return fmaxf(f.x, f.y);
+    }
     static __device__ __forceinline__ float value(const T* x) {
         return Elem<T>::to_float2(*reinterpret_cast<const uint16_t*>(x)).x;
     }
     static __device__ __forceinline__ void put(uint32_t* w, int i, const T* src) {
-        const uint32_t h = src ? *reinterpret_cast<const uint16_t*>(src) : kLow2 & 0xffffu;
+        const uint32_t h = src ? *reinterpret_cast<const uint16_t*>(src) : kLow & 0xffffu;
         w[i >> 1] = i & 1 ? (w[i >> 1] & 0xffffu) | h << 16 : h;
     }
 };
@@ -124,7 +125,7 @@ __device__ __forceinline__ float2 pair_of(uint32_t a, uint32_t b) {
     else return Elem<T>::to_float2(a);
 }
 
-// Bytes `from` .. `from` + 15 of two words (0 < from < 16, the same for the CTA).
+// Bytes `from` .. `from` + 15 of two words (0 < from < 16, the same for the warp).
 __device__ __forceinline__ uint4 bytes_from(const uint4& a, const uint4& b, uint32_t from) {
     uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     if (from & 8u) {
@@ -149,34 +150,30 @@ __device__ __forceinline__ bool reads_row(const BeamSelectParams& p, int row) {
     return s > -INFINITY;   // (NaN counts as -inf)
 }
 
-// kVecs: 16-byte words per thread.
-template <typename T, int kVecs>
-__global__ void __launch_bounds__(kSelThreads, kVecs > 4 ? 4 : 6) beam_pieces_kernel(const BeamSelectParams p) {
+// One warp per piece of a row: kSelVecs * 512 bytes.
+template <typename T>
+__global__ void __launch_bounds__(kSelThreads, 4) beam_pieces_kernel(const BeamSelectParams p) {
     using L = Logits<T>;
-    constexpr int kPer = L::kPer, kWords = kVecs * 4;
+    constexpr int kPer = L::kPer, kVecs = kSelVecs, kWords = kVecs * 4;
     constexpr bool kWide = std::is_same<T, float>::value;   // one logit a word
-    __shared__ __align__(16) uint32_t s_group[kSelGroups];
-    __shared__ float s_m[kSelThreads / 32], s_s[kSelThreads / 32];
-    __shared__ float s_tau;
-    __shared__ int s_count;
-    __shared__ u64 s_key[kSelCap];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int row = static_cast<int>(blockIdx.x) / p.chunks, piece = static_cast<int>(blockIdx.x) - row * p.chunks;
-    if (tid == 0) s_count = 0;
+    const int lane = threadIdx.x & 31;
+    const int64_t all = static_cast<int64_t>(p.num_seqs) * p.beams * p.pieces;
+    const int64_t slot = static_cast<int64_t>(blockIdx.x) * (kSelThreads / 32) + (threadIdx.x >> 5);
     pdl_trigger();
     pdl_wait();
+    if (slot >= all) return;
+    const int row = static_cast<int>(slot / p.pieces), piece = static_cast<int>(slot - static_cast<int64_t>(row) * p.pieces);
     if (!reads_row(p, row)) return;
     const T* x = static_cast<const T*>(p.logits) + row * p.stride;
-    const int k = p.k;
-    // index of the first element of this thread's word j
-    auto at = [&](int j) { return ((piece * kVecs + j) * kSelThreads + tid) * kPer; };
+    // index of the first logit of this lane's word j
+    auto at = [&](int j) { return ((piece * kVecs + j) * 32 + lane) * kPer; };
 
-    // Words count from the row's first element, wherever that lies, so that equal
-    // rows have equal sums: off a 16-byte boundary a thread takes its 16 bytes from
-    // the two aligned words that hold them.
+    // Words count from the row's first logit, wherever that lies, so that equal rows
+    // have equal sums: off a 16-byte boundary a lane takes its 16 bytes from the two
+    // aligned words that hold them.
     uint32_t v[kWords];
     const uint32_t lead = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(x) & 15u);
-    const int before = static_cast<int>(lead / sizeof(T));   // elements of the first of them in front of ours
+    const int before = static_cast<int>(lead / sizeof(T));   // logits of the first of them in front of ours
     auto one_by_one = [&](int j) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) L::put(v + 4 * j, i, at(j) + i < p.vocab ? x + at(j) + i : nullptr);
@@ -187,8 +184,7 @@ __global__ void __launch_bounds__(kSelThreads, kVecs > 4 ? 4 : 6) beam_pieces_ke
         v[4 * j + 2] = w.z;
         v[4 * j + 3] = w.w;
     };
-    const int end = (piece + 1) * kVecs * kSelThreads * kPer;   // of the CTA's piece
-    if (lead == 0 && end <= p.vocab) {
+    if (lead == 0 && (piece + 1) * kVecs * 32 * kPer <= p.vocab) {
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) keep(j, __ldcs(reinterpret_cast<const uint4*>(x + at(j))));
     } else if (lead == 0) {
@@ -198,30 +194,54 @@ __global__ void __launch_bounds__(kSelThreads, kVecs > 4 ? 4 : 6) beam_pieces_ke
             else one_by_one(j);
         }
     } else {
+        auto inside = [&](int j) { return at(j) >= before && at(j) - before + 2 * kPer <= p.vocab; };
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-            if (at(j) >= before && at(j) - before + 2 * kPer <= p.vocab) {
-                const uint4* w = reinterpret_cast<const uint4*>(x + at(j) - before);
-                keep(j, bytes_from(w[0], w[1], lead));
-            } else {
-                one_by_one(j);
+        for (int half = 0; half < kVecs; half += kVecs / 2) {   // (all of a half's loads in flight)
+            uint4 a[kVecs / 2], b[kVecs / 2];
+#pragma unroll
+            for (int j = 0; j < kVecs / 2; ++j) {
+                const uint4* w = reinterpret_cast<const uint4*>(x + at(half + j) - before);
+                a[j] = b[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (inside(half + j)) {
+                    a[j] = w[0];
+                    b[j] = w[1];
+                }
             }
+#pragma unroll
+            for (int j = 0; j < kVecs / 2; ++j) keep(half + j, bytes_from(a[j], b[j], lead));
         }
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j)
+            if (!inside(j)) one_by_one(j);
     }
 
-    // This thread's, its group's and its warp's largest, and the warp's sum of
-    // 2^((x - wm) log2 e), as 2^(x log2 e - c) with c = wm log2 e rounded, and that
+    // The groups' largest: lane l ends with that of every lane's word l % 8 (three
+    // exchanges halve the words in hand, two more join the quarters), the warp's,
+    // and the warp's sum of 2^((x - wm) log2 e), as 2^(x log2 e - c) with c = wm log2 e rounded, and that
     // rounding taken back from the sum.  A NaN or +inf makes the sum NaN, and from
     // logits of some 100,000 on c is too coarse: only then are the words cleaned and
     // the sum taken from the differences.
-    float tm, gm, wm, sum;
+    float gm, wm, sum;
     auto largest = [&]() {
-        typename L::Most most;
+        static_assert(kVecs == 8, "eight words over eight lanes");
+        uint32_t m[kVecs];
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) most.take(v[i]);
-        tm = most.get();
-        gm = fmaxf(tm, __shfl_xor_sync(kFull, tm, 1));
-        gm = fmaxf(gm, __shfl_xor_sync(kFull, gm, 2));
+        for (int j = 0; j < kVecs; ++j) {
+            // (kLow first: of two NaN a maximum keeps one)
+            m[j] = L::larger(L::larger(L::larger(v[4 * j], L::kLow), v[4 * j + 1]), L::larger(L::larger(v[4 * j + 2], L::kLow), v[4 * j + 3]));
+        }
+#pragma unroll
+        for (int n = 4; n > 0; n >>= 1) {
+            const bool upper = lane & n;
+#pragma unroll
+            for (int j = 0; j < n; ++j) {
+                const uint32_t send = upper ? m[j] : m[j + n], mine = upper ? m[j + n] : m[j];
+                m[j] = L::larger(mine, __shfl_xor_sync(kFull, send, n));
+            }
+        }
+        m[0] = L::larger(m[0], __shfl_xor_sync(kFull, m[0], 8));
+        m[0] = L::larger(m[0], __shfl_xor_sync(kFull, m[0], 16));
+        gm = L::most(m[0]);
         wm = unordered(__reduce_max_sync(kFull, ordered(gm)));
     };
     largest();
@@ -263,111 +283,8 @@ __global__ void __launch_bounds__(kSelThreads, kVecs > 4 ? 4 : 6) beam_pieces_ke
     }
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) sum += __shfl_xor_sync(kFull, sum, off);
-    // (a group's number in the lowest bits makes its maximum distinct; a tau that is
-    // lower by them is one as well)
-    const uint32_t gkey = (ordered(gm) & ~(kSelGroups - 1u)) | static_cast<uint32_t>(tid >> 2);
-    if ((lane & 3) == 0) s_group[tid >> 2] = gkey;
-    if (lane == 0) {
-        s_m[warp] = wm;
-        s_s[warp] = sum;
-    }
-    __syncthreads();
-    // tau: the k-th largest of the groups' maxima.  k groups hold an element at
-    // least as large, so the k best are not below it; with 64 groups they are few
-    // (8 of 8192 logits: 8 or 9 pass; 64: about 300).  A group's four threads
-    // count a quarter of the others each.
-    {
-        int better = 0;
-#pragma unroll
-        for (int i = 0; i < kSelGroups / 4; i += 4) {
-            const uint4 o = *reinterpret_cast<const uint4*>(s_group + (tid & 3) * (kSelGroups / 4) + i);
-            better += (o.x > gkey) + (o.y > gkey) + (o.z > gkey) + (o.w > gkey);
-        }
-        better += __shfl_xor_sync(kFull, better, 1);
-        better += __shfl_xor_sync(kFull, better, 2);
-        if (better == k - 1) s_tau = unordered(gkey & ~(kSelGroups - 1u));
-    }
-    __syncthreads();
-    const float tau = fmaxf(s_tau, -L::kTop);   // (-inf is no candidate)
-    if (tm >= tau) {
-        // a bit for each logit that passes; their values come from memory again
-        // (registers have no index): few of a thread's do
-        constexpr int kMasks = kWide ? (kWords + 31) / 32 : (kWords + 15) / 16;
-        uint32_t mask[kMasks];
-#pragma unroll
-        for (int b = 0; b < kMasks; ++b) mask[b] = 0u;
-        if constexpr (kWide) {
-#pragma unroll
-            for (int i = 0; i < kWords; ++i) mask[i >> 5] |= __uint_as_float(v[i]) >= tau ? 1u << (i & 31) : 0u;
-        } else {
-            const uint32_t t2 = Elem<T>::pack(tau, tau);
-#pragma unroll
-            for (int i = 0; i < kWords; ++i)
-                mask[i >> 4] |= __hge2_mask(L::two(v[i]), L::two(t2)) & (0x00010001u << (i & 15));
-        }
-#pragma unroll
-        for (int b = 0; b < kMasks; ++b) {
-            while (mask[b]) {
-                const int bit = __ffs(mask[b]) - 1;
-                mask[b] &= mask[b] - 1u;
-                const int i = kWide ? 32 * b + bit : 16 * b + (bit & 15);
-                const int e = at(i >> 2) + (kWide ? i & 3 : (i & 3) * 2 + (bit >> 4));
-                const int c = atomicAdd(&s_count, 1);
-                if (c < kSelCap) s_key[c] = key_of(fminf(L::value(x + e), L::kTop), e);
-            }
-        }
-    }
-    __syncthreads();
-    const int found = s_count;
-    const int64_t slot = static_cast<int64_t>(row) * p.chunks + piece;
-    u64* best = p.best + slot * k;
-    if (found <= kSelCap) {
-        // rank them against one another
-        for (int i = tid; i < found; i += kSelThreads) {
-            const u64 mine = s_key[i];
-            int better = 0;
-            for (int o = 0; o < found; ++o) better += s_key[o] > mine;
-            if (better < k) best[better] = mine;
-        }
-    } else {
-        // many equal logits: the largest key below the last one, k times (read again:
-        // kept in registers as keys they would not fit)
-        u64 last = ~0ull;
-        for (int r = 0; r < k; ++r) {
-            u64 top = 0;
-#pragma unroll 1
-            for (int j = 0; j < kVecs; ++j) {
-                const int stop = min(at(j) + kPer, p.vocab);
-#pragma unroll 1
-                for (int e = at(j); e < stop; ++e) {
-                    const float f = L::value(x + e);   // (NaN and -inf pass by)
-                    const u64 key = f >= -L::kTop ? key_of(fminf(f, L::kTop), e) : 0;
-                    if (key < last && key > top) top = key;
-                }
-            }
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) top = max(top, __shfl_xor_sync(kFull, top, off));
-            __syncthreads();
-            if (lane == 0) s_key[warp] = top;
-            __syncthreads();
-            top = s_key[0];
-#pragma unroll
-            for (int w = 1; w < kSelThreads / 32; ++w) top = max(top, s_key[w]);
-            if (tid == 0) best[r] = top;
-            last = top;
-        }
-    }
-    if (tid == 0) {
-        float m = s_m[0];
-#pragma unroll
-        for (int w = 1; w < kSelThreads / 32; ++w) m = fmaxf(m, s_m[w]);
-        float s = 0.f;
-        if (m > -INFINITY) {
-#pragma unroll
-            for (int w = 0; w < kSelThreads / 32; ++w) s += s_s[w] * fast_exp2((s_m[w] - m) * kLog2e);
-        }
-        p.piece[slot] = make_uint4(__float_as_uint(m), __float_as_uint(s), static_cast<uint32_t>(min(found, k)), 0u);
-    }
+    if (lane < kVecs) p.groups[slot * kVecs + lane] = gm;
+    if (lane == 0) p.sums[slot] = make_float2(wm, sum);
 }
 
 // Sums of two fp32 numbers, about 48 bits: fp64 runs at a small fraction of their
@@ -403,7 +320,7 @@ __device__ const float kLogTable[32][2] = {
 };
 // The logarithm of a positive normal x, to about 2^-30 absolute: x = 2^e m, m in [1, 2)
 // near c = (65 + 2 i) / 64, log m = log c + log(1 + (m - c) / c).
-__device__ __forceinline__ Two two_log(float x) {
+__device__ __forceinline__ Two two_log(float x, const Two* table) {
     const uint32_t b = __float_as_uint(x);
     const float e = static_cast<float>(static_cast<int>(b >> 23) - 127);
     const int i = static_cast<int>(b >> 18) & 31;
@@ -411,16 +328,19 @@ __device__ __forceinline__ Two two_log(float x) {
     const float u = (m - c) / c;   // |u| <= 1 / 65
     // u - u^2 / 2 + ... : the next term, u^6 / 6, is below 2^-38
     const float v = u * u * fmaf(u, fmaf(u, fmaf(u, 0.2f, -0.25f), 0.33333333f), -0.5f);
-    Two r = {kLogTable[i][0], kLogTable[i][1]};
+    Two r = table[i];
     r = two_add(r, two_sum(u, v));
     return two_add(r, {e * 0.693115234375f, e * 3.194618329871446e-05f});   // (the first product is exact)
 }
 
-constexpr int kJoinThreads = 256;
-constexpr int kMaxPieces = 256;   // of a row
-constexpr int kJoinCap = 512;     // candidates ranked at once
+constexpr int kJoinThreads = 512;
+constexpr int kJoinSets = kJoinThreads / 4;   // sets of groups, of four threads each
+constexpr int kHeld = 8;                      // groups that a thread holds on to
+constexpr int kJoinCap = 512;                 // groups, and candidates, ranked at once
+static_assert(kJoinSets >= kMaxBeamOut, "k sets give k groups");
 
-// A candidate: its score, then the lower beam, then its row's order (key 0: none).
+// A candidate, or a group by its best one: the score, then the lower beam, then the
+// order within the row (key 0: none).
 struct Cand {
     u64 score, key;
     int beam;
@@ -430,123 +350,156 @@ __device__ __forceinline__ bool better_than(const Cand& a, const Cand& b) {
     return a.beam != b.beam ? a.beam < b.beam : a.key > b.key;
 }
 
-// One CTA per request: the sums of its rows' pieces, then, of the ordered lists of
-// all pieces, the entries that can be among the k best, ranked against one another.
+// One CTA per request.  The k best groups are found by scores in fp32 (x plus a term
+// of its beam), with room for their roundings; the candidates that come through are
+// ranked by the exact ones.  Where too many come through (equal scores), groups and
+// candidates are taken one by one.
+template <typename T>
 __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelectParams p) {
+    using L = Logits<T>;
+    constexpr int kGroup = 32 * L::kPer;   // logits of a group
+    constexpr int kWarps = kJoinThreads / 32;
     // score, the row's largest logit and the logarithm of its sum: a candidate is
     // score + ((x - largest) - logarithm), in this order, as the largest may be huge
     __shared__ float s_score[kMaxBeams], s_most[kMaxBeams];
-    __shared__ Two s_log[kMaxBeams];
+    __shared__ Two s_log[kMaxBeams], s_table[32];
+    __shared__ float s_add[kMaxBeams];                // score - largest - logarithm; -inf: no row of candidates
     __shared__ int8_t s_kind[kMaxBeams];              // 0: no candidates, 1: a row of logits, 2: ended
-    __shared__ __align__(16) uint32_t s_probe[kJoinThreads];
-    __shared__ uint32_t s_tau;
-    __shared__ int s_count;
+    __shared__ __align__(16) uint32_t s_set[kJoinSets];
+    __shared__ float s_tau;
+    __shared__ int s_groups, s_count;
     __shared__ u64 s_cs[kJoinCap], s_ck[kJoinCap];
-    __shared__ int s_cb[kJoinCap];
-    __shared__ uint8_t s_pos[kMaxBeams * kMaxPieces];
+    __shared__ int s_cb[kJoinCap], s_list[kJoinCap];
     __shared__ int s_flat[kMaxBeamOut];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int s = static_cast<int>(blockIdx.x);
-    const int W = p.beams, k = p.k, C = p.chunks, lists = W * C;
-    // Every list gives its d-th entry, d the smallest with lists * d >= k.  The
-    // ceil(k / d)-th largest of these (of a thread's, the largest) has k entries
-    // not below it.
-    const int d = (k + lists - 1) / lists, q = (k + d - 1) / d;
-    if (tid == 0) s_count = 0;
+    const int W = p.beams, k = p.k, C = p.pieces;
+    const int per_row = C * kSelVecs, total = W * per_row;   // groups (those past the row are -inf)
+    if (tid < 32) s_table[tid] = {kLogTable[tid][0], kLogTable[tid][1]};
+    if (tid == 0) s_groups = s_count = 0;
+    __syncthreads();
     pdl_trigger();
     pdl_wait();
-    const int64_t slot0 = static_cast<int64_t>(s) * lists;
-    // this thread's first list: asked for before the rows' sums are needed
-    // (a row that was not read has whatever the workspace holds)
-    const bool has = tid < lists;
-    const int n_first = has ? static_cast<int>(p.piece[slot0 + tid].z) : 0;
-    const u64 k_first = has ? p.best[(slot0 + tid) * k] : 0, k_probe = has && d > 1 ? p.best[(slot0 + tid) * k + d - 1] : k_first;
-    for (int w = warp; w < W; w += kJoinThreads / 32) {
+    const float* groups = p.groups + static_cast<int64_t>(s) * total;
+    // this thread's first groups, asked for before the rows' sums are needed (a row
+    // that was not read has whatever the workspace held)
+    float held[kHeld];
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+        const int g = tid + u * kJoinThreads;
+        held[u] = g < total ? groups[g] : -INFINITY;
+    }
+    for (int w = warp; w < W; w += kWarps) {
         const int row = s * W + w;
-        const float score = fminf(p.scores[row], FLT_MAX);
-        const int64_t slot = slot0 + w * C;
-        uint4 mine = lane < C ? p.piece[slot + lane] : make_uint4(0xff800000u, 0u, 0u, 0u);
-        if (!reads_row(p, row)) {
-            // an ended beam goes on as it is, with its one candidate
-            const bool ended = p.finished && p.finished[row] && p.scores[row] > -INFINITY;
-            if (lane == 0) {
-                s_kind[w] = ended ? 2 : 0;
-                s_score[w] = score;
-                s_most[w] = 0.f;
-                s_log[w] = {0.f, 0.f};
-            }
-            continue;
-        }
-        float m = __uint_as_float(mine.x);
-        for (int c = lane + 32; c < C; c += 32) m = fmaxf(m, __uint_as_float(p.piece[slot + c].x));
-        m = unordered(__reduce_max_sync(kFull, ordered(m)));
-        float sum = 0.f;
-        if (m > -INFINITY)
-            for (int c = lane; c < C; c += 32) {
-                if (c != lane) mine = p.piece[slot + c];
-                sum += __uint_as_float(mine.y) * fast_exp2((__uint_as_float(mine.x) - m) * kLog2e);
+        const float2* sums = p.sums + static_cast<int64_t>(row) * C;
+        const float2 none = make_float2(-INFINITY, 0.f);
+        const float2 a = lane < C ? sums[lane] : none, b = lane + 32 < C ? sums[lane + 32] : none;
+        const float given = p.scores[row];
+        const bool over = p.finished && p.finished[row], alive = given > -INFINITY;
+        const float score = fminf(given, FLT_MAX);
+        float m = fmaxf(a.x, b.x), sum = 0.f;
+        if (!over && alive) {
+            for (int c = lane + 64; c < C; c += 32) m = fmaxf(m, sums[c].x);
+            m = unordered(__reduce_max_sync(kFull, ordered(m)));
+            if (m > -INFINITY) {
+                sum = a.y * fast_exp2((a.x - m) * kLog2e) + b.y * fast_exp2((b.x - m) * kLog2e);
+                for (int c = lane + 64; c < C; c += 32) sum += sums[c].y * fast_exp2((sums[c].x - m) * kLog2e);
             }
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) sum += __shfl_xor_sync(kFull, sum, off);
+            for (int off = 1; off < 32; off <<= 1) sum += __shfl_xor_sync(kFull, sum, off);
+        }
         if (lane == 0) {
-            s_kind[w] = 1;
+            // an ended beam goes on as it is, with its one candidate
+            const int kind = !alive ? 0 : over ? 2 : m > -INFINITY ? 1 : 0;
+            const Two lg = kind == 1 ? two_log(sum, s_table) : Two{0.f, 0.f};   // (the sum is 1 at least, but for its rounding)
+            s_kind[w] = static_cast<int8_t>(kind);
             s_score[w] = score;
-            s_most[w] = m;
-            s_log[w] = two_log(sum);   // (at least 1, where the row has candidates)
+            s_most[w] = kind == 1 ? m : 0.f;
+            s_log[w] = lg;
+            s_add[w] = kind == 1 ? (score - lg.hi) - m : -INFINITY;
         }
     }
     __syncthreads();
-    auto count_of = [&](int l, int n) -> int {   // entries of list l, n those of its piece
-        const int kind = s_kind[l / C];
-        return kind == 1 ? n : kind == 2 && l % C == 0 ? 1 : 0;
+    auto cand_of = [&](int beam, u64 key) {
+        const float x = unordered(static_cast<uint32_t>(key >> 32));
+        const Two lg = s_log[beam];
+        const Two lp = two_add(two_sum(x, -s_most[beam]), {-lg.hi, -lg.lo});
+        const Two t = two_add({s_score[beam], 0.f}, lp);
+        // (below fp32's range: -inf, and no candidate)
+        return t.hi >= -FLT_MAX ? Cand{order_of({fminf(t.hi, FLT_MAX), t.lo}), key, beam} : Cand{0, 0, 0};
     };
-    auto cand_of = [&](int l, u64 key) {
-        Cand c;
-        c.beam = l / C;
-        c.key = s_kind[c.beam] == 2 ? key_of(0.f, p.end_token) : key;
-        const float x = unordered(static_cast<uint32_t>(c.key >> 32));
-        const Two lg = s_log[c.beam];
-        const Two lp = two_add(two_sum(x, -s_most[c.beam]), {-lg.hi, -lg.lo});
-        Two t = two_add({s_score[c.beam], 0.f}, lp);
-        if (!(t.hi >= -FLT_MAX && t.hi <= FLT_MAX)) t = {__fadd_rn(s_score[c.beam], lp.hi >= -FLT_MAX ? lp.hi : -FLT_MAX), 0.f};
-        c.score = order_of(t);
-        return c;
-    };
-    auto entry = [&](int l, int i) { return cand_of(l, p.best[(slot0 + l) * k + i]); };
-    // (scores are compared by hi alone here: the order of both is never the other way)
-    uint32_t probe = 0;
-    const int n0 = has ? count_of(tid, n_first) : 0;
-    const Cand first = n0 > 0 ? cand_of(tid, k_first) : Cand{0, 0, 0};
-    if (n0 >= d) probe = static_cast<uint32_t>((d > 1 ? cand_of(tid, k_probe) : first).score >> 32);
-    for (int l = tid + kJoinThreads; l < lists; l += kJoinThreads)
-        if (count_of(l, static_cast<int>(p.piece[slot0 + l].z)) >= d)
-            probe = max(probe, static_cast<uint32_t>(entry(l, d - 1).score >> 32));
-    s_probe[tid] = probe;
+    auto ended = [&](int beam) { return cand_of(beam, key_of(0.f, p.end_token)); };
+    auto row_of = [&](int beam) { return static_cast<const T*>(p.logits) + (s * W + beam) * p.stride; };
+
+    // tau: the k-th best of the sets' best (a set's four threads take every 512th
+    // group each): k groups, or ended beams, are not below it.  A set's number in
+    // the lowest bits tells equal ones apart; what it takes off is part of the room.
+    float best = -INFINITY, room = 0.f;
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+        const int g = tid + u * kJoinThreads;
+        held[u] = g < total ? held[u] + s_add[g / per_row] : -INFINITY;
+        best = fmaxf(best, held[u]);
+    }
+    for (int g = tid + kHeld * kJoinThreads; g < total; g += kJoinThreads) best = fmaxf(best, groups[g] + s_add[g / per_row]);
+    if (tid < W && s_kind[tid] == 2) best = fmaxf(best, s_score[tid]);
+    for (int w = 0; w < W; ++w) room = fmaxf(room, s_kind[w] == 1 ? fabsf(s_score[w]) + fabsf(s_most[w]) + s_log[w].hi : 0.f);
+    best = fmaxf(best, __shfl_xor_sync(kFull, best, 1));
+    best = fmaxf(best, __shfl_xor_sync(kFull, best, 2));
+    const uint32_t mine = (ordered(best) & ~(kJoinSets - 1u)) | static_cast<uint32_t>(tid >> 2);
+    if ((lane & 3) == 0) s_set[tid >> 2] = mine;
     __syncthreads();
-    if (tid < lists) {
-        const int n = min(lists, kJoinThreads);
+    {
         int better = 0;
-        for (int i = 0; i < n; i += 4) {
-            const uint4 o = *reinterpret_cast<const uint4*>(s_probe + i);   // (0 behind the last)
-            better += o.x > probe || (o.x == probe && i < tid);
-            better += o.y > probe || (o.y == probe && i + 1 < tid);
-            better += o.z > probe || (o.z == probe && i + 2 < tid);
-            better += o.w > probe || (o.w == probe && i + 3 < tid);
+#pragma unroll
+        for (int i = 0; i < kJoinSets / 4; i += 4) {
+            const uint4 o = *reinterpret_cast<const uint4*>(s_set + (tid & 3) * (kJoinSets / 4) + i);
+            better += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
         }
-        if (better == q - 1) s_tau = probe;
+        better += __shfl_xor_sync(kFull, better, 1);
+        better += __shfl_xor_sync(kFull, better, 2);
+        if (better == k - 1) s_tau = unordered(mine);
     }
     __syncthreads();
-    const uint32_t tau = s_tau;
-    for (int l = tid; l < lists; l += kJoinThreads) {
-        const int n = l == tid ? n0 : count_of(l, static_cast<int>(p.piece[slot0 + l].z));
-        for (int i = 0; i < n; ++i) {
-            const Cand c = l == tid && i == 0 ? first : entry(l, i);
-            if (static_cast<uint32_t>(c.score >> 32) < tau) break;
-            const int at = atomicAdd(&s_count, 1);
-            if (at < kJoinCap) {
-                s_cs[at] = c.score;
-                s_ck[at] = c.key;
-                s_cb[at] = c.beam;
+    // A score in fp32 is off by less than 2^-21 of `room` and itself (four roundings,
+    // of numbers up to these), the number in the low bits is 2^-16 of tau, and both
+    // sides are.  (tau of no group: below every number.)
+    const float t0 = s_tau, tau = t0 > -FLT_MAX ? t0 - 9.5367431640625e-7f * room - 3.0517578125e-5f * fabsf(t0) : -FLT_MAX;
+    auto push = [&](const Cand& c) {
+        const int i = atomicAdd(&s_count, 1);
+        if (i < kJoinCap) {
+            s_cs[i] = c.score;
+            s_ck[i] = c.key;
+            s_cb[i] = c.beam;
+        }
+    };
+    if (best >= tau) {
+        auto list = [&](int g) {
+            const int i = atomicAdd(&s_groups, 1);
+            if (i < kJoinCap) s_list[i] = g;
+        };
+#pragma unroll
+        for (int u = 0; u < kHeld; ++u)
+            if (held[u] >= tau) list(tid + u * kJoinThreads);
+        for (int g = tid + kHeld * kJoinThreads; g < total; g += kJoinThreads)
+            if (groups[g] + s_add[g / per_row] >= tau) list(g);
+        if (tid < W && s_kind[tid] == 2 && s_score[tid] >= tau) push(ended(tid));
+    }
+    __syncthreads();
+    const int listed = s_groups;
+    // their logits that reach it, a warp for each group (NaN, as -inf, does not)
+    for (int i = warp; i < min(listed, kJoinCap); i += kWarps) {
+        const int g = s_list[i], beam = g / per_row, e0 = (g - beam * per_row) * kGroup + lane;
+        const T* x = row_of(beam) + e0;
+        const float add = s_add[beam];
+        float f[L::kPer];
+#pragma unroll
+        for (int u = 0; u < L::kPer; ++u) f[u] = e0 + u * 32 < p.vocab ? fminf(L::value(x + u * 32), L::kTop) : -INFINITY;
+#pragma unroll
+        for (int u = 0; u < L::kPer; ++u) {
+            if (f[u] + add >= tau && (f[u] < L::kTop || L::value(x + u * 32) >= L::kTop)) {   // (a NaN is kTop here)
+                const Cand c = cand_of(beam, key_of(f[u], e0 + u * 32));
+                if (c.key) push(c);
             }
         }
     }
@@ -561,38 +514,24 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
         if (p.out_finished) p.out_finished[o + r] = s_kind[c.beam] == 2 || token == p.end_token;
     };
     int found = s_count;
-    if (found <= kJoinCap) {
-        for (int i = tid; i < found; i += kJoinThreads) {
-            const Cand mine{s_cs[i], s_ck[i], s_cb[i]};
+    if (listed <= kJoinCap && found <= kJoinCap) {
+        // rank them against one another, a warp for each
+        for (int i = warp; i < found; i += kWarps) {
+            const Cand c{s_cs[i], s_ck[i], s_cb[i]};
             int better = 0;
-            for (int j = 0; j < found; ++j) {
-                const u64 other = s_cs[j];
-                better += other > mine.score || (other == mine.score && better_than({other, s_ck[j], s_cb[j]}, mine));
-            }
-            if (better < k) put(better, mine);
+            for (int j = lane; j < found; j += 32) better += better_than({s_cs[j], s_ck[j], s_cb[j]}, c);
+            better = __reduce_add_sync(kFull, better);
+            if (lane == 0 && better < k) put(better, c);
         }
         found = min(found, k);
     } else {
-        // many equal scores: the best of the lists' heads, k times
-        for (int l = tid; l < lists; l += kJoinThreads) s_pos[l] = 0;
-        for (found = 0; found < k; ++found) {
-            Cand top{0, 0, 0};
-            int from = -1;
-            for (int l = tid; l < lists; l += kJoinThreads) {
-                if (s_pos[l] >= count_of(l, static_cast<int>(p.piece[slot0 + l].z))) continue;
-                const Cand c = entry(l, s_pos[l]);
-                if (better_than(c, top)) {
-                    top = c;
-                    from = l;
-                }
-            }
-            const Cand mine = top;
+        // Many equal scores.  The best of all threads' `mine`:
+        auto best_of_all = [&](const Cand& mine) {
+            Cand top = mine;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
-                Cand c;
-                c.score = __shfl_xor_sync(kFull, top.score, off);
-                c.key = __shfl_xor_sync(kFull, top.key, off);
-                c.beam = __shfl_xor_sync(kFull, top.beam, off);
+                const Cand c{__shfl_xor_sync(kFull, top.score, off), __shfl_xor_sync(kFull, top.key, off),
+                             __shfl_xor_sync(kFull, top.beam, off)};
                 if (better_than(c, top)) top = c;
             }
             __syncthreads();
@@ -604,15 +543,47 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
             __syncthreads();
             top = {s_cs[0], s_ck[0], s_cb[0]};
 #pragma unroll
-            for (int w = 1; w < kJoinThreads / 32; ++w) {
+            for (int w = 1; w < kWarps; ++w) {
                 const Cand c{s_cs[w], s_ck[w], s_cb[w]};
                 if (better_than(c, top)) top = c;
             }
-            // (candidates are distinct: one thread)
-            if (from >= 0 && mine.score == top.score && mine.key == top.key && mine.beam == top.beam) {
-                put(found, mine);
-                ++s_pos[from];
+            return top;
+        };
+        // the k best groups by their exact scores, one after another (a group's key
+        // holds its number, whose order is that of its logits' indices) ...
+        Cand last{~0ull, ~0ull, -1};
+        int n = 0;
+        for (; n < k; ++n) {
+            Cand top{0, 0, 0};
+            for (int g = tid; g < total; g += kJoinThreads) {
+                const int beam = g / per_row;
+                if (s_kind[beam] != 1 || !(groups[g] > -INFINITY)) continue;
+                const Cand c = cand_of(beam, key_of(groups[g], g - beam * per_row));
+                if (c.key && better_than(last, c) && better_than(c, top)) top = c;
             }
+            last = best_of_all(top);
+            if (last.key == 0) break;
+            if (tid == 0) s_list[n] = last.beam * per_row + static_cast<int>(~static_cast<uint32_t>(last.key));
+        }
+        __syncthreads();
+        // ... and the k best candidates of these
+        last = {~0ull, ~0ull, -1};
+        for (found = 0; found < k; ++found) {
+            Cand top{0, 0, 0};
+            for (int i = tid; i < n * kGroup; i += kJoinThreads) {
+                const int g = s_list[i / kGroup], beam = g / per_row, e = (g - beam * per_row) * kGroup + i % kGroup;
+                const float f = e < p.vocab ? L::value(row_of(beam) + e) : -INFINITY;
+                if (!(f >= -L::kTop)) continue;
+                const Cand c = cand_of(beam, key_of(fminf(f, L::kTop), e));
+                if (c.key && better_than(last, c) && better_than(c, top)) top = c;
+            }
+            if (tid < W && s_kind[tid] == 2) {
+                const Cand c = ended(tid);
+                if (better_than(last, c) && better_than(c, top)) top = c;
+            }
+            last = best_of_all(top);
+            if (last.key == 0) break;
+            if (tid == 0) put(found, last);
         }
     }
     __syncthreads();
@@ -807,28 +778,21 @@ __global__ void __launch_bounds__(kCopyThreads) beam_tables_kernel(const __grid_
 
 }  // namespace
 
-// 16-byte words per thread
-static int select_vecs(int rows, int vocab, int dtype) {
-    const long long bytes = static_cast<long long>(vocab) * (dtype == 2 ? 4 : 2);
-    return rows * ((bytes + 32767) / 32768) >= 4LL * 152 ? 8 : 4;
-}
-
-int beam_pieces(int rows, int vocab, int dtype) {
-    const int per = kSelThreads * select_vecs(rows, vocab, dtype) * (dtype == 2 ? 4 : 8);
+int beam_pieces(int vocab, int dtype) {
+    const int per = 32 * kSelVecs * (dtype == 2 ? 4 : 8);
     return (vocab + per - 1) / per;
 }
 
 cudaError_t launch_beam_select(const BeamSelectParams& p, int dtype, cudaStream_t s) {
-    const int rows = p.num_seqs * p.beams;
-    const dim3 grid(static_cast<unsigned>(p.chunks) * rows);
-    const bool wide = select_vecs(rows, p.vocab, dtype) == 8;
+    const long long warps = static_cast<long long>(p.num_seqs) * p.beams * p.pieces;
+    const dim3 grid(static_cast<unsigned>((warps + kSelThreads / 32 - 1) / (kSelThreads / 32)));
     auto go = [&](auto t) {
         using T = decltype(t);
-        return launch_pdl(wide ? beam_pieces_kernel<T, 8> : beam_pieces_kernel<T, 4>, grid, dim3(kSelThreads), 0, s, p);
+        const cudaError_t e = launch_pdl(beam_pieces_kernel<T>, grid, dim3(kSelThreads), 0, s, p);
+        if (e != cudaSuccess) return e;
+        return launch_pdl(beam_join_kernel<T>, dim3(p.num_seqs), dim3(kJoinThreads), 0, s, p);
     };
-    const cudaError_t e = dtype == 0 ? go(__half{}) : dtype == 1 ? go(__nv_bfloat16{}) : go(0.f);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(beam_join_kernel, dim3(p.num_seqs), dim3(kJoinThreads), 0, s, p);
+    return dtype == 0 ? go(__half{}) : dtype == 1 ? go(__nv_bfloat16{}) : go(0.f);
 }
 
 cudaError_t launch_beam_copy(const BeamReorderParams& p, cudaStream_t s) {

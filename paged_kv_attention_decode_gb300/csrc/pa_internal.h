@@ -167,9 +167,9 @@ struct BeamSelectParams {
     const uint8_t* finished;      // [S, W] or nullptr
     int64_t stride;
     int num_seqs, beams, vocab, k, end_token;
-    int chunks;                   // pieces of a row
-    uint4* piece;                 // [S * W, chunks]: maximum, sum (fp32 bits), entries
-    unsigned long long* best;     // [S * W, chunks, k] keys, best first
+    int pieces;                   // of a row (beam_pieces)
+    float2* sums;                 // [S * W, pieces]: largest logit, sum of the exponentials
+    float* groups;                // [S * W, pieces, 8]: largest logit of every 512 bytes
 };
 
 // Reordering of beams: kinds of pool are runs of `run_bytes` per token, `runs`
@@ -259,7 +259,7 @@ cudaError_t launch_uniform_rows(int32_t* cu, int num_seqs, int per, cudaStream_t
 cudaError_t launch_cross(const CrossParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int head_dim,
                          int dtype, cudaStream_t s);
 // dtype: 0 fp16, 1 bf16, 2 fp32
-int beam_pieces(int rows, int vocab, int dtype);   // CTAs for a row of logits
+int beam_pieces(int vocab, int dtype);   // pieces of a row of logits, 4 KB each
 cudaError_t launch_beam_select(const BeamSelectParams& p, int dtype, cudaStream_t s);
 cudaError_t launch_beam_copy(const BeamReorderParams& p, cudaStream_t s);
 cudaError_t launch_beam_tables(const BeamReorderParams& p, cudaStream_t s);   // in place, behind the copies
