@@ -38,7 +38,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 //
 // -inf (and NaN, which counts as -inf) is no candidate: a request with fewer than k
 // finite ones fills up with the lowest other indices.
-constexpr int kSelThreads = 256;
+constexpr int kSelThreads = 64;
 constexpr int kSelVecs = 8;                     // 16-byte words per thread
 
 using u64 = unsigned long long;
@@ -152,7 +152,7 @@ __device__ __forceinline__ bool reads_row(const BeamSelectParams& p, int row) {
 
 // One warp per piece of a row: kSelVecs * 512 bytes.
 template <typename T>
-__global__ void __launch_bounds__(kSelThreads, 4) beam_pieces_kernel(const BeamSelectParams p) {
+__global__ void __launch_bounds__(kSelThreads, 16) beam_pieces_kernel(const BeamSelectParams p) {
     using L = Logits<T>;
     constexpr int kPer = L::kPer, kVecs = kSelVecs, kWords = kVecs * 4;
     constexpr bool kWide = std::is_same<T, float>::value;   // one logit a word
@@ -367,6 +367,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
     __shared__ int8_t s_kind[kMaxBeams];              // 0: no candidates, 1: a row of logits, 2: ended
     __shared__ __align__(16) uint32_t s_set[kJoinSets];
     __shared__ float s_tau;
+    __shared__ uint32_t s_room;                       // (bits of a float, 0 or more)
     __shared__ int s_groups, s_count;
     __shared__ u64 s_cs[kJoinCap], s_ck[kJoinCap];
     __shared__ int s_cb[kJoinCap], s_list[kJoinCap];
@@ -376,7 +377,10 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
     const int W = p.beams, k = p.k, C = p.pieces;
     const int per_row = C * kSelVecs, total = W * per_row;   // groups (those past the row are -inf)
     if (tid < 32) s_table[tid] = {kLogTable[tid][0], kLogTable[tid][1]};
-    if (tid == 0) s_groups = s_count = 0;
+    if (tid == 0) {
+        s_groups = s_count = 0;
+        s_room = 0u;
+    }
     __syncthreads();
     pdl_trigger();
     pdl_wait();
@@ -417,9 +421,13 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
             s_most[w] = kind == 1 ? m : 0.f;
             s_log[w] = lg;
             s_add[w] = kind == 1 ? (score - lg.hi) - m : -INFINITY;
+            if (kind == 1) atomicMax(&s_room, __float_as_uint(fabsf(score) + fabsf(m) + fabsf(lg.hi)));
         }
     }
     __syncthreads();
+    // the beam of group g: the quotient's error, 2^-18 at most, is below half a group
+    const float inv_row = 1.f / static_cast<float>(per_row);
+    auto beam_of = [&](int g) { return static_cast<int>((static_cast<float>(g) + 0.5f) * inv_row); };
     auto cand_of = [&](int beam, u64 key) {
         const float x = unordered(static_cast<uint32_t>(key >> 32));
         const Two lg = s_log[beam];
@@ -434,16 +442,15 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
     // tau: the k-th best of the sets' best (a set's four threads take every 512th
     // group each): k groups, or ended beams, are not below it.  A set's number in
     // the lowest bits tells equal ones apart; what it takes off is part of the room.
-    float best = -INFINITY, room = 0.f;
+    float best = -INFINITY;
 #pragma unroll
     for (int u = 0; u < kHeld; ++u) {
         const int g = tid + u * kJoinThreads;
-        held[u] = g < total ? held[u] + s_add[g / per_row] : -INFINITY;
+        held[u] = g < total ? held[u] + s_add[beam_of(g)] : -INFINITY;
         best = fmaxf(best, held[u]);
     }
-    for (int g = tid + kHeld * kJoinThreads; g < total; g += kJoinThreads) best = fmaxf(best, groups[g] + s_add[g / per_row]);
+    for (int g = tid + kHeld * kJoinThreads; g < total; g += kJoinThreads) best = fmaxf(best, groups[g] + s_add[beam_of(g)]);
     if (tid < W && s_kind[tid] == 2) best = fmaxf(best, s_score[tid]);
-    for (int w = 0; w < W; ++w) room = fmaxf(room, s_kind[w] == 1 ? fabsf(s_score[w]) + fabsf(s_most[w]) + s_log[w].hi : 0.f);
     best = fmaxf(best, __shfl_xor_sync(kFull, best, 1));
     best = fmaxf(best, __shfl_xor_sync(kFull, best, 2));
     const uint32_t mine = (ordered(best) & ~(kJoinSets - 1u)) | static_cast<uint32_t>(tid >> 2);
@@ -452,8 +459,8 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
     {
         int better = 0;
 #pragma unroll
-        for (int i = 0; i < kJoinSets / 4; i += 4) {
-            const uint4 o = *reinterpret_cast<const uint4*>(s_set + (tid & 3) * (kJoinSets / 4) + i);
+        for (int i = 0; i < kJoinSets / 4; i += 4) {   // (a fourth of the sets a thread)
+            const uint4 o = *reinterpret_cast<const uint4*>(s_set + 4 * i + 4 * (tid & 3));
             better += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
         }
         better += __shfl_xor_sync(kFull, better, 1);
@@ -464,7 +471,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
     // A score in fp32 is off by less than 2^-21 of `room` and itself (four roundings,
     // of numbers up to these), the number in the low bits is 2^-16 of tau, and both
     // sides are.  (tau of no group: below every number.)
-    const float t0 = s_tau, tau = t0 > -FLT_MAX ? t0 - 9.5367431640625e-7f * room - 3.0517578125e-5f * fabsf(t0) : -FLT_MAX;
+    const float t0 = s_tau, tau = t0 > -FLT_MAX ? t0 - 9.5367431640625e-7f * __uint_as_float(s_room) - 3.0517578125e-5f * fabsf(t0) : -FLT_MAX;
     auto push = [&](const Cand& c) {
         const int i = atomicAdd(&s_count, 1);
         if (i < kJoinCap) {
@@ -482,24 +489,35 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
         for (int u = 0; u < kHeld; ++u)
             if (held[u] >= tau) list(tid + u * kJoinThreads);
         for (int g = tid + kHeld * kJoinThreads; g < total; g += kJoinThreads)
-            if (groups[g] + s_add[g / per_row] >= tau) list(g);
+            if (groups[g] + s_add[beam_of(g)] >= tau) list(g);
         if (tid < W && s_kind[tid] == 2 && s_score[tid] >= tau) push(ended(tid));
     }
     __syncthreads();
     const int listed = s_groups;
     // their logits that reach it, a warp for each group (NaN, as -inf, does not)
-    for (int i = warp; i < min(listed, kJoinCap); i += kWarps) {
-        const int g = s_list[i], beam = g / per_row, e0 = (g - beam * per_row) * kGroup + lane;
-        const T* x = row_of(beam) + e0;
-        const float add = s_add[beam];
-        float f[L::kPer];
+    const int looked = min(listed, kJoinCap);
+    for (int i = warp; i < looked; i += 2 * kWarps) {   // (two groups' loads in flight)
+        float f[2][L::kPer], add[2];
+        const T* x[2];
+        int beam[2], e0[2];
 #pragma unroll
-        for (int u = 0; u < L::kPer; ++u) f[u] = e0 + u * 32 < p.vocab ? fminf(L::value(x + u * 32), L::kTop) : -INFINITY;
+        for (int v = 0; v < 2; ++v) {
+            const int g = s_list[min(i + v * kWarps, looked - 1)];
+            beam[v] = beam_of(g);
+            e0[v] = (g - beam[v] * per_row) * kGroup + lane;
+            x[v] = row_of(beam[v]) + e0[v];
+            add[v] = i + v * kWarps < looked ? s_add[beam[v]] : -INFINITY;
 #pragma unroll
-        for (int u = 0; u < L::kPer; ++u) {
-            if (f[u] + add >= tau && (f[u] < L::kTop || L::value(x + u * 32) >= L::kTop)) {   // (a NaN is kTop here)
-                const Cand c = cand_of(beam, key_of(f[u], e0 + u * 32));
-                if (c.key) push(c);
+            for (int u = 0; u < L::kPer; ++u) f[v][u] = e0[v] + u * 32 < p.vocab ? L::value(x[v] + u * 32) : -INFINITY;
+        }
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+#pragma unroll
+            for (int u = 0; u < L::kPer; ++u) {
+                if (f[v][u] + add[v] >= tau) {   // (not a NaN)
+                    const Cand c = cand_of(beam[v], key_of(fminf(f[v][u], L::kTop), e0[v] + u * 32));
+                    if (c.key) push(c);
+                }
             }
         }
     }
@@ -556,7 +574,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
         for (; n < k; ++n) {
             Cand top{0, 0, 0};
             for (int g = tid; g < total; g += kJoinThreads) {
-                const int beam = g / per_row;
+                const int beam = beam_of(g);
                 if (s_kind[beam] != 1 || !(groups[g] > -INFINITY)) continue;
                 const Cand c = cand_of(beam, key_of(groups[g], g - beam * per_row));
                 if (c.key && better_than(last, c) && better_than(c, top)) top = c;
@@ -571,7 +589,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
         for (found = 0; found < k; ++found) {
             Cand top{0, 0, 0};
             for (int i = tid; i < n * kGroup; i += kJoinThreads) {
-                const int g = s_list[i / kGroup], beam = g / per_row, e = (g - beam * per_row) * kGroup + i % kGroup;
+                const int g = s_list[i / kGroup], beam = beam_of(g), e = (g - beam * per_row) * kGroup + i % kGroup;
                 const float f = e < p.vocab ? L::value(row_of(beam) + e) : -INFINITY;
                 if (!(f >= -L::kTop)) continue;
                 const Cand c = cand_of(beam, key_of(fminf(f, L::kTop), e));
