@@ -958,6 +958,7 @@ def paged_cross_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
 # --------------------------------------------------------------------------
 
 _LOGITS = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+_U8, _BOOL = torch.uint8, torch.bool
 
 
 def beam_select_workspace_bytes(num_seqs: int, num_beams: int, vocab: int, num_out: int, dtype: torch.dtype) -> int:
@@ -979,62 +980,71 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int, finish
     if stream is not None:
         return _given(stream, beam_select, logits, scores, num_out, finished, end_token, out, workspace)
     S, W = scores.shape
-    V = logits.shape[-1]
-    rows = logits
+    rows, dtype, dev = logits, logits.dtype, logits.get_device()
     if logits.dim() == 3 and logits.shape[:2] == (S, W) and (
             S == 1 or W == 1 or logits.stride(0) == W * logits.stride(1)):
         rows = logits[:, 0] if W == 1 else logits[0] if S == 1 else logits.flatten(0, 1)
-    dev = logits.get_device()
-    code = _LOGITS.get(logits.dtype)
+    shape = rows.shape
+    V = shape[-1]
     num_out, end_token = int(num_out), int(end_token)
-    shape = (S, num_out)
-    if not (dev >= 0 and _cuda_device() == dev and code is not None and rows.dim() == 2 and rows.shape[0] == S * W
-            and (V <= 1 or rows.stride(1) == 1)
+    code = _LOGITS.get(dtype)
+    ended = _U8 if finished is None else finished.dtype
+    if not (dev >= 0 and _cuda_device() == dev and code is not None and len(shape) == 2 and shape[0] == S * W
+            and (rows.is_contiguous() or V <= 1 or rows.stride(1) == 1) and num_out > 0
             and scores.get_device() == dev and scores.dtype == _F32 and scores.is_contiguous()
             and (finished is None or (finished.get_device() == dev and finished.shape == scores.shape
-                                      and finished.dtype in (torch.uint8, torch.bool) and finished.is_contiguous()
+                                      and (ended == _U8 or ended == _BOOL) and finished.is_contiguous()
                                       and 0 <= end_token < V))
             and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous()))):
         _refuse("beam_select",
                 (_current(dev, scores, finished, workspace), "tensors must be on the current CUDA device"),
-                (code is not None, f"unsupported dtype {logits.dtype}"),
-                (rows.dim() == 2 and rows.shape[0] == S * W and (V <= 1 or rows.stride(1) == 1),
+                (code is not None, f"unsupported dtype {dtype}"),
+                (len(shape) == 2 and shape[0] == S * W and (V <= 1 or rows.stride(1) == 1),
                  "logits: [S * W, V], or [S, W, V] with evenly spaced rows, dense within a row"),
+                (num_out > 0, "num_out: at least 1"),
                 (scores.dtype == _F32 and scores.is_contiguous(), "scores: contiguous float32 [S, W]"),
-                (finished is None or (finished.shape == scores.shape and finished.dtype in (torch.uint8, torch.bool)
+                (finished is None or (finished.shape == scores.shape and (ended == _U8 or ended == _BOOL)
                                       and finished.is_contiguous()), "finished: contiguous uint8 or bool [S, W]"),
                 (False, "end_token: a token, with finished"))
-    kinds = (_F32, _I32T, _I32T, finished.dtype) if finished is not None else (_F32, _I32T, _I32T)
     if out is None:
-        _need(num_out > 0, "num_out: at least 1")
-        out = tuple(torch.empty(shape, dtype=t, device=logits.device) for t in kinds)
+        size, where = (S, num_out), logits.device
+        out = (torch.empty(size, dtype=_F32, device=where), torch.empty(size, dtype=_I32T, device=where),
+               torch.empty(size, dtype=_I32T, device=where))
+        if finished is not None:
+            out += (torch.empty(size, dtype=ended, device=where),)
     else:
         out = tuple(out)
-        _need(len(out) == len(kinds) and all(t.get_device() == dev and t.shape == shape and t.dtype == d
+        kinds = (_F32, _I32T, _I32T) if finished is None else (_F32, _I32T, _I32T, ended)
+        _need(len(out) == len(kinds) and all(t.get_device() == dev and t.shape == (S, num_out) and t.dtype == d
                                              and t.is_contiguous() for t, d in zip(out, kinds)),
               "out: contiguous tensors [S, num_out] of the results' types")
     lib = _lib or load_library()
-    nbytes = lib.pa_beam_select_workspace_bytes(S, W, V, num_out, code)
-    workspace, ws_bytes = _ws(nbytes, logits, workspace)
+    workspace, ws_bytes = _ws(lib.pa_beam_select_workspace_bytes(S, W, V, num_out, code), logits, workspace)
+    if finished is None:
+        done, over = None, None
+    else:
+        done, over = finished.data_ptr(), out[3].data_ptr()
     rc = lib.pa_beam_select(
-        out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr() if finished is not None else None,
-        rows.data_ptr(), rows.stride(0) if S * W > 1 else V, scores.data_ptr(),
-        None if finished is None else finished.data_ptr(), end_token, S, W, V, num_out, code, workspace.data_ptr(),
-        ws_bytes, _raw_stream(dev))
+        out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), over, rows.data_ptr(),
+        rows.stride(0) if S * W > 1 else V, scores.data_ptr(), done, end_token, S, W, V, num_out, code,
+        workspace.data_ptr(), ws_bytes, _raw_stream(dev))
     if rc:
         _check(rc, "pa_beam_select")
     return out
 
 
+_PTRS = {}   # number of layers -> type of an array of that many pointers
+
+
 def _pool_kind(t: torch.Tensor):
     """(kind, num_blocks, num_kv_heads, head_dim) of a pool of any kind."""
-    shape = t.shape
-    if t.dim() == 3 and t.element_size() == 1 and shape[2] % 9 == 0:      # 4-bit tiles
-        return 2, shape[0], shape[1], shape[2] // 9
-    if t.dim() == 4 and t.element_size() == 1 and shape[2] == PA_BLOCK_SIZE:
-        return 1, shape[0], shape[1], shape[3]
-    if t.dim() == 4 and t.element_size() == 2 and shape[1] == PA_BLOCK_SIZE:
+    shape, size = t.shape, t.element_size()
+    if len(shape) == 4 and size == 2 and shape[1] == PA_BLOCK_SIZE:
         return 0, shape[0], shape[2], shape[3]
+    if len(shape) == 4 and size == 1 and shape[2] == PA_BLOCK_SIZE:
+        return 1, shape[0], shape[1], shape[3]
+    if len(shape) == 3 and size == 1 and shape[2] % 9 == 0:      # 4-bit tiles
+        return 2, shape[0], shape[1], shape[2] // 9
     _need(False, "pools: 16-bit [NB, 16, Hkv, D], FP8 [NB, Hkv, 16, D] or 4-bit tiles [NB, Hkv, bytes]")
 
 
@@ -1055,35 +1065,41 @@ def beam_reorder(block_tables: torch.Tensor, seq_lens: torch.Tensor, parents: to
         return _given(stream, beam_reorder, block_tables, seq_lens, parents, k_caches, v_caches, out)
     ks = [k_caches] if isinstance(k_caches, torch.Tensor) else list(k_caches)
     vs = [v_caches] if isinstance(v_caches, torch.Tensor) else list(v_caches)
-    if out is None:
-        out = block_tables
+    pools = ks + vs
     S, W = parents.shape
     dev = block_tables.get_device()
-    kind, NB, H, D = _pool_kind(ks[0]) if ks else (0, 2 ** 27 - 1, 1, 64)
-    if not (dev >= 0 and _cuda_device() == dev and block_tables.dtype == _I32T and block_tables.dim() == 2
-            and block_tables.shape[0] == S * W and block_tables.is_contiguous()
-            and out.get_device() == dev and out.shape == block_tables.shape and out.dtype == _I32T
-            and out.is_contiguous()
+    shape = block_tables.shape
+    kind, NB, H, D = _pool_kind(pools[0]) if pools else (0, 2 ** 27 - 1, 1, 64)
+    same = len(ks) == len(vs)
+    if pools:
+        shape0, dtype0 = pools[0].shape, pools[0].dtype
+        for t in pools:
+            if not (t.shape == shape0 and t.dtype == dtype0 and t.get_device() == dev and t.is_contiguous()):
+                same = False
+    if out is None:
+        out = block_tables
+    elif not (out is block_tables or (out.get_device() == dev and out.shape == shape and out.dtype == _I32T
+                                      and out.is_contiguous())):
+        _need(False, "out: the shape, dtype and device of block_tables")
+    if not (same and dev >= 0 and _cuda_device() == dev and len(shape) == 2 and shape[0] == S * W
+            and block_tables.dtype == _I32T and block_tables.is_contiguous()
             and seq_lens.get_device() == dev and seq_lens.dtype == _I32T and seq_lens.numel() == S * W
             and seq_lens.is_contiguous()
-            and parents.get_device() == dev and parents.dtype == _I32T and parents.is_contiguous()
-            and len(vs) == len(ks) and all(t.get_device() == dev and t.shape == ks[0].shape
-                                           and t.dtype == ks[0].dtype and t.is_contiguous() for t in ks + vs)):
+            and parents.get_device() == dev and parents.dtype == _I32T and parents.is_contiguous()):
         _refuse("beam_reorder",
-                (_current(dev, block_tables, seq_lens, parents, out, *ks, *vs),
-                 "tensors must be on the current CUDA device"),
-                (block_tables.dtype == _I32T and block_tables.dim() == 2 and block_tables.shape[0] == S * W
+                (_current(dev, block_tables, seq_lens, parents, *pools), "tensors must be on the current CUDA device"),
+                (block_tables.dtype == _I32T and len(shape) == 2 and shape[0] == S * W
                  and block_tables.is_contiguous(), "block_tables: contiguous int32 [S * W, max_blocks]"),
-                (out.shape == block_tables.shape and out.dtype == _I32T and out.is_contiguous(),
-                 "out: the shape and dtype of block_tables"),
                 (seq_lens.dtype == _I32T and seq_lens.numel() == S * W and seq_lens.is_contiguous(),
                  "seq_lens: int32 [S * W]"),
                 (parents.dtype == _I32T and parents.is_contiguous(), "parents: contiguous int32 [S, W]"),
                 (False, "k_caches and v_caches: as many, contiguous, of one shape and dtype"))
     n = len(ks)
-    ptrs = _p * n
+    ptrs = _PTRS.get(n)
+    if ptrs is None:
+        ptrs = _PTRS[n] = _p * n
     rc = (_lib or load_library()).pa_beam_reorder(
-        out.data_ptr(), block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(), parents.data_ptr(), S, W,
+        out.data_ptr(), block_tables.data_ptr(), shape[1], seq_lens.data_ptr(), parents.data_ptr(), S, W,
         ptrs(*[t.data_ptr() for t in ks]), ptrs(*[t.data_ptr() for t in vs]), n, NB, H, D, PA_BLOCK_SIZE, kind,
         _raw_stream(dev))
     if rc:
