@@ -33,8 +33,11 @@ template <int D, int NT>
 struct CrossShape {
     static constexpr int kCols = 8 * NT;
     static constexpr int kTileBytes = 16 * D * 2;
-    static constexpr int kStageBytes = 2 * kTileBytes;   // K and V of one block
-    static constexpr int kStages = (NT > 1 ? 3 : 2) * (128 / D);
+    // blocks of a step: 8 KB of K and V either way, so that a step's latency and its
+    // reductions are spent on as many bytes
+    static constexpr int kBlocks = 128 / D;
+    static constexpr int kStageBytes = 2 * kBlocks * kTileBytes;   // the K tiles, then the V tiles
+    static constexpr int kStages = NT > 1 ? 3 : 2;
     static constexpr int kMinCtas = NT > 1 ? 2 : 3;
     static constexpr int kRingBytes = kCrossWarps * kStages * kStageBytes;
     // the join: one fp32 accumulator [column][D] per warp, over the rings
@@ -87,37 +90,56 @@ struct CrossState {
     float o[KS][NT][4];       // O^T
     float m[NT][2], l[NT][2];
 
-    // One block: tiles of 16 states, of which the first nvalid are the sequence's.
-    __device__ __forceinline__ void step(uint8_t* kt, uint8_t* vt, int nvalid, int lane, float scale_log2) {
-        const uint32_t ka = smem_addr(kt), va = smem_addr(vt);
-        float c[NT][4], c2[NT][4];   // two chains: even and odd k-steps
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) c[nt][e] = c2[nt][e] = 0.f;
+    // kBlocks tiles of 16 states, of which the first valid[b] are the sequence's.
+    static constexpr int NB = CrossShape<D, NT>::kBlocks, kTile = CrossShape<D, NT>::kTileBytes;
+    __device__ __forceinline__ void step(uint8_t* stage, uint32_t valid, int lane, float scale_log2) {
+        const uint32_t ka = smem_addr(stage), va = ka + NB * kTile;
+        float c[NB][NT][4];
         {
             const int tok = (lane & 7) + ((lane >> 3) & 1) * 8, dsub = ((lane >> 4) & 1) * 8;
+            float c2[NB][NT][4];   // two chains: even and odd k-steps
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) c[b][nt][e] = c2[b][nt][e] = 0.f;
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
-                uint32_t a[4];
-                ldsm_x4(ka + tile_off<D>(tok, kk * 16 + dsub), a[0], a[1], a[2], a[3]);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) Mma<T>::run(kk & 1 ? c2[nt] : c[nt], a, qb[kk][nt][0], qb[kk][nt][1]);
+                for (int b = 0; b < NB; ++b) {
+                    uint32_t a[4];
+                    ldsm_x4(ka + b * kTile + tile_off<D>(tok, kk * 16 + dsub), a[0], a[1], a[2], a[3]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) Mma<T>::run(kk & 1 ? c2[b][nt] : c[b][nt], a, qb[kk][nt][0], qb[kk][nt][1]);
+                }
             }
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) c[b][nt][e] = (c[b][nt][e] + c2[b][nt][e]) * scale_log2;
         }
-        const int r0 = lane >> 2;   // this lane's states: r0 and r0 + 8
+        const bool full = valid == (NB == 2 ? 0x1010u : 0x10u);
+        if (!full) {
+            const int r0 = lane >> 2;   // this lane's states: r0 and r0 + 8
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (r0 + (e >> 1) * 8 >= static_cast<int>(valid >> (8 * b) & 0xffu)) c[b][nt][e] = -INFINITY;
+        }
         float mx[NT][2];
         bool grow = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                c[nt][e] = (c[nt][e] + c2[nt][e]) * scale_log2;
-                if (r0 + (e >> 1) * 8 >= nvalid) c[nt][e] = -INFINITY;
-            }
-#pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float x = fmaxf(c[nt][e], c[nt][2 + e]);
+                float x = fmaxf(c[0][nt][e], c[0][nt][2 + e]);
+                if constexpr (NB == 2) x = fmaxf(x, fmaxf(c[1][nt][e], c[1][nt][2 + e]));
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, off));
                 mx[nt][e] = x;
@@ -141,41 +163,51 @@ struct CrossState {
                 }
         }
         // P, rounded to T for the product with V (weights of 0 to 2^8), its sum kept in fp32
-        uint32_t b0[NT], b1[NT];
+        uint32_t b0[NB][NT], b1[NB][NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             // (a column whose scores are all -inf, or NaN, has no reference yet)
             const float mu0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], mu1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-            const float p0 = fast_exp2(c[nt][0] - mu0), p1 = fast_exp2(c[nt][1] - mu1);
-            const float p2 = fast_exp2(c[nt][2] - mu0), p3 = fast_exp2(c[nt][3] - mu1);
-            l[nt][0] += p0 + p2;
-            l[nt][1] += p1 + p3;
-            // the B operand wants P[state 2 (l % 4) + e (+ 8)][column l / 4]
-            const uint32_t lo = Elem<T>::pack(p0, p1), hi = Elem<T>::pack(p2, p3);
-            const int src = ((lane & 3) << 3) + (lane >> 3);
-            const uint32_t x0 = __shfl_sync(kFull, lo, src), x1 = __shfl_sync(kFull, lo, src + 4);
-            const uint32_t y0 = __shfl_sync(kFull, hi, src), y1 = __shfl_sync(kFull, hi, src + 4);
-            const uint32_t sel = ((lane >> 2) & 1) ? 0x7632u : 0x5410u;
-            b0[nt] = __byte_perm(x0, x1, sel);
-            b1[nt] = __byte_perm(y0, y1, sel);
-        }
-        if (nvalid < 16) {
-            // rows behind the last state may hold anything: 0 * NaN must not reach O
-            const int n16 = (16 - nvalid) * 8;
 #pragma unroll
-            for (int h = 0; h < D / 64; ++h) {
-                uint4* z = reinterpret_cast<uint4*>(vt + h * TileGeom<D>::kHalfBytes + nvalid * 128);
-                for (int i = lane; i < n16; i += 32) z[i] = make_uint4(0, 0, 0, 0);
+            for (int b = 0; b < NB; ++b) {
+                const float p0 = fast_exp2(c[b][nt][0] - mu0), p1 = fast_exp2(c[b][nt][1] - mu1);
+                const float p2 = fast_exp2(c[b][nt][2] - mu0), p3 = fast_exp2(c[b][nt][3] - mu1);
+                l[nt][0] += p0 + p2;
+                l[nt][1] += p1 + p3;
+                // the B operand wants P[state 2 (l % 4) + e (+ 8)][column l / 4]
+                const uint32_t lo = Elem<T>::pack(p0, p1), hi = Elem<T>::pack(p2, p3);
+                const int src = ((lane & 3) << 3) + (lane >> 3);
+                const uint32_t x0 = __shfl_sync(kFull, lo, src), x1 = __shfl_sync(kFull, lo, src + 4);
+                const uint32_t y0 = __shfl_sync(kFull, hi, src), y1 = __shfl_sync(kFull, hi, src + 4);
+                const uint32_t sel = ((lane >> 2) & 1) ? 0x7632u : 0x5410u;
+                b0[b][nt] = __byte_perm(x0, x1, sel);
+                b1[b][nt] = __byte_perm(y0, y1, sel);
+            }
+        }
+        if (!full) {
+            // rows behind the last state (and tiles not loaded) may hold anything:
+            // 0 * NaN must not reach O
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const int v = static_cast<int>(valid >> (8 * b) & 0xffu), n16 = (16 - v) * 8;
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h) {
+                    uint4* z = reinterpret_cast<uint4*>(stage + (NB + b) * kTile + h * TileGeom<D>::kHalfBytes + v * 128);
+                    for (int i = lane; i < n16; i += 32) z[i] = make_uint4(0, 0, 0, 0);
+                }
             }
             __syncwarp();
         }
         const int tok = (lane & 7) + ((lane >> 4) & 1) * 8, dsub = ((lane >> 3) & 1) * 8;
 #pragma unroll
-        for (int mt = 0; mt < KS; ++mt) {
-            uint32_t a[4];
-            ldsm_x4_t(va + tile_off<D>(tok, mt * 16 + dsub), a[0], a[1], a[2], a[3]);
+        for (int b = 0; b < NB; ++b) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) Mma<T>::run(o[mt][nt], a, b0[nt], b1[nt]);
+            for (int mt = 0; mt < KS; ++mt) {
+                uint32_t a[4];
+                ldsm_x4_t(va + b * kTile + tile_off<D>(tok, mt * 16 + dsub), a[0], a[1], a[2], a[3]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) Mma<T>::run(o[mt][nt], a, b0[b][nt], b1[b][nt]);
+            }
         }
     }
 };
@@ -188,6 +220,7 @@ __global__ void __launch_bounds__(kCrossWarps * 32, CrossShape<D, NT>::kMinCtas)
     constexpr int kCols = Sh::kCols;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bars[kCrossWarps][Sh::kStages];
+    __shared__ uint32_t s_valid[kCrossWarps][Sh::kStages];   // states of a stage's tiles, a byte each
     __shared__ float s_m[kCrossWarps][kCols];   // the warps' maxima, then [0]: the CTA's
     __shared__ float s_l[kCrossWarps][kCols];
 
@@ -213,6 +246,17 @@ __global__ void __launch_bounds__(kCrossWarps * 32, CrossShape<D, NT>::kMinCtas)
     const int g = item % p.num_kv_heads, b = item / p.num_kv_heads;
     if (!p.overlap) pdl_wait();
 
+    // The length, the rows and this warp's first block ids are asked for together
+    // (entries of the sequence's table row, used only if the length reaches them).
+    constexpr int NB = Sh::kBlocks;
+    const int first = rank * kCrossWarps + warp, stride = S * kCrossWarps;   // this warp's steps: first, first + stride, ...
+    const int32_t* table = p.block_tables + static_cast<int64_t>(b) * p.max_blocks;
+    int n = p.seq_lens[b], ids[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+        const int64_t blk = (static_cast<int64_t>(first) + static_cast<int64_t>(lane) * stride) * NB + i;
+        ids[i] = blk < p.max_blocks ? table[blk] : 0;
+    }
     int row0 = b * p.q_per_seq, qlen = p.q_per_seq;
     if (p.cu_q_lens) {
         row0 = p.cu_q_lens[b];
@@ -230,38 +274,51 @@ __global__ void __launch_bounds__(kCrossWarps * 32, CrossShape<D, NT>::kMinCtas)
         if (p.overlap) pdl_wait();
         return;
     }
-    int n = p.seq_lens[b];
     if (n < 0 || n > p.max_len || n > p.max_blocks * 16) {   // rows of zeros, as for no states
         if (g == 0 && chunk == 0 && rank == 0 && tid == 0) record_error(p.err, PA_DEVERR_SEQ_LEN_);
         n = 0;
     }
     const int nblk = (n + 15) >> 4;
 
-    // this warp's blocks: first, first + stride, ...
-    const int first = rank * kCrossWarps + warp, stride = S * kCrossWarps;
-    const int count = nblk > first ? (nblk - first + stride - 1) / stride : 0;
-    const int32_t* table = p.block_tables + static_cast<int64_t>(b) * p.max_blocks + first;
-    int at = 0, issued = 0, ids = 0;
-    bool partial = false;   // the last block issued is the sequence's last, and not full
-    auto fetch = [&]() {    // the next block whose id is in the pool (others contribute nothing)
+    const int steps = (nblk + NB - 1) / NB;
+    const int count = steps > first ? (steps - first + stride - 1) / stride : 0;
+    int at = 0, issued = 0;
+    auto fetch = [&]() {    // the next step with a block in the pool (others contribute nothing)
         while (at < count) {
-            if ((at & 31) == 0) ids = at + lane < count ? table[static_cast<int64_t>(at + lane) * stride] : 0;
-            const int id = __shfl_sync(kFull, ids, at & 31);
-            const int blk = first + at * stride;
-            ++at;
-            if (id < 0 || id >= p.num_blocks) {
-                if (lane == 0) record_error(p.err, PA_DEVERR_BLOCK_ID_);
-                continue;
+            if ((at & 31) == 0 && at > 0) {
+                const int blk = (first + (at + lane) * stride) * NB;
+#pragma unroll
+                for (int i = 0; i < NB; ++i) ids[i] = at + lane < count && blk + i < nblk ? table[blk + i] : 0;
             }
+            const int blk = (first + at * stride) * NB;
+            uint32_t valid = 0;
+            int id[NB], live = 0;
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                id[i] = __shfl_sync(kFull, ids[i], at & 31);
+                if (blk + i >= nblk) continue;
+                if (id[i] < 0 || id[i] >= p.num_blocks) {
+                    if (lane == 0) record_error(p.err, PA_DEVERR_BLOCK_ID_);
+                    continue;
+                }
+                valid |= static_cast<uint32_t>(min(16, n - (blk + i) * 16)) << (8 * i);
+                ++live;
+            }
+            ++at;
+            if (live == 0) continue;
             if (lane == 0) {
                 const int slot = issued % Sh::kStages;
                 uint8_t* dst = ring + slot * Sh::kStageBytes;
-                mbar_arrive_expect_tx(&bar[slot], Sh::kStageBytes);
-                tma_load_4d(dst, &kmap, &bar[slot], 0, id * 16, 0, g);
-                tma_load_4d(dst + Sh::kTileBytes, &vmap, &bar[slot], 0, id * 16, 0, g);
+                s_valid[warp][slot] = valid;
+                mbar_arrive_expect_tx(&bar[slot], live * 2 * Sh::kTileBytes);
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    if (!(valid >> (8 * i) & 0xffu)) continue;
+                    tma_load_4d(dst + i * Sh::kTileBytes, &kmap, &bar[slot], 0, id[i] * 16, 0, g);
+                    tma_load_4d(dst + (NB + i) * Sh::kTileBytes, &vmap, &bar[slot], 0, id[i] * 16, 0, g);
+                }
             }
             ++issued;
-            partial = blk == nblk - 1 && (n & 15);
             return;
         }
     };
@@ -297,8 +354,7 @@ __global__ void __launch_bounds__(kCrossWarps * 32, CrossShape<D, NT>::kMinCtas)
         const int slot = done % Sh::kStages;
         ok = __all_sync(kFull, mbar_wait(&bar[slot], (done / Sh::kStages) & 1));
         if (!ok) break;
-        uint8_t* t = ring + slot * Sh::kStageBytes;
-        st.step(t, t + Sh::kTileBytes, partial && done + 1 == issued ? n & 15 : 16, lane, p.scale_log2);
+        st.step(ring + slot * Sh::kStageBytes, s_valid[warp][slot], lane, p.scale_log2);
         ++done;
         __syncwarp();
         fetch();
@@ -443,7 +499,7 @@ cudaError_t launch_cross(const CrossParams& p, const CUtensorMap& kmap, const CU
     const long long items = static_cast<long long>(p.num_seqs) * p.num_kv_heads * p.col_chunks;
     const int blocks = (p.max_len + 15) / 16;
     int splits = 1;
-    while (splits < kMaxSplits && items * splits < 6LL * sm_count() && blocks >= splits * kCrossWarps * 4) splits *= 2;
+    while (splits < kMaxSplits && items * splits < 4LL * sm_count() && blocks >= splits * kCrossWarps * 4) splits *= 2;
     const bool wide = p.max_q * p.group > 8;
     auto go = [&](auto t, auto d) {
         using T = decltype(t);
