@@ -24,12 +24,13 @@ namespace pa {
 
 namespace {
 
-constexpr int kCrossWarps = 4;
 constexpr int kMaxSplits = 8;         // CTAs of a cluster (the portable limit)
+constexpr int kSortMax = 128;         // sequences that a CTA orders by length, one a thread
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLazyRescaleLog2 = 8.f;   // a column's reference maximum moves only when it has grown by this much
 
-template <int D, int NT>
+// kWarps: 8, one CTA an SM, for as few items as there are SMs; else 4.
+template <int D, int NT, int kWarps>
 struct CrossShape {
     static constexpr int kCols = 8 * NT;
     static constexpr int kTileBytes = 16 * D * 2;
@@ -37,13 +38,13 @@ struct CrossShape {
     // reductions are spent on as many bytes
     static constexpr int kBlocks = 128 / D;
     static constexpr int kStageBytes = 2 * kBlocks * kTileBytes;   // the K tiles, then the V tiles
+    static constexpr int kMinCtas = kWarps == 8 ? 1 : NT > 1 ? 2 : 3;   // an SM holds, by registers
     static constexpr int kStages = NT > 1 ? 3 : 2;
-    static constexpr int kMinCtas = NT > 1 ? 2 : 3;
-    static constexpr int kRingBytes = kCrossWarps * kStages * kStageBytes;
+    static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
     // the join: one fp32 accumulator [column][D] per warp, over the rings
     static constexpr int kPitch = D + 4;
     static constexpr int kAccBytes = kCols * kPitch * 4;
-    static_assert(kCrossWarps * kAccBytes <= kRingBytes, "the accumulators are joined where the rings were");
+    static_assert(kWarps * kAccBytes <= kRingBytes, "the accumulators are joined where the rings were");
     static constexpr int kSmemBytes = kRingBytes + 1024;
 };
 
@@ -91,7 +92,7 @@ struct CrossState {
     float m[NT][2], l[NT][2];
 
     // kBlocks tiles of 16 states, of which the first valid[b] are the sequence's.
-    static constexpr int NB = CrossShape<D, NT>::kBlocks, kTile = CrossShape<D, NT>::kTileBytes;
+    static constexpr int NB = 128 / D, kTile = 16 * D * 2;
     __device__ __forceinline__ void step(uint8_t* stage, uint32_t valid, int lane, float scale_log2) {
         const uint32_t ka = smem_addr(stage), va = ka + NB * kTile;
         float c[NB][NT][4];
@@ -212,26 +213,29 @@ struct CrossState {
     }
 };
 
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kCrossWarps * 32, CrossShape<D, NT>::kMinCtas)
+template <typename T, int D, int NT, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32, CrossShape<D, NT, kWarps>::kMinCtas)
     cross_step_kernel(const CrossParams p, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap) {
-    using Sh = CrossShape<D, NT>;
+    using Sh = CrossShape<D, NT, kWarps>;
+    constexpr int kStages = Sh::kStages;
     constexpr int kCols = Sh::kCols;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bars[kCrossWarps][Sh::kStages];
-    __shared__ uint32_t s_valid[kCrossWarps][Sh::kStages];   // states of a stage's tiles, a byte each
-    __shared__ float s_m[kCrossWarps][kCols];   // the warps' maxima, then [0]: the CTA's
-    __shared__ float s_l[kCrossWarps][kCols];
+    __shared__ uint64_t bars[kWarps][kStages];
+    __shared__ __align__(16) int s_len[kWarps == 4 ? kSortMax : 4];
+    __shared__ int s_seq;
+    __shared__ uint32_t s_valid[kWarps][kStages];   // states of a stage's tiles, a byte each
+    __shared__ float s_m[kWarps][kCols];   // the warps' maxima, then [0]: the CTA's
+    __shared__ float s_l[kWarps][kCols];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_trigger();
     // (the same offset in every CTA of the cluster: the accumulators are read across it)
     uint8_t* smem = smem_raw + (((smem_addr(smem_raw) + 1023u) & ~1023u) - smem_addr(smem_raw));
-    uint8_t* ring = smem + warp * Sh::kStages * Sh::kStageBytes;
+    uint8_t* ring = smem + warp * kStages * Sh::kStageBytes;
     uint64_t* bar = bars[warp];
     if (lane == 0) {
-        for (int s = 0; s < Sh::kStages; ++s) mbar_init(&bar[s], 1);
+        for (int s = 0; s < kStages; ++s) mbar_init(&bar[s], 1);
         fence_barrier_init();
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
@@ -243,13 +247,32 @@ __global__ void __launch_bounds__(kCrossWarps * 32, CrossShape<D, NT>::kMinCtas)
     int item = static_cast<int>(blockIdx.x) / S;
     const int chunk = item % p.col_chunks;
     item /= p.col_chunks;
-    const int g = item % p.num_kv_heads, b = item / p.num_kv_heads;
+    const int g = item % p.num_kv_heads;
+    int b = item / p.num_kv_heads;
     if (!p.overlap) pdl_wait();
+    if (kWarps == 4 && p.longest_first) {
+        // the b-th longest sequence: the CTAs that start last are the short ones
+        const int mine = tid < p.num_seqs ? p.seq_lens[tid] : -0x7fffffff;
+        s_len[tid] = mine;
+        __syncthreads();
+        int longer = 0;
+#pragma unroll 4
+        for (int i = 0; i < p.num_seqs; i += 4) {   // (behind the last one: shorter than any)
+            const int4 o = *reinterpret_cast<const int4*>(s_len + i);
+            longer += o.x > mine || (o.x == mine && i < tid);
+            longer += o.y > mine || (o.y == mine && i + 1 < tid);
+            longer += o.z > mine || (o.z == mine && i + 2 < tid);
+            longer += o.w > mine || (o.w == mine && i + 3 < tid);
+        }
+        if (tid < p.num_seqs && longer == b) s_seq = tid;
+        __syncthreads();
+        b = s_seq;
+    }
 
     // The length, the rows and this warp's first block ids are asked for together
     // (entries of the sequence's table row, used only if the length reaches them).
     constexpr int NB = Sh::kBlocks;
-    const int first = rank * kCrossWarps + warp, stride = S * kCrossWarps;   // this warp's steps: first, first + stride, ...
+    const int first = rank * kWarps + warp, stride = S * kWarps;   // this warp's steps: first, first + stride, ...
     const int32_t* table = p.block_tables + static_cast<int64_t>(b) * p.max_blocks;
     int n = p.seq_lens[b], ids[NB];
 #pragma unroll
@@ -282,7 +305,7 @@ __global__ void __launch_bounds__(kCrossWarps * 32, CrossShape<D, NT>::kMinCtas)
 
     const int steps = (nblk + NB - 1) / NB;
     const int count = steps > first ? (steps - first + stride - 1) / stride : 0;
-    int at = 0, issued = 0;
+    int at = 0, issued = 0, next = 0;   // steps looked at and issued, the ring's next slot
     auto fetch = [&]() {    // the next step with a block in the pool (others contribute nothing)
         while (at < count) {
             if ((at & 31) == 0 && at > 0) {
@@ -307,7 +330,7 @@ __global__ void __launch_bounds__(kCrossWarps * 32, CrossShape<D, NT>::kMinCtas)
             ++at;
             if (live == 0) continue;
             if (lane == 0) {
-                const int slot = issued % Sh::kStages;
+                const int slot = next;
                 uint8_t* dst = ring + slot * Sh::kStageBytes;
                 s_valid[warp][slot] = valid;
                 mbar_arrive_expect_tx(&bar[slot], live * 2 * Sh::kTileBytes);
@@ -319,10 +342,11 @@ __global__ void __launch_bounds__(kCrossWarps * 32, CrossShape<D, NT>::kMinCtas)
                 }
             }
             ++issued;
+            next = next + 1 < kStages ? next + 1 : 0;
             return;
         }
     };
-    for (int s = 0; s < Sh::kStages; ++s) fetch();
+    for (int s = 0; s < kStages; ++s) fetch();
 
     CrossState<T, D, NT> st;
 #pragma unroll
@@ -348,14 +372,21 @@ __global__ void __launch_bounds__(kCrossWarps * 32, CrossShape<D, NT>::kMinCtas)
 #pragma unroll
             for (int e = 0; e < 4; ++e) st.o[mt][nt][e] = 0.f;
 
-    int done = 0;
+    int done = 0, slot = 0;
+    uint32_t phase = 0;
     bool ok = true;
+    auto pass = [&]() {
+        ++done;
+        if (++slot == kStages) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    };
     while (done < issued) {
-        const int slot = done % Sh::kStages;
-        ok = __all_sync(kFull, mbar_wait(&bar[slot], (done / Sh::kStages) & 1));
+        ok = __all_sync(kFull, mbar_wait(&bar[slot], phase));
         if (!ok) break;
         st.step(ring + slot * Sh::kStageBytes, s_valid[warp][slot], lane, p.scale_log2);
-        ++done;
+        pass();
         __syncwarp();
         fetch();
     }
@@ -363,7 +394,7 @@ __global__ void __launch_bounds__(kCrossWarps * 32, CrossShape<D, NT>::kMinCtas)
         // give up: the copies still in flight first (another bounded wait each)
         if (lane == 0) {
             record_error(p.err, PA_DEVERR_TIMEOUT_);
-            for (int i = done + 1; i < issued; ++i) (void)mbar_wait(&bar[i % Sh::kStages], (i / Sh::kStages) & 1);
+            for (; done < issued; pass()) (void)mbar_wait(&bar[slot], phase);
         }
         __syncwarp();
     }
@@ -389,7 +420,7 @@ __global__ void __launch_bounds__(kCrossWarps * 32, CrossShape<D, NT>::kMinCtas)
             const int col = nt * 8 + 2 * (lane & 3) + e;
             float m = s_m[0][col];
 #pragma unroll
-            for (int w = 1; w < kCrossWarps; ++w) m = fmaxf(m, s_m[w][col]);
+            for (int w = 1; w < kWarps; ++w) m = fmaxf(m, s_m[w][col]);
             mc[nt][e] = m;
             const float f = st.m[nt][e] == -INFINITY ? 0.f : fast_exp2(st.m[nt][e] - m);
             if (lane < 4) s_l[warp][col] = st.l[nt][e] * f;
@@ -410,15 +441,15 @@ __global__ void __launch_bounds__(kCrossWarps * 32, CrossShape<D, NT>::kMinCtas)
                 s_m[0][col] = mc[nt][e];
                 float l = s_l[0][col];
 #pragma unroll
-                for (int w = 1; w < kCrossWarps; ++w) l += s_l[w][col];
+                for (int w = 1; w < kWarps; ++w) l += s_l[w][col];
                 s_l[0][col] = l;
             }
     }
-    for (int i = tid; i < ncols * (D / 4); i += kCrossWarps * 32) {
+    for (int i = tid; i < ncols * (D / 4); i += kWarps * 32) {
         float4* x = reinterpret_cast<float4*>(acc + (i / (D / 4)) * Sh::kPitch) + i % (D / 4);
         float4 sum = *x;
 #pragma unroll
-        for (int w = 1; w < kCrossWarps; ++w) {
+        for (int w = 1; w < kWarps; ++w) {
             const float4 y = x[w * (Sh::kAccBytes / 16)];
             sum.x += y.x; sum.y += y.y; sum.z += y.z; sum.w += y.w;
         }
@@ -428,7 +459,7 @@ __global__ void __launch_bounds__(kCrossWarps * 32, CrossShape<D, NT>::kMinCtas)
     if (S > 1) cluster_sync();
     else __syncthreads();
     const uint32_t a_acc = smem_addr(acc), a_m = smem_addr(&s_m[0][0]), a_l = smem_addr(&s_l[0][0]);
-    for (int i = rank * kCrossWarps * 32 + tid; i < ncols * (D / 8); i += S * kCrossWarps * 32) {
+    for (int i = rank * kWarps * 32 + tid; i < ncols * (D / 8); i += S * kWarps * 32) {
         const int col = i / (D / 8), piece = i % (D / 8);
         const uint32_t off = static_cast<uint32_t>((col * Sh::kPitch + piece * 8) * 4);
         float m = -INFINITY;
@@ -457,16 +488,16 @@ __global__ void __launch_bounds__(kCrossWarps * 32, CrossShape<D, NT>::kMinCtas)
     if (p.overlap) pdl_wait();
 }
 
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, int kWarps>
 cudaError_t launch_t(const CrossParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int splits,
                      cudaStream_t s) {
-    constexpr int smem = CrossShape<D, NT>::kSmemBytes;
-    auto kern = cross_step_kernel<T, D, NT>;
+    constexpr int smem = CrossShape<D, NT, kWarps>::kSmemBytes;
+    auto kern = cross_step_kernel<T, D, NT, kWarps>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.num_seqs) * p.num_kv_heads * p.col_chunks * splits);
-    cfg.blockDim = dim3(kCrossWarps * 32);
+    cfg.blockDim = dim3(kWarps * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -492,19 +523,28 @@ cudaError_t launch_uniform_rows(int32_t* cu, int num_seqs, int per, cudaStream_t
     return launch_pdl(uniform_rows_kernel, dim3(std::min(num_seqs / 256 + 1, 64)), dim3(256), 0, s, cu, num_seqs, per);
 }
 
-cudaError_t launch_cross(const CrossParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int head_dim,
-                         int dtype, cudaStream_t s) {
-    // CTAs for one item: more while the items alone do not fill the GPU and every
-    // warp still has a few blocks
+cudaError_t launch_cross(CrossParams p, const CUtensorMap& kmap, const CUtensorMap& vmap, int head_dim, int dtype,
+                         cudaStream_t s) {
+    // CTAs for one item: as many (of 1, 2, 4, 8) as give the GPU two CTAs an SM, while
+    // every warp still has a few blocks.  More cost a cluster's meetings and come a
+    // second time: 128 items of 1000 to 2000 states (32/8 heads of 128, 4 rows) took
+    // 30, 23, 29, 44 us with 1, 2, 4, 8 CTAs; 256 items 38, 41, 54, 81; 16 items 23,
+    // 14, 10.5, 9.8.
     const long long items = static_cast<long long>(p.num_seqs) * p.num_kv_heads * p.col_chunks;
     const int blocks = (p.max_len + 15) / 16;
+    const bool few = items <= sm_count();
     int splits = 1;
-    while (splits < kMaxSplits && items * splits < 4LL * sm_count() && blocks >= splits * kCrossWarps * 4) splits *= 2;
+    while (splits < kMaxSplits && items * splits <= sm_count() && blocks >= splits * 4 * 4) splits *= 2;
     const bool wide = p.max_q * p.group > 8;
+    // more CTAs than run at once: in order of length (64 requests of 512 to 4096
+    // states, 512 items: 96 us instead of 112; the step of prompts beside beams 38
+    // instead of 45)
+    p.longest_first = p.num_seqs > 1 && p.num_seqs <= kSortMax && items * splits > 2LL * sm_count();
     auto go = [&](auto t, auto d) {
         using T = decltype(t);
         constexpr int D = decltype(d)::value;
-        return wide ? launch_t<T, D, 2>(p, kmap, vmap, splits, s) : launch_t<T, D, 1>(p, kmap, vmap, splits, s);
+        if (few) return wide ? launch_t<T, D, 2, 8>(p, kmap, vmap, splits, s) : launch_t<T, D, 1, 8>(p, kmap, vmap, splits, s);
+        return wide ? launch_t<T, D, 2, 4>(p, kmap, vmap, splits, s) : launch_t<T, D, 1, 4>(p, kmap, vmap, splits, s);
     };
     auto of = [&](auto t) {
         return head_dim == 128 ? go(t, std::integral_constant<int, 128>{}) : go(t, std::integral_constant<int, 64>{});

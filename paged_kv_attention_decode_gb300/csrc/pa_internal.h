@@ -153,6 +153,7 @@ struct CrossParams {
     // 1: launched right behind a prefill kernel that allows dependent launch;
     // what this one reads was complete before that one started
     int overlap;
+    int longest_first;            // 1: CTAs take the sequences in order of length
 };
 
 // Selection of the best continuations (see pa_beam.cu).
@@ -256,8 +257,8 @@ cudaError_t launch_decode_mod(const DecodeParams& p, const CUtensorMap& kmap, co
 cudaError_t launch_decode_fp4(const DecodeParams& p, int head_dim, int dtype, cudaStream_t s);
 // cu[i] = i * per, i <= num_seqs
 cudaError_t launch_uniform_rows(int32_t* cu, int num_seqs, int per, cudaStream_t s);
-cudaError_t launch_cross(const CrossParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int head_dim,
-                         int dtype, cudaStream_t s);
+cudaError_t launch_cross(CrossParams p, const CUtensorMap& kmap, const CUtensorMap& vmap, int head_dim, int dtype,
+                         cudaStream_t s);
 // dtype: 0 fp16, 1 bf16, 2 fp32
 int beam_pieces(int vocab, int dtype);   // pieces of a row of logits, 4 KB each
 cudaError_t launch_beam_select(const BeamSelectParams& p, int dtype, cudaStream_t s);
