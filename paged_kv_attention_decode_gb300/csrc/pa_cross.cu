@@ -525,16 +525,19 @@ cudaError_t launch_uniform_rows(int32_t* cu, int num_seqs, int per, cudaStream_t
 
 cudaError_t launch_cross(CrossParams p, const CUtensorMap& kmap, const CUtensorMap& vmap, int head_dim, int dtype,
                          cudaStream_t s) {
-    // CTAs for one item: as many (of 1, 2, 4, 8) as give the GPU two CTAs an SM, while
-    // every warp still has a few blocks.  More cost a cluster's meetings and come a
-    // second time: 128 items of 1000 to 2000 states (32/8 heads of 128, 4 rows) took
-    // 30, 23, 29, 44 us with 1, 2, 4, 8 CTAs; 256 items 38, 41, 54, 81; 16 items 23,
-    // 14, 10.5, 9.8.
+    // An SM needs 8 warps to keep up with its share of the memory: two or three CTAs
+    // of 4 where there are more items than SMs, else one CTA of 8, and for still
+    // fewer items a cluster of 2, 4 or 8 of these, while all run at once (a cluster
+    // lies within a GPC: 32 clusters of 4 do, 16 of 8 do not) and every warp still
+    // has a block or two.  1000 to 2000 states, 32/8 heads of 128, 4 rows, us with
+    // 1, 2, 4, 8 CTAs of 8 warps: 16 items 14.9, 11.3, 9.5, 17.3; 32 items 15.2,
+    // 12.4, 11.8, 27.7; 64 items 18.3, 15.0, 22.2, 46.3; 128 items 22.5, 28.9, 41.0,
+    // 82.9 (one of 4 warps: 29.0); 192 items 36.6 (one of 4 warps: 33.3).
     const long long items = static_cast<long long>(p.num_seqs) * p.num_kv_heads * p.col_chunks;
     const int blocks = (p.max_len + 15) / 16;
     const bool few = items <= sm_count();
     int splits = 1;
-    while (splits < kMaxSplits && items * splits <= sm_count() && blocks >= splits * 4 * 4) splits *= 2;
+    while (few && splits < kMaxSplits && 2 * splits * items <= (splits < 4 ? 128 : 96) && blocks >= splits * 16) splits *= 2;
     const bool wide = p.max_q * p.group > 8;
     // more CTAs than run at once: in order of length (64 requests of 512 to 4096
     // states, 512 items: 96 us instead of 112; the step of prompts beside beams 38
