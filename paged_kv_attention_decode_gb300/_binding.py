@@ -163,7 +163,8 @@ def _given(stream, call, *args, **kw):
         stream = torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
     with torch.cuda.stream(stream):
         made = call(*args, **kw)
-    theirs = (*args, *kw.values())
+    theirs = [*args, *kw.values()]
+    theirs += [t for a in theirs if isinstance(a, (tuple, list)) for t in a]
     for t in made if isinstance(made, tuple) else (made,):
         if not any(t is x for x in theirs):
             t.record_stream(before)
