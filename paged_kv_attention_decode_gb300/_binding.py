@@ -977,7 +977,8 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int, finish
     bool [S, W]: an ended beam's only candidate is end_token, at its own score.
     Returns (scores float32, parents int32, tokens int32), each [S, num_out], and
     with `finished` a fourth like it: the parent had ended, or the token is
-    end_token.  `out`: these tensors, to write to."""
+    end_token.  `out`: these tensors, to write to (with num_out == W they may be
+    scores and finished themselves)."""
     if stream is not None:
         return _given(stream, beam_select, logits, scores, num_out, finished, end_token, out, workspace)
     S, W = scores.shape

@@ -365,6 +365,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
     __shared__ Two s_log[kMaxBeams], s_table[32];
     __shared__ float s_add[kMaxBeams];                // score - largest - logarithm; -inf: no row of candidates
     __shared__ int8_t s_kind[kMaxBeams];              // 0: no candidates, 1: a row of logits, 2: ended
+    __shared__ bool s_over[kMaxBeams];                // (as given: the results may take the inputs' place)
     __shared__ __align__(16) uint32_t s_set[kJoinSets];
     __shared__ float s_tau;
     __shared__ uint32_t s_room;                       // (bits of a float, 0 or more)
@@ -417,6 +418,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
             const int kind = !alive ? 0 : over ? 2 : m > -INFINITY ? 1 : 0;
             const Two lg = kind == 1 ? two_log(sum, s_table) : Two{0.f, 0.f};   // (the sum is 1 at least, but for its rounding)
             s_kind[w] = static_cast<int8_t>(kind);
+            s_over[w] = over;
             s_score[w] = score;
             s_most[w] = kind == 1 ? m : 0.f;
             s_log[w] = lg;
@@ -616,7 +618,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
             p.out_parents[o + r] = w;
             p.out_tokens[o + r] = token;
             if (p.out_finished)
-                p.out_finished[o + r] = (p.finished && p.finished[s * W + w]) || token == p.end_token;
+                p.out_finished[o + r] = s_over[w] || token == p.end_token;
         }
         ++r;
     }

@@ -252,7 +252,8 @@ __global__ void __launch_bounds__(kWarps * 32, CrossShape<D, NT, kWarps>::kMinCt
     if (!p.overlap) pdl_wait();
     if (kWarps == 4 && p.longest_first) {
         // the b-th longest sequence: the CTAs that start last are the short ones
-        const int mine = tid < p.num_seqs ? p.seq_lens[tid] : -0x7fffffff;
+        // (negative lengths, which are refused below, rank before the threads without one)
+        const int mine = tid < p.num_seqs ? max(p.seq_lens[tid], -1) : -2;
         s_len[tid] = mine;
         __syncthreads();
         int longer = 0;

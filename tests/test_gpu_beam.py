@@ -195,6 +195,45 @@ def test_select_same_results_every_time_and_captured():
     check(want, x.flip(0, 1), scores, k)
 
 
+def test_select_in_place_and_captured():
+    """With as many results as beams, scores and flags take the results' place:
+    replays go on from one another."""
+    S, W, V, end = 3, 4, 1500, 9
+    x, scores = make(S, W, V, torch.float16, seed=8, kind="peaked")
+    xd = x.view(S * W, V).to(DEV)
+    cum, fin = torch.from_numpy(scores).to(DEV), torch.zeros((S, W), dtype=torch.uint8, device=DEV)
+    par, tok = torch.empty((S, W), dtype=torch.int32, device=DEV), torch.empty((S, W), dtype=torch.int32, device=DEV)
+    ws = torch.empty(pa.beam_select_workspace_bytes(S, W, V, W, torch.float16), dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pa.beam_select(xd, cum, W, finished=fin, end_token=end, out=(cum, par, tok, fin), workspace=ws)
+    for step in range(6):
+        before, ended = cum.cpu().numpy().copy(), fin.cpu().numpy().copy()
+        if step == 3:                                        # a request without candidates: its flags stay with the fill
+            before[1], ended[1] = -np.inf, [1, 0, 1, 0]
+            cum[1], fin[1] = torch.from_numpy(before[1]).to(DEV), torch.from_numpy(ended[1]).to(DEV)
+        xd.copy_(torch.from_numpy(np.roll(x.view(S * W, V).float().numpy(), step, 1)).half())
+        g.replay()
+        torch.cuda.synchronize()
+        check((cum, par, tok, fin), xd.view(S, W, V).cpu(), before, W, ended, end)
+
+
+def test_select_ranks_what_fp32_does_not_tell_apart():
+    """Two beams whose best differ by less than a unit of the fp32 score."""
+    S, W, V = 1, 2, 64
+    x = torch.full((S, W, V), -30.0)
+    x[0, 0, 5], x[0, 1, 9] = 0.0, 0.0
+    check.dtype = torch.float32
+    a = np.float32(-1000.0)
+    for first in (0, 1):
+        scores = np.full((S, W), a)
+        x[0, first, 20:] = -12.0                             # more mass elsewhere: a lower score, by 44 e^-12
+        x[0, 1 - first, 20:] = -30.0
+        sc, par, tok = run(x.view(W, V).to(DEV), scores, 2)
+        assert par[0].tolist() == [1 - first, first] and tok[0].tolist() == [9 if first == 0 else 5, 5 if first == 0 else 9]
+
+
 # ---------------------------------------------------------------------------
 # reordering
 # ---------------------------------------------------------------------------
@@ -326,6 +365,25 @@ def test_requests_that_cannot_be_reordered_stay(what, flag, in_place):
     new, copies = B.reorder(tables, lens, p2)
     assert np.array_equal(out.cpu().numpy().reshape(tables.shape), new)
     assert torch.equal(bytes_of(expect(k, copies, "bf16")), bytes_of(kd))
+
+
+def test_reorder_on_a_given_stream():
+    lens, W = [37, 200], 4
+    tables, parents, nb = beams(lens, W, 1, seed=7)
+    ks, vs = pools_of("f16", nb, 2, 2, 64, seed=7)
+    kd, vd = [x.to(DEV) for x in ks], [x.to(DEV) for x in vs]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        t = torch.from_numpy(tables).to(DEV).flatten(0, 1)
+        n = torch.tensor(np.repeat(lens, W).astype(np.int32), device=DEV)
+        par = torch.from_numpy(parents).to(DEV)
+    pa.beam_reorder(t, n, par, kd, vd, stream=side)
+    torch.cuda.synchronize()
+    new, copies = B.reorder(tables, lens, parents)
+    assert np.array_equal(t.cpu().numpy().reshape(tables.shape), new)
+    for a, b in zip(ks + vs, kd + vd):
+        assert torch.equal(bytes_of(expect(a, copies, "f16")), bytes_of(b))
 
 
 def test_reorder_captured_in_place():

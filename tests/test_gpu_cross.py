@@ -287,3 +287,43 @@ def test_single_rows_agree_with_decode():
     dec = pa.paged_attention_decode(q.to(DEV), pools[0].to(DEV), pools[1].to(DEV), t, n, 0.09, 1300)
     check(out, q, pools, tables, lens, [1] * 4, 0.09)
     check(dec, q, pools, tables, lens, [1] * 4, 0.09)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_sequences_in_order_of_length(D):
+    """More items than run at once, which CTAs take longest first: equal lengths,
+    none, and lengths that are refused (the lowest number among them)."""
+    lens = [int(x) for x in np.random.default_rng(16).integers(0, 90, 50)]
+    lens[3] = lens[4] = lens[20] = 33
+    qlens = [1 + i % 3 for i in range(50)]
+    q, pools, tables = build(lens, qlens, 8, 8, D, torch.float16, seed=16)
+    t, n, cu = dev(tables, lens, qlens)
+    bad = {0: -2 ** 31, 7: -1, 8: -7, 49: 2 ** 31 - 1, 30: 10 ** 6}
+    for b, v in bad.items():
+        n[b] = v
+    out = pa.paged_cross_attention(q.to(DEV), pools[0].to(DEV), pools[1].to(DEV), t, n, 0.125, max_enc_len=90,
+                                   cu_q_lens=cu, max_q_len=3)
+    torch.cuda.synchronize()
+    assert pa.device_error() == SEQ_LEN
+    check(out, q, pools, tables, [0 if b in bad else x for b, x in enumerate(lens)], qlens, 0.125)
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, with chunks and without, share nothing."""
+    cases = []
+    for seed, qlens in ((17, [4] * 30), (18, [1, 40, 3] * 10)):
+        lens = [int(x) for x in np.random.default_rng(seed).integers(0, 300, 30)]
+        q, pools, tables = build(lens, qlens, 8, 2, 64, torch.float16, seed=seed)
+        cases.append((q, pools, tables, lens, qlens, dev(tables, lens, qlens), q.to(DEV), pools[0].to(DEV), pools[1].to(DEV)))
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in cases], [[], []]
+    for _ in range(8):
+        for i, (s, c) in enumerate(zip(streams, cases)):
+            t, n, cu = c[5]
+            outs[i].append(pa.paged_cross_attention(c[6], c[7], c[8], t, n, 0.125, max_enc_len=300, cu_q_lens=cu,
+                                                    max_q_len=max(c[4]), stream=s))
+    torch.cuda.synchronize()
+    for c, got in zip(cases, outs):
+        check(got[0], *c[:5], 0.125)
+        assert all(torch.equal(g, got[0]) for g in got)
+    assert pa.device_error() == 0
