@@ -1021,7 +1021,10 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int, finish
                                              and t.is_contiguous() for t, d in zip(out, kinds)),
               "out: contiguous tensors [S, num_out] of the results' types")
     lib = _lib or load_library()
-    workspace, ws_bytes = _ws(lib.pa_beam_select_workspace_bytes(S, W, V, num_out, code), logits, workspace)
+    nbytes, ws = lib.pa_beam_select_workspace_bytes(S, W, V, num_out, code), None
+    if nbytes:
+        workspace, nbytes = _ws(nbytes, logits, workspace)
+        ws = workspace.data_ptr()
     if finished is None:
         done, over = None, None
     else:
@@ -1029,7 +1032,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int, finish
     rc = lib.pa_beam_select(
         out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), over, rows.data_ptr(),
         rows.stride(0) if S * W > 1 else V, scores.data_ptr(), done, end_token, S, W, V, num_out, code,
-        workspace.data_ptr(), ws_bytes, _raw_stream(dev))
+        ws, nbytes, _raw_stream(dev))
     if rc:
         _check(rc, "pa_beam_select")
     return out

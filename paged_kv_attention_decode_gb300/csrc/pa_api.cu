@@ -1062,6 +1062,7 @@ size_t pa_beam_select_workspace_bytes(int num_seqs, int num_beams, int vocab, in
     if (num_seqs <= 0 || num_seqs > kMaxGrid || num_beams <= 0 || num_beams > PA_MAX_BEAMS || vocab <= 0 || vocab > PA_MAX_VOCAB ||
         num_out <= 0 || num_out > PA_MAX_BEAM_OUT || dtype < PA_F16 || dtype > PA_F32)
         return 0;
+    if (pa::beam_cluster(num_seqs, num_beams, vocab, dtype)) return 0;
     const size_t n = static_cast<size_t>(num_seqs) * num_beams * pa::beam_pieces(vocab, dtype);
     return align256(n * sizeof(float2)) + n * 8 * sizeof(float);
 }
@@ -1080,8 +1081,10 @@ int pa_beam_select(float* out_scores, int32_t* out_parents, int32_t* out_tokens,
     if (!out_scores || !out_parents || !out_tokens || !logits || !scores) return PA_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(logits) % (dtype == PA_F32 ? 4 : 2)) return PA_ERR_INVALID_ARG;
     const size_t need = pa_beam_select_workspace_bytes(num_seqs, num_beams, vocab, num_out, dtype);
-    if (!workspace || workspace_bytes < need) return PA_ERR_WORKSPACE_TOO_SMALL;
-    if (!aligned256(workspace)) return PA_ERR_INVALID_ARG;
+    if (need) {
+        if (!workspace || workspace_bytes < need) return PA_ERR_WORKSPACE_TOO_SMALL;
+        if (!aligned256(workspace)) return PA_ERR_INVALID_ARG;
+    }
     pa::BeamSelectParams p{};
     p.out_scores = out_scores;
     p.out_parents = out_parents;
@@ -1099,8 +1102,10 @@ int pa_beam_select(float* out_scores, int32_t* out_parents, int32_t* out_tokens,
     p.pieces = pa::beam_pieces(vocab, dtype);
     const size_t n = static_cast<size_t>(num_seqs) * num_beams * p.pieces;
     if (n > (1u << 30)) return PA_ERR_INVALID_ARG;
-    p.sums = static_cast<float2*>(workspace);
-    p.groups = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256(n * sizeof(float2)));
+    if (need) {
+        p.sums = static_cast<float2*>(workspace);
+        p.groups = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256(n * sizeof(float2)));
+    }
     return pa::launch_beam_select(p, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

@@ -150,20 +150,14 @@ __device__ __forceinline__ bool reads_row(const BeamSelectParams& p, int row) {
     return s > -INFINITY;   // (NaN counts as -inf)
 }
 
-// One warp per piece of a row: kSelVecs * 512 bytes.
+// One warp's piece of a row, kSelVecs * 512 bytes: lane l leaves with the largest
+// logit of group l % kSelVecs, and every lane with the piece's and its sum.
 template <typename T>
-__global__ void __launch_bounds__(kSelThreads, 16) beam_pieces_kernel(const BeamSelectParams p) {
+__device__ __forceinline__ void sum_piece(const BeamSelectParams& p, int row, int piece, int lane, float& gm, float& wm,
+                                          float& sum) {
     using L = Logits<T>;
     constexpr int kPer = L::kPer, kVecs = kSelVecs, kWords = kVecs * 4;
     constexpr bool kWide = std::is_same<T, float>::value;   // one logit a word
-    const int lane = threadIdx.x & 31;
-    const int64_t all = static_cast<int64_t>(p.num_seqs) * p.beams * p.pieces;
-    const int64_t slot = static_cast<int64_t>(blockIdx.x) * (kSelThreads / 32) + (threadIdx.x >> 5);
-    pdl_trigger();
-    pdl_wait();
-    if (slot >= all) return;
-    const int row = static_cast<int>(slot / p.pieces), piece = static_cast<int>(slot - static_cast<int64_t>(row) * p.pieces);
-    if (!reads_row(p, row)) return;
     const T* x = static_cast<const T*>(p.logits) + row * p.stride;
     // index of the first logit of this lane's word j
     auto at = [&](int j) { return ((piece * kVecs + j) * 32 + lane) * kPer; };
@@ -221,7 +215,6 @@ __global__ void __launch_bounds__(kSelThreads, 16) beam_pieces_kernel(const Beam
     // rounding taken back from the sum.  A NaN or +inf makes the sum NaN, and from
     // logits of some 100,000 on c is too coarse: only then are the words cleaned and
     // the sum taken from the differences.
-    float gm, wm, sum;
     auto largest = [&]() {
         static_assert(kVecs == 8, "eight words over eight lanes");
         uint32_t m[kVecs];
@@ -283,7 +276,21 @@ __global__ void __launch_bounds__(kSelThreads, 16) beam_pieces_kernel(const Beam
     }
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) sum += __shfl_xor_sync(kFull, sum, off);
-    if (lane < kVecs) p.groups[slot * kVecs + lane] = gm;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kSelThreads, 16) beam_pieces_kernel(const BeamSelectParams p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t all = static_cast<int64_t>(p.num_seqs) * p.beams * p.pieces;
+    const int64_t slot = static_cast<int64_t>(blockIdx.x) * (kSelThreads / 32) + (threadIdx.x >> 5);
+    pdl_trigger();
+    pdl_wait();
+    if (slot >= all) return;
+    const int row = static_cast<int>(slot / p.pieces), piece = static_cast<int>(slot - static_cast<int64_t>(row) * p.pieces);
+    if (!reads_row(p, row)) return;
+    float gm, wm, sum;
+    sum_piece<T>(p, row, piece, lane, gm, wm, sum);
+    if (lane < kSelVecs) p.groups[slot * kSelVecs + lane] = gm;
     if (lane == 0) p.sums[slot] = make_float2(wm, sum);
 }
 
@@ -335,6 +342,7 @@ __device__ __forceinline__ Two two_log(float x, const Two* table) {
 
 constexpr int kJoinThreads = 512;
 constexpr int kJoinSets = kJoinThreads / 4;   // sets of groups, of four threads each
+constexpr int kFewPieces = 128;                // of a request that one cluster takes
 constexpr int kHeld = 8;                      // groups that a thread holds on to
 constexpr int kJoinCap = 512;                 // groups, and candidates, ranked at once
 static_assert(kJoinSets >= kMaxBeamOut, "k sets give k groups");
@@ -350,12 +358,14 @@ __device__ __forceinline__ bool better_than(const Cand& a, const Cand& b) {
     return a.beam != b.beam ? a.beam < b.beam : a.key > b.key;
 }
 
-// One CTA per request.  The k best groups are found by scores in fp32 (x plus a term
-// of its beam), with room for their roundings; the candidates that come through are
-// ranked by the exact ones.  Where too many come through (equal scores), groups and
-// candidates are taken one by one.
-template <typename T>
-__global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelectParams p) {
+// One CTA per request, after its pieces: `all_sums` and `groups` are the request's.
+// The k best groups are found by scores in fp32 (x plus a term of its beam), with
+// room for their roundings; the candidates that come through are ranked by the exact
+// ones.  Where too many come through (equal scores), groups and candidates are taken
+// one by one.  `ready` comes between what needs no piece and the rest.
+template <typename T, typename Ready>
+__device__ __forceinline__ void join_request(const BeamSelectParams& p, int s, const float2* all_sums,
+                                             const float* groups, Ready ready) {
     using L = Logits<T>;
     constexpr int kGroup = 32 * L::kPer;   // logits of a group
     constexpr int kWarps = kJoinThreads / 32;
@@ -374,7 +384,6 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
     __shared__ int s_cb[kJoinCap], s_list[kJoinCap];
     __shared__ int s_flat[kMaxBeamOut];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int s = static_cast<int>(blockIdx.x);
     const int W = p.beams, k = p.k, C = p.pieces;
     const int per_row = C * kSelVecs, total = W * per_row;   // groups (those past the row are -inf)
     if (tid < 32) s_table[tid] = {kLogTable[tid][0], kLogTable[tid][1]};
@@ -382,21 +391,20 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
         s_groups = s_count = 0;
         s_room = 0u;
     }
-    __syncthreads();
-    pdl_trigger();
-    pdl_wait();
-    const float* groups = p.groups + static_cast<int64_t>(s) * total;
-    // this thread's first groups, asked for before the rows' sums are needed (a row
-    // that was not read has whatever the workspace held)
+    ready();
+    // This thread's groups: every 512th, so that the first 128 lie in different sets.
+    // The first ones are asked for before the rows' sums are needed (a row that was
+    // not read has whatever the workspace held).
+    const int mine0 = (tid >> 2) + (tid & 3) * kJoinSets;
     float held[kHeld];
 #pragma unroll
     for (int u = 0; u < kHeld; ++u) {
-        const int g = tid + u * kJoinThreads;
+        const int g = mine0 + u * kJoinThreads;
         held[u] = g < total ? groups[g] : -INFINITY;
     }
     for (int w = warp; w < W; w += kWarps) {
         const int row = s * W + w;
-        const float2* sums = p.sums + static_cast<int64_t>(row) * C;
+        const float2* sums = all_sums + w * C;
         const float2 none = make_float2(-INFINITY, 0.f);
         const float2 a = lane < C ? sums[lane] : none, b = lane + 32 < C ? sums[lane + 32] : none;
         const float given = p.scores[row];
@@ -441,17 +449,33 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
     auto ended = [&](int beam) { return cand_of(beam, key_of(0.f, p.end_token)); };
     auto row_of = [&](int beam) { return static_cast<const T*>(p.logits) + (s * W + beam) * p.stride; };
 
-    // tau: the k-th best of the sets' best (a set's four threads take every 512th
-    // group each): k groups, or ended beams, are not below it.  A set's number in
-    // the lowest bits tells equal ones apart; what it takes off is part of the room.
+    // tau: the k-th best of the sets' best: k groups, or ended beams, are not below
+    // it.  A set's number in the lowest bits tells equal ones apart; what it takes
+    // off is part of the room.  With fewer groups than twice k the logits themselves
+    // are shared out instead (at most 2^15 of them).
+    const bool direct = W * ((p.vocab + kGroup - 1) / kGroup) < 2 * k;
+    auto direct_logit = [&](int i, int& beam, int& e) {   // -inf: no candidate
+        beam = i / p.vocab;
+        e = i - beam * p.vocab;
+        const float f = s_kind[beam] == 1 ? L::value(row_of(beam) + e) : -INFINITY;
+        return f >= -L::kTop ? fminf(f, L::kTop) : -INFINITY;   // (not a NaN)
+    };
     float best = -INFINITY;
+    if (direct) {
+        for (int i = tid; i < W * p.vocab; i += kJoinThreads) {
+            int beam, e;
+            const float f = direct_logit(i, beam, e);
+            best = fmaxf(best, f + s_add[beam]);
+        }
+    } else {
 #pragma unroll
-    for (int u = 0; u < kHeld; ++u) {
-        const int g = tid + u * kJoinThreads;
-        held[u] = g < total ? held[u] + s_add[beam_of(g)] : -INFINITY;
-        best = fmaxf(best, held[u]);
+        for (int u = 0; u < kHeld; ++u) {
+            const int g = mine0 + u * kJoinThreads;
+            held[u] = g < total ? held[u] + s_add[beam_of(g)] : -INFINITY;
+            best = fmaxf(best, held[u]);
+        }
+        for (int g = mine0 + kHeld * kJoinThreads; g < total; g += kJoinThreads) best = fmaxf(best, groups[g] + s_add[beam_of(g)]);
     }
-    for (int g = tid + kHeld * kJoinThreads; g < total; g += kJoinThreads) best = fmaxf(best, groups[g] + s_add[beam_of(g)]);
     if (tid < W && s_kind[tid] == 2) best = fmaxf(best, s_score[tid]);
     best = fmaxf(best, __shfl_xor_sync(kFull, best, 1));
     best = fmaxf(best, __shfl_xor_sync(kFull, best, 2));
@@ -482,18 +506,27 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
             s_cb[i] = c.beam;
         }
     };
-    if (best >= tau) {
+    if (direct) {
+        for (int i = tid; i < W * p.vocab; i += kJoinThreads) {
+            int beam, e;
+            const float f = direct_logit(i, beam, e);
+            if (f + s_add[beam] >= tau) {
+                const Cand c = cand_of(beam, key_of(f, e));
+                if (c.key) push(c);
+            }
+        }
+    } else if (best >= tau) {
         auto list = [&](int g) {
             const int i = atomicAdd(&s_groups, 1);
             if (i < kJoinCap) s_list[i] = g;
         };
 #pragma unroll
         for (int u = 0; u < kHeld; ++u)
-            if (held[u] >= tau) list(tid + u * kJoinThreads);
-        for (int g = tid + kHeld * kJoinThreads; g < total; g += kJoinThreads)
+            if (held[u] >= tau) list(mine0 + u * kJoinThreads);
+        for (int g = mine0 + kHeld * kJoinThreads; g < total; g += kJoinThreads)
             if (groups[g] + s_add[beam_of(g)] >= tau) list(g);
-        if (tid < W && s_kind[tid] == 2 && s_score[tid] >= tau) push(ended(tid));
     }
+    if (tid < W && s_kind[tid] == 2 && s_score[tid] >= tau) push(ended(tid));
     __syncthreads();
     const int listed = s_groups;
     // their logits that reach it, a warp for each group (NaN, as -inf, does not)
@@ -622,6 +655,48 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelec
         }
         ++r;
     }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamSelectParams p) {
+    const int s = static_cast<int>(blockIdx.x);
+    const int64_t first = static_cast<int64_t>(s) * p.beams * p.pieces;
+    join_request<T>(p, s, p.sums + first, p.groups + first * kSelVecs, [] {
+        __syncthreads();
+        pdl_trigger();
+        pdl_wait();
+    });
+}
+
+// Few requests: both in one launch.  A cluster takes a request; its warps leave
+// their pieces' sums and groups in the first CTA's shared memory, which then joins
+// them.  No workspace.
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads, 1) beam_few_kernel(const BeamSelectParams p) {
+    extern __shared__ __align__(16) uint8_t few_smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t rank = cluster_rank(), ctas = cluster_size();
+    const int s = static_cast<int>(blockIdx.x / ctas), all = p.beams * p.pieces;
+    float2* sums = reinterpret_cast<float2*>(few_smem);                       // [all]
+    float* groups = reinterpret_cast<float*>(few_smem + kFewPieces * sizeof(float2));   // [all, kSelVecs]
+    const uint32_t sums0 = map_rank(smem_addr(sums), 0), groups0 = map_rank(smem_addr(groups), 0);
+    pdl_trigger();
+    cluster_sync();   // (the first CTA runs: its shared memory may be written)
+    pdl_wait();
+    for (int i = static_cast<int>(rank) * (kJoinThreads / 32) + warp; i < all; i += static_cast<int>(ctas) * (kJoinThreads / 32)) {
+        const int w = i / p.pieces, row = s * p.beams + w;
+        if (!reads_row(p, row)) continue;
+        float gm, wm, sum;
+        sum_piece<T>(p, row, i - w * p.pieces, lane, gm, wm, sum);
+        if (lane < kSelVecs) st_cluster(groups0 + (i * kSelVecs + lane) * 4, gm);
+        if (lane == 0) {
+            st_cluster(sums0 + i * 8, wm);
+            st_cluster(sums0 + i * 8 + 4, sum);
+        }
+    }
+    cluster_sync();
+    if (rank > 0) return;
+    join_request<T>(p, s, sums, groups, [] { __syncthreads(); });
 }
 
 // ---------------------------------------------------------------------------
@@ -804,11 +879,42 @@ int beam_pieces(int vocab, int dtype) {
     return (vocab + per - 1) / per;
 }
 
+// A request in one cluster while all clusters run at once (see launch_cross) and a
+// warp has one piece of it: the second launch's gap then costs more than the fewer
+// warps.  us of one cluster of 8, 4, 2, 1 CTAs and of two launches: 1 request of 4
+// beams, 32000 tokens 6.8, 6.8, 8.1, 10.5 and 6.5 (but 4 us less on the host, that
+// sets the pace there); 32 of them 12.5, 7.3, 8.8, 11.4 and 8.8; 64 of 2 beams, 8000
+// tokens 18.4, 12.9, 7.1, 6.8 and 7.6; 1 of 8 beams, 131072 tokens (4 pieces a warp
+// of 8 CTAs) 11.5, 16.3, 25.3, 43.4 and 7.5.
+int beam_cluster(int num_seqs, int beams, int vocab, int dtype) {
+    const long long pieces = static_cast<long long>(beams) * beam_pieces(vocab, dtype);
+    for (int ctas = 1; ctas <= kFewPieces / (kJoinThreads / 32); ctas *= 2)
+        if (pieces <= ctas * (kJoinThreads / 32)) return num_seqs * ctas <= (ctas == 8 ? 64 : 128) ? ctas : 0;
+    return 0;
+}
+
 cudaError_t launch_beam_select(const BeamSelectParams& p, int dtype, cudaStream_t s) {
+    const int ctas = beam_cluster(p.num_seqs, p.beams, p.vocab, dtype);
     const long long warps = static_cast<long long>(p.num_seqs) * p.beams * p.pieces;
     const dim3 grid(static_cast<unsigned>((warps + kSelThreads / 32 - 1) / (kSelThreads / 32)));
     auto go = [&](auto t) {
         using T = decltype(t);
+        if (ctas) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>(p.num_seqs) * ctas);
+            cfg.blockDim = dim3(kJoinThreads);
+            cfg.dynamicSmemBytes = kFewPieces * (sizeof(float2) + kSelVecs * sizeof(float));
+            cfg.stream = s;
+            cudaLaunchAttribute attr[2];
+            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[0].val.programmaticStreamSerializationAllowed = 1;
+            attr[1].id = cudaLaunchAttributeClusterDimension;
+            attr[1].val.clusterDim.x = ctas;
+            attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 2;
+            return cudaLaunchKernelEx(&cfg, beam_few_kernel<T>, p);
+        }
         const cudaError_t e = launch_pdl(beam_pieces_kernel<T>, grid, dim3(kSelThreads), 0, s, p);
         if (e != cudaSuccess) return e;
         return launch_pdl(beam_join_kernel<T>, dim3(p.num_seqs), dim3(kJoinThreads), 0, s, p);

@@ -261,6 +261,8 @@ cudaError_t launch_cross(CrossParams p, const CUtensorMap& kmap, const CUtensorM
                          cudaStream_t s);
 // dtype: 0 fp16, 1 bf16, 2 fp32
 int beam_pieces(int vocab, int dtype);   // pieces of a row of logits, 4 KB each
+// CTAs of the cluster that takes a request in one launch without a workspace, or 0
+int beam_cluster(int num_seqs, int beams, int vocab, int dtype);
 cudaError_t launch_beam_select(const BeamSelectParams& p, int dtype, cudaStream_t s);
 cudaError_t launch_beam_copy(const BeamReorderParams& p, cudaStream_t s);
 cudaError_t launch_beam_tables(const BeamReorderParams& p, cudaStream_t s);   // in place, behind the copies

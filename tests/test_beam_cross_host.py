@@ -59,7 +59,7 @@ def test_cross_workspace(lib):
     assert 4 * (65 + 65 + 2 * (1000 + 64)) <= n <= 4 * (65 + 65 + 2 * (1000 + 64)) + 1024
 
 
-SELECT = dict(sc=F, par=F, tok=F, fin=None, x=F, stride=32000, cum=F, ended=None, end=-1, S=2, W=4, V=32000, k=8, dt=0,
+SELECT = dict(sc=F, par=F, tok=F, fin=None, x=F, stride=200000, cum=F, ended=None, end=-1, S=2, W=4, V=200000, k=8, dt=0,
               ws=F, wsb=1 << 24)
 
 
@@ -68,8 +68,8 @@ SELECT = dict(sc=F, par=F, tok=F, fin=None, x=F, stride=32000, cum=F, ended=None
     (dict(cum=None), INVALID), (dict(x=F + 1), INVALID), (dict(x=F + 2, dt=2), INVALID), (dict(S=-1), INVALID),
     (dict(S=65536), INVALID), (dict(W=0), INVALID), (dict(W=33), UNSUPPORTED), (dict(V=0), INVALID),
     (dict(V=(1 << 20) + 1, stride=1 << 21), UNSUPPORTED), (dict(k=0), INVALID), (dict(k=65), UNSUPPORTED),
-    (dict(V=1, k=5, stride=1), INVALID), (dict(end=32000), INVALID), (dict(end=-2), INVALID), (dict(ended=F), INVALID),
-    (dict(stride=31999), INVALID), (dict(dt=3), UNSUPPORTED), (dict(dt=-1), UNSUPPORTED), (dict(ws=None), WORKSPACE),
+    (dict(V=1, k=5, stride=1), INVALID), (dict(end=200000), INVALID), (dict(end=-2), INVALID), (dict(ended=F), INVALID),
+    (dict(stride=199999), INVALID), (dict(dt=3), UNSUPPORTED), (dict(dt=-1), UNSUPPORTED), (dict(ws=None), WORKSPACE),
     (dict(wsb=100), WORKSPACE), (dict(ws=F + 128), INVALID), (dict(S=0), 0),
 ])
 def test_select_refusals(lib, kw, status):
@@ -82,8 +82,11 @@ def test_select_workspace(lib):
                 (1, 4, 100, 4, 3), (1, 0, 100, 4, 0), (65536, 4, 100, 4, 0)):
         assert f(*bad) == 0
     # 10 numbers of 4 bytes for every 4 KB of a row
-    assert f(3, 4, 32000, 8, 0) == 12 * 16 * 32 + ((12 * 16 * 8 + 255) & ~255)
-    assert f(3, 4, 32000, 8, 2) > f(3, 4, 32000, 8, 1) == pa.beam_select_workspace_bytes(3, 4, 32000, 8, torch.bfloat16)
+    assert f(40, 4, 32000, 8, 0) == 160 * 16 * 32 + ((160 * 16 * 8 + 255) & ~255)
+    assert f(40, 4, 32000, 8, 2) > f(40, 4, 32000, 8, 1) == pa.beam_select_workspace_bytes(40, 4, 32000, 8, torch.bfloat16)
+    # few requests, or small ones, need none
+    assert f(1, 4, 32000, 8, 0) == f(8, 8, 32000, 64, 1) == f(32, 4, 32000, 8, 0) == f(128, 1, 30000, 2, 0) == 0
+    assert f(9, 8, 32000, 8, 0) and f(33, 4, 32000, 8, 0) and f(129, 1, 30000, 2, 0) and f(1, 9, 32000, 8, 0)
 
 
 PTR = ctypes.c_void_p * 2

@@ -83,7 +83,9 @@ def make(S, W, V, dt, seed, kind="normal"):
 @pytest.mark.parametrize("kind", ["normal", "peaked", "masked", "equal", "steps", "sorted"])
 @pytest.mark.parametrize("dn", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("S,W,V,k", [(1, 1, 1, 1), (1, 4, 7, 8), (3, 5, 1001, 10), (2, 4, 32000, 8), (1, 2, 8193, 64),
-                                     (5, 1, 4097, 1), (1, 32, 129, 64), (2, 3, 50001, 6)])
+                                     (5, 1, 4097, 1), (1, 32, 129, 64), (2, 3, 50001, 6),
+                                     (9, 4, 5001, 8), (40, 2, 3001, 4), (2, 12, 150000, 24),
+                                     (140, 1, 700, 3), (3, 4, 1000, 24), (2, 1, 1000, 64), (70, 3, 20000, 6)])
 def test_select(S, W, V, k, dn, kind):
     x, scores = make(S, W, V, DT[dn], seed=V + k, kind=kind)
     got = run(x.view(S * W, V).to(DEV), scores, k)
@@ -122,6 +124,21 @@ def test_what_is_not_finite(dn):
     assert np.isneginf(sc[2, 2:]).all() and list(tk[2, 2:]) == list(range(k - 2)) and (pr[2, 2:] == 0).all()
     assert (pr[3] == 0).all()
     assert list(tk[1, :2]) == [3, 4999] or pr[1, 0] != 2
+
+
+@pytest.mark.parametrize("dn", ["f16", "bf16", "f32"])
+def test_what_is_not_finite_in_few_logits(dn):
+    S, W, V, k = 3, 2, 90, 20
+    x, scores = make(S, W, V, DT[dn], seed=9)
+    x[0, 0, ::3] = float("nan")
+    x[0, 1, 5], x[0, 1, 40] = float("inf"), torch.finfo(DT[dn]).max
+    x[1, 0, :80] = -float("inf")
+    x[1, 1] = float("nan")
+    x[2, :, 1:] = -float("inf")
+    fin = np.zeros((S, W), np.uint8)
+    fin[2, 1] = 1
+    check(run(x.view(S * W, V).to(DEV), scores, k), x, scores, k)
+    check(run(x.view(S * W, V).to(DEV), scores, k, fin, 89), x, scores, k, fin, 89)
 
 
 def test_first_step_and_dead_requests():
