@@ -24,11 +24,14 @@ constexpr float kLog2e = 1.4426950408889634f;
 // largest logit of every 512 bytes (a group).  The second, a CTA per request, joins
 // the sums and looks for the k best groups: the k best candidates lie in them, as
 // the groups' largest are k candidates that are not worse than any outside.  Their
-// logits are read again, k * 512 bytes.
+// logits are read again, k * 512 bytes.  (Few requests take both steps in one launch,
+// a cluster each.)
 // Bound by the logits' bytes; each logit costs a conversion, half a multiply-add, a
 // 2^x, half an addition and half a maximum.  (Listing the k best of every 16 KB in
-// the first kernel took three times as many instructions: 64 requests of 8 beams,
-// 131072 tokens, 16 bits, 49 us.)
+// the first kernel took three times as many instructions.)  64 requests of 8 beams,
+// 131072 tokens, 16 bits: 28.5 us, of which the first kernel takes 21 (134 MB at 6.4
+// TB/s, 0.94 of the copy rate) and the second, whose chain of loads and meetings one
+// request cannot shorten, 7.5; with lists it was 49.
 //
 // Within a row the order of scores is the order of logits, so the first kernel
 // needs no sum.  Across rows, scores are compared as sums of two fp32 numbers: a sum
@@ -295,7 +298,8 @@ __global__ void __launch_bounds__(kSelThreads, 16) beam_pieces_kernel(const Beam
 }
 
 // Sums of two fp32 numbers, about 48 bits: fp64 runs at a small fraction of their
-// rate here (the join took 23 us with it, 64 requests of 8 beams).
+// rate here (with it the second kernel took 23 us under ncu, 64 requests of 8 beams,
+// where it now takes 11).
 struct Two {
     float hi, lo;   // |lo| at most half a unit of hi's last place
 };
