@@ -621,7 +621,7 @@ size_t pa_cross_workspace_bytes(int num_seqs, int num_tokens, int max_q_len);
  * (beam w, token v) of request s scores scores[s, w] + x - log(sum of exp) of row
  * w's logits x (a log-softmax); the best come first, ties go to the lowest
  * w * vocab + v.  Scores are compared as sums of two fp32 numbers (about 48 bits)
- * and rounded once.
+ * and rounded once; one below fp32's range is -inf.
  *   out_scores, out_parents, out_tokens  fp32, int32, int32 [num_seqs, num_out];
  *                 a parent is a beam of the request, 0 .. num_beams - 1.
  *   logits        [num_seqs * num_beams, vocab] of `dtype` (fp16, bf16 or fp32),

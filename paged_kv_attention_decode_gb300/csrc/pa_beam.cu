@@ -384,6 +384,7 @@ __device__ __forceinline__ void join_request(const BeamSelectParams& p, int s, c
     __shared__ float s_tau;
     __shared__ uint32_t s_room;                       // (bits of a float, 0 or more)
     __shared__ int s_groups, s_count;
+    __shared__ bool s_far;                            // some s_add is past fp32's range
     __shared__ u64 s_cs[kJoinCap], s_ck[kJoinCap];
     __shared__ int s_cb[kJoinCap], s_list[kJoinCap];
     __shared__ int s_flat[kMaxBeamOut];
@@ -393,6 +394,7 @@ __device__ __forceinline__ void join_request(const BeamSelectParams& p, int s, c
     if (tid < 32) s_table[tid] = {kLogTable[tid][0], kLogTable[tid][1]};
     if (tid == 0) {
         s_groups = s_count = 0;
+        s_far = false;
         s_room = 0u;
     }
     ready();
@@ -435,6 +437,7 @@ __device__ __forceinline__ void join_request(const BeamSelectParams& p, int s, c
             s_most[w] = kind == 1 ? m : 0.f;
             s_log[w] = lg;
             s_add[w] = kind == 1 ? (score - lg.hi) - m : -INFINITY;
+            if (kind == 1 && !(fabsf(s_add[w]) <= FLT_MAX)) s_far = true;
             if (kind == 1) atomicMax(&s_room, __float_as_uint(fabsf(score) + fabsf(m) + fabsf(lg.hi)));
         }
     }
@@ -500,8 +503,9 @@ __device__ __forceinline__ void join_request(const BeamSelectParams& p, int s, c
     __syncthreads();
     // A score in fp32 is off by less than 2^-21 of `room` and itself (four roundings,
     // of numbers up to these), the number in the low bits is 2^-16 of tau, and both
-    // sides are.  (tau of no group: below every number.)
-    const float t0 = s_tau, tau = t0 > -FLT_MAX ? t0 - 9.5367431640625e-7f * __uint_as_float(s_room) - 3.0517578125e-5f * fabsf(t0) : -FLT_MAX;
+    // sides are.  (tau of no group: the lowest number; -inf is never a candidate.)
+    const float t0 = s_tau;
+    const float tau = t0 > -FLT_MAX ? fmaxf(t0 - 9.5367431640625e-7f * __uint_as_float(s_room) - 3.0517578125e-5f * fabsf(t0), -FLT_MAX) : -FLT_MAX;
     auto push = [&](const Cand& c) {
         const int i = atomicAdd(&s_count, 1);
         if (i < kJoinCap) {
@@ -571,7 +575,7 @@ __device__ __forceinline__ void join_request(const BeamSelectParams& p, int s, c
         if (p.out_finished) p.out_finished[o + r] = s_kind[c.beam] == 2 || token == p.end_token;
     };
     int found = s_count;
-    if (listed <= kJoinCap && found <= kJoinCap) {
+    if (listed <= kJoinCap && found <= kJoinCap && !s_far) {
         // rank them against one another, a warp for each
         for (int i = warp; i < found; i += kWarps) {
             const Cand c{s_cs[i], s_ck[i], s_cb[i]};
@@ -582,7 +586,7 @@ __device__ __forceinline__ void join_request(const BeamSelectParams& p, int s, c
         }
         found = min(found, k);
     } else {
-        // Many equal scores.  The best of all threads' `mine`:
+        // Many equal scores, or huge ones.  The best of all threads' `mine`:
         auto best_of_all = [&](const Cand& mine) {
             Cand top = mine;
 #pragma unroll

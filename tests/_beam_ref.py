@@ -60,6 +60,7 @@ def candidate_scores(logits, scores, finished=None, end_token=-1, top=None):
                 e = np.exp(x[s, w] - m)
                 lse = math.log(math.fsum(e)) if V <= 4096 else math.log(e.sum())
                 out[s, w] = cum[s, w] + (x[s, w] - m - lse)
+    out[out < -float(np.finfo(np.float32).max)] = -np.inf
     return out
 
 

@@ -171,6 +171,28 @@ def test_ended_beams(kind):
     assert bool(got[3][2].any()) and float(got[0][2, 3]) == -math.inf
 
 
+@pytest.mark.parametrize("V", [40, 5000])
+@pytest.mark.parametrize("dn", ["bf16", "f32"])
+def test_scores_and_logits_at_the_ends_of_the_range(dn, V):
+    """Sums past fp32's range on the way, and scores below it; ended beams beside them."""
+    S, W, k = 5, 3, 9
+    x, scores = make(S, W, V, DT[dn], seed=V)
+    big, top = 2.0 ** 127, float(np.finfo(np.float32).max)
+    x[0, 0, 7], x[0, 1, 11] = big, -big                           # one huge logit: the others are far below it
+    scores[0] = [-big, 1.0, -1.5 * big]
+    x[1] = x[1] * 2.0 ** 120
+    scores[1] = [top, -top, 0.0]
+    scores[2] = [-top, -top, -top]
+    x[3, 1] = -big                                                # equal ones
+    scores[3] = [-5.0, big, 2.0]
+    x[4, 0, ::2] = -big
+    scores[4] = [0.0, -big, top]
+    fin = np.zeros((S, W), np.uint8)
+    fin[0, 2] = fin[1, 1] = fin[3, 2] = fin[4, 2] = 1
+    check(run(x.view(S * W, V).to(DEV), scores, k), x, scores, k)
+    check(run(x.view(S * W, V).to(DEV), scores, k, fin, 3), x, scores, k, fin, 3)
+
+
 def test_equal_rows_prefer_the_lower_beam():
     S, W, V, k = 2, 6, 999, 12
     x, scores = make(S, 1, V, torch.float32, seed=4)
