@@ -145,6 +145,17 @@ __device__ __forceinline__ uint4 bytes_from(const uint4& a, const uint4& b, uint
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// 16 bytes that are not soon read again (volatile: not ahead of the wait for the
+// kernel that writes them).
+__device__ __forceinline__ uint4 load_once(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
 // Whether row `row` of the logits has candidates (a dead beam's are all -inf, an
 // ended one has its single one).
 __device__ __forceinline__ bool reads_row(const BeamSelectParams& p, int row) {
@@ -183,11 +194,11 @@ __device__ __forceinline__ void sum_piece(const BeamSelectParams& p, int row, in
     };
     if (lead == 0 && (piece + 1) * kVecs * 32 * kPer <= p.vocab) {
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j) keep(j, __ldcs(reinterpret_cast<const uint4*>(x + at(j))));
+        for (int j = 0; j < kVecs; ++j) keep(j, load_once(x + at(j)));
     } else if (lead == 0) {
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
-            if (at(j) <= p.vocab - kPer) keep(j, __ldcs(reinterpret_cast<const uint4*>(x + at(j))));
+            if (at(j) <= p.vocab - kPer) keep(j, load_once(x + at(j)));
             else one_by_one(j);
         }
     } else {
@@ -537,29 +548,46 @@ __device__ __forceinline__ void join_request(const BeamSelectParams& p, int s, c
     if (tid < W && s_kind[tid] == 2 && s_score[tid] >= tau) push(ended(tid));
     __syncthreads();
     const int listed = s_groups;
-    // their logits that reach it, a warp for each group (NaN, as -inf, does not)
+    // their logits that reach it, a warp for each group and 16 bytes a lane, two
+    // groups' loads in flight (NaN, as -inf, does not reach it)
     const int looked = min(listed, kJoinCap);
-    for (int i = warp; i < looked; i += 2 * kWarps) {   // (two groups' loads in flight)
-        float f[2][L::kPer], add[2];
-        const T* x[2];
+    for (int i = warp; i < looked; i += 2 * kWarps) {
+        uint32_t v[2][4];
+        float add[2];
         int beam[2], e0[2];
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            const int g = s_list[min(i + v * kWarps, looked - 1)];
-            beam[v] = beam_of(g);
-            e0[v] = (g - beam[v] * per_row) * kGroup + lane;
-            x[v] = row_of(beam[v]) + e0[v];
-            add[v] = i + v * kWarps < looked ? s_add[beam[v]] : -INFINITY;
+        for (int u = 0; u < 2; ++u) {
+            const int g = s_list[min(i + u * kWarps, looked - 1)];
+            beam[u] = beam_of(g);
+            e0[u] = (g - beam[u] * per_row) * kGroup + lane * L::kPer;
+            add[u] = i + u * kWarps < looked ? s_add[beam[u]] : -INFINITY;
+            const T* x = row_of(beam[u]) + e0[u];
+            if ((reinterpret_cast<uintptr_t>(x) & 15u) == 0 && e0[u] <= p.vocab - L::kPer) {
+                const uint4 w = *reinterpret_cast<const uint4*>(x);
+                v[u][0] = w.x;
+                v[u][1] = w.y;
+                v[u][2] = w.z;
+                v[u][3] = w.w;
+            } else {
 #pragma unroll
-            for (int u = 0; u < L::kPer; ++u) f[v][u] = e0[v] + u * 32 < p.vocab ? L::value(x[v] + u * 32) : -INFINITY;
+                for (int c = 0; c < L::kPer; ++c) L::put(v[u], c, e0[u] + c < p.vocab ? x + c : nullptr);
+            }
         }
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
+        for (int u = 0; u < 2; ++u) {
+            auto look = [&](float f, int e) {
+                if (!(f + add[u] >= tau)) return;
+                const Cand c = cand_of(beam[u], key_of(fminf(f, L::kTop), e));
+                if (c.key) push(c);
+            };
 #pragma unroll
-            for (int u = 0; u < L::kPer; ++u) {
-                if (f[v][u] + add[v] >= tau) {   // (not a NaN)
-                    const Cand c = cand_of(beam[v], key_of(fminf(f[v][u], L::kTop), e0[v] + u * 32));
-                    if (c.key) push(c);
+            for (int c = 0; c < 4; ++c) {
+                const float2 f = pair_of<T>(v[u][c], v[u][c]);
+                if constexpr (std::is_same<T, float>::value) {
+                    look(f.x, e0[u] + c);
+                } else {
+                    look(f.x, e0[u] + 2 * c);
+                    look(f.y, e0[u] + 2 * c + 1);
                 }
             }
         }
@@ -576,13 +604,26 @@ __device__ __forceinline__ void join_request(const BeamSelectParams& p, int s, c
     };
     int found = s_count;
     if (listed <= kJoinCap && found <= kJoinCap && !s_far) {
-        // rank them against one another, a warp for each
-        for (int i = warp; i < found; i += kWarps) {
-            const Cand c{s_cs[i], s_ck[i], s_cb[i]};
-            int better = 0;
-            for (int j = lane; j < found; j += 32) better += better_than({s_cs[j], s_ck[j], s_cb[j]}, c);
-            better = __reduce_add_sync(kFull, better);
-            if (lane == 0 && better < k) put(better, c);
+        // rank them against one another: a warp for each, or a few lanes for each
+        // when they are few
+        if (found <= kJoinThreads / 16) {
+            const int i = tid >> 4, sub = tid & 15;
+            if (i < found) {
+                const Cand c{s_cs[i], s_ck[i], s_cb[i]};
+                int better = 0;
+                for (int j = sub; j < found; j += 16) better += better_than({s_cs[j], s_ck[j], s_cb[j]}, c);
+                const uint32_t half = lane < 16 ? 0xffffu : 0xffff0000u;
+                better = __reduce_add_sync(half, better);
+                if (sub == 0 && better < k) put(better, c);
+            }
+        } else {
+            for (int i = warp; i < found; i += kWarps) {
+                const Cand c{s_cs[i], s_ck[i], s_cb[i]};
+                int better = 0;
+                for (int j = lane; j < found; j += 32) better += better_than({s_cs[j], s_ck[j], s_cb[j]}, c);
+                better = __reduce_add_sync(kFull, better);
+                if (lane == 0 && better < k) put(better, c);
+            }
         }
         found = min(found, k);
     } else {
