@@ -639,8 +639,9 @@ size_t pa_cross_workspace_bytes(int num_seqs, int num_tokens, int max_q_len);
  * other w * vocab + v, at -inf.  num_beams <= PA_MAX_BEAMS, num_out <=
  * PA_MAX_BEAM_OUT and num_beams * vocab, vocab <= PA_MAX_VOCAB.  With num_out ==
  * num_beams out_scores may be scores and out_finished finished (a step in place);
- * otherwise the outputs must not overlap the inputs.  workspace: pa_beam_select_workspace_bytes(...) bytes,
- * 256-byte aligned; 0 (and NULL) for few requests, which take one launch.
+ * otherwise the outputs must not overlap the inputs.  workspace:
+ * pa_beam_select_workspace_bytes(...) bytes, 256-byte aligned; none (0, NULL) for few
+ * or small requests, which take one launch.
  */
 #define PA_MAX_BEAMS 32
 #define PA_MAX_BEAM_OUT 64

@@ -357,7 +357,7 @@ __device__ __forceinline__ Two two_log(float x, const Two* table) {
 
 constexpr int kJoinThreads = 512;
 constexpr int kJoinSets = kJoinThreads / 4;   // sets of groups, of four threads each
-constexpr int kFewPieces = 128;                // of a request that one cluster takes
+constexpr int kFewPieces = 256;                // of a request that one cluster takes
 constexpr int kHeld = 8;                      // groups that a thread holds on to
 constexpr int kJoinCap = 512;                 // groups, and candidates, ranked at once
 static_assert(kJoinSets >= kMaxBeamOut, "k sets give k groups");
@@ -929,18 +929,25 @@ int beam_pieces(int vocab, int dtype) {
 }
 
 // A request in one cluster while all clusters run at once (see launch_cross) and a
-// warp has one piece of it: the second launch's gap then costs more than the fewer
-// warps.  us of one cluster of 8, 4, 2, 1 CTAs and of two launches: 1 request of 4
-// beams, 32000 tokens 6.8, 6.8, 8.1, 10.5 and 6.5 (but 4 us less on the host, that
-// sets the pace there); 32 of them 12.5, 7.3, 8.8, 11.4 and 8.8; 64 of 2 beams, 8000
-// tokens 18.4, 12.9, 7.1, 6.8 and 7.6; 1 of 8 beams, 131072 tokens (4 pieces a warp
-// of 8 CTAs) 11.5, 16.3, 25.3, 43.4 and 7.5.
+// warp has a piece of it, or two: the second launch's gap then costs about what the
+// fewer warps do, and the host, which sets the pace of calls this short, saves a
+// launch and a workspace (4 to 5 us).  us of one cluster of 8, 4, 2, 1 CTAs and of
+// two launches: 1 request of 4 beams, 32000 tokens (64 pieces) 6.8, 6.8, 8.1, 10.5
+// and 6.5; 32 of them 12.5, 7.3, 8.8, 11.4 and 8.8; 64 of 2 beams, 8000 tokens 18.4,
+// 12.9, 7.1, 6.8 and 7.6; 1 of 8 beams, 131072 tokens (512 pieces) 11.5, 16.3, 25.3,
+// 43.4 and 7.5.  Two pieces a warp (8, 4, 4, 2, 1 CTAs) and two launches: 1 request
+// of 8 beams, 50001 tokens 10.4 and 8.3; 16 of 5, 40000 8.6 and 8.5; 32 of 8, 32000
+// 10.1 and 10.4; 64 of 4 10.3 and 11.0; 128 of 2 10.1 and 11.0.
 int beam_cluster(int num_seqs, int beams, int vocab, int dtype) {
+    constexpr int kWarps = kJoinThreads / 32;
     const long long pieces = static_cast<long long>(beams) * beam_pieces(vocab, dtype);
-    for (int ctas = 1; ctas <= kFewPieces / (kJoinThreads / 32); ctas *= 2)
-        if (pieces <= ctas * (kJoinThreads / 32)) return num_seqs * ctas <= (ctas == 8 ? 64 : 128) ? ctas : 0;
-    return 0;
+    const int most = num_seqs <= 8 ? 8 : num_seqs <= 32 ? 4 : num_seqs <= 64 ? 2 : num_seqs <= 128 ? 1 : 0;
+    if (pieces > 2 * kWarps * most) return 0;
+    int ctas = 1;
+    while (ctas < most && pieces > kWarps * ctas) ctas *= 2;
+    return ctas;
 }
+static_assert(kFewPieces == 2 * (kJoinThreads / 32) * 8, "two pieces a warp of the largest cluster");
 
 cudaError_t launch_beam_select(const BeamSelectParams& p, int dtype, cudaStream_t s) {
     const int ctas = beam_cluster(p.num_seqs, p.beams, p.vocab, dtype);

@@ -82,11 +82,12 @@ def test_select_workspace(lib):
                 (1, 4, 100, 4, 3), (1, 0, 100, 4, 0), (65536, 4, 100, 4, 0)):
         assert f(*bad) == 0
     # 10 numbers of 4 bytes for every 4 KB of a row
-    assert f(40, 4, 32000, 8, 0) == 160 * 16 * 32 + ((160 * 16 * 8 + 255) & ~255)
-    assert f(40, 4, 32000, 8, 2) > f(40, 4, 32000, 8, 1) == pa.beam_select_workspace_bytes(40, 4, 32000, 8, torch.bfloat16)
+    assert f(140, 4, 32000, 8, 0) == 560 * 16 * 32 + ((560 * 16 * 8 + 255) & ~255)
+    assert f(140, 4, 32000, 8, 2) > f(140, 4, 32000, 8, 1) == pa.beam_select_workspace_bytes(140, 4, 32000, 8, torch.bfloat16)
     # few requests, or small ones, need none
-    assert f(1, 4, 32000, 8, 0) == f(8, 8, 32000, 64, 1) == f(32, 4, 32000, 8, 0) == f(128, 1, 30000, 2, 0) == 0
-    assert f(9, 8, 32000, 8, 0) and f(33, 4, 32000, 8, 0) and f(129, 1, 30000, 2, 0) and f(1, 9, 32000, 8, 0)
+    assert f(1, 16, 32000, 8, 0) == f(8, 16, 32000, 64, 1) == f(32, 8, 32000, 8, 0) == f(128, 2, 32000, 2, 0) == 0
+    assert f(1, 17, 32000, 8, 0) and f(9, 9, 32000, 8, 0) and f(33, 5, 32000, 8, 0) and f(65, 3, 32000, 8, 0)
+    assert f(129, 1, 300, 2, 0)
 
 
 PTR = ctypes.c_void_p * 2
