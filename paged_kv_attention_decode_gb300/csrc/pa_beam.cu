@@ -26,8 +26,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 // the groups' largest are k candidates that are not worse than any outside.  Their
 // logits are read again, k * 512 bytes.  (Few requests take both steps in one launch,
 // a cluster each.)
-// Bound by the logits' bytes; each logit costs a conversion, half a multiply-add, a
-// 2^x, half an addition and half a maximum.  (Listing the k best of every 16 KB in
+// Bound by the logits' bytes; each logit costs a conversion, a 2^x, and half of two
+// additions, a product and a maximum.  (Listing the k best of every 16 KB in
 // the first kernel took three times as many instructions.)  64 requests of 8 beams,
 // 131072 tokens, 16 bits: 28.5 us, of which the first kernel takes 21 (134 MB at 6.4
 // TB/s, 0.94 of the copy rate) and the second, whose chain of loads and meetings one
@@ -60,18 +60,18 @@ __device__ __forceinline__ u64 key_of(float x, int index) {
     return static_cast<u64>(ordered(x + 0.f)) << 32 | static_cast<uint32_t>(~index);
 }
 
-// (x, y) <- (x + a, y + b) and (x * f + a, y * f + a), one instruction each
+// (x, y) <- (x + a, y + b) and (x * f, y * f), one instruction each
 __device__ __forceinline__ void add_pair(float& x, float& y, float a, float b) {
     asm("{\n\t.reg .b64 p, q, d;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
         "add.rn.f32x2 d, p, q;\n\tmov.b64 {%0, %1}, d;\n\t}"
         : "+f"(x), "+f"(y)
         : "f"(a), "f"(b));
 }
-__device__ __forceinline__ void fma_pair(float& x, float& y, float f, float a) {
-    asm("{\n\t.reg .b64 p, q, r, d;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\tmov.b64 r, {%3, %3};\n\t"
-        "fma.rn.f32x2 d, p, q, r;\n\tmov.b64 {%0, %1}, d;\n\t}"
+__device__ __forceinline__ void mul_pair(float& x, float& y, float f) {
+    asm("{\n\t.reg .b64 p, q, d;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\t"
+        "mul.rn.f32x2 d, p, q;\n\tmov.b64 {%0, %1}, d;\n\t}"
         : "+f"(x), "+f"(y)
-        : "f"(f), "f"(a));
+        : "f"(f));
 }
 
 // Register words of a row: one fp32 logit, or two of 16 bits.  `clean` takes NaN to
@@ -225,10 +225,9 @@ __device__ __forceinline__ void sum_piece(const BeamSelectParams& p, int row, in
 
     // The groups' largest: lane l ends with that of every lane's word l % 8 (three
     // exchanges halve the words in hand, two more join the quarters), the warp's,
-    // and the warp's sum of 2^((x - wm) log2 e), as 2^(x log2 e - c) with c = wm log2 e rounded, and that
-    // rounding taken back from the sum.  A NaN or +inf makes the sum NaN, and from
-    // logits of some 100,000 on c is too coarse: only then are the words cleaned and
-    // the sum taken from the differences.
+    // and the warp's sum of 2^((x - wm) log2 e): the largest counts as 1 exactly, so
+    // that a beam with one candidate left keeps its score.  A NaN or +inf makes the
+    // sum NaN: only then are the words cleaned and the sum taken again.
     auto largest = [&]() {
         static_assert(kVecs == 8, "eight words over eight lanes");
         uint32_t m[kVecs];
@@ -253,7 +252,6 @@ __device__ __forceinline__ void sum_piece(const BeamSelectParams& p, int row, in
     };
     largest();
     {
-        const float c = wm * kLog2e;
         float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
         for (int i = 0; i < kWords; i += 2) {
@@ -263,16 +261,15 @@ __device__ __forceinline__ void sum_piece(const BeamSelectParams& p, int row, in
             } else {
                 a = pair_of<T>(v[i], 0u);
                 float2 b = pair_of<T>(v[i + 1], 0u);
-                fma_pair(b.x, b.y, kLog2e, -c);
+                add_pair(b.x, b.y, -wm, -wm);
+                mul_pair(b.x, b.y, kLog2e);
                 add_pair(s2, s3, fast_exp2(b.x), fast_exp2(b.y));
             }
-            fma_pair(a.x, a.y, kLog2e, -c);
+            add_pair(a.x, a.y, -wm, -wm);
+            mul_pair(a.x, a.y, kLog2e);
             add_pair(s0, s1, fast_exp2(a.x), fast_exp2(a.y));
         }
         sum = (s0 + s1) + (s2 + s3);
-        const float e = 0.6931471805599453f * fmaf(wm, kLog2e, -c);   // times 1 - e + e^2 / 2
-        sum = fmaf(sum, fmaf(0.5f * e, e, -e), sum);
-        if (!(fabsf(e) < 0.0078125f)) sum = INFINITY;
     }
     if (__any_sync(kFull, !(sum < INFINITY))) {   // (also where all of the warp's are -inf)
 #pragma unroll
@@ -341,16 +338,19 @@ __device__ const float kLogTable[32][2] = {
     {0.6369074583053589f, 3.931710068627581e-09f}, {0.6533012986183167f, -2.660557107958539e-08f}, {0.669430673122406f, -1.9179775989641712e-08f}, {0.6853039860725403f, 1.702637852929456e-08f},
 };
 // The logarithm of a positive normal x, to about 2^-30 absolute: x = 2^e m, m in [1, 2)
-// near c = (65 + 2 i) / 64, log m = log c + log(1 + (m - c) / c).
+// near c = (65 + 2 i) / 64, log m = log c + log(1 + (m - c) / c).  Near 1 itself, c =
+// 1: a beam with one candidate left scores what it scored.
 __device__ __forceinline__ Two two_log(float x, const Two* table) {
     const uint32_t b = __float_as_uint(x);
-    const float e = static_cast<float>(static_cast<int>(b >> 23) - 127);
+    const bool near_one = x > 0.984375f && x < 1.03125f;
+    const float e = near_one ? 0.f : static_cast<float>(static_cast<int>(b >> 23) - 127);
     const int i = static_cast<int>(b >> 18) & 31;
-    const float m = __uint_as_float((b & 0x7fffffu) | 0x3f800000u), c = (65 + 2 * i) * 0.015625f;
-    const float u = (m - c) / c;   // |u| <= 1 / 65
-    // u - u^2 / 2 + ... : the next term, u^6 / 6, is below 2^-38
+    const float m = near_one ? x : __uint_as_float((b & 0x7fffffu) | 0x3f800000u);
+    const float c = near_one ? 1.f : (65 + 2 * i) * 0.015625f;
+    const float u = (m - c) / c;   // |u| <= 1 / 32
+    // u - u^2 / 2 + ... : the next term, u^6 / 6, is below 2^-32
     const float v = u * u * fmaf(u, fmaf(u, fmaf(u, 0.2f, -0.25f), 0.33333333f), -0.5f);
-    Two r = table[i];
+    Two r = near_one ? Two{0.f, 0.f} : table[i];
     r = two_add(r, two_sum(u, v));
     return two_add(r, {e * 0.693115234375f, e * 3.194618329871446e-05f});   // (the first product is exact)
 }
@@ -513,10 +513,12 @@ __device__ __forceinline__ void join_request(const BeamSelectParams& p, int s, c
     }
     __syncthreads();
     // A score in fp32 is off by less than 2^-21 of `room` and itself (four roundings,
-    // of numbers up to these), the number in the low bits is 2^-16 of tau, and both
-    // sides are.  (tau of no group: the lowest number; -inf is never a candidate.)
+    // of numbers up to these), the number in the low bits is 2^-16 of tau (beside a
+    // score of 0 less than the smallest normal number), and both sides are.  (tau of
+    // no group: the lowest number; -inf is never a candidate.)
     const float t0 = s_tau;
-    const float tau = t0 > -FLT_MAX ? fmaxf(t0 - 9.5367431640625e-7f * __uint_as_float(s_room) - 3.0517578125e-5f * fabsf(t0), -FLT_MAX) : -FLT_MAX;
+    const float room = 9.5367431640625e-7f * __uint_as_float(s_room) + 3.0517578125e-5f * fabsf(t0) + FLT_MIN;
+    const float tau = t0 > -FLT_MAX ? fmaxf(t0 - room, -FLT_MAX) : -FLT_MAX;
     auto push = [&](const Cand& c) {
         const int i = atomicAdd(&s_count, 1);
         if (i < kJoinCap) {

@@ -193,6 +193,30 @@ def test_scores_and_logits_at_the_ends_of_the_range(dn, V):
     check(run(x.view(S * W, V).to(DEV), scores, k, fin, 3), x, scores, k, fin, 3)
 
 
+@pytest.mark.parametrize("dn", ["f16", "f32"])
+@pytest.mark.parametrize("logit", [0.0, 3.5, -7.0])
+@pytest.mark.parametrize("V", [1, 3, 700, 70_000])
+def test_one_token_allowed(V, logit, dn):
+    """A forced token costs nothing: the beam's score comes back as it was, 0 as 0."""
+    S, W = 4, 5
+    x = torch.full((S, W, V), -float("inf"), dtype=DT[dn])
+    tok = np.random.default_rng(V).integers(0, V, (S, W))
+    for s in range(S):
+        for w in range(W):
+            x[s, w, tok[s, w]] = logit
+    scores = np.zeros((S, W), np.float32)
+    scores[1] = [-1, -2, 0, -3, -4]
+    scores[2, 1:] = -np.inf
+    scores[3] = -np.float32(1e-40)
+    check.dtype = DT[dn]
+    for k in (1, 2, 5):
+        got = run(x.view(S * W, V).to(DEV), scores, min(k, W * V))
+        check(got, x, scores, min(k, W * V))
+        assert float(got[0][0, 0]) == 0 and int(got[1][0, 0]) == 0 and int(got[2][0, 0]) == tok[0, 0]
+        assert float(got[0][1, 0]) == 0 and int(got[1][1, 0]) == 2
+        assert float(got[0][2, 0]) == 0 and int(got[2][2, 0]) == tok[2, 0]
+
+
 def test_equal_rows_prefer_the_lower_beam():
     S, W, V, k = 2, 6, 999, 12
     x, scores = make(S, 1, V, torch.float32, seed=4)
