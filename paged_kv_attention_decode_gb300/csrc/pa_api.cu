@@ -952,10 +952,11 @@ int pa_paged_attention_prefill_fp8(void* out, const void* q, const void* k_cache
 }
 
 // Cross attention's workspace, for chunks only: [rows of every sequence (without
-// cu_q_lens) | tile plan].
+// cu_q_lens) | tile plan, with the items dealt out behind its pair lists].
 size_t pa_cross_workspace_bytes(int num_seqs, int num_tokens, int max_q_len) {
     if (num_seqs <= 0 || num_tokens < 0 || max_q_len <= PA_VERIFY_MAX_Q) return 0;
-    return align256((static_cast<size_t>(num_seqs) + 1) * sizeof(int32_t)) + plan_bytes(num_seqs, num_tokens);
+    return align256((static_cast<size_t>(num_seqs) + 1) * sizeof(int32_t)) + plan_bytes(num_seqs, num_tokens) +
+           align256((1 + PA_DEAL_ROUNDS_ * PA_DEAL_CTAS_) * sizeof(int32_t));
 }
 
 int pa_paged_cross_attention(void* out, const void* q, const void* k_cache, const void* v_cache,

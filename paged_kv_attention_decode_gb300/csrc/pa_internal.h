@@ -40,6 +40,10 @@ inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, siz
 // rows, speculative-verify rows) run in the decode kernel; longer chunks run
 // in the prefill kernels.
 #define PA_VERIFY_MAX_Q_ 8
+// Cross attention's chunks are dealt out to the CTAs by their work in up to so many
+// rounds, to so many CTAs at the most.
+#define PA_DEAL_ROUNDS_ 8
+#define PA_DEAL_CTAS_ 256
 
 
 // Modified scores (all zero: none).  With raw = q . k:

@@ -491,11 +491,98 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const int32_t* __res
         }
         order[atomicAdd(&hist[k], 1)] = l;
     }
+    if (cross && tid == 0) seq_of_pair[pair_cap] = 0;   // (not dealt out: see cross_plan_kernel)
     // This kernel runs beside the decode plan, which it was launched after
     // (each writes its own part of the workspace, and the decode plan starts
     // only when all earlier work on the stream is complete).  Having waited
     // for it here, this grid's completion is also the decode plan's.
     pdl_wait();
+}
+
+// The same lists for cross attention of up to kCrossPlanSeqs sequences, a thread for
+// each: all pairs of a sequence cost the same, so that one pass over the others'
+// lengths and pairs gives a sequence's places in both lists (prefill_plan_kernel
+// takes 6.5 us for them).  More items than CTAs, but no more than PA_DEAL_ROUNDS_
+// times as many, are also dealt out: round by round the CTA with the least work so
+// far takes the longest item left.  deal[0] = CTAs << 16 | rounds (0: not dealt),
+// then an item, or -1, for every round and CTA; it lies behind the pair lists.
+constexpr int kCrossPlanSeqs = 256;
+static_assert(PA_DEAL_CTAS_ <= kCrossPlanSeqs, "a thread for each CTA");
+
+__global__ void __launch_bounds__(kCrossPlanSeqs) cross_plan_kernel(const int32_t* cu_q_lens, const int32_t* seq_lens,
+                                                                    int num_seqs, int num_tokens, int q_per_tile,
+                                                                    int32_t* offsets, int pair_cap, unsigned int* err,
+                                                                    int max_seq_len, int num_kv_heads, int ctas) {
+    __shared__ __align__(16) int s_tiles[kCrossPlanSeqs], s_pairs[kCrossPlanSeqs];
+    __shared__ __align__(16) int s_load[PA_DEAL_CTAS_];   // cost so far * 256 + CTA
+    __shared__ int s_cost[PA_DEAL_ROUNDS_ * PA_DEAL_CTAS_];
+    int32_t* order = offsets + num_seqs + 1;
+    int32_t* seq_of_pair = order + pair_cap;
+    int32_t* deal = seq_of_pair + pair_cap;
+    const int b = threadIdx.x;
+    pdl_trigger();
+    pdl_wait();   // (plain loads behind it: the rows may be the kernel's in front)
+    int c0 = 0, c1 = 0, n = 0;
+    if (b < num_seqs) {
+        c0 = cu_q_lens[b];
+        c1 = cu_q_lens[b + 1];
+        n = seq_lens[b];
+    }
+    const bool falls = __syncthreads_or(c1 < c0);
+    // (a chunk outside the num_tokens query rows, or on rows of another one, has no pair)
+    const bool ok = c0 >= 0 && c1 >= c0 && c1 <= num_tokens && !(falls && b < num_seqs && !rows_in_order(cu_q_lens, b));
+    if (!ok && c1 != c0) record_error(err, PA_DEVERR_SEQ_LEN_);
+    const int ql = ok ? c1 - c0 : 0;
+    const int tiles = ql > PA_VERIFY_MAX_Q_ ? (ql + q_per_tile - 1) / q_per_tile : 0;
+    const int pairs = (tiles + kTcTiles - 1) / kTcTiles;
+    const int cost = pairs > 0 && n > 0 && n <= max_seq_len ? cross_key_tiles(n) : 0;
+    s_tiles[b] = cost;
+    s_pairs[b] = pairs;
+    if (b < PA_DEAL_CTAS_) s_load[b] = b < ctas ? b : 0x7fffffff;   // (behind the last CTA: never the least)
+    __syncthreads();
+    int first = 0, place = 0, total = 0;   // pairs before b's by number, before b's by cost, of all
+#pragma unroll 4
+    for (int i = 0; i < num_seqs; ++i) {
+        const int p = s_pairs[i], t = s_tiles[i];
+        total += p;
+        if (i < b) first += p;
+        if (t > cost || (t == cost && i < b)) place += p;
+    }
+    if (b < num_seqs) {
+        offsets[b] = first;
+        for (int i = 0; i < pairs; ++i) {
+            seq_of_pair[first + i] = b;
+            order[place + i] = first + i;
+            // an item takes 1.3 us a key tile and 5.5 besides (query tiles, first and
+            // last products, output): as long as 4 tiles
+            if (place + i < PA_DEAL_ROUNDS_ * PA_DEAL_CTAS_) s_cost[place + i] = cost + 4;
+        }
+    }
+    const long long items = static_cast<long long>(total) * num_kv_heads;
+    const bool dealt = ctas <= PA_DEAL_CTAS_ && items > ctas && items <= static_cast<long long>(PA_DEAL_ROUNDS_) * ctas;
+    const int rounds = dealt ? static_cast<int>((items + ctas - 1) / ctas) : 0;
+    if (b == 0) {
+        offsets[num_seqs] = total;
+        deal[0] = ctas << 16 | rounds;
+    }
+    for (int r = 0; r < rounds; ++r) {
+        __syncthreads();
+        int mine = 0;
+        if (b < ctas) {
+            mine = s_load[b];
+            int less = 0;
+#pragma unroll 4
+            for (int i = 0; i < ctas; i += 4) {
+                const int4 o = *reinterpret_cast<const int4*>(s_load + i);
+                less += (o.x < mine) + (o.y < mine) + (o.z < mine) + (o.w < mine);
+            }
+            const int item = r * ctas + less;
+            deal[1 + r * ctas + b] = item < items ? item : -1;
+            if (item < items) mine += s_cost[item / num_kv_heads] * 256;
+        }
+        __syncthreads();
+        if (b < ctas) s_load[b] = mine;
+    }
 }
 
 // FP8 (E4M3) cache: the blocks of the chunks the plan listed, widened to
@@ -758,7 +845,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // the CTA's k-th item: kNoMoreItems past the end, -1 when round k has
     // none for this CTA (a partial last round)
     constexpr int kNoMoreItems = -2;
+    // (cross attention: dealt out, and to as many CTAs as there are -- max_q_len may
+    // have been too low)
+    const int32_t* deal = plan + p.num_seqs + 1 + 2 * p.pair_cap;
+    const int rounds = kMode == kCross && deal[0] >> 16 == ctas ? deal[0] & 0xffff : 0;
     auto item_at = [&](int k) -> int {
+        if (kMode == kCross && rounds > 0) return k < rounds ? deal[1 + k * ctas + static_cast<int>(blockIdx.x)] : kNoMoreItems;
         const long long base = static_cast<long long>(k) * ctas;
         if (base >= total_items) return kNoMoreItems;
         const int i = static_cast<int>(blockIdx.x);
@@ -1294,11 +1386,14 @@ cudaError_t launch_t(const PrefillParams& p, int32_t* plan, const CUtensorMap& k
                       copy ? *copy : none, p.max_seq_len, p.max_blocks, p.mod.window, p.split, sm_count(),
                       p.decode_weight, p.cross);
     };
-    e = p.cross ? plan_args([&](auto... a) {
+    e = p.cross && p.num_seqs <= kCrossPlanSeqs
+            ? launch_pdl(cross_plan_kernel, dim3(1), dim3(kCrossPlanSeqs), 0, s, p.cu_q_lens, p.seq_lens, p.num_seqs,
+                         num_tokens, p.q_per_tile, plan, p.pair_cap, p.err, p.max_seq_len, p.num_kv_heads, sm_count())
+        : p.cross ? plan_args([&](auto... a) {
         prefill_plan_kernel<<<1, 1024, 0, s>>>(a...);
         return cudaGetLastError();
     })
-                : plan_args([&](auto... a) { return launch_pdl(prefill_plan_kernel, dim3(1), dim3(1024), 0, s, a...); });
+                  : plan_args([&](auto... a) { return launch_pdl(prefill_plan_kernel, dim3(1), dim3(1024), 0, s, a...); });
     if (e != cudaSuccess) return e;
     if (copy && copy->fp4) {
         e = launch_widen_fp4(*copy, p.seq_lens, p.max_blocks, p.num_kv_heads, D, std::is_same<T, __half>::value ? 0 : 1,

@@ -56,7 +56,8 @@ def test_cross_workspace(lib):
     assert pa.cross_workspace_bytes(64, 512, 8) == 0 and pa.cross_workspace_bytes(0, 0, 100) == 0
     assert pa.cross_workspace_bytes(64, -1, 100) == 0
     n = pa.cross_workspace_bytes(64, 4000, 100)
-    assert 4 * (65 + 65 + 2 * (1000 + 64)) <= n <= 4 * (65 + 65 + 2 * (1000 + 64)) + 1024
+    lists = 4 * (65 + 65 + 2 * (1000 + 64) + 1 + 8 * 256)
+    assert lists <= n <= lists + 1024
 
 
 SELECT = dict(sc=F, par=F, tok=F, fin=None, x=F, stride=200000, cum=F, ended=None, end=-1, S=2, W=4, V=200000, k=8, dt=0,

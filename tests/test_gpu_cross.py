@@ -327,3 +327,21 @@ def test_two_streams_at_once():
         check(got[0], *c[:5], 0.125)
         assert all(torch.equal(g, got[0]) for g in got)
     assert pa.device_error() == 0
+
+
+@pytest.mark.parametrize("low", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,chunks", [(8, 8, 20), (8, 8, 160), (64, 64, 3), (64, 64, 19), (16, 1, 170),
+                                           (2, 2, 256), (2, 2, 257), (1, 1, 600)])
+def test_more_chunks_than_ctas(Hq, Hkv, chunks, low):
+    """Items in two rounds and more, up to and past those that are dealt out by
+    their work; also with max_q_len below the chunks' lengths."""
+    rng = np.random.default_rng(chunks)
+    lens = [int(x) for x in rng.integers(0, 400, chunks)]
+    qlens = [int(x) for x in rng.integers(9, 30 if Hkv > 1 else 90, chunks)]
+    q, pools, tables = build(lens, qlens, Hq, Hkv, 64, torch.float16, seed=chunks)
+    t, n, cu = dev(tables, lens, qlens)
+    out = pa.paged_cross_attention(q.to(DEV), pools[0].to(DEV), pools[1].to(DEV), t, n, 0.125, max_enc_len=400,
+                                   cu_q_lens=cu, max_q_len=9 if low else max(qlens))
+    torch.cuda.synchronize()
+    assert pa.device_error() == 0
+    check(out, q, pools, tables, lens, qlens, 0.125)
