@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kCrossPlanSeqs) cross_plan_kernel(const int32_
             order[place + i] = first + i;
             // an item takes 1.3 us a key tile and 5.5 besides (query tiles, first and
             // last products, output): as long as 4 tiles
-            if (place + i < PA_DEAL_ROUNDS_ * PA_DEAL_CTAS_) s_cost[place + i] = cost + 4;
+            if (place + i < PA_DEAL_ROUNDS_ * PA_DEAL_CTAS_) s_cost[place + i] = min(cost + 4, 1 << 19);   // (eight of them times 256 fit)
         }
     }
     const long long items = static_cast<long long>(total) * num_kv_heads;
