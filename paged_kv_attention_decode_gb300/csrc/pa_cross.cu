@@ -167,6 +167,9 @@ struct CrossState {
                     for (int i = lane; i < n16; i += 32) z[i] = make_uint4(0, 0, 0, 0);
                 }
             }
+            // (these stores come before the copy that refills the slot; a step with a
+            // block outside the pool need not be the warp's last)
+            fence_proxy_async_smem();
             __syncwarp();
         }
         const int tok = (lane & 7) + ((lane >> 4) & 1) * 8, dsub = ((lane >> 3) & 1) * 8;
