@@ -458,9 +458,14 @@ __device__ __forceinline__ void join_request(const BeamSelectParams& p, int s, c
     auto beam_of = [&](int g) { return static_cast<int>((static_cast<float>(g) + 0.5f) * inv_row); };
     auto cand_of = [&](int beam, u64 key) {
         const float x = unordered(static_cast<uint32_t>(key >> 32));
-        const Two lg = s_log[beam];
-        const Two lp = two_add(two_sum(x, -s_most[beam]), {-lg.hi, -lg.lo});
-        const Two t = two_add({s_score[beam], 0.f}, lp);
+        const Two lg = s_log[beam], less{-lg.hi, -lg.lo};
+        const float most = s_most[beam], score = s_score[beam];
+        Two t;
+        if (x - most >= -FLT_MAX) {
+            t = two_add({score, 0.f}, two_add(two_sum(x, -most), less));
+        } else {   // (this difference alone is below the range: the large numbers of opposite signs first)
+            t = two_add(two_add(two_sum(score, -most), {x, 0.f}), less);
+        }
         // (below fp32's range: -inf, and no candidate)
         return t.hi >= -FLT_MAX ? Cand{order_of({fminf(t.hi, FLT_MAX), t.lo}), key, beam} : Cand{0, 0, 0};
     };
