@@ -671,6 +671,8 @@ typedef enum { PA_CACHE_16BIT = 0, PA_CACHE_FP8 = 1, PA_CACHE_FP4 = 2 } pa_cache
  * lives; the prompt's whole blocks may be shared).
  *   tables_out    int32 [num_seqs * num_beams, max_blocks_per_seq]: block_tables
  *                 itself (in place) or an array apart from it.
+ *                 max_blocks_per_seq is below 2^27 (16 tokens a block: lengths are
+ *                 32-bit numbers), num_beams * max_blocks_per_seq at most 2^30.
  *   seq_lens      int32 [num_seqs * num_beams]: tokens cached, one length for all
  *                 rows of a request.
  *   parents       int32 [num_seqs, num_beams], as pa_beam_select gives them.

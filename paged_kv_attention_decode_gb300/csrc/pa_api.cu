@@ -1118,8 +1118,9 @@ int pa_beam_reorder(int32_t* tables_out, const int32_t* block_tables, int max_bl
     if (cache_kind != PA_CACHE_16BIT && cache_kind != PA_CACHE_FP8 && cache_kind != PA_CACHE_FP4)
         return PA_ERR_UNSUPPORTED;
     if (head_dim != 128 && (head_dim != 64 || cache_kind == PA_CACHE_FP8)) return PA_ERR_UNSUPPORTED;
-    if (num_seqs < 0 || num_seqs > kMaxGrid || num_beams <= 0 || max_blocks_per_seq <= 0 || num_layers < 0 ||
-        num_blocks <= 0 || num_blocks > kMaxPoolBlocks || num_kv_heads <= 0 || num_kv_heads > kMaxGrid)
+    if (num_seqs < 0 || num_seqs > kMaxGrid || num_beams <= 0 || max_blocks_per_seq <= 0 ||
+        max_blocks_per_seq > kMaxPoolBlocks || num_layers < 0 || num_blocks <= 0 || num_blocks > kMaxPoolBlocks ||
+        num_kv_heads <= 0 || num_kv_heads > kMaxGrid)
         return PA_ERR_INVALID_ARG;
     // a request's table entries are counted in 32 bits
     if (static_cast<long long>(num_beams) * max_blocks_per_seq > (1LL << 30)) return PA_ERR_INVALID_ARG;
