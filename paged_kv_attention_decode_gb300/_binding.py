@@ -752,6 +752,11 @@ def _window(window) -> int:
     return max(-2 ** 31, min(int(window), 2 ** 31 - 1))
 
 
+def _upper(bound) -> int:
+    """An upper bound of lengths as a C int: past its range, the largest (no bound) or a negative one (refused)."""
+    return max(-2 ** 31, min(int(bound), 2 ** 31 - 1))
+
+
 def _pool16(q, k_cache, v_cache):
     NB, bs, Hkv, D = k_cache.shape
     if q.shape[2] != D or v_cache.shape != k_cache.shape or k_cache.dtype != q.dtype or v_cache.dtype != q.dtype:
@@ -935,8 +940,12 @@ def paged_cross_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
         max_q_len = T // B
     elif max_q_len is None:
         max_q_len = int((cu_q_lens[1:] - cu_q_lens[:-1]).max().item()) if B else 0
+    else:
+        max_q_len = _upper(max_q_len)
     if max_enc_len is None:
         max_enc_len = int(enc_lens.max().item()) if B else 0
+    else:
+        max_enc_len = _upper(max_enc_len)
     if out is None:
         out = torch.empty_like(q)
     lib = _lib or load_library()
@@ -992,7 +1001,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int, finish
     code = _LOGITS.get(dtype)
     ended = _U8 if finished is None else finished.dtype
     if not (dev >= 0 and _cuda_device() == dev and code is not None and len(shape) == 2 and shape[0] == S * W
-            and (rows.is_contiguous() or V <= 1 or rows.stride(1) == 1) and num_out > 0
+            and (rows.is_contiguous() or V <= 1 or rows.stride(1) == 1) and 0 < num_out < 2 ** 31
             and scores.get_device() == dev and scores.dtype == _F32 and scores.is_contiguous()
             and (finished is None or (finished.get_device() == dev and finished.shape == scores.shape
                                       and (ended == _U8 or ended == _BOOL) and finished.is_contiguous()
@@ -1003,7 +1012,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int, finish
                 (code is not None, f"unsupported dtype {dtype}"),
                 (len(shape) == 2 and shape[0] == S * W and (V <= 1 or rows.stride(1) == 1),
                  "logits: [S * W, V], or [S, W, V] with evenly spaced rows, dense within a row"),
-                (num_out > 0, "num_out: at least 1"),
+                (0 < num_out < 2 ** 31, "num_out: at least 1, and an int"),
                 (scores.dtype == _F32 and scores.is_contiguous(), "scores: contiguous float32 [S, W]"),
                 (finished is None or (finished.shape == scores.shape and (ended == _U8 or ended == _BOOL)
                                       and finished.is_contiguous()), "finished: contiguous uint8 or bool [S, W]"),

@@ -508,7 +508,7 @@ cudaError_t launch_cross(CrossParams p, const CUtensorMap& kmap, const CUtensorM
     // 12.4, 11.8, 27.7; 64 items 18.3, 15.0, 22.2, 46.3; 128 items 22.5, 28.9, 41.0,
     // 82.9 (one of 4 warps: 29.0); 192 items 36.6 (one of 4 warps: 33.3).
     const long long items = static_cast<long long>(p.num_seqs) * p.num_kv_heads * p.col_chunks;
-    const int blocks = (p.max_len + 15) / 16;
+    const int blocks = p.max_len / 16 + (p.max_len % 16 != 0);   // (a bound up to the largest int)
     const bool few = items <= sm_count();
     int splits = 1;
     while (few && splits < kMaxSplits && 2 * splits * items <= (splits < 4 ? 128 : 96) && blocks >= splits * 16) splits *= 2;

@@ -1408,10 +1408,12 @@ cudaError_t launch_t(const PrefillParams& p, int32_t* plan, const CUtensorMap& k
     }
     // upper bound on the work items: each listed chunk (length > 8) has at
     // most ceil(len / q_per_tile) <= len / 2 tiles, and there are at most
-    // max_q_len tokens per chunk; an item is a pair of tiles.  One CTA per SM.
+    // max_q_len tokens per chunk (a bound that may be any int); an item is a pair
+    // of tiles.  One CTA per SM.
     const long long bound_tiles = std::min<long long>(static_cast<long long>(num_tokens) / 2 + 1,
                                                       static_cast<long long>(p.num_seqs) *
-                                                          ((max_q_len + p.q_per_tile - 1) / p.q_per_tile));
+                                                          ((static_cast<long long>(max_q_len) + p.q_per_tile - 1) /
+                                                           p.q_per_tile));
     const long long items = (bound_tiles + p.num_seqs) / kTcTiles * p.num_kv_heads + p.num_kv_heads;
     const int grid = static_cast<int>(std::max<long long>(1, std::min<long long>(items, sm_count())));
     return launch_pdl(kern, dim3(grid), dim3(kTcThreads), smem, s, p, plan, kmap, vmap, qmap);
