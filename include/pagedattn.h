@@ -597,16 +597,20 @@ int pa_get_device_error(int* code, int clear, void* stream);
  *   cu_q_lens     int32 [num_seqs + 1]: sequence b owns rows cu_q_lens[b] ..
  *                 cu_q_lens[b+1]-1 (it must not fall); or NULL: num_tokens /
  *                 num_seqs rows each (max_q_len is then ignored).
- *   max_q_len, max_enc_len  host-side upper bounds.
+ *   max_q_len, max_enc_len  host-side upper bounds (2^31 - 1: none).  max_q_len
+ *                 says whether chunks of more than PA_VERIFY_MAX_Q rows are looked
+ *                 for, and above that only sizes the launch.
  *   workspace     pa_cross_workspace_bytes(...) bytes, 256-byte aligned; none
  *                 (NULL) while no sequence has more than PA_VERIFY_MAX_Q rows.
  * Sequences of at most PA_VERIFY_MAX_Q rows take one launch that splits long
  * states over a cluster of CTAs; longer chunks run in the tensor-core prefill
  * kernel.  Rows of no sequence are left as they were.  Errors on the device: an
  * enc_len below 0, above max_enc_len or past the table sets PA_DEVERR_SEQ_LEN and
- * gives rows of zeros; so does a sequence with rows outside 0 .. num_tokens - 1
- * or more of them than max_q_len, which are not written; blocks outside the pool
- * set PA_DEVERR_BLOCK_ID and contribute nothing.
+ * gives rows of zeros.  A sequence with rows outside 0 .. num_tokens - 1 sets it
+ * too, and none of its rows is written; so does, while max_q_len <=
+ * PA_VERIFY_MAX_Q, one with more rows than max_q_len.  (With a larger max_q_len
+ * longer chunks are computed like any other, only on fewer CTAs.)  Blocks outside
+ * the pool set PA_DEVERR_BLOCK_ID and contribute nothing.
  */
 int pa_paged_cross_attention(void* out, const void* q, const void* k_cache, const void* v_cache,
                              const int32_t* block_tables, int max_blocks_per_seq, const int32_t* enc_lens,

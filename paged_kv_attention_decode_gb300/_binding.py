@@ -925,8 +925,9 @@ def paged_cross_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     cache: every row of sequence b sees its enc_lens[b] states (none: a row of
     zeros).  The beams of a request, or a prompt's tokens, are rows of one
     sequence: T / B rows each, or, with cu_q_lens, rows cu_q_lens[b] ..
-    cu_q_lens[b + 1] - 1 (at most max_q_len; both lengths are read from the
-    device when they are not given)."""
+    cu_q_lens[b + 1] - 1.  max_q_len and max_enc_len are read from the device when
+    they are not given; a max_q_len of 8 or less says that there are no longer
+    chunks (one that is there all the same is flagged and not written)."""
     if stream is not None:
         return _given(stream, paged_cross_attention, q, k_cache, v_cache, block_tables, enc_lens, scale, max_enc_len,
                       cu_q_lens, max_q_len, out, workspace)

@@ -24,3 +24,26 @@ def test_bounds_that_say_nothing(qlens, bound):
     torch.cuda.synchronize()
     check(out, q, pools, tables, lens, qlens, 0.125)
     assert pa.device_error() == 0
+
+
+@pytest.mark.parametrize("max_q", [1, 5, 8, 9, 40, 10 ** 6])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (64, 1)])
+def test_rows_beyond_max_q_len(Hq, Hkv, max_q):
+    """With max_q_len of 8 or less, more rows than that are flagged and not written;
+    above, longer chunks are computed."""
+    lens, qlens = [70, 300, 33, 500, 0, 64], [1, 150, 5, 41, 60, 8]
+    q, pools, tables = build(lens, qlens, Hq, Hkv, 64, torch.float16, seed=21)
+    t, n, cu = dev(tables, lens, qlens)
+    out = torch.full(q.shape, 7.0, dtype=q.dtype, device=DEV)
+    pa.paged_cross_attention(q.to(DEV), pools[0].to(DEV), pools[1].to(DEV), t, n, 0.125, max_enc_len=500,
+                             cu_q_lens=cu, max_q_len=max_q, out=out)
+    torch.cuda.synchronize()
+    assert pa.device_error() == (SEQ_LEN if max_q <= 8 else 0)
+    at = 0
+    for b, c in enumerate(qlens):
+        rows = slice(at, at + c)
+        at += c
+        if c <= max_q or max_q > 8:
+            check(out[rows], q[rows], pools, tables[b:b + 1], lens[b:b + 1], [c], 0.125)
+        else:
+            assert bool((out[rows] == 7).all())
