@@ -673,6 +673,14 @@ typedef enum { PA_CACHE_16BIT = 0, PA_CACHE_FP8 = 1, PA_CACHE_FP4 = 2 } pa_cache
  * they had together, and these are freed together.  Before the first call every
  * row must have a last block of its own (one of them filled, if only one beam
  * lives; the prompt's whole blocks may be shared).
+ * With pa_block_manager.h: a row is a sequence (pa_bm_fork of the one that has the
+ * prompt), whose blocks are allotted ahead of the steps by pa_bm_append_tokens
+ * with an id that no prompt has and pa_bm_allocate_slots (its copies come before
+ * the first reordering; they give every row its last block).  From the first
+ * reordering on the device's tables are their own: only the entries of newly
+ * allotted blocks are copied into them, at their places in the row.  A beam that
+ * dies leaves whole blocks that no table names; they stay allotted until the
+ * request's sequences are freed, all of them together.
  *   tables_out    int32 [num_seqs * num_beams, max_blocks_per_seq]: block_tables
  *                 itself (in place) or an array apart from it.
  *                 max_blocks_per_seq is below 2^27 (16 tokens a block: lengths are
