@@ -591,12 +591,18 @@ int pa_get_device_error(int* code, int clear, void* stream);
  * states (0 or more) and any number of query rows, each of which sees every
  * state: out[r, h] = sum_t softmax_t(scale * q[r, h] . k_t) v_t over t = 0 ..
  * enc_lens[b] - 1.  The beams of a request, or the tokens of a decoder prompt,
- * are rows of one sequence, so that its states are read once for all of them.
+ * are rows of one sequence, so that its states are read once for 16 (row, query
+ * head of a KV head) pairs, or for a tile of a chunk, and not for every row.  The
+ * softmax weights are rounded to the queries' type before their product with v, as
+ * in the self-attention calls; scores, maxima and sums are fp32.
  *   out, q        [num_tokens, num_q_heads, head_dim]
  *   enc_lens      int32 [num_seqs]; 0 gives rows of zeros.
  *   cu_q_lens     int32 [num_seqs + 1]: sequence b owns rows cu_q_lens[b] ..
- *                 cu_q_lens[b+1]-1 (it must not fall); or NULL: num_tokens /
- *                 num_seqs rows each (max_q_len is then ignored).
+ *                 cu_q_lens[b+1]-1; or NULL: num_tokens / num_seqs rows each
+ *                 (max_q_len is then ignored).  It must not fall: where it does,
+ *                 PA_DEVERR_SEQ_LEN is set, chunks that begin before an earlier
+ *                 sequence's end are not written, and a row that several short
+ *                 sequences claim holds the result of any of them.
  *   max_q_len, max_enc_len  host-side upper bounds (2^31 - 1: none).  max_q_len
  *                 says whether chunks of more than PA_VERIFY_MAX_Q rows are looked
  *                 for, and above that only sizes the launch.
@@ -624,8 +630,12 @@ size_t pa_cross_workspace_bytes(int num_seqs, int num_tokens, int max_q_len);
  * Beam search: the num_out best continuations of every request.  Candidate
  * (beam w, token v) of request s scores scores[s, w] + x - log(sum of exp) of row
  * w's logits x (a log-softmax); the best come first, ties go to the lowest
- * w * vocab + v.  Scores are compared as sums of two fp32 numbers (about 48 bits)
- * and rounded once; one below fp32's range is -inf.
+ * w * vocab + v.  The candidates of one beam are ordered by their logits, exactly.
+ * The beams' logarithms are right to about 2^-24 absolute (sums of fp32
+ * exponentials; 3e-7 at most in rows of up to 2^20 normal logits), and with them
+ * scores are compared as sums of two fp32 numbers: candidates of different beams
+ * closer than the logarithms' errors may come in either order.  Scores are rounded
+ * once; one below fp32's range is -inf.
  *   out_scores, out_parents, out_tokens  fp32, int32, int32 [num_seqs, num_out];
  *                 a parent is a beam of the request, 0 .. num_beams - 1.
  *   logits        [num_seqs * num_beams, vocab] of `dtype` (fp16, bf16 or fp32),

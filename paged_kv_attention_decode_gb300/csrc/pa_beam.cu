@@ -31,13 +31,21 @@ constexpr float kLog2e = 1.4426950408889634f;
 // the first kernel took three times as many instructions.)  64 requests of 8 beams,
 // 131072 tokens, 16 bits: 28.5 us, of which the first kernel takes 21 (134 MB at 6.4
 // TB/s, 0.94 of the copy rate) and the second, whose chain of loads and meetings one
-// request cannot shorten, 7.5; with lists it was 49.
+// request cannot shorten, 7.5; with lists it was 49.  The first kernel runs 16 CTAs an
+// SM, at 64 registers a thread, and spills for it (bytes stored and loaded a thread:
+// bf16 78 and 100, fp16 44 and 44, fp32 36 and 40): with 14, 12 and 10 CTAs, where
+// less spills, and with 10 nothing, the call takes 29.5, 30.6 and 31.9 us, not 28.7.
 //
-// Within a row the order of scores is the order of logits, so the first kernel
-// needs no sum.  Across rows, scores are compared as sums of two fp32 numbers: a sum
-// of fp32 exponentials is good to 2^-24 (the terms' errors are independent), but a
-// score of magnitude 16 rounded to fp32 only to 2^-21, and the k best lie close
-// together.
+// Within a row the order of scores is the order of logits, and the logarithm of the
+// row's sum cancels, so that a beam's own candidates are in their order whatever the
+// sum's error.  Across rows, scores are compared as sums of two fp32 numbers, as a
+// score of magnitude 16 rounded to fp32 is good to 2^-21 only, and the k best lie close
+// together.  The logarithm in them is less exact than their 48 bits: fp32 exponentials
+// and sums leave it off by about 2^-24 (64 rows each of 1000 to 2^20 normal logits of
+// deviations 0.1 to 3, the three types: mean 0 to 0.9, deviation 0.5 to 1.1, at most
+// 5, in 2^-24; log2 e rounded to fp32 alone moves every exponent by 1.3e-8 of itself
+// in one direction).  Candidates of different beams closer than that may come in
+// either order.
 //
 // -inf (and NaN, which counts as -inf) is no candidate: a request with fewer than k
 // finite ones fills up with the lowest other indices.
@@ -337,9 +345,12 @@ __device__ const float kLogTable[32][2] = {
     {0.5685047507286072f, -1.5375938744455198e-08f}, {0.5860490202903748f, 2.4713203927717586e-08f}, {0.603290855884552f, -4.446467638530294e-09f}, {0.6202403903007507f, 1.9451107391432743e-08f},
     {0.6369074583053589f, 3.931710068627581e-09f}, {0.6533012986183167f, -2.660557107958539e-08f}, {0.669430673122406f, -1.9179775989641712e-08f}, {0.6853039860725403f, 1.702637852929456e-08f},
 };
-// The logarithm of a positive normal x, to about 2^-30 absolute: x = 2^e m, m in [1, 2)
-// near c = (65 + 2 i) / 64, log m = log c + log(1 + (m - c) / c).  Near 1 itself, c =
-// 1: a beam with one candidate left scores what it scored.
+// The logarithm of a positive normal x, to 2^-29 absolute: x = 2^e m, m in [1, 2) near
+// c = (65 + 2 i) / 64, log m = log c + log(1 + (m - c) / c), from a table of log c and
+// the series of log(1 + u) (a table-driven logarithm as in P. T. P. Tang, ACM
+// Transactions on Mathematical Software 16, 1990, with the midpoints of 32 intervals,
+// Taylor coefficients and sums of two fp32 numbers).  Near 1 itself, c = 1: a beam with one
+// candidate left scores what it scored.
 __device__ __forceinline__ Two two_log(float x, const Two* table) {
     const uint32_t b = __float_as_uint(x);
     const bool near_one = x > 0.984375f && x < 1.03125f;

@@ -3,21 +3,24 @@
 //
 // Sequence b has n encoder states (keys) and c query rows, and every row sees
 // every state: out[r, h] = sum_t softmax_t(scale q[r, h] . k_t) v_t, t < n.  The
-// beams of one request are rows of one sequence, so its states are read once
-// for all of them.  Rows and query heads of a KV head together are columns of
-// two products, S^T = K Q^T and O^T += V^T P^T (mma.sync m16n8k16: 16 states, one
-// block, are the M dimension and 8 or 16 columns the N; with so few columns the
-// work is bound by the states' bytes).  Longer chunks take the tcgen05 kernel.
+// beams of one request are rows of one sequence.  Rows and query heads of a KV
+// head together are columns of two products, S^T = K Q^T and O^T += V^T P^T
+// (mma.sync m16n8k16: 16 states, one block, are the M dimension and 8 or 16 columns
+// the N; with so few columns the work is bound by the states' bytes).  The states
+// are read once for 16 columns; with more, every 16 are another CTA's, next to one
+// another in the grid: 64 requests over 512 to 4096 states, 32/8 heads, 4 rows (16
+// columns) 96 us, 8 rows 125; 32 requests of 8 rows, 64/1 heads (512 columns) 128,
+// by the products.  Longer chunks take the tcgen05 kernel.
 //
 // One launch, no plan and no second kernel: a CTA, or a cluster of `splits` CTAs,
 // takes one (sequence, KV head, chunk of columns); its warps take the blocks in
 // turn, each with its own ring of TMA tiles and its own running maximum, sum and
 // accumulator.  The warps of a CTA join theirs in shared memory, the CTAs of a
 // cluster through distributed shared memory, each CTA writing its share of the
-// output.  Measured: 128 rows over 128 to 2048 states, 32/32 heads of 128, fp16, 349
-// us (7.15 TB/s of states, at the copy rate and above); 64 requests of 4 beams over
-// 512 to 4096 states, 32/8 heads, bf16, 95 us (6.4 TB/s, 0.95 of the copy rate); 1
-// request of 4 beams, 1200 states, 12 heads of 64, 5.1 us (launch, four dependent
+// output.  Measured: 128 rows over 128 to 2048 states, 32/32 heads of 128, fp16, 350
+// us (7.1 TB/s of states, at the copy rate and above); 64 requests of 4 beams over
+// 512 to 4096 states, 32/8 heads, bf16, 95 us (6.4 TB/s, 0.94 of the copy rate); 1
+// request of 4 beams, 1200 states, 12 heads of 64, 5.3 us (launch, four dependent
 // loads, a step and a half a warp, the join).
 #include <algorithm>
 #include <type_traits>
@@ -29,7 +32,9 @@ namespace pa {
 namespace {
 
 constexpr int kMaxSplits = 8;         // CTAs of a cluster (the portable limit)
-constexpr int kSortMax = 128;         // sequences that a CTA orders by length, one a thread
+// Sequences that a CTA orders by length, one a thread (4 rows over 512 to 4096 states,
+// 32/8 heads: 128 sequences 1.034 of the bytes' time, in order; 129, as they come, 1.049).
+constexpr int kSortMax = 128;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLazyRescaleLog2 = 8.f;   // a column's reference maximum moves only when it has grown by this much
 
@@ -133,7 +138,10 @@ struct CrossState {
                     }
                 }
         }
-        // P, rounded to T for the product with V (weights of 0 to 2^8), its sum kept in fp32
+        // P, rounded to T for the product with V (weights of 0 to 2^8), its sum kept in
+        // fp32: matrix operands have 16 bits, and this rounding weighs as much as the
+        // output's own (both together 1.4 times that alone: against 64 bits 2.3e-3 of
+        // the norm in bf16, 2.9e-4 in fp16)
         uint32_t b0[NB][NT], b1[NB][NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {

@@ -658,7 +658,9 @@ __global__ void __launch_bounds__(kWidenThreads) widen_chunk_blocks_kernel(const
 // their keys are masked and their V rows cleared.  kCross (cross attention):
 // every query sits at the last key, so that all tiles of a chunk read all keys
 // and only the last key tile is masked; a sequence without keys gets rows of
-// zeros.
+// zeros.  (P is rounded to T for its product, here as in every kind: half of the
+// output's error against 64 bits, 2.3e-3 of the norm in bf16 and 2.9e-4 in fp16;
+// the other half is the output's own rounding.)
 template <typename T, int D, int kMode>
 __global__ void __launch_bounds__(kTcThreads, 1)
     prefill_tc_kernel(const PrefillParams p, const int32_t* plan,
