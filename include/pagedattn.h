@@ -634,8 +634,9 @@ size_t pa_cross_workspace_bytes(int num_seqs, int num_tokens, int max_q_len);
  * The beams' logarithms are right to about 2^-24 absolute (sums of fp32
  * exponentials; 3e-7 at most in rows of up to 2^20 normal logits), and with them
  * scores are compared as sums of two fp32 numbers: candidates of different beams
- * closer than the logarithms' errors may come in either order.  Scores are rounded
- * once; one below fp32's range is -inf.
+ * closer than the logarithms' errors may come in either order (rows with the same
+ * logits in the same places tie exactly).  Scores are rounded once; one below
+ * fp32's range is -inf.
  *   out_scores, out_parents, out_tokens  fp32, int32, int32 [num_seqs, num_out];
  *                 a parent is a beam of the request, 0 .. num_beams - 1.
  *   logits        [num_seqs * num_beams, vocab] of `dtype` (fp16, bf16 or fp32),
